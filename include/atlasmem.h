@@ -78,6 +78,9 @@ typedef enum {
 } atlasmem_memory_kind;
 typedef enum { ATLASMEM_PER_TOKEN = 0, ATLASMEM_PER_CHUNK = 1 } atlasmem_gate_mode;
 typedef enum { ATLASMEM_F32 = 0, ATLASMEM_BF16 = 1 } atlasmem_dtype;
+/* Order of a [batch, heads, T, d] tensor in memory: as written, or [batch, T, heads, d] (the rows of
+ * a projection of all heads). */
+typedef enum { ATLASMEM_HEADS_FIRST = 0, ATLASMEM_TOKENS_FIRST = 1 } atlasmem_layout;
 
 /* Operand precision of the matrix-core products (state and accumulation are fp32 always).
  * BF16X3 splits every fp32 operand x into hi = bf16(x), lo = bf16(x - hi) and sums
@@ -405,6 +408,57 @@ atlasmem_status atlasmem_short_conv(const void* X, int32_t in_dtype, int64_t M, 
 atlasmem_status atlasmem_gates(const void* U, int64_t B, int64_t T, int32_t d_model, int32_t heads,
                                int32_t n_gates, const float* Wg, const float* bg, const float* scale,
                                int32_t chunk, float* out, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Around the memory: a token mixer without an inner loop, the normalisation of the rows it or a
+ * memory answers with, and the outer loss whose gradient trains all of them.  Every call is
+ * asynchronous on `stream`, works on the device current at the call (where its arrays lie), never
+ * allocates, and can be captured into a graph.  Calls that run at the same time need a workspace
+ * each.  No array that a call writes may overlap another of its arrays (E_INVALID), but where
+ * stated.  Arrays are aligned to their elements; 16-byte aligned rows are read faster.
+ * ------------------------------------------------------------------------------------- */
+
+/* Linear attention with a decay for each head: the linear memory with a Hebbian write in place of
+ * the gradient step (titans-pytorch-mlx README, Core Equations: W_t = (1 - alpha) W_{t-1} + S_t, with
+ * S_t = v_t k_t^T), per (b, h) and with lambda = exp(log_decay[h]):
+ *   W_t = lambda W_{t-1} + v_t k_t^T,   Y[t] = scale W_t q_t
+ * Calls of at most 16 tokens run the recurrence (each state read and written once); longer ones run
+ * in chunks of 64 tokens on the matrix cores.
+ *   Q, K: [batch, heads, T, d_key], V, Y: [batch, heads, T, d_value] of `dtype`, in `layout`;
+ *         d_key, d_value 1..128
+ *   log_decay: fp32 [heads], <= 0 (0: nothing is forgotten; -INFINITY: only the own token is read)
+ *   lengths: int32 [batch] or NULL (T each): tokens of each sequence of a padded batch, clamped to
+ *         0..T; later rows are not read and their Y is zero
+ *   W0:   fp32 [batch, heads, d_value, d_key], the state before the first token, or NULL (zeros)
+ *   W_T:  the same shape, the state behind each sequence's last token, or NULL; may be W0
+ *   workspace: atlasmem_linear_attention_workspace_bytes(..., backward = 0) bytes, 16-byte aligned
+ *         (NULL where that is 0)
+ * bf16 inputs enter the products as they are, fp32 ones as three bf16 planes (24 bits); states and
+ * sums are fp32, Y is rounded once.  Errors: E_INVALID for bad sizes, enums, null or overlapping
+ * pointers, a short workspace; E_SHAPE beyond the limits (batch * heads <= 2^20).
+ * The workspace function returns -1 for sizes that the calls refuse. */
+int64_t atlasmem_linear_attention_workspace_bytes(int32_t dtype, int32_t batch, int32_t heads, int64_t T,
+                                                  int32_t d_key, int32_t d_value, int32_t backward);
+atlasmem_status atlasmem_linear_attention(const void* Q, const void* K, const void* V, int32_t dtype, int32_t batch,
+                                          int32_t heads, int64_t T, int32_t d_key, int32_t d_value, int32_t layout,
+                                          const float* log_decay, const int32_t* lengths, float scale, const float* W0,
+                                          void* Y, float* W_T, void* workspace, int64_t workspace_bytes,
+                                          void* stream);
+
+/* Gradients of an outer loss through atlasmem_linear_attention, given dY = dL/dY and the adjoint dW_T
+ * of the final state (NULL: zero).
+ *   dQ, dK, dV: of `dtype`, in the shape and layout of Q, K, V; zero behind a sequence's last token
+ *   dW0: fp32 like W0, or NULL; may be dW_T
+ *   dlog_decay: fp32 [heads], or NULL (not computed)
+ *   workspace: atlasmem_linear_attention_workspace_bytes(..., backward = 1) bytes
+ * Sums run in one order: equal calls give equal bits.  Errors as above. */
+atlasmem_status atlasmem_linear_attention_backward(const void* Q, const void* K, const void* V, int32_t dtype,
+                                                   int32_t batch, int32_t heads, int64_t T, int32_t d_key,
+                                                   int32_t d_value, int32_t layout, const float* log_decay,
+                                                   const int32_t* lengths, float scale, const float* W0,
+                                                   const void* dY, const float* dW_T, void* dQ, void* dK, void* dV,
+                                                   float* dW0, float* dlog_decay, void* workspace,
+                                                   int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

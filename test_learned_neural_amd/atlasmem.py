@@ -18,6 +18,7 @@ OK, E_INVALID, E_SHAPE, E_UNSUPPORTED, E_DEVICE, E_NOMEM, E_NONFINITE = range(7)
 LINEAR, MLP2_SILU, MLP2_SILU_RESIDUAL, MLP2_GATED = 0, 1, 2, 3
 PER_TOKEN, PER_CHUNK = 0, 1
 F32, BF16 = 0, 1
+HEADS_FIRST, TOKENS_FIRST = 0, 1
 PREC_AUTO, PREC_BF16, PREC_BF16X3, PREC_F32 = 0, 1, 2, 3
 FLAG_NO_FUSED = 1
 FLAG_PER_TOKEN_RETRIEVE = 2
@@ -34,6 +35,7 @@ EXPORTS = (
     "atlasmem_feature_map", "atlasmem_backward_workspace_bytes", "atlasmem_update_backward",
     "atlasmem_calibrate_mfma", "atlasmem_calibrate_copy", "atlasmem_update_chunked_static",
     "atlasmem_update_chunked_conv",
+    "atlasmem_linear_attention_workspace_bytes", "atlasmem_linear_attention", "atlasmem_linear_attention_backward",
 )
 STATIC_MAX_MEMORIES = 128
 
@@ -105,6 +107,11 @@ def load():
         "atlasmem_update_chunked_static": ([ctypes.POINTER(Config)] + [_vp] * 6 + [_i64] + [_vp] * 5, ctypes.c_int),
         "atlasmem_update_chunked_conv": ([_vp, _vp, _vp, _vp, ctypes.POINTER(ConvParams), _vp, _vp, _vp, _vp, _i64, _vp,
                                           _vp], ctypes.c_int),
+        "atlasmem_linear_attention_workspace_bytes": ([_i32, _i32, _i32, _i64, _i32, _i32, _i32], _i64),
+        "atlasmem_linear_attention": ([_vp] * 3 + [_i32] * 3 + [_i64] + [_i32] * 3 + [_vp, _vp, _f] + [_vp] * 4
+                                      + [_i64, _vp], ctypes.c_int),
+        "atlasmem_linear_attention_backward": ([_vp] * 3 + [_i32] * 3 + [_i64] + [_i32] * 3 + [_vp, _vp, _f]
+                                               + [_vp] * 9 + [_i64, _vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -293,3 +300,30 @@ def feature_map(X, in_dtype: int, n: int, d: int, degree: int, out, coeffs=None,
     _check(load().atlasmem_feature_map(_ptr(X), in_dtype, n, d, degree, c, _ptr(P), d_out, _ptr(out),
                                        _stream(stream)), "atlasmem_feature_map")
 
+
+def _nbytes(workspace) -> int:
+    return 0 if workspace is None else int(workspace.numel() * workspace.element_size())
+
+
+def linear_attention_workspace_bytes(dtype: int, batch: int, heads: int, T: int, d_key: int, d_value: int,
+                                     backward: bool = False) -> int:
+    return int(load().atlasmem_linear_attention_workspace_bytes(dtype, batch, heads, T, d_key, d_value, int(backward)))
+
+
+def linear_attention(Q, K, V, dtype: int, batch: int, heads: int, T: int, d_key: int, d_value: int, log_decay,
+                     scale: float, Y, W0=None, W_T=None, lengths=None, layout: int = HEADS_FIRST, workspace=None,
+                     stream=None):
+    _check(load().atlasmem_linear_attention(_ptr(Q), _ptr(K), _ptr(V), dtype, batch, heads, T, d_key, d_value, layout,
+                                            _ptr(log_decay), _ptr(lengths), scale, _ptr(W0), _ptr(Y), _ptr(W_T),
+                                            _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "atlasmem_linear_attention")
+
+
+def linear_attention_backward(Q, K, V, dtype: int, batch: int, heads: int, T: int, d_key: int, d_value: int, log_decay,
+                              scale: float, dY, dQ, dK, dV, W0=None, dW_T=None, dW0=None, dlog_decay=None, lengths=None,
+                              layout: int = HEADS_FIRST, workspace=None, stream=None):
+    _check(load().atlasmem_linear_attention_backward(_ptr(Q), _ptr(K), _ptr(V), dtype, batch, heads, T, d_key, d_value,
+                                                     layout, _ptr(log_decay), _ptr(lengths), scale, _ptr(W0), _ptr(dY),
+                                                     _ptr(dW_T), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dW0),
+                                                     _ptr(dlog_decay), _ptr(workspace), _nbytes(workspace),
+                                                     _stream(stream)), "atlasmem_linear_attention_backward")

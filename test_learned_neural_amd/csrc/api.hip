@@ -411,6 +411,45 @@ static atlasmem_status stream_rows(Handle* h, const void* Q, const void* K, cons
 
 }  // namespace
 
+namespace {
+
+// Memory that a call reads or writes (null: none).
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+bool apart(const Range& a, const Range& b) {
+  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return true;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x + (uint64_t)a.bytes <= y || y + (uint64_t)b.bytes <= x;
+}
+// No output overlaps an input or another output.
+bool disjoint(const Range* out, int n_out, const Range* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (!apart(out[i], out[j])) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (!apart(out[i], in[j])) return false;
+  }
+  return true;
+}
+
+// Checked sizes of a linear attention call.
+atlasmem_status lin_attn_of(int32_t dtype, int32_t batch, int32_t heads, int64_t T, int32_t d_key, int32_t d_value,
+                            int32_t layout, LinAttn& s) {
+  if (batch < 1 || heads < 1 || T < 0 || d_key < 1 || d_value < 1 ||
+      (dtype != ATLASMEM_F32 && dtype != ATLASMEM_BF16) ||
+      (layout != ATLASMEM_HEADS_FIRST && layout != ATLASMEM_TOKENS_FIRST))
+    return ATLASMEM_E_INVALID;
+  if (d_key > kLinAttnMaxDim || d_value > kLinAttnMaxDim || T > INT32_MAX - 64 ||
+      (int64_t)batch * heads > (1 << 20))
+    return ATLASMEM_E_SHAPE;
+  s = {batch, heads, T, d_key, d_value, dtype == ATLASMEM_BF16, layout == ATLASMEM_TOKENS_FIRST, nullptr, nullptr};
+  return ATLASMEM_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 atlasmem_status atlasmem_update_chunked_static(const atlasmem_config* cfg, const void* K, const void* Q,
@@ -760,6 +799,56 @@ atlasmem_status atlasmem_update_backward(atlasmem_handle hh, const void* K, cons
   if (!g.ok) return ATLASMEM_E_DEVICE;
   return backward(h, K, Q, V, theta, eta, alpha, gamma, T, Y, dY, dW_T, dS_T, workspace, dK, dQ, dV, dtheta, deta,
                   dalpha, dgamma, dW0, dS0, S(stream));
+}
+
+int64_t atlasmem_linear_attention_workspace_bytes(int32_t dtype, int32_t batch, int32_t heads, int64_t T,
+                                                  int32_t d_key, int32_t d_value, int32_t backward) {
+  LinAttn s;
+  if (lin_attn_of(dtype, batch, heads, T, d_key, d_value, ATLASMEM_HEADS_FIRST, s) != ATLASMEM_OK) return -1;
+  return linear_attention_workspace_bytes(s, backward != 0);
+}
+
+atlasmem_status atlasmem_linear_attention(const void* Q, const void* K, const void* V, int32_t dtype, int32_t batch,
+                                          int32_t heads, int64_t T, int32_t d_key, int32_t d_value, int32_t layout,
+                                          const float* log_decay, const int32_t* lengths, float scale, const float* W0,
+                                          void* Y, float* W_T, void* workspace, int64_t workspace_bytes,
+                                          void* stream) {
+  LinAttn s;
+  const atlasmem_status e = lin_attn_of(dtype, batch, heads, T, d_key, d_value, layout, s);
+  if (e != ATLASMEM_OK) return e;
+  if (!log_decay || (T > 0 && (!Q || !K || !V || !Y))) return ATLASMEM_E_INVALID;
+  const int64_t need = linear_attention_workspace_bytes(s, false);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4, M = (int64_t)batch * heads;
+  const int64_t nk = M * T * d_key * el, nv = M * T * d_value * el, ns = M * d_key * d_value * 4;
+  const Range out[] = {{Y, nv}, {W_T, ns}, {workspace, need}};
+  const Range in[] = {{Q, nk}, {K, nk}, {V, nv}, {W0 == W_T ? nullptr : W0, ns}, {log_decay, heads * 4}, {lengths, batch * 4}};
+  if (!disjoint(out, 3, in, 6)) return ATLASMEM_E_INVALID;
+  s.log_decay = log_decay, s.lengths = lengths;
+  return linear_attention(s, Q, K, V, scale, W0, W_T, Y, workspace, S(stream));
+}
+
+atlasmem_status atlasmem_linear_attention_backward(const void* Q, const void* K, const void* V, int32_t dtype,
+                                                   int32_t batch, int32_t heads, int64_t T, int32_t d_key,
+                                                   int32_t d_value, int32_t layout, const float* log_decay,
+                                                   const int32_t* lengths, float scale, const float* W0,
+                                                   const void* dY, const float* dW_T, void* dQ, void* dK, void* dV,
+                                                   float* dW0, float* dlog_decay, void* workspace,
+                                                   int64_t workspace_bytes, void* stream) {
+  LinAttn s;
+  const atlasmem_status e = lin_attn_of(dtype, batch, heads, T, d_key, d_value, layout, s);
+  if (e != ATLASMEM_OK) return e;
+  if (!log_decay || !workspace || (T > 0 && (!Q || !K || !V || !dY || !dQ || !dK || !dV))) return ATLASMEM_E_INVALID;
+  const int64_t need = linear_attention_workspace_bytes(s, true);
+  if (workspace_bytes < need) return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4, M = (int64_t)batch * heads;
+  const int64_t nk = M * T * d_key * el, nv = M * T * d_value * el, ns = M * d_key * d_value * 4;
+  const Range out[] = {{dQ, nk}, {dK, nk}, {dV, nv}, {dW0, ns}, {dlog_decay, heads * 4}, {workspace, need}};
+  const Range in[] = {{Q, nk},  {K, nk},  {V, nv}, {dY, nv}, {W0, ns}, {dW0 == dW_T ? nullptr : dW_T, ns},
+                      {log_decay, heads * 4}, {lengths, batch * 4}};
+  if (!disjoint(out, 6, in, 8)) return ATLASMEM_E_INVALID;
+  s.log_decay = log_decay, s.lengths = lengths;
+  return linear_attention_backward(s, Q, K, V, scale, W0, dY, dW_T, dQ, dK, dV, dW0, dlog_decay, workspace, S(stream));
 }
 
 }  // extern "C"

@@ -282,4 +282,22 @@ bool gates_supported(int dm, int chunk);
 atlasmem_status launch_gates(const void* U, int64_t B, int64_t T, int dm, int H, int n_gates, const float* Wg,
                              const float* bg, const float* scale, int chunk, float* out, hipStream_t st);
 
+// Linear attention with a decay for each head (k_linattn.hip)
+struct LinAttn {
+  int B, H;
+  int64_t T;
+  int dk, dv;
+  bool bf16, tokens_first;
+  const float* log_decay;  // [H]
+  const int32_t* lengths;  // [B] or null
+};
+constexpr int kLinAttnMaxDim = 128;
+constexpr int kLinAttnStepTokens = 16;  // calls of at most so many tokens run the recurrence itself
+int64_t linear_attention_workspace_bytes(const LinAttn& s, bool backward);
+atlasmem_status linear_attention(const LinAttn& s, const void* Q, const void* K, const void* V, float scale,
+                                 const float* W0, float* WT, void* Y, void* workspace, hipStream_t st);
+atlasmem_status linear_attention_backward(const LinAttn& s, const void* Q, const void* K, const void* V, float scale,
+                                          const float* W0, const void* dY, const float* dWT, void* dQ, void* dK,
+                                          void* dV, float* dW0, float* dlog_decay, void* workspace, hipStream_t st);
+
 }  // namespace am

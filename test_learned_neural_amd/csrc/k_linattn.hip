@@ -1,0 +1,761 @@
+// Linear attention with a decay for each head (gfx950).
+//
+// Per memory m = (b, h), lambda = exp(log_decay[h]):
+//   W_t = lambda W_{t-1} + v_t k_t^T,   y_t = scale W_t q_t            (W: d_value x d_key, fp32)
+// in the chunked form for many tokens and the recurrence itself for a few; and the gradients of an
+// outer loss with respect to q, k, v, W_0 and log_decay.
+//
+// One chunk kernel serves the forward and the three backward products.  With "queries" x, "keys" y,
+// "values" z and a state S [x, z] (chunks of 64 positions i, j; S_0 the state before the chunk):
+//   out_i = c_out (lambda^(i+1-e) S_0^T x_i + c_upd sum_{j<=i} lambda^(i-j) (x_i . y_j) z_j)
+//   S'    = lambda^r S_0 + c_upd sum_j lambda^(r-1-j+e) y_j z_j^T            (r rows in the chunk)
+//   forward   x = q,  y = k,  z = v,  e = 0: y_t, state W^T
+//   dq        x = dy, y = v,  z = k,  e = 0: dq_t = scale W_t^T dy_t
+//   dk, dv    positions run backwards, e = 1, c_upd = scale, state A_t = lambda A_{t+1} + scale dy_t q_t^T
+//             (A_T = dW_T):  dk_t = A_t^T v_t (x = v, y = dy, z = q), dv_t = A_t k_t (x = k, y = q, z = dy)
+// and d log_decay is the tangent state's share (dS/dlog lambda, carried beside S) of the outputs:
+//   sum_i scale dy_i . (dS_i / dlog lambda)^T q_i + <dW_T, dS_T / dlog lambda>,
+// every term a product that is there: the shorter identity through sum_t (q.dq - k.dk) cancels.
+#include <algorithm>
+
+#include "common.h"
+#include "internal.h"
+#include "mfma_tiles.h"
+
+namespace am {
+
+namespace {
+
+constexpr int kC = 64;          // tokens per chunk: two 32-row matrix-core tiles
+constexpr int kPad = 8;         // LDS row padding (elements): consecutive rows 16 bytes apart in bank order
+
+struct LaRows {                 // a [B, H, T, w] tensor of either layout
+  const void* p;
+  int64_t sb, sh, st;           // element strides of b, h, t
+  int w;
+  int vec;                      // rows are whole, aligned 16-byte pieces
+};
+
+struct LaArgs {
+  LaRows x, y, z, o;            // o: the output rows (z.w wide)
+  LaRows t;                     // the rows that the tangent's outputs are multiplied with
+  const float* log_decay;       // [H]
+  const int32_t* len;           // [B] or null
+  const float* s0;              // start states, or null (zeros)
+  float* sT;                    // final states, or null
+  const float* t0;              // tangent's start states (nseg > 1), or null (zeros)
+  const float* adj;             // tangent: dW_T, or null
+  double* dec;                  // tangent: one sum for each (memory, segment, column block, wave)
+  float* u;                     // state pass: segment s's own sum goes to slot s + 1
+  float* ut;                    // ... and its tangent's
+  int64_t T;
+  int64_t lseg;                 // tokens of a segment (a multiple of kC)
+  int H, nseg;
+  int ssx, ssz;                 // element strides of a state's x and z index
+  int64_t P;                    // elements of a state
+  int svec;                     // states are whole, aligned 16-byte pieces
+  float c_out, c_upd;
+  int e, rev;
+};
+
+// lambda^n
+__device__ __forceinline__ float decay_pow(float g, int64_t n) { return n <= 0 ? 1.0f : expf((float)n * g); }
+
+// An operand in N bf16 planes, x = p[0] + p[1] + p[2] (8 significant bits each).
+template <int N>
+struct Op {
+  u32x4 p[N];
+};
+
+template <int N>
+__device__ __forceinline__ void split8(const float* v, Op<N>& o) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
+      o.p[n][i] = w;
+      if (n + 1 < N) {
+        r[2 * i] -= __uint_as_float(w << 16);
+        r[2 * i + 1] -= __uint_as_float(w & 0xFFFF0000u);
+      }
+    }
+}
+
+// Products of planes down to 2^-16 of the leading one: the rest is below fp32's rounding.
+template <int NA, int NB>
+__device__ __forceinline__ f32x16 mm(const Op<NA>& a, const Op<NB>& b, f32x16 c) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) c = mfma32(a.p[i], b.p[s - i], c);
+  return c;
+}
+
+// Eight consecutive elements of a row as read from memory.
+template <bool F32>
+struct Raw {
+  u32x4 a[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_group(const LaRows& r, int64_t base, int64_t t, int c0) {
+  Raw<F32> g;
+  g.a[0] = u32x4{0, 0, 0, 0};
+  if constexpr (F32) g.a[1] = u32x4{0, 0, 0, 0};
+  if (t < 0 || c0 >= r.w) return g;
+  const int64_t at = base + t * r.st + c0;
+  if constexpr (F32) {
+    const float* p = (const float*)r.p + at;
+    if (r.vec) {
+      g.a[0] = *(const u32x4*)p;
+      if (c0 + 4 < r.w) g.a[1] = *(const u32x4*)(p + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i < r.w) g.a[i >> 2][i & 3] = __float_as_uint(p[i]);
+    }
+  } else {
+    const uint16_t* p = (const uint16_t*)r.p + at;
+    if (r.vec) {
+      g.a[0] = *(const u32x4*)p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i < r.w) g.a[0][i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    }
+  }
+  return g;
+}
+
+// ... into an LDS tile of planes (plane stride ps elements).
+template <bool F32>
+__device__ __forceinline__ void store_group(uint16_t* s, int ps, const Raw<F32>& g) {
+  if constexpr (F32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(g.a[i >> 2][i & 3]);
+    Op<3> o;
+    split8(v, o);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) *(u32x4*)(s + n * ps) = o.p[n];
+  } else {
+    *(u32x4*)s = g.a[0];
+  }
+}
+
+// A row operand: lane l takes row l % 32 and, of every 16 columns, those that an accumulator tile
+// has in its registers (4 (l / 32) + {0..3, 8..11}).
+template <int NP>
+__device__ __forceinline__ Op<NP> row_op(const uint16_t* s, int ps, int ld, int row, int k, int hf) {
+  Op<NP> o;
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    const uint16_t* q = s + n * ps + row * ld + 16 * k + 4 * hf;
+    o.p[n] = cat2(*(const uint2*)q, *(const uint2*)(q + 8));
+  }
+  return o;
+}
+// A column operand: lane l takes column c0 + l % 32 and the rows in the same order.
+template <int NP>
+__device__ __forceinline__ Op<NP> col_op(const uint16_t* s, int ps, int ld, int c0, int k, int lane) {
+  const int hf = lane >> 5;
+  const int off = (16 * k + 4 * hf + ((lane & 15) >> 2)) * ld + c0 + (lane & 16) + 4 * (lane & 3);
+  Op<NP> o;
+#pragma unroll
+  for (int n = 0; n < NP; ++n) o.p[n] = cat2(lds_tr16(s + n * ps + off), lds_tr16(s + n * ps + off + 8 * ld));
+  return o;
+}
+
+// DX: 32-column tiles of x and y; NW: waves, each with 32 columns of z; OUT: outputs (else the
+// segment's own state alone); DEC: the tangent too.
+template <int DX, int NW, bool F32, bool OUT, bool DEC>
+__global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
+  constexpr int NP = F32 ? 3 : 1;                    // planes of an input
+  constexpr int NC = F32 || DEC ? 3 : 2;             // planes of a computed operand of the outputs
+  constexpr int LX = DX * 32 + kPad, LZ = NW * 32 + kPad;
+  constexpr int NT = NW * 64;
+  constexpr int GX = kC * DX * 4 / NT, GZ = kC * NW * 4 / NT;  // 8-element groups per thread
+  constexpr int PSX = kC * LX, PSZ = kC * LZ;
+  extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
+  uint16_t* sx = sm;
+  uint16_t* sy = sx + (OUT ? NP * PSX : 0);
+  uint16_t* sz = sy + NP * PSX;
+  float* pw = (float*)(sz + NP * PSZ);               // lambda^0 .. lambda^64
+
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hf = lane >> 5, col = lane & 31;
+  const int nrun = OUT ? a.nseg : a.nseg - 1;        // the last segment's own sum starts nothing
+  const int seg = blockIdx.x % nrun;
+  const int m = blockIdx.x / nrun;
+  const int b = m / a.H, h = m % a.H;
+  const int z0 = blockIdx.y * NW * 32;
+  const int zc = z0 + wave * 32;
+  const int64_t len = a.len ? min((int64_t)max(a.len[b], 0), a.T) : a.T;
+  const int64_t p0 = (int64_t)seg * a.lseg, p1 = min(p0 + a.lseg, a.T);
+  const float g = a.log_decay[h];
+  for (int i = tid; i <= kC; i += NT) pw[i] = decay_pow(g, i);
+
+  const int64_t bx = b * a.x.sb + h * a.x.sh, by = b * a.y.sb + h * a.y.sh, bz = b * a.z.sb + h * a.z.sh;
+  // position -> token; -1 behind the sequence
+  auto token = [&](int64_t p) -> int64_t { return p < len && p < p1 ? (a.rev ? len - 1 - p : p) : -1; };
+
+  // state tiles: column zc + col, rows 32 xt + 8 q + 4 hf + u
+  f32x16 S[DX], St[DEC ? DX : 1];
+#pragma unroll
+  for (int xt = 0; xt < DX; ++xt) {
+    S[xt] = zero16();
+    if constexpr (DEC) St[xt] = zero16();
+  }
+  const int64_t slot = (int64_t)m * a.nseg + seg;
+  if constexpr (OUT) {
+    auto get = [&](f32x16* D, const float* src) {
+      if (!src || zc + col >= a.z.w) return;
+      const float* p = src + slot * a.P + (int64_t)(zc + col) * a.ssz;
+#pragma unroll
+      for (int xt = 0; xt < DX; ++xt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
+          if (x < a.x.w) D[xt][i] = p[(int64_t)x * a.ssx];
+        }
+    };
+    get(S, a.s0);
+    if constexpr (DEC) get(St, a.t0);
+  }
+
+  Raw<F32> rx[OUT ? GX : 1], ry[GX], rz[GZ];
+  auto fetch = [&](int64_t p) {
+#pragma unroll
+    for (int i = 0; i < GX; ++i) {
+      const int id = tid + i * NT, row = id / (DX * 4), c = (id % (DX * 4)) * 8;
+      const int64_t t = token(p + row);
+      if constexpr (OUT) rx[i] = load_group<F32>(a.x, bx, t, c);
+      ry[i] = load_group<F32>(a.y, by, t, c);
+    }
+#pragma unroll
+    for (int i = 0; i < GZ; ++i) {
+      const int id = tid + i * NT, row = id / (NW * 4), c = (id % (NW * 4)) * 8;
+      rz[i] = load_group<F32>(a.z, bz, token(p + row), z0 + c);
+    }
+  };
+  double dec = 0.0;
+
+  if (p0 < p1) fetch(p0);
+  for (int64_t p = p0; p < p1; p += kC) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < GX; ++i) {
+      const int id = tid + i * NT, row = id / (DX * 4), c = (id % (DX * 4)) * 8;
+      if constexpr (OUT) store_group<F32>(sx + row * LX + c, PSX, rx[i]);
+      store_group<F32>(sy + row * LX + c, PSX, ry[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < GZ; ++i) {
+      const int id = tid + i * NT, row = id / (NW * 4), c = (id % (NW * 4)) * 8;
+      store_group<F32>(sz + row * LZ + c, PSZ, rz[i]);
+    }
+    __syncthreads();
+    if (p + kC < p1) fetch(p + kC);
+    const int r = (int)max((int64_t)0, min((int64_t)kC, min(len, p1) - p));
+
+    Op<NP> zo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) zo[k] = col_op<NP>(sz, PSZ, LZ, wave * 32, k, lane);
+
+    if constexpr (OUT) {
+      f32x16 O[2], Ot[DEC ? 2 : 1], P[3];  // P: (j-tile, i-tile) = (0,0), (0,1), (1,1)
+      O[0] = O[1] = zero16();
+      if constexpr (DEC) Ot[0] = Ot[1] = zero16();
+      P[0] = P[1] = P[2] = zero16();
+#pragma unroll
+      for (int k = 0; k < 2 * DX; ++k) {
+        const Op<NP> x0 = row_op<NP>(sx, PSX, LX, col, k, hf), x1 = row_op<NP>(sx, PSX, LX, 32 + col, k, hf);
+        const Op<NP> y0 = row_op<NP>(sy, PSX, LX, col, k, hf), y1 = row_op<NP>(sy, PSX, LX, 32 + col, k, hf);
+        P[0] = mm(y0, x0, P[0]);
+        P[1] = mm(y0, x1, P[1]);
+        P[2] = mm(y1, x1, P[2]);
+        Op<NC> s;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = S[k >> 1][8 * (k & 1) + i];
+        split8(v, s);
+        O[0] = mm(s, x0, O[0]);
+        O[1] = mm(s, x1, O[1]);
+        if constexpr (DEC) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = St[k >> 1][8 * (k & 1) + i];
+          split8(v, s);
+          Ot[0] = mm(s, x0, Ot[0]);
+          Ot[1] = mm(s, x1, Ot[1]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const int i = 32 * it + col;
+        const float w = pw[i + 1 - a.e];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          O[it][n] *= w;
+          if constexpr (DEC) Ot[it][n] = Ot[it][n] * w + (float)(i + 1) * O[it][n];
+        }
+      }
+      // decay between rows: position i of the lane's column, j of the register
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const int i = (q ? 32 : 0) + col;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int j = (q == 2 ? 32 : 0) + 8 * (n >> 2) + 4 * hf + (n & 3);
+          P[q][n] = i >= j ? P[q][n] * (pw[max(i - j, 0)] * a.c_upd) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const int it = q ? 1 : 0, jt = q == 2 ? 1 : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) v[n] = P[q][8 * k + n];
+          Op<NC> s;
+          split8(v, s);
+          O[it] = mm(zo[2 * jt + k], s, O[it]);
+          if constexpr (DEC) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+              v[n] *= (float)(32 * it + col - (32 * jt + 16 * k + 8 * (n >> 2) + 4 * hf + (n & 3)));
+            split8(v, s);
+            Ot[it] = mm(zo[2 * jt + k], s, Ot[it]);
+          }
+        }
+      }
+      // rows: lane's position, four consecutive columns a register group
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const int64_t pos = p + 32 * it + col;
+        if (pos < p1) {
+          const bool live = pos < len;
+          const int64_t t = live ? token(pos) : pos;
+          const int64_t at = b * a.o.sb + h * a.o.sh + t * a.o.st;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = zc + 8 * q + 4 * hf;
+            float v[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = live ? O[it][4 * q + n] * a.c_out : 0.0f;
+            if constexpr (DEC) {
+              if (live) {
+                const int64_t ta = b * a.t.sb + h * a.t.sh + t * a.t.st;
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  if (c + n < a.z.w)
+                    dec += (double)(Ot[it][4 * q + n] * a.c_out) * load_in(a.t.p, ta + c + n, !F32);
+              }
+            }
+            if (c >= a.z.w) continue;
+            if constexpr (F32) {
+              float* o = (float*)a.o.p + at + c;
+              if (a.o.vec) {
+                *(float4*)o = float4{v[0], v[1], v[2], v[3]};
+              } else {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  if (c + n < a.z.w) o[n] = v[n];
+              }
+            } else {
+              uint16_t* o = (uint16_t*)a.o.p + at + c;
+              const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+              if (a.o.vec) {
+                *(uint2*)o = w;
+              } else {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  if (c + n < a.z.w) o[n] = (uint16_t)((n & 2 ? w.y : w.x) >> (16 * (n & 1)));
+              }
+            }
+          }
+        }
+      }
+    }
+
+    // state: column operands of y times the weighted z (three planes: the state is an fp32 result)
+    {
+      const float keep = pw[r];
+#pragma unroll
+      for (int xt = 0; xt < DX; ++xt)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          if constexpr (DEC) St[xt][n] = keep * (St[xt][n] + (float)r * S[xt][n]);
+          S[xt][n] *= keep;
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[8], vt[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int j = 16 * k + 8 * (n >> 2) + 4 * hf + (n & 3);
+          float zv = 0.0f;
+#pragma unroll
+          for (int s = NP - 1; s >= 0; --s) {
+            const uint32_t w = zo[k].p[s][n >> 1];
+            zv += __uint_as_float(n & 1 ? w & 0xFFFF0000u : w << 16);
+          }
+          const int left = max(r - 1 - j, 0);
+          v[n] = j < r ? zv * (pw[left + (j < r ? a.e : 0)] * a.c_upd) : 0.0f;
+          vt[n] = v[n] * (float)left;
+        }
+        Op<3> s, st;
+        split8(v, s);
+        if constexpr (DEC) split8(vt, st);
+#pragma unroll
+        for (int xt = 0; xt < DX; ++xt) {
+          const Op<NP> yo = col_op<NP>(sy, PSX, LX, 32 * xt, k, lane);
+          S[xt] = mm(yo, s, S[xt]);
+          if constexpr (DEC) St[xt] = mm(yo, st, St[xt]);
+        }
+      }
+    }
+  }
+
+  // the state out: C-layout tiles to the caller's order
+  auto put = [&](const f32x16* D, float* dst) {
+    if (zc + col >= a.z.w) return;
+    float* o = dst + (int64_t)(zc + col) * a.ssz;
+#pragma unroll
+    for (int xt = 0; xt < DX; ++xt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
+        if (x < a.x.w) o[(int64_t)x * a.ssx] = D[xt][i];
+      }
+  };
+  if constexpr (OUT) {
+    if (seg == a.nseg - 1) {
+      if (a.sT) put(S, a.sT + (int64_t)m * a.P);
+      if constexpr (DEC) {
+        if (a.adj && zc + col < a.z.w) {
+          const float* q = a.adj + (int64_t)m * a.P + (int64_t)(zc + col) * a.ssz;
+#pragma unroll
+          for (int xt = 0; xt < DX; ++xt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
+              if (x < a.x.w) dec += (double)St[xt][i] * q[(int64_t)x * a.ssx];
+            }
+        }
+      }
+    }
+    if constexpr (DEC) {
+#pragma unroll
+      for (int s = 32; s; s >>= 1) dec += __shfl_xor(dec, s);
+      if (lane == 0) a.dec[(slot * gridDim.y + blockIdx.y) * NW + wave] = dec;
+    }
+  } else {
+    put(S, a.u + (slot + 1) * a.P);
+    if constexpr (DEC) put(St, a.ut + (slot + 1) * a.P);
+  }
+}
+
+// Start states of the segments: slot 0 takes the initial state, slot s + 1 (holding segment s's own
+// sum) its start state.  Tangent (ut != null): T' = lambda^n (T + n S) + U'.
+__global__ void la_scan(const float* w0, float* u, float* ut, const float* log_decay, const int32_t* len, int H,
+                        int64_t T, int64_t lseg, int nseg, int64_t P) {
+  const int per = (int)((P + 255) / 256);  // workgroups of a memory
+  const int64_t i = (int64_t)(blockIdx.x % per) * 256 + threadIdx.x;
+  if (i >= P) return;
+  const int m = blockIdx.x / per, b = m / H;
+  const float g = log_decay[m % H];
+  const int64_t n = len ? min((int64_t)max(len[b], 0), T) : T;
+  float s = w0 ? w0[(int64_t)m * P + i] : 0.0f, t = 0.0f;
+  float* p = u + (int64_t)m * nseg * P + i;
+  float* pt = ut ? ut + (int64_t)m * nseg * P + i : nullptr;
+  p[0] = s;
+  if (pt) pt[0] = 0.0f;
+  for (int k = 1; k < nseg; ++k) {
+    const int64_t cnt = min(lseg, max((int64_t)0, n - (k - 1) * lseg));
+    const float keep = decay_pow(g, cnt);
+    if (pt) {
+      t = keep * (t + (float)cnt * s) + pt[(int64_t)k * P];
+      pt[(int64_t)k * P] = t;
+    }
+    s = keep * s + p[(int64_t)k * P];
+    p[(int64_t)k * P] = s;
+  }
+}
+
+// d log_decay[h]: the waves' sums of every memory of the head, in one order.
+__global__ void la_decay_sum(const double* dec, int B, int H, int per, float* out) {
+  __shared__ double s[256];
+  const int h = blockIdx.x;
+  double v = 0.0;
+  for (int i = threadIdx.x; i < B * per; i += 256) v += dec[((int64_t)(i / per) * H + h) * per + i % per];
+  s[threadIdx.x] = v;
+  __syncthreads();
+  for (int k = 128; k; k >>= 1) {
+    if ((int)threadIdx.x < k) s[threadIdx.x] += s[threadIdx.x + k];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) out[h] = (float)s[0];
+}
+
+// The recurrence for a few tokens: LPR lanes of a row of W hold four columns each, RPT rows a thread.
+template <int LPR, bool F32>
+__global__ __launch_bounds__(256) void la_step(LaArgs a) {
+  constexpr int RPT = 4, RPB = 256 / LPR * RPT;
+  const int m = blockIdx.x, b = m / a.H, h = m % a.H;
+  const int lr = threadIdx.x % LPR, r0 = blockIdx.y * RPB + threadIdx.x / LPR;
+  const int dk = a.x.w, dv = a.z.w, c = 4 * lr;
+  const int len = a.len ? min(max(a.len[b], 0), (int)a.T) : (int)a.T;
+  const float g = a.log_decay[h], lam = decay_pow(g, 1);
+  const bool vec = a.svec;
+  float W[RPT][4];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int row = r0 + i * (256 / LPR);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) W[i][n] = 0.0f;
+    if (a.s0 && row < dv && c < dk) {
+      const float* p = a.s0 + (int64_t)m * a.P + (int64_t)row * dk + c;
+      if (vec) {
+        const float4 f = *(const float4*)p;
+        W[i][0] = f.x, W[i][1] = f.y, W[i][2] = f.z, W[i][3] = f.w;
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (c + n < dk) W[i][n] = p[n];
+      }
+    }
+  }
+  for (int t = 0; t < (int)a.T; ++t) {
+    const bool live = t < len;
+    float q[4] = {0, 0, 0, 0}, k[4] = {0, 0, 0, 0};
+    if (live) {
+      const int64_t aq = b * a.x.sb + h * a.x.sh + t * a.x.st + c, ak = b * a.y.sb + h * a.y.sh + t * a.y.st + c;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (c + n < dk) {
+          q[n] = load_in(a.x.p, aq + n, !F32);
+          k[n] = load_in(a.y.p, ak + n, !F32);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int row = r0 + i * (256 / LPR);
+      float y = 0.0f;
+      if (live) {
+        const float v = row < dv ? load_in(a.z.p, b * a.z.sb + h * a.z.sh + t * a.z.st + row, !F32) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          W[i][n] = lam * W[i][n] + v * k[n];
+          y += W[i][n] * q[n];
+        }
+      }
+#pragma unroll
+      for (int s = LPR / 2; s; s >>= 1) y += __shfl_xor(y, s);
+      if (lr == 0 && row < dv) {
+        const int64_t at = b * a.o.sb + h * a.o.sh + t * a.o.st + row;
+        y = live ? y * a.c_out : 0.0f;
+        if constexpr (F32) ((float*)a.o.p)[at] = y;
+        else ((uint16_t*)a.o.p)[at] = (uint16_t)bf16_bits(y);
+      }
+    }
+  }
+  if (!a.sT) return;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int row = r0 + i * (256 / LPR);
+    if (row < dv && c < dk) {
+      float* p = a.sT + (int64_t)m * a.P + (int64_t)row * dk + c;
+      if (vec) {
+        *(float4*)p = float4{W[i][0], W[i][1], W[i][2], W[i][3]};
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (c + n < dk) p[n] = W[i][n];
+      }
+    }
+  }
+}
+
+LaRows rows_of(const void* p, const LinAttn& s, int w) {
+  LaRows r;
+  r.p = p;
+  r.w = w;
+  if (s.tokens_first) {
+    r.sb = s.T * s.H * (int64_t)w, r.sh = w, r.st = (int64_t)s.H * w;
+  } else {
+    r.sb = s.H * s.T * (int64_t)w, r.sh = s.T * (int64_t)w, r.st = w;
+  }
+  r.vec = ((uintptr_t)p & 15) == 0 && w % (s.bf16 ? 8 : 4) == 0;
+  return r;
+}
+
+int tiles(int w) { return w <= 64 ? 2 : 4; }
+int waves(int w) { return w <= 64 ? 2 : 4; }
+
+template <int DX, int NW, bool F32, bool OUT, bool DEC>
+atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
+  constexpr int NP = F32 ? 3 : 1;
+  constexpr int lds = 2 * kC * NP * ((OUT ? 2 : 1) * (DX * 32 + kPad) + NW * 32 + kPad) + 4 * (kC + 4);
+  auto kern = la_chunk<DX, NW, F32, OUT, DEC>;
+  if (lds > 65536 &&
+      hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+    return ATLASMEM_E_DEVICE;
+  const dim3 grid((unsigned)blocks, (unsigned)((a.z.w + NW * 32 - 1) / (NW * 32)));
+  kern<<<grid, NW * 64, lds, st>>>(a);
+  AM_LAUNCH_CHECK();
+  return ATLASMEM_OK;
+}
+
+template <bool F32, bool OUT, bool DEC>
+atlasmem_status chunk_pick(const LaArgs& a, int64_t blocks, hipStream_t st) {
+  const int dx = tiles(a.x.w), nw = waves(a.z.w);
+  if (dx == 2) return nw == 2 ? chunk_launch<2, 2, F32, OUT, DEC>(a, blocks, st) : chunk_launch<2, 4, F32, OUT, DEC>(a, blocks, st);
+  return nw == 2 ? chunk_launch<4, 2, F32, OUT, DEC>(a, blocks, st) : chunk_launch<4, 4, F32, OUT, DEC>(a, blocks, st);
+}
+
+template <bool OUT>
+atlasmem_status chunk_run(const LaArgs& a, bool bf16, bool dec, int64_t M, hipStream_t st) {
+  const int64_t blocks = M * (OUT ? a.nseg : a.nseg - 1);
+  if (bf16) return dec ? chunk_pick<false, OUT, true>(a, blocks, st) : chunk_pick<false, OUT, false>(a, blocks, st);
+  return dec ? chunk_pick<true, OUT, true>(a, blocks, st) : chunk_pick<true, OUT, false>(a, blocks, st);
+}
+
+// Segments of the token axis: enough workgroups to fill the chip several times where the memories
+// alone do not, none shorter than four chunks.
+int segments(const LinAttn& s, int64_t& lseg) {
+  const int64_t chunks = std::max<int64_t>((s.T + kC - 1) / kC, 1);
+  const int64_t M = (int64_t)s.B * s.H;
+  int64_t n = std::min<int64_t>((1024 + M - 1) / M, (chunks + 3) / 4);
+  const int64_t per = (chunks + n - 1) / n;
+  lseg = per * kC;
+  return (int)((chunks + per - 1) / per);
+}
+
+LaArgs base_args(const LinAttn& s) {
+  LaArgs a = {};
+  a.log_decay = s.log_decay;
+  a.len = s.lengths;
+  a.T = s.T;
+  a.H = s.H;
+  a.P = (int64_t)s.dk * s.dv;
+  a.nseg = segments(s, a.lseg);
+  a.c_out = 1.0f, a.c_upd = 1.0f;
+  return a;
+}
+
+atlasmem_status run_scan(const LaArgs& a, const float* w0, float* u, float* ut, int64_t M, hipStream_t st) {
+  la_scan<<<(unsigned)(M * ((a.P + 255) / 256)), 256, 0, st>>>(w0, u, ut, a.log_decay, a.len, a.H, a.T, a.lseg, a.nseg, a.P);
+  AM_LAUNCH_CHECK();
+  return ATLASMEM_OK;
+}
+
+int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+}  // namespace
+
+int64_t linear_attention_workspace_bytes(const LinAttn& s, bool backward) {
+  int64_t lseg;
+  const int64_t M = (int64_t)s.B * s.H, P = (int64_t)s.dk * s.dv, nseg = segments(s, lseg);
+  const int64_t states = nseg > 1 ? align256(4 * M * nseg * P) : 0;
+  if (!backward) return s.T <= kLinAttnStepTokens ? 0 : states;
+  return 2 * states + align256(8 * M * nseg * 4);
+}
+
+atlasmem_status linear_attention(const LinAttn& s, const void* Q, const void* K, const void* V, float scale,
+                                 const float* W0, float* WT, void* Y, void* workspace, hipStream_t st) {
+  LaArgs a = base_args(s);
+  const int64_t M = (int64_t)s.B * s.H;
+  a.x = rows_of(Q, s, s.dk), a.y = rows_of(K, s, s.dk), a.z = rows_of(V, s, s.dv), a.o = rows_of(Y, s, s.dv);
+  a.c_out = scale;
+  a.ssx = 1, a.ssz = s.dk;
+  a.s0 = W0, a.sT = WT;
+  a.svec = s.dk % 4 == 0 && (((uintptr_t)W0 | (uintptr_t)WT) & 15) == 0;
+  if (s.T <= kLinAttnStepTokens) {
+    const int lpr = s.dk <= 32 ? 8 : s.dk <= 64 ? 16 : 32;
+    const dim3 grid((unsigned)M, (unsigned)((s.dv + 1024 / lpr - 1) / (1024 / lpr)));
+    if (s.bf16) {
+      if (lpr == 8) la_step<8, false><<<grid, 256, 0, st>>>(a);
+      else if (lpr == 16) la_step<16, false><<<grid, 256, 0, st>>>(a);
+      else la_step<32, false><<<grid, 256, 0, st>>>(a);
+    } else {
+      if (lpr == 8) la_step<8, true><<<grid, 256, 0, st>>>(a);
+      else if (lpr == 16) la_step<16, true><<<grid, 256, 0, st>>>(a);
+      else la_step<32, true><<<grid, 256, 0, st>>>(a);
+    }
+    AM_LAUNCH_CHECK();
+    return ATLASMEM_OK;
+  }
+  if (a.nseg > 1) {
+    a.u = (float*)workspace;
+    atlasmem_status e = chunk_run<false>(a, s.bf16, false, M, st);
+    if (e == ATLASMEM_OK) e = run_scan(a, W0, a.u, nullptr, M, st);
+    if (e != ATLASMEM_OK) return e;
+    a.s0 = a.u;
+  }
+  return chunk_run<true>(a, s.bf16, false, M, st);
+}
+
+atlasmem_status linear_attention_backward(const LinAttn& s, const void* Q, const void* K, const void* V, float scale,
+                                          const float* W0, const void* dY, const float* dWT, void* dQ, void* dK,
+                                          void* dV, float* dW0, float* dlog_decay, void* workspace, hipStream_t st) {
+  const LaArgs base = base_args(s);
+  const int64_t M = (int64_t)s.B * s.H;
+  const int64_t states = base.nseg > 1 ? align256(4 * M * base.nseg * base.P) : 0;
+  float* u = (float*)workspace;
+  float* ut = (float*)((char*)workspace + states);
+  double* dec = (double*)((char*)workspace + 2 * states);
+  const bool want = dlog_decay != nullptr;
+  atlasmem_status e = ATLASMEM_OK;
+
+  // dq (and the tangent's share): forward over (v, k)
+  LaArgs a = base;
+  a.x = rows_of(dY, s, s.dv), a.y = rows_of(V, s, s.dv), a.z = rows_of(K, s, s.dk), a.o = rows_of(dQ, s, s.dk);
+  a.t = rows_of(Q, s, s.dk);
+  a.ssx = s.dk, a.ssz = 1;
+  a.c_out = scale;
+  a.s0 = W0;
+  a.adj = dWT;
+  a.dec = dec;
+  if (a.nseg > 1) {
+    a.u = u, a.ut = ut;
+    e = chunk_run<false>(a, s.bf16, want, M, st);
+    if (e == ATLASMEM_OK) e = run_scan(a, W0, u, want ? ut : nullptr, M, st);
+    if (e != ATLASMEM_OK) return e;
+    a.s0 = u;
+    a.t0 = want ? ut : nullptr;
+  }
+  e = chunk_run<true>(a, s.bf16, want, M, st);
+  if (e != ATLASMEM_OK) return e;
+  if (want) {
+    const int nw = waves(s.dk), per = a.nseg * nw * ((s.dk + nw * 32 - 1) / (nw * 32));
+    la_decay_sum<<<s.H, 256, 0, st>>>(dec, s.B, s.H, per, dlog_decay);
+    AM_LAUNCH_CHECK();
+  }
+
+  // dk, dv: backwards over (q, dy)
+  a = base;
+  a.rev = 1, a.e = 1, a.c_upd = scale;
+  a.x = rows_of(V, s, s.dv), a.y = rows_of(dY, s, s.dv), a.z = rows_of(Q, s, s.dk), a.o = rows_of(dK, s, s.dk);
+  a.ssx = s.dk, a.ssz = 1;
+  a.s0 = dWT;
+  if (a.nseg > 1) {
+    a.u = u;
+    e = chunk_run<false>(a, s.bf16, false, M, st);
+    if (e == ATLASMEM_OK) e = run_scan(a, dWT, u, nullptr, M, st);
+    if (e != ATLASMEM_OK) return e;
+    a.s0 = u;
+  }
+  e = chunk_run<true>(a, s.bf16, false, M, st);
+  if (e != ATLASMEM_OK) return e;
+  a.x = rows_of(K, s, s.dk), a.y = rows_of(Q, s, s.dk), a.z = rows_of(dY, s, s.dv), a.o = rows_of(dV, s, s.dv);
+  a.ssx = 1, a.ssz = s.dk;
+  a.sT = dW0;
+  return chunk_run<true>(a, s.bf16, false, M, st);
+}
+
+}  // namespace am
