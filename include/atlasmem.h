@@ -81,6 +81,7 @@ typedef enum { ATLASMEM_F32 = 0, ATLASMEM_BF16 = 1 } atlasmem_dtype;
 /* Order of a [batch, heads, T, d] tensor in memory: as written, or [batch, T, heads, d] (the rows of
  * a projection of all heads). */
 typedef enum { ATLASMEM_HEADS_FIRST = 0, ATLASMEM_TOKENS_FIRST = 1 } atlasmem_layout;
+typedef enum { ATLASMEM_ACT_NONE = 0, ATLASMEM_ACT_SILU = 1 } atlasmem_activation;
 
 /* Operand precision of the matrix-core products (state and accumulation are fp32 always).
  * BF16X3 splits every fp32 operand x into hi = bf16(x), lo = bf16(x - hi) and sums
@@ -459,6 +460,38 @@ atlasmem_status atlasmem_linear_attention_backward(const void* Q, const void* K,
                                                    const void* dY, const float* dW_T, void* dQ, void* dK, void* dV,
                                                    float* dW0, float* dlog_decay, void* workspace,
                                                    int64_t workspace_bytes, void* stream);
+
+/* Group norm with an activation, channels last: the channels of every sample are cut into `groups`
+ * equal groups, each normalised over its L positions and channels:
+ *   Y = act(gamma (X - mean) rstd + beta),   rstd = 1 / sqrt(variance + eps)
+ * L = 1 normalises the heads of a token's row by themselves, [batch * T rows, heads * d] as a memory or
+ * atlasmem_linear_attention (TOKENS_FIRST) answers, groups = heads.
+ *   X, Y: [n, L, channels] of `dtype`; Y may be X.  channels <= 65536, a multiple of groups
+ *   gamma, beta: fp32 [channels], or NULL (one; zero);  eps >= 0
+ *   activation: atlasmem_activation
+ *   mean, rstd: fp32 [n, groups], what the backward needs, or NULL
+ *   workspace: atlasmem_group_norm_workspace_bytes(..., backward = 0) bytes, 16-byte aligned (NULL where
+ *         that is 0)
+ * Statistics are fp32 sums of differences to a mean; Y is rounded once.  n = 0 is valid.
+ * Errors: E_INVALID for bad sizes, enums, null or overlapping pointers, a short workspace; E_SHAPE beyond
+ * the limits (n * groups < 2^31, 2^40 elements).  The workspace function returns -1 for those sizes. */
+int64_t atlasmem_group_norm_workspace_bytes(int64_t n, int64_t L, int32_t channels, int32_t groups,
+                                            int32_t backward);
+atlasmem_status atlasmem_group_norm(const void* X, int32_t dtype, int64_t n, int64_t L, int32_t channels,
+                                    int32_t groups, const float* gamma, const float* beta, float eps,
+                                    int32_t activation, void* Y, float* mean, float* rstd, void* workspace,
+                                    int64_t workspace_bytes, void* stream);
+
+/* Its gradients, from dY of `dtype` and the forward's mean and rstd.
+ *   dX: of `dtype`, may be X or dY;  dgamma, dbeta: fp32 [channels] or NULL (not computed), written, not
+ *       added to
+ *   workspace: atlasmem_group_norm_workspace_bytes(..., backward = 1) bytes
+ * Sums run in one order: equal calls give equal bits. */
+atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int32_t dtype, int64_t n, int64_t L,
+                                             int32_t channels, int32_t groups, const float* gamma, const float* beta,
+                                             const float* mean, const float* rstd, int32_t activation, void* dX,
+                                             float* dgamma, float* dbeta, void* workspace, int64_t workspace_bytes,
+                                             void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@ LINEAR, MLP2_SILU, MLP2_SILU_RESIDUAL, MLP2_GATED = 0, 1, 2, 3
 PER_TOKEN, PER_CHUNK = 0, 1
 F32, BF16 = 0, 1
 HEADS_FIRST, TOKENS_FIRST = 0, 1
+ACT_NONE, ACT_SILU = 0, 1
 PREC_AUTO, PREC_BF16, PREC_BF16X3, PREC_F32 = 0, 1, 2, 3
 FLAG_NO_FUSED = 1
 FLAG_PER_TOKEN_RETRIEVE = 2
@@ -36,6 +37,7 @@ EXPORTS = (
     "atlasmem_calibrate_mfma", "atlasmem_calibrate_copy", "atlasmem_update_chunked_static",
     "atlasmem_update_chunked_conv",
     "atlasmem_linear_attention_workspace_bytes", "atlasmem_linear_attention", "atlasmem_linear_attention_backward",
+    "atlasmem_group_norm_workspace_bytes", "atlasmem_group_norm", "atlasmem_group_norm_backward",
 )
 STATIC_MAX_MEMORIES = 128
 
@@ -112,6 +114,11 @@ def load():
                                       + [_i64, _vp], ctypes.c_int),
         "atlasmem_linear_attention_backward": ([_vp] * 3 + [_i32] * 3 + [_i64] + [_i32] * 3 + [_vp, _vp, _f]
                                                + [_vp] * 9 + [_i64, _vp], ctypes.c_int),
+        "atlasmem_group_norm_workspace_bytes": ([_i64, _i64, _i32, _i32, _i32], _i64),
+        "atlasmem_group_norm": ([_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _f, _i32] + [_vp] * 4 + [_i64, _vp],
+                                ctypes.c_int),
+        "atlasmem_group_norm_backward": ([_vp, _vp, _i32, _i64, _i64, _i32, _i32] + [_vp] * 4 + [_i32] + [_vp] * 4
+                                         + [_i64, _vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -327,3 +334,22 @@ def linear_attention_backward(Q, K, V, dtype: int, batch: int, heads: int, T: in
                                                      _ptr(dW_T), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dW0),
                                                      _ptr(dlog_decay), _ptr(workspace), _nbytes(workspace),
                                                      _stream(stream)), "atlasmem_linear_attention_backward")
+
+
+def group_norm_workspace_bytes(n: int, L: int, channels: int, groups: int, backward: bool = False) -> int:
+    return int(load().atlasmem_group_norm_workspace_bytes(n, L, channels, groups, int(backward)))
+
+
+def group_norm(X, dtype: int, n: int, L: int, channels: int, groups: int, gamma, beta, eps: float, activation: int, Y,
+               mean=None, rstd=None, workspace=None, stream=None):
+    _check(load().atlasmem_group_norm(_ptr(X), dtype, n, L, channels, groups, _ptr(gamma), _ptr(beta), eps, activation,
+                                      _ptr(Y), _ptr(mean), _ptr(rstd), _ptr(workspace), _nbytes(workspace),
+                                      _stream(stream)), "atlasmem_group_norm")
+
+
+def group_norm_backward(X, dY, dtype: int, n: int, L: int, channels: int, groups: int, gamma, beta, mean, rstd,
+                        activation: int, dX, dgamma=None, dbeta=None, workspace=None, stream=None):
+    _check(load().atlasmem_group_norm_backward(_ptr(X), _ptr(dY), dtype, n, L, channels, groups, _ptr(gamma),
+                                               _ptr(beta), _ptr(mean), _ptr(rstd), activation, _ptr(dX), _ptr(dgamma),
+                                               _ptr(dbeta), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "atlasmem_group_norm_backward")

@@ -434,6 +434,20 @@ bool disjoint(const Range* out, int n_out, const Range* in, int n_in) {
   return true;
 }
 
+// Checked sizes of a group norm call.
+atlasmem_status group_norm_of(int32_t dtype, int64_t n, int64_t L, int32_t channels, int32_t groups,
+                              int32_t activation, GroupNorm& s) {
+  if (n < 0 || L < 1 || channels < 1 || groups < 1 || channels % groups != 0 ||
+      (dtype != ATLASMEM_F32 && dtype != ATLASMEM_BF16) ||
+      (activation != ATLASMEM_ACT_NONE && activation != ATLASMEM_ACT_SILU))
+    return ATLASMEM_E_INVALID;
+  if (channels > (1 << 16) || L > INT32_MAX || n > INT32_MAX / groups ||
+      (n > 0 && L > (INT64_C(1) << 40) / (n * (int64_t)channels)))
+    return ATLASMEM_E_SHAPE;
+  s = {n, L, channels, groups, dtype == ATLASMEM_BF16, activation == ATLASMEM_ACT_SILU, nullptr, nullptr, 0.0f};
+  return ATLASMEM_OK;
+}
+
 // Checked sizes of a linear attention call.
 atlasmem_status lin_attn_of(int32_t dtype, int32_t batch, int32_t heads, int64_t T, int32_t d_key, int32_t d_value,
                             int32_t layout, LinAttn& s) {
@@ -849,6 +863,53 @@ atlasmem_status atlasmem_linear_attention_backward(const void* Q, const void* K,
   if (!disjoint(out, 6, in, 8)) return ATLASMEM_E_INVALID;
   s.log_decay = log_decay, s.lengths = lengths;
   return linear_attention_backward(s, Q, K, V, scale, W0, dY, dW_T, dQ, dK, dV, dW0, dlog_decay, workspace, S(stream));
+}
+
+int64_t atlasmem_group_norm_workspace_bytes(int64_t n, int64_t L, int32_t channels, int32_t groups,
+                                            int32_t backward) {
+  GroupNorm s;
+  if (group_norm_of(ATLASMEM_F32, n, L, channels, groups, ATLASMEM_ACT_NONE, s) != ATLASMEM_OK) return -1;
+  return group_norm_workspace_bytes(s, backward != 0);
+}
+
+atlasmem_status atlasmem_group_norm(const void* X, int32_t dtype, int64_t n, int64_t L, int32_t channels,
+                                    int32_t groups, const float* gamma, const float* beta, float eps,
+                                    int32_t activation, void* Y, float* mean, float* rstd, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+  GroupNorm s;
+  const atlasmem_status e = group_norm_of(dtype, n, L, channels, groups, activation, s);
+  if (e != ATLASMEM_OK) return e;
+  if (!(eps >= 0.0f)) return ATLASMEM_E_INVALID;
+  if (n == 0) return ATLASMEM_OK;
+  if (!X || !Y) return ATLASMEM_E_INVALID;
+  const int64_t need = group_norm_workspace_bytes(s, false);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATLASMEM_E_INVALID;
+  const int64_t nx = n * L * channels * (s.bf16 ? 2 : 4), ns = n * groups * 4, nc = channels * (int64_t)4;
+  const Range out[] = {{Y, nx}, {mean, ns}, {rstd, ns}, {workspace, need}};
+  const Range in[] = {{X == Y ? nullptr : X, nx}, {gamma, nc}, {beta, nc}};
+  if (!disjoint(out, 4, in, 3)) return ATLASMEM_E_INVALID;
+  s.gamma = gamma, s.beta = beta, s.eps = eps;
+  return group_norm(s, X, Y, mean, rstd, workspace, S(stream));
+}
+
+atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int32_t dtype, int64_t n, int64_t L,
+                                             int32_t channels, int32_t groups, const float* gamma, const float* beta,
+                                             const float* mean, const float* rstd, int32_t activation, void* dX,
+                                             float* dgamma, float* dbeta, void* workspace, int64_t workspace_bytes,
+                                             void* stream) {
+  GroupNorm s;
+  const atlasmem_status e = group_norm_of(dtype, n, L, channels, groups, activation, s);
+  if (e != ATLASMEM_OK) return e;
+  if (n > 0 && (!X || !dY || !mean || !rstd || !dX)) return ATLASMEM_E_INVALID;
+  const int64_t need = group_norm_workspace_bytes(s, true);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATLASMEM_E_INVALID;
+  const int64_t nx = n * L * channels * (s.bf16 ? 2 : 4), ns = n * groups * 4, nc = channels * (int64_t)4;
+  const Range out[] = {{dX, nx}, {dgamma, nc}, {dbeta, nc}, {workspace, need}};
+  const Range in[] = {{X == dX ? nullptr : X, nx}, {dY == dX ? nullptr : dY, nx}, {mean, ns}, {rstd, ns}, {gamma, nc},
+                      {beta, nc}};
+  if (!disjoint(out, 4, in, 6)) return ATLASMEM_E_INVALID;
+  s.gamma = gamma, s.beta = beta;
+  return group_norm_backward(s, X, dY, mean, rstd, dX, dgamma, dbeta, workspace, S(stream));
 }
 
 }  // extern "C"

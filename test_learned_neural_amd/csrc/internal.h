@@ -300,4 +300,20 @@ atlasmem_status linear_attention_backward(const LinAttn& s, const void* Q, const
                                           const float* W0, const void* dY, const float* dWT, void* dQ, void* dK,
                                           void* dV, float* dW0, float* dlog_decay, void* workspace, hipStream_t st);
 
+// Group norm with an activation, channels last (k_groupnorm.hip)
+struct GroupNorm {
+  int64_t n, L;
+  int C, G;
+  bool bf16, silu;
+  const float* gamma;  // [C] or null (one)
+  const float* beta;   // [C] or null (zero)
+  float eps;
+};
+int64_t group_norm_workspace_bytes(const GroupNorm& s, bool backward);
+atlasmem_status group_norm(const GroupNorm& s, const void* X, void* Y, float* mean, float* rstd, void* workspace,
+                           hipStream_t st);
+atlasmem_status group_norm_backward(const GroupNorm& s, const void* X, const void* dY, const float* mean,
+                                    const float* rstd, void* dX, float* dgamma, float* dbeta, void* workspace,
+                                    hipStream_t st);
+
 }  // namespace am
