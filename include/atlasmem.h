@@ -493,6 +493,35 @@ atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int3
                                              float* dgamma, float* dbeta, void* workspace, int64_t workspace_bytes,
                                              void* stream);
 
+/* Softmax cross entropy of n rows over `vocab` classes, the outer loss of a model whose last product is
+ * z = X W^T, without keeping the logits z:
+ *   lse_i = log sum_v exp(z_iv),   loss_i = lse_i - z_i,label_i
+ *   X: [n, d], W: [vocab, d] of `dtype`; d <= 16384, n and vocab <= 2^24
+ *   labels: int64 [n]; a row whose label is no class (negative, or >= vocab) is left out: its loss, lse
+ *         and gradient are zero, whatever its X holds
+ *   loss, lse: fp32 [n]
+ *   workspace: atlasmem_cross_entropy_workspace_bytes(..., backward = 0) bytes, 16-byte aligned
+ * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits); sums are
+ * fp32.  n = 0 is valid.  Errors: E_INVALID for bad sizes, enums, null or overlapping pointers, a short
+ * workspace; E_SHAPE beyond the limits.  The workspace function returns -1 for sizes that are refused. */
+int64_t atlasmem_cross_entropy_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab,
+                                               int32_t backward);
+atlasmem_status atlasmem_cross_entropy(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                       int64_t vocab, const int64_t* labels, float* loss, float* lse, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+
+/* Its gradients: with G_iv = dloss_i (exp(z_iv - lse_i) - [v = label_i]), dX = G W and dW = G^T X.  The
+ * logits are computed again, a piece of the vocabulary at a time; G's pieces pass through the workspace
+ * in bf16 (fp32 calls: in three planes).
+ *   lse: the forward's;  dloss: fp32 [n], or NULL (one each)
+ *   dX: [n, d], dW: [vocab, d] of `dtype`, written, not added to; either may be NULL (not computed)
+ *   workspace: atlasmem_cross_entropy_workspace_bytes(..., backward = 1) bytes
+ * Sums run in one order: equal calls give equal bits. */
+atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                                int64_t vocab, const int64_t* labels, const float* lse,
+                                                const float* dloss, void* dX, void* dW, void* workspace,
+                                                int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

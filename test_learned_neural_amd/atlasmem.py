@@ -38,6 +38,7 @@ EXPORTS = (
     "atlasmem_update_chunked_conv",
     "atlasmem_linear_attention_workspace_bytes", "atlasmem_linear_attention", "atlasmem_linear_attention_backward",
     "atlasmem_group_norm_workspace_bytes", "atlasmem_group_norm", "atlasmem_group_norm_backward",
+    "atlasmem_cross_entropy_workspace_bytes", "atlasmem_cross_entropy", "atlasmem_cross_entropy_backward",
 )
 STATIC_MAX_MEMORIES = 128
 
@@ -119,6 +120,10 @@ def load():
                                 ctypes.c_int),
         "atlasmem_group_norm_backward": ([_vp, _vp, _i32, _i64, _i64, _i32, _i32] + [_vp] * 4 + [_i32] + [_vp] * 4
                                          + [_i64, _vp], ctypes.c_int),
+        "atlasmem_cross_entropy_workspace_bytes": ([_i32, _i64, _i32, _i64, _i32], _i64),
+        "atlasmem_cross_entropy": ([_vp, _vp, _i32, _i64, _i32, _i64] + [_vp] * 4 + [_i64, _vp], ctypes.c_int),
+        "atlasmem_cross_entropy_backward": ([_vp, _vp, _i32, _i64, _i32, _i64] + [_vp] * 6 + [_i64, _vp],
+                                            ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -353,3 +358,21 @@ def group_norm_backward(X, dY, dtype: int, n: int, L: int, channels: int, groups
                                                _ptr(beta), _ptr(mean), _ptr(rstd), activation, _ptr(dX), _ptr(dgamma),
                                                _ptr(dbeta), _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "atlasmem_group_norm_backward")
+
+
+def cross_entropy_workspace_bytes(dtype: int, n: int, d: int, vocab: int, backward: bool = False) -> int:
+    return int(load().atlasmem_cross_entropy_workspace_bytes(dtype, n, d, vocab, int(backward)))
+
+
+def cross_entropy(X, W, dtype: int, n: int, d: int, vocab: int, labels, loss, lse, workspace, stream=None):
+    _check(load().atlasmem_cross_entropy(_ptr(X), _ptr(W), dtype, n, d, vocab, _ptr(labels), _ptr(loss), _ptr(lse),
+                                         _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "atlasmem_cross_entropy")
+
+
+def cross_entropy_backward(X, W, dtype: int, n: int, d: int, vocab: int, labels, lse, dloss, dX, dW, workspace,
+                           stream=None):
+    _check(load().atlasmem_cross_entropy_backward(_ptr(X), _ptr(W), dtype, n, d, vocab, _ptr(labels), _ptr(lse),
+                                                  _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(workspace),
+                                                  _nbytes(workspace), _stream(stream)),
+           "atlasmem_cross_entropy_backward")

@@ -434,6 +434,14 @@ bool disjoint(const Range* out, int n_out, const Range* in, int n_in) {
   return true;
 }
 
+// Checked sizes of a cross entropy call.
+atlasmem_status cross_entropy_of(int32_t dtype, int64_t n, int32_t d, int64_t vocab, CrossEntropy& s) {
+  if (n < 0 || d < 1 || vocab < 1 || (dtype != ATLASMEM_F32 && dtype != ATLASMEM_BF16)) return ATLASMEM_E_INVALID;
+  if (d > (1 << 14) || n > (1 << 24) || vocab > (1 << 24)) return ATLASMEM_E_SHAPE;
+  s = {n, vocab, d, dtype == ATLASMEM_BF16};
+  return ATLASMEM_OK;
+}
+
 // Checked sizes of a group norm call.
 atlasmem_status group_norm_of(int32_t dtype, int64_t n, int64_t L, int32_t channels, int32_t groups,
                               int32_t activation, GroupNorm& s) {
@@ -910,6 +918,48 @@ atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int3
   if (!disjoint(out, 4, in, 6)) return ATLASMEM_E_INVALID;
   s.gamma = gamma, s.beta = beta;
   return group_norm_backward(s, X, dY, mean, rstd, dX, dgamma, dbeta, workspace, S(stream));
+}
+
+int64_t atlasmem_cross_entropy_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab,
+                                               int32_t backward) {
+  CrossEntropy s;
+  if (cross_entropy_of(dtype, n, d, vocab, s) != ATLASMEM_OK) return -1;
+  return cross_entropy_workspace_bytes(s, backward != 0);
+}
+
+atlasmem_status atlasmem_cross_entropy(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                       int64_t vocab, const int64_t* labels, float* loss, float* lse, void* workspace,
+                                       int64_t workspace_bytes, void* stream) {
+  CrossEntropy s;
+  const atlasmem_status e = cross_entropy_of(dtype, n, d, vocab, s);
+  if (e != ATLASMEM_OK) return e;
+  if (n == 0) return ATLASMEM_OK;
+  if (!X || !W || !labels || !loss || !lse || !workspace) return ATLASMEM_E_INVALID;
+  const int64_t need = cross_entropy_workspace_bytes(s, false);
+  if (workspace_bytes < need) return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4;
+  const Range out[] = {{loss, n * 4}, {lse, n * 4}, {workspace, need}};
+  const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {labels, n * 8}};
+  if (!disjoint(out, 3, in, 3)) return ATLASMEM_E_INVALID;
+  return cross_entropy(s, X, W, labels, loss, lse, workspace, S(stream));
+}
+
+atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                                int64_t vocab, const int64_t* labels, const float* lse,
+                                                const float* dloss, void* dX, void* dW, void* workspace,
+                                                int64_t workspace_bytes, void* stream) {
+  CrossEntropy s;
+  const atlasmem_status e = cross_entropy_of(dtype, n, d, vocab, s);
+  if (e != ATLASMEM_OK) return e;
+  if (n > 0 && (!X || !W || !labels || !lse || !workspace)) return ATLASMEM_E_INVALID;
+  if (!dX && !dW) return ATLASMEM_OK;
+  const int64_t need = cross_entropy_workspace_bytes(s, true);
+  if (n > 0 && workspace_bytes < need) return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4;
+  const Range out[] = {{dX, n * d * el}, {dW, vocab * d * el}, {workspace, n > 0 ? need : 0}};
+  const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {labels, n * 8}, {lse, n * 4}, {dloss, n * 4}};
+  if (!disjoint(out, 3, in, 5)) return ATLASMEM_E_INVALID;
+  return cross_entropy_backward(s, X, W, labels, lse, dloss, dX, dW, workspace, S(stream));
 }
 
 }  // extern "C"

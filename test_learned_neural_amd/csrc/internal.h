@@ -316,4 +316,17 @@ atlasmem_status group_norm_backward(const GroupNorm& s, const void* X, const voi
                                     const float* rstd, void* dX, float* dgamma, float* dbeta, void* workspace,
                                     hipStream_t st);
 
+// Softmax cross entropy over a large vocabulary (k_xent.hip)
+struct CrossEntropy {
+  int64_t n, vocab;
+  int d;
+  bool bf16;
+};
+int64_t cross_entropy_workspace_bytes(const CrossEntropy& s, bool backward);
+atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* W, const int64_t* labels, float* loss,
+                              float* lse, void* workspace, hipStream_t st);
+atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, const void* W, const int64_t* labels,
+                                       const float* lse, const float* dloss, void* dX, void* dW, void* workspace,
+                                       hipStream_t st);
+
 }  // namespace am
