@@ -1,6 +1,6 @@
 // Softmax cross entropy over a large vocabulary, without keeping the logits (gfx950).
 //   z = X W^T, lse_i = log sum_v exp z_iv, loss_i = lse_i - z_i,y_i
-//   G_iv = dloss_i (exp(z_iv - lse_i) - [v = y_i]),  dX = G W,  dW = G^T X
+//   G_iv = exp(z_iv - lse_i) - [v = y_i],  dX_i = dloss_i (G W)_i,  dW = G^T (dloss X)
 // The forward computes tiles of z and leaves of each row and tile its maximum and sum of exponentials;
 // the backward computes them again by pieces of the vocabulary, writes the piece's G (bf16), and both
 // products read it.  Three matrix products of one engine:
@@ -8,7 +8,9 @@
 //   dX  a = W (lanes d, rows across the contraction: read transposed from LDS), b = G
 //   dW  a = X, b = G, both across the contraction
 // An output tile has b's index in its lanes and a's, four at a time, in its registers.  bf16 inputs are
-// used as they are; fp32 ones (and then G) as three bf16 planes, the six products of planes down to
+// used as they are.  G is rounded without its weight: the label's entry, -1 + p, is the large one and in
+// bf16 nearly exact while p is small; dX's weight goes to the fp32 sums, and dW's to X, relative to the
+// largest one, so that equal weights round nothing.  fp32 inputs (and then G) as three bf16 planes, the six products of planes down to
 // 2^-16 of the leading one summed in fp32 (relative 2^-24, at the matrix cores' bf16 rate over six).
 #include <algorithm>
 
@@ -42,14 +44,14 @@ struct GemmArgs {
   int part0;
   const int64_t* labels;   // [nb]
   const float* lse;
-  const float* dloss;
   int64_t v0, vocab;
   uint16_t* g;             // GRAD: [nb][ldg], planes of pg elements
   int64_t ldg, pg;
   int planes;
   float* acc;              // ACC: [splits][nb][na]
   int first, add;
-  void* out;               // OUT: [nb][ldo]
+  const float* scale;      // OUT: one factor, or null
+  void* out;               // [nb][ldo]
   int64_t ldo;
   int out_bf16;
 };
@@ -120,6 +122,51 @@ struct Stage {
   }
 };
 
+// A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
+// through LDS, so that a row's columns leave in whole 16-byte pieces side by side.  With `rest` the
+// accumulators keep what the rounding left.
+template <int TA, int TB, int MA, int NB>
+__device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, bool rest, uint16_t* out,
+                         int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr) {
+  constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
+  const int lane = tid & 63, hf = lane >> 5, col = lane & 31;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int r = wb + 32 * j + col;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x16& x = acc[i][j];
+        const uint2 o = {cvt_pk_bf16(x[4 * q], x[4 * q + 1]), cvt_pk_bf16(x[4 * q + 2], x[4 * q + 3])};
+        const int c = (wa + 32 * i + 8 * q) >> 3;
+        *(uint2*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3) + 4 * hf) = o;
+        if (rest) {
+          x[4 * q] -= __uint_as_float(o.x << 16), x[4 * q + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
+          x[4 * q + 2] -= __uint_as_float(o.y << 16), x[4 * q + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
+        }
+      }
+  }
+  __syncthreads();
+  const bool vec = ld % 8 == 0 && ((uintptr_t)out & 15) == 0;
+#pragma unroll 4
+  for (int id = tid; id < TB * CH; id += 256) {
+    const int r = id / CH, c = id % CH;
+    const int64_t row = r0 + r, at = c0 + 8 * c;
+    if (row >= nr || at >= nc) continue;
+    const u32x4 v = *(const u32x4*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3));
+    uint16_t* p = out + row * ld + at;
+    if (vec) {
+      *(u32x4*)p = v;
+    } else {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (at + n < nc) p[n] = (uint16_t)(v[n >> 1] >> (16 * (n & 1)));
+    }
+  }
+}
+
 template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI>
 __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs g) {
   static_assert(WA * WB == 4, "four waves");
@@ -158,40 +205,63 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
       for (int n = 0; n < 16; ++n) acc[i][j][n] = 0.0f;
 
+  // Steps: tile t is computed from one LDS buffer while t + 1, already in registers, is written to the
+  // other and t + 2 is on its way from memory; the operands of a quarter of a step are read a quarter
+  // ahead.  One barrier a step, before its last quarter.  Past the end fetches are masked off.
   Stage<TA, AX> sa;
   Stage<TB, BX> sb;
-  auto fetch = [&](int it) {
-    const int q = it / steps;
-    const int64_t k = k0 + (int64_t)(it - q * steps) * kBK;
-    const int p = g.products == 1 ? kProducts - 1 : q;
-    sa.load(g.a + kPlaneA[p] * g.pa, g.lda, a0, g.na, k, k1, tid);
-    sb.load(g.b + kPlaneB[p] * g.pb, g.ldb, b0, g.nb, k, k1, tid);
+  int q = 0;
+  int64_t k = k0;
+  auto fetch = [&]() {
+    const int p = g.products == 1 ? kProducts - 1 : min(q, kProducts - 1);
+    const int64_t at = q < g.products ? k : k1;
+    sa.load(g.a + kPlaneA[p] * g.pa, g.lda, a0, g.na, at, k1, tid);
+    sb.load(g.b + kPlaneB[p] * g.pb, g.ldb, b0, g.nb, at, k1, tid);
+    k += kBK;
+    if (k >= k1) k = k0, ++q;
+  };
+  u32x4 ao[2][MA], bo[2][NB];
+  auto read = [&](int set, const uint16_t* s, int ks) {
+#pragma unroll
+    for (int i = 0; i < MA; ++i) ao[set][i] = A::op(s, wa + 32 * i, ks, lane);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) bo[set][j] = B::op(s + A::kElems, wb + 32 * j, ks, lane);
   };
   if (iters > 0) {
-    fetch(0);
+    fetch();
     sa.store(sm, tid);
     sb.store(sm + A::kElems, tid);
+    fetch();
+    __syncthreads();
+    read(0, sm, 0);
   }
   for (int it = 0; it < iters; ++it) {
-    __syncthreads();
     const uint16_t* s = sm + (it & 1) * kStage;
-    if (it + 1 < iters) fetch(it + 1);
+    uint16_t* d = sm + ((it + 1) & 1) * kStage;
 #pragma unroll
-    for (int ks = 0; ks < kBK / 16; ++ks) {
-      u32x4 ao[MA], bo[NB];
-#pragma unroll
-      for (int i = 0; i < MA; ++i) ao[i] = A::op(s, wa + 32 * i, ks, lane);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) bo[j] = B::op(s + A::kElems, wb + 32 * j, ks, lane);
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks < 3) read((ks + 1) & 1, s, ks + 1);
+      if (ks == 0) sa.store(d, tid);
+      if (ks == 1) sb.store(d + A::kElems, tid);
+      if (ks == 2) fetch();
+      if (ks == 3) {
+        __syncthreads();
+        read(0, d, 0);
+      }
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ao[i], bo[j], acc[i][j]);
-    }
-    if (it + 1 < iters) {
-      uint16_t* d = sm + ((it + 1) & 1) * kStage;
-      sa.store(d, tid);
-      sb.store(d + A::kElems, tid);
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ao[ks & 1][i], bo[ks & 1][j], acc[i][j]);
+      // one matrix instruction, then a share of the loads and stores
+      constexpr int kReads = (AX ? 2 : 1) * MA + (BX ? 2 : 1) * NB, kSlots = MA * NB / 2;
+#pragma unroll
+      for (int n = 0; n < kSlots; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kSlots - 1) / kSlots, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+      }
     }
   }
 
@@ -239,34 +309,36 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int64_t r = b0 + wb + 32 * j + col;
-      if (r >= g.nb) continue;
-      const int64_t y = g.labels[r];
+      const int64_t y = r < g.nb ? g.labels[r] : -1;
       const bool kept = y >= 0 && y < g.vocab;
-      const float l = kept ? g.lse[r] : 0.0f, w = kept ? (g.dloss ? g.dloss[r] : 1.0f) : 0.0f;
+      const float l = kept ? g.lse[r] : 0.0f;
       const int64_t at = kept ? y - g.v0 : -1;
-      uint16_t* out = g.g + r * g.ldg;
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t v = a0 + wa + 32 * i + 8 * q + 4 * hf;
-          if (v >= g.ldg) continue;
-          float x[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float p = __expf(acc[i][j][4 * q + n] - l) - (v + n == at ? 1.0f : 0.0f);
-            x[n] = kept && v + n < g.na ? p * w : 0.0f;
-          }
-          for (int n = 0; n < g.planes; ++n) {
-            const uint2 o = {cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])};
-            *(uint2*)(out + n * g.pg + v) = o;
-            x[0] -= __uint_as_float(o.x << 16), x[1] -= __uint_as_float(o.x & 0xFFFF0000u);
-            x[2] -= __uint_as_float(o.y << 16), x[3] -= __uint_as_float(o.y & 0xFFFF0000u);
-          }
+        for (int n = 0; n < 16; ++n) {
+          const int64_t v = a0 + wa + 32 * i + 8 * (n >> 2) + 4 * hf + (n & 3);
+          const float p = __expf(acc[i][j][n] - l) - (v == at ? 1.0f : 0.0f);
+          acc[i][j][n] = kept && v < g.na ? p : 0.0f;
         }
     }
+    for (int n = 0; n < g.planes; ++n)
+      put_rows<TA, TB, MA, NB>(sm, acc, wa, wb, tid, n + 1 < g.planes, g.g + n * g.pg, g.ldg, a0, g.ldg, b0, g.nb);
   }
 
+  if constexpr (EPI == EPI_OUT) {
+    const float w = g.scale ? *g.scale : 1.0f;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
+    if (g.out_bf16) {
+      put_rows<TA, TB, MA, NB>(sm, acc, wa, wb, tid, false, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
+      return;
+    }
+  }
   if constexpr (EPI == EPI_ACC || EPI == EPI_OUT) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -278,33 +350,49 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
         for (int q = 0; q < 4; ++q) {
           const int64_t c = a0 + wa + 32 * i + 8 * q + 4 * hf;
           if (c >= g.na) continue;
-          float x[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) x[n] = acc[i][j][4 * q + n];
+          float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           if constexpr (EPI == EPI_ACC) {
             float4* p = (float4*)(g.acc + ((int64_t)blockIdx.y * g.nb + r) * g.lda + c);
             if (g.add) {
               const float4 o = *p;
-              x[0] += o.x, x[1] += o.y, x[2] += o.z, x[3] += o.w;
+              x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
             }
-            *p = float4{x[0], x[1], x[2], x[3]};
+            *p = x;
           } else {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-              if (c + n < g.ldo) {
-                if (g.out_bf16) ((uint16_t*)g.out)[r * g.ldo + c + n] = (uint16_t)bf16_bits(x[n]);
-                else ((float*)g.out)[r * g.ldo + c + n] = x[n];
-              }
+            float* p = (float*)g.out + r * g.ldo + c;
+            if (c + 0 < g.ldo) p[0] = x.x;
+            if (c + 1 < g.ldo) p[1] = x.y;
+            if (c + 2 < g.ldo) p[2] = x.z;
+            if (c + 3 < g.ldo) p[3] = x.w;
           }
         }
     }
   }
 }
 
-// Rows of an input as bf16 planes [planes][rows][dp], zero from column d on; rows whose label is no
-// class become zero (what they hold must not reach the other rows' sums).
+// The largest |dloss| of the rows that count (one workgroup), 1 without weights.
+__global__ __launch_bounds__(1024) void xe_largest(const float* dloss, const int64_t* labels, int64_t n, int64_t vocab,
+                                                   float* out) {
+  __shared__ float s[16];
+  float m = 0.0f;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) {
+    const float w = fabsf(dloss[i]);
+    if (labels[i] >= 0 && labels[i] < vocab) m = fmaxf(m, w <= 3.0e38f ? w : 0.0f);
+  }
+  for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 16; ++k) m = fmaxf(m, s[k]);
+    *out = m > 0.0f ? m : 1.0f;
+  }
+}
+
+// Rows of an input as bf16 planes [planes][rows][dp], zero from column d on.  With labels, for dW: rows
+// that count times dloss / largest, and zeros for those whose label is no class (what they hold must
+// not reach the other rows' sums).
 __global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int dp, int planes, const int64_t* labels,
-                          int64_t vocab, uint16_t* out) {
+                          int64_t vocab, const float* dloss, const float* largest, uint16_t* out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // a pair of columns
   const int64_t per = dp / 2;
   if (i >= rows * per) return;
@@ -313,6 +401,10 @@ __global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int d
   const bool kept = !labels || (labels[r] >= 0 && labels[r] < vocab);
   float v0 = kept && c < d ? load_in(x, r * d + c, in_bf16) : 0.0f;
   float v1 = kept && c + 1 < d ? load_in(x, r * d + c + 1, in_bf16) : 0.0f;
+  if (dloss && kept) {
+    const float w = dloss[r] / *largest;
+    v0 *= w, v1 *= w;
+  }
   for (int n = 0; n < planes; ++n) {
     const uint32_t w = cvt_pk_bf16(v0, v1);
     *(uint32_t*)(out + (n * rows + r) * dp + c) = w;
@@ -360,13 +452,17 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
   }
 }
 
-// dX from the partial sums of the contraction's pieces.
-__global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, void* out, int out_bf16) {
+// dX from the partial sums of the contraction's pieces, times the rows' weights.
+__global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int64_t* labels, int64_t vocab,
+                       const float* dloss, void* out, int out_bf16) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n * d) return;
   const int64_t at = i / d * dp + i % d;
   float v = 0.0f;
   for (int s = 0; s < splits; ++s) v += acc[s * n * dp + at];
+  const int64_t y = labels[i / d];
+  if (y < 0 || y >= vocab) v = 0.0f;
+  else if (dloss) v *= dloss[i / d];
   if (out_bf16) ((uint16_t*)out)[i] = (uint16_t)bf16_bits(v);
   else ((float*)out)[i] = v;
 }
@@ -442,10 +538,11 @@ Plan plan_of(const CrossEntropy& s) {
 bool direct(const void* p, const CrossEntropy& s) { return s.bf16 && s.d % 8 == 0 && ((uintptr_t)p & 15) == 0; }
 
 atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int64_t* labels,
-                          uint16_t* out, hipStream_t st) {
+                          const float* dloss, const float* largest, uint16_t* out, hipStream_t st) {
   const int64_t blocks = (rows * (p.dp / 2) + 255) / 256;
   if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
-  xe_planes<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, p.planes, labels, s.vocab, out);
+  xe_planes<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, p.planes, labels, s.vocab, dloss,
+                                            largest, out);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -455,7 +552,7 @@ atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, i
 int64_t cross_entropy_workspace_bytes(const CrossEntropy& s, bool backward) {
   const Plan p = plan_of(s);
   const int64_t inputs = p.x_bytes + p.w_bytes;
-  return backward ? inputs + p.g_bytes + p.acc_bytes : inputs + p.part_bytes;
+  return backward ? inputs + p.x_bytes + p.g_bytes + p.acc_bytes + 256 : inputs + p.part_bytes;
 }
 
 atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* W, const int64_t* labels, float* loss,
@@ -467,8 +564,8 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   GemmArgs g = {};
   g.part = (float2*)(ws + p.x_bytes + p.w_bytes);
   atlasmem_status e = ATLASMEM_OK;
-  if (!direct(X, s)) e = planes_of(X, s, p, s.n, nullptr, xp, st);
-  if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, wp, st);
+  if (!direct(X, s)) e = planes_of(X, s, p, s.n, nullptr, nullptr, nullptr, xp, st);
+  if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, wp, st);
   if (e != ATLASMEM_OK) return e;
   g.a = direct(W, s) ? (const uint16_t*)W : wp;
   g.b = direct(X, s) ? (const uint16_t*)X : xp;
@@ -501,11 +598,20 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   char* ws = (char*)workspace;
   uint16_t* xp = (uint16_t*)ws;
   uint16_t* wp = (uint16_t*)(ws + p.x_bytes);
-  uint16_t* gp = (uint16_t*)(ws + p.x_bytes + p.w_bytes);
-  float* acc = (float*)(ws + p.x_bytes + p.w_bytes + p.g_bytes);
-  // rows that are left out are copied as zeros: their values must not meet G's zeros in dW
-  atlasmem_status e = planes_of(X, s, p, s.n, labels, xp, st);
-  if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, wp, st);
+  uint16_t* xw = (uint16_t*)(ws + p.x_bytes + p.w_bytes);  // weighted, for dW
+  uint16_t* gp = (uint16_t*)(ws + 2 * p.x_bytes + p.w_bytes);
+  float* acc = (float*)(ws + 2 * p.x_bytes + p.w_bytes + p.g_bytes);
+  float* largest = (float*)(ws + 2 * p.x_bytes + p.w_bytes + p.g_bytes + p.acc_bytes);
+  atlasmem_status e = ATLASMEM_OK;
+  if (dW) {
+    if (dloss) {
+      xe_largest<<<1, 1024, 0, st>>>(dloss, labels, s.n, s.vocab, largest);
+      AM_LAUNCH_CHECK();
+    }
+    e = planes_of(X, s, p, s.n, labels, dloss, largest, xw, st);
+  }
+  if (e == ATLASMEM_OK && !direct(X, s)) e = planes_of(X, s, p, s.n, nullptr, nullptr, nullptr, xp, st);
+  if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, wp, st);
   if (e != ATLASMEM_OK) return e;
   const uint16_t* wa = direct(W, s) ? (const uint16_t*)W : wp;
   const int products = s.bf16 ? 1 : kProducts;
@@ -514,11 +620,11 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     GemmArgs g = {};
     g.products = products;
     // G of the piece
-    g.a = wa + v0 * p.dp, g.b = xp;
+    g.a = wa + v0 * p.dp, g.b = direct(X, s) ? (const uint16_t*)X : xp;
     g.lda = g.ldb = p.dp;
     g.pa = s.vocab * p.dp, g.pb = s.n * p.dp;
     g.na = nv, g.nb = s.n, g.K = p.dp;
-    g.labels = labels, g.lse = lse, g.dloss = dloss, g.v0 = v0, g.vocab = s.vocab;
+    g.labels = labels, g.lse = lse, g.v0 = v0, g.vocab = s.vocab;
     g.g = gp, g.ldg = ldg, g.pg = s.n * ldg, g.planes = p.planes;
     e = gemm<false, false, EPI_GRAD>(g, wide(nv, s.n), st);
     if (e != ATLASMEM_OK) return e;
@@ -535,7 +641,8 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     if (dW) {
       GemmArgs x = {};
       x.products = products;
-      x.a = xp, x.lda = p.dp, x.pa = s.n * p.dp, x.na = p.dp;
+      x.a = xw, x.lda = p.dp, x.pa = s.n * p.dp, x.na = p.dp;
+      x.scale = dloss ? largest : nullptr;
       x.b = gp, x.ldb = ldg, x.pb = s.n * ldg, x.nb = nv;
       x.K = s.n;
       x.out = (char*)dW + v0 * s.d * (s.bf16 ? 2 : 4), x.ldo = s.d, x.out_bf16 = s.bf16;
@@ -544,7 +651,8 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     }
   }
   if (dX) {
-    xe_sum<<<(unsigned)((s.n * s.d + 255) / 256), 256, 0, st>>>(acc, p.splits, s.n, s.d, p.dp, dX, s.bf16);
+    xe_sum<<<(unsigned)((s.n * s.d + 255) / 256), 256, 0, st>>>(acc, p.splits, s.n, s.d, p.dp, labels, s.vocab, dloss,
+                                                              dX, s.bf16);
     AM_LAUNCH_CHECK();
   }
   return ATLASMEM_OK;
