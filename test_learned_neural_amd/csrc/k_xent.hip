@@ -21,10 +21,12 @@ namespace am {
 
 namespace {
 
-constexpr int kBK = 64;        // contraction elements of a step
+constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
+constexpr int kStages = 4;     // steps in LDS: one in use, three on their way
 constexpr int kProducts = 6;   // of planes, fp32
-__constant__ const int kPlaneA[kProducts] = {2, 0, 1, 1, 0, 0};
-__constant__ const int kPlaneB[kProducts] = {0, 2, 1, 0, 1, 0};
+// The planes of product p, the small products first: a's 2 0 1 1 0 0, b's 0 2 1 0 1 0 (four bits each).
+__device__ __forceinline__ int plane_a(int p) { return (0x001102 >> (4 * p)) & 3; }
+__device__ __forceinline__ int plane_b(int p) { return (0x010120 >> (4 * p)) & 3; }
 
 enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT };
 
@@ -56,21 +58,53 @@ struct GemmArgs {
   int out_bf16;
 };
 
-// One operand's tile in LDS.  Along the contraction: [R][64], 16-byte pieces of a row exchanged by the
-// row's low bits; across: [64][R], 32-byte pieces exchanged by the contraction index's low bits.  Either
-// way the lanes of a read lie on distinct banks.
+// One operand's step in LDS.  Along the contraction: [R][32], the 16-byte pieces of four rows (256 bytes,
+// all banks) exchanged by the four's index; across: [32][R], pairs of 32-byte pieces exchanged by the
+// contraction index's low bits.  Either way the lanes that are served together lie on distinct banks.
+// Loads go straight to LDS, 64 pieces of 16 bytes an instruction, in LDS order: the exchange is in the
+// lanes' global offsets.  Those outside the matrix have the top bit, and the range check writes zeros.
+//
+// The load is written out because the compiler, knowing it, waits for all of them before every
+// transposing read.  It has no result register: its address is read when it is issued, and what it
+// writes, LDS, is waited for by wait_all alone.  m0 has no other use in these kernels.
+__device__ __forceinline__ void load_to_lds(rsrc_t rs, uint32_t voff, const uint16_t* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(rs)
+               : "memory");
+}
 template <int R, bool ACROSS>
 struct Tile {
   static constexpr int kElems = R * kBK;
-  static constexpr int kLoads = R * kBK / 8 / 256;
-  __device__ static int place(int i, int tid) {
-    const int id = tid + i * 256;
+  static constexpr int kLoads = R * kBK / 8 / 256;  // instructions of a wave
+  uint32_t off[kLoads];
+  int kc;  // along: the lane's first contraction element
+
+  __device__ void init(int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
+    kc = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = (wave * kLoads + i) * 64 + lane;  // piece in LDS order
+      if constexpr (ACROSS) {
+        const int k = id / (R / 8), at = id % (R / 8);
+        const int c = ((((at >> 1) ^ ((k & 3) << 1)) << 1) | (at & 1)) * 8;
+        off[i] = c < rows - r0 ? (uint32_t)((k * ld + c) * 2) : 0x80000000u;
+      } else {
+        const int r = id >> 2;
+        off[i] = r < rows - r0 ? (uint32_t)((r * ld + kc) * 2) : 0x80000000u;
+      }
+    }
+  }
+  // load number i of a step.  p: the matrix at (row or column r0, contraction k); left: contraction
+  // elements from k on (none: zeros); room: elements of a row from r0 on (across)
+  __device__ void load(int i, uint16_t* s, const uint16_t* p, int left, int64_t ld, int64_t room, int wave) const {
+    const uint16_t* d = s + (wave * kLoads + i) * 512;
     if constexpr (ACROSS) {
-      const int k = id / (R / 8), c = id % (R / 8);
-      return k * R + ((((c >> 1) ^ (k & 3)) << 1) | (c & 1)) * 8;
+      const int n = left < kBK ? left : kBK;
+      const rsrc_t rs = make_rsrc(p, n > 0 ? (uint32_t)(((n - 1) * ld + room) * 2) : 0u);
+      load_to_lds(rs, off[i], d);
     } else {
-      const int r = id >> 3, c = id & 7;
-      return r * kBK + ((c ^ (r & 7)) << 3);
+      const rsrc_t rs = make_rsrc(p, 0x7fffffffu);
+      load_to_lds(rs, off[i] | (kc < left ? 0u : 0x80000000u), d);
     }
   }
   // lane's eight contraction elements 16 ks + 8 (lane / 32) + 0..7 of row (column) r0 + lane % 32
@@ -79,7 +113,7 @@ struct Tile {
     if constexpr (ACROSS) {
       const int e = (lane & 15) >> 2;
       const int k = 16 * ks + 8 * hf + e;
-      const int c = (((r0 + (lane & 16)) >> 4) ^ e) * 16 + 4 * (lane & 3);
+      const int c = (((r0 + (lane & 16)) >> 4) ^ (e << 1)) * 16 + 4 * (lane & 3);
       typedef short v4i16 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) v4i16* lds4;
       const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(s + k * R + c)));
@@ -87,40 +121,17 @@ struct Tile {
       return u32x4{lo.x, lo.y, hi.x, hi.y};
     } else {
       const int r = r0 + (lane & 31);
-      return *(const u32x4*)(s + r * kBK + (((2 * ks + hf) ^ (r & 7)) << 3));
+      return *(const u32x4*)(s + r * kBK + (((2 * ks + hf) ^ ((r >> 2) & 3)) << 3));
     }
   }
 };
 
-// Global side: one step's pieces of a tile in registers.
-template <int R, bool ACROSS>
-struct Stage {
-  u32x4 v[Tile<R, ACROSS>::kLoads];
-  // rows r0.. of a matrix along the contraction, or columns r0.. of one across it; contraction k0..
-  __device__ void load(const uint16_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k1, int tid) {
-    const int64_t left = rows - r0;
-    if constexpr (ACROSS) {
-      const int64_t ks = min(k1 - k0, (int64_t)kBK);
-      const rsrc_t rs = make_rsrc(p + k0 * ld + r0, (uint32_t)(ks <= 0 ? 0 : (ks * ld - r0) * 2));
-#pragma unroll
-      for (int i = 0; i < Tile<R, true>::kLoads; ++i) {
-        const int id = tid + i * 256, k = id / (R / 8), c = (id % (R / 8)) * 8;
-        v[i] = buf_ld16(rs, k < ks && c < left ? (int)((k * ld + c) * 2) : -1, 0);
-      }
-    } else {
-      const rsrc_t rs = make_rsrc(p + r0 * ld + k0, (uint32_t)((min(left, (int64_t)R) * ld - k0) * 2));
-#pragma unroll
-      for (int i = 0; i < Tile<R, false>::kLoads; ++i) {
-        const int id = tid + i * 256, r = id >> 3, c = (id & 7) * 8;
-        v[i] = buf_ld16(rs, r < left && k0 + c < k1 ? (int)((r * ld + c) * 2) : -1, 0);
-      }
-    }
-  }
-  __device__ void store(uint16_t* s, int tid) const {
-#pragma unroll
-    for (int i = 0; i < Tile<R, ACROSS>::kLoads; ++i) *(u32x4*)(s + Tile<R, ACROSS>::place(i, tid)) = v[i];
-  }
-};
+// Waits until at most N of the wave's loads are on their way and its LDS reads are done, then for the
+// other waves: what was loaded before is in LDS, and what was read before may be overwritten.
+template <int N>
+__device__ __forceinline__ void wait_all() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 // A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
 // through LDS, so that a row's columns leave in whole 16-byte pieces side by side.  With `rest` the
@@ -175,7 +186,8 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
   using B = Tile<TB, BX>;
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   constexpr int kStage = A::kElems + B::kElems;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hf = lane >> 5, col = lane & 31;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hf = lane >> 5,
+            col = lane & 31;
   const int wa = (wave % WA) * (TA / WA), wb = (wave / WA) * (TB / WB);
 
   // tiles of one XCD are neighbours: eight tiles of b beside four of a at a time share its L2
@@ -205,68 +217,71 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
       for (int n = 0; n < 16; ++n) acc[i][j][n] = 0.0f;
 
-  // Steps: tile t is computed from one LDS buffer while t + 1, already in registers, is written to the
-  // other and t + 2 is on its way from memory; the operands of a quarter of a step are read a quarter
-  // ahead.  One barrier a step, before its last quarter.  Past the end fetches are masked off.
-  Stage<TA, AX> sa;
-  Stage<TB, BX> sb;
-  int q = 0;
-  int64_t k = k0;
-  auto fetch = [&]() {
-    const int p = g.products == 1 ? kProducts - 1 : min(q, kProducts - 1);
-    const int64_t at = q < g.products ? k : k1;
-    sa.load(g.a + kPlaneA[p] * g.pa, g.lda, a0, g.na, at, k1, tid);
-    sb.load(g.b + kPlaneB[p] * g.pb, g.ldb, b0, g.nb, at, k1, tid);
-    k += kBK;
-    if (k >= k1) k = k0, ++q;
+  // Step t is computed from one of four LDS buffers while t + 1 .. t + 3 are on their way to the others;
+  // operands are read one matrix-instruction depth ahead.  One barrier a step, between its two depths:
+  // behind it step t's buffer takes t + 4's loads, and step t + 1 is there.  Past the end loads are
+  // masked off.  The source order below is the schedule: each matrix instruction with one read or load.
+  A ta;
+  B tb;
+  ta.init(g.lda, a0, g.na, wave, lane);
+  tb.init(g.ldb, b0, g.nb, wave, lane);
+  const int64_t step_a = AX ? kBK * g.lda : kBK, step_b = BX ? kBK * g.ldb : kBK;
+  const int64_t start_a = AX ? k0 * g.lda + a0 : a0 * g.lda + k0, start_b = BX ? k0 * g.ldb + b0 : b0 * g.ldb + k0;
+  int q = g.products == 1 ? kProducts - 1 : 0;
+  const uint16_t *pa = g.a + plane_a(q) * g.pa + start_a, *pb = g.b + plane_b(q) * g.pb + start_b;
+  int left = (int)(k1 - k0);
+  auto load = [&](int n, uint16_t* d) {
+    if (n < A::kLoads) ta.load(n, d, pa, left, g.lda, g.lda - a0, wave);
+    else tb.load(n - A::kLoads, d + A::kElems, pb, left, g.ldb, g.ldb - b0, wave);
   };
+  auto next = [&]() {
+    left -= kBK;
+    pa += step_a, pb += step_b;
+    if (left <= 0 && q + 1 < kProducts) {
+      ++q;
+      left = (int)(k1 - k0);
+      pa = g.a + plane_a(q) * g.pa + start_a, pb = g.b + plane_b(q) * g.pb + start_b;
+    }
+  };
+  constexpr int kLoads = A::kLoads + B::kLoads;
   u32x4 ao[2][MA], bo[2][NB];
-  auto read = [&](int set, const uint16_t* s, int ks) {
-#pragma unroll
-    for (int i = 0; i < MA; ++i) ao[set][i] = A::op(s, wa + 32 * i, ks, lane);
-#pragma unroll
-    for (int j = 0; j < NB; ++j) bo[set][j] = B::op(s + A::kElems, wb + 32 * j, ks, lane);
+  // operands in the order in which the products need them: a 0, b 0.., a 1..
+  auto read = [&](int n, int set, const uint16_t* s, int ks) {
+    if (n == 0) ao[set][0] = A::op(s, wa, ks, lane);
+    else if (n <= NB) bo[set][n - 1] = B::op(s + A::kElems, wb + 32 * (n - 1), ks, lane);
+    else ao[set][n - NB] = A::op(s, wa + 32 * (n - NB), ks, lane);
   };
   if (iters > 0) {
-    fetch();
-    sa.store(sm, tid);
-    sb.store(sm + A::kElems, tid);
-    fetch();
-    __syncthreads();
-    read(0, sm, 0);
+#pragma unroll
+    for (int t = 0; t < kStages; ++t) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) load(n, sm + t * kStage);
+      next();
+    }
+    wait_all<(kStages - 1) * kLoads>();
+#pragma unroll
+    for (int n = 0; n < MA + NB; ++n) read(n, 0, sm, 0);
   }
   for (int it = 0; it < iters; ++it) {
-    const uint16_t* s = sm + (it & 1) * kStage;
-    uint16_t* d = sm + ((it + 1) & 1) * kStage;
+    uint16_t* s = sm + (it & (kStages - 1)) * kStage;
+    const uint16_t* d = sm + ((it + 1) & (kStages - 1)) * kStage;
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks < 3) read((ks + 1) & 1, s, ks + 1);
-      if (ks == 0) sa.store(d, tid);
-      if (ks == 1) sb.store(d + A::kElems, tid);
-      if (ks == 2) fetch();
-      if (ks == 3) {
-        __syncthreads();
-        read(0, d, 0);
-      }
+    for (int ks = 0; ks < 2; ++ks) {
+      if (ks == 1) wait_all<(kStages - 2) * kLoads>();
 #pragma unroll
-      for (int i = 0; i < MA; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ao[ks & 1][i], bo[ks & 1][j], acc[i][j]);
-      // one matrix instruction, then a share of the loads and stores
-      constexpr int kReads = (AX ? 2 : 1) * MA + (BX ? 2 : 1) * NB, kSlots = MA * NB / 2;
-#pragma unroll
-      for (int n = 0; n < kSlots; ++n) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kSlots - 1) / kSlots, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+      for (int n = 0; n < MA * NB; ++n) {
+        acc[n / NB][n % NB] = mfma32(ao[ks][n / NB], bo[ks][n % NB], acc[n / NB][n % NB]);
+        if (n < MA + NB) read(n, ks ^ 1, ks ? d : s, ks ^ 1);
+        if (ks == 1 && n >= MA * NB - kLoads) load(n - (MA * NB - kLoads), s);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    next();
   }
+  // loads past the end may still be on their way to LDS
+  wait_all<0>();
 
   if constexpr (EPI == EPI_LSE) {
-    __syncthreads();
     float2* red = (float2*)sm;  // [WA][TB]
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -481,7 +496,7 @@ int64_t align256(int64_t b) { return up(b, 256); }
 
 template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI>
 atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
-  constexpr int lds = 2 * (TA + TB) * kBK * 2;
+  constexpr int lds = std::max(kStages * (TA + TB) * kBK * 2, TA * TB * 2);
   auto kern = xe_gemm<TA, TB, WA, WB, AX, BX, EPI>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)

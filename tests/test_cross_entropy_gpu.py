@@ -6,6 +6,8 @@ Bounds from the arithmetic, u = 2^-24, A the sum of a product's absolute terms:
   lse    el = max ez + (|z - m| + 16) 2 u + (u |lse|) for hardware exponentials and the joins
   G      |G| (ez + el + (|z - lse| + 8) 2 u) (of the probability's part) and its rounding, 2^-8 in bf16,
          3 u in planes;  products with it as z
+  dW     takes the rows of X times their weight over the largest one, another rounding of every term:
+         2^-8 |G x| in bf16, 3 u in planes, and 3 u for the quotient, its product and the factor outside
 and one rounding of the output (2^-8 for bf16, u for fp32).
 """
 
@@ -102,7 +104,7 @@ def check(c, block=2000):
         within("dX", dX[r:r + block], dx, eX)
         x0 = np.where(on[:, None], x, 0.0)
         want_dW += G.T @ x0
-        bound_dW += eG.T @ np.abs(x0) + e_of(c.n) * (np.abs(G).T @ np.abs(x0))
+        bound_dW += eG.T @ np.abs(x0) + (e_of(c.n) + gr + 3 * U) * (np.abs(G).T @ np.abs(x0))
     within("dW", dW, want_dW, bound_dW + out * np.abs(want_dW))
 
 
