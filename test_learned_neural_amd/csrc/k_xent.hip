@@ -37,7 +37,6 @@ struct GemmArgs {
   int64_t pa, pb;          // elements from plane to plane
   int64_t na, nb;          // rows (or, across the contraction, columns) of a and b
   int64_t K;
-  int products;            // 1 or kProducts
   int ta, tb;              // tiles of a and b
   int splits;              // pieces of the contraction (EPI_ACC)
   // epilogues
@@ -178,7 +177,7 @@ __device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, in
   }
 }
 
-template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI>
+template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI, bool F32>
 __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs g) {
   static_assert(WA * WB == 4, "four waves");
   constexpr int MA = TA / WA / 32, NB = TB / WB / 32;
@@ -207,7 +206,7 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
     k1 = min(k0 + each * kBK, g.K);
   }
   const int steps = (int)((k1 - k0 + kBK - 1) / kBK);
-  const int iters = steps * g.products;
+  const int iters = steps * (F32 ? kProducts : 1);
 
   f32x16 acc[MA][NB];
 #pragma unroll
@@ -219,25 +218,25 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 
   // Step t is computed from one of four LDS buffers while t + 1 .. t + 3 are on their way to the others;
   // operands are read one matrix-instruction depth ahead.  One barrier a step, between its two depths:
-  // behind it step t's buffer takes t + 4's loads, and step t + 1 is there.  Past the end loads are
-  // masked off.  The source order below is the schedule: each matrix instruction with one read or load.
+  // behind it step t's buffer takes t + 4's loads (a's at once, b's in the next step), and step t + 1 is
+  // there.  Past the end loads are masked off.  The source order is the schedule: reads and loads are
+  // spread over the matrix instructions, since a burst of them from all four waves fills the LDS queue
+  // and holds up the matrix instructions behind it.
   A ta;
   B tb;
   ta.init(g.lda, a0, g.na, wave, lane);
   tb.init(g.ldb, b0, g.nb, wave, lane);
   const int64_t step_a = AX ? kBK * g.lda : kBK, step_b = BX ? kBK * g.ldb : kBK;
   const int64_t start_a = AX ? k0 * g.lda + a0 : a0 * g.lda + k0, start_b = BX ? k0 * g.ldb + b0 : b0 * g.ldb + k0;
-  int q = g.products == 1 ? kProducts - 1 : 0;
+  int q = F32 ? 0 : kProducts - 1;
   const uint16_t *pa = g.a + plane_a(q) * g.pa + start_a, *pb = g.b + plane_b(q) * g.pb + start_b;
   int left = (int)(k1 - k0);
-  auto load = [&](int n, uint16_t* d) {
-    if (n < A::kLoads) ta.load(n, d, pa, left, g.lda, g.lda - a0, wave);
-    else tb.load(n - A::kLoads, d + A::kElems, pb, left, g.ldb, g.ldb - b0, wave);
-  };
+  auto load_a = [&](int n, uint16_t* d) { ta.load(n, d, pa, left, g.lda, g.lda - a0, wave); };
+  auto load_b = [&](int n, uint16_t* d) { tb.load(n, d + A::kElems, pb, left, g.ldb, g.ldb - b0, wave); };
   auto next = [&]() {
     left -= kBK;
     pa += step_a, pb += step_b;
-    if (left <= 0 && q + 1 < kProducts) {
+    if (F32 && left <= 0 && q + 1 < kProducts) {
       ++q;
       left = (int)(k1 - k0);
       pa = g.a + plane_a(q) * g.pa + start_a, pb = g.b + plane_b(q) * g.pb + start_b;
@@ -255,28 +254,40 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
     for (int t = 0; t < kStages; ++t) {
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) load(n, sm + t * kStage);
+      for (int n = 0; n < A::kLoads; ++n) load_a(n, sm + t * kStage);
+      if (t + 1 == kStages) break;
+#pragma unroll
+      for (int n = 0; n < B::kLoads; ++n) load_b(n, sm + t * kStage);
       next();
     }
-    wait_all<(kStages - 1) * kLoads>();
+    wait_all<(kStages - 1) * kLoads - B::kLoads>();
 #pragma unroll
     for (int n = 0; n < MA + NB; ++n) read(n, 0, sm, 0);
   }
   for (int it = 0; it < iters; ++it) {
     uint16_t* s = sm + (it & (kStages - 1)) * kStage;
     const uint16_t* d = sm + ((it + 1) & (kStages - 1)) * kStage;
+    uint16_t* e = sm + ((it + kStages - 1) & (kStages - 1)) * kStage;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (ks == 1) wait_all<(kStages - 2) * kLoads>();
+      constexpr int kM = MA * NB, kR = MA + NB;
 #pragma unroll
-      for (int n = 0; n < MA * NB; ++n) {
+      for (int n = 0; n < kM; ++n) {
         acc[n / NB][n % NB] = mfma32(ao[ks][n / NB], bo[ks][n % NB], acc[n / NB][n % NB]);
-        if (n < MA + NB) read(n, ks ^ 1, ks ? d : s, ks ^ 1);
-        if (ks == 1 && n >= MA * NB - kLoads) load(n - (MA * NB - kLoads), s);
+#pragma unroll
+        for (int r = n * kR / kM; r < (n + 1) * kR / kM; ++r) read(r, ks ^ 1, ks ? d : s, ks ^ 1);
+        if (ks == 0) {
+#pragma unroll
+          for (int r = n * B::kLoads / kM; r < (n + 1) * B::kLoads / kM; ++r) load_b(r, e);
+        } else {
+          if (n == 0) next();
+#pragma unroll
+          for (int r = n * A::kLoads / kM; r < (n + 1) * A::kLoads / kM; ++r) load_a(r, s);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    next();
   }
   // loads past the end may still be on their way to LDS
   wait_all<0>();
@@ -285,15 +296,19 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
     float2* red = (float2*)sm;  // [WA][TB]
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
+      if (a0 + TA > g.na) {
+        const int end = (int)(g.na - a0) - wa - 4 * hf;
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (32 * i + 8 * (n >> 2) + (n & 3) >= end) acc[i][j][n] = -INFINITY;
+      }
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const int64_t v = a0 + wa + 32 * i + 8 * (n >> 2) + 4 * hf + (n & 3);
-          if (v >= g.na) acc[i][j][n] = -INFINITY;
-          m = fmaxf(m, acc[i][j][n]);
-        }
+        for (int n = 0; n < 16; ++n) m = fmaxf(m, acc[i][j][n]);
       m = fmaxf(m, __shfl_xor(m, 32));
       float s = 0.0f;
       if (m > -INFINITY) {
@@ -327,15 +342,25 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
       const int64_t y = r < g.nb ? g.labels[r] : -1;
       const bool kept = y >= 0 && y < g.vocab;
       const float l = kept ? g.lse[r] : 0.0f;
-      const int64_t at = kept ? y - g.v0 : -1;
+      // the lane's label and the end of the vocabulary, counted from its first class
+      const int64_t first = a0 + wa + 4 * hf;
+      const int at = kept && y - g.v0 >= first && y - g.v0 < first + TA ? (int)(y - g.v0 - first) : -1;
+      const int end = (int)min(g.na - first, (int64_t)TA);
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const int64_t v = a0 + wa + 32 * i + 8 * (n >> 2) + 4 * hf + (n & 3);
-          const float p = __expf(acc[i][j][n] - l) - (v == at ? 1.0f : 0.0f);
-          acc[i][j][n] = kept && v < g.na ? p : 0.0f;
+          const int v = 32 * i + 8 * (n >> 2) + (n & 3);
+          const float p = __expf(acc[i][j][n] - l);
+          acc[i][j][n] = v == at ? p - 1.0f : p;
         }
+      if (!__all(kept) || a0 + TA > g.na) {
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (!kept || 32 * i + 8 * (n >> 2) + (n & 3) >= end) acc[i][j][n] = 0.0f;
+      }
     }
     for (int n = 0; n < g.planes; ++n)
       put_rows<TA, TB, MA, NB>(sm, acc, wa, wb, tid, n + 1 < g.planes, g.g + n * g.pg, g.ldg, a0, g.ldg, b0, g.nb);
@@ -494,10 +519,10 @@ __global__ void xe_zero(void* out, int64_t count, int bf16) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 int64_t align256(int64_t b) { return up(b, 256); }
 
-template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI>
+template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
   constexpr int lds = std::max(kStages * (TA + TB) * kBK * 2, TA * TB * 2);
-  auto kern = xe_gemm<TA, TB, WA, WB, AX, BX, EPI>;
+  auto kern = xe_gemm<TA, TB, WA, WB, AX, BX, EPI, F32>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return ATLASMEM_E_DEVICE;
@@ -514,9 +539,10 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
 bool wide(int64_t na, int64_t nb) { return ((na + 255) / 256) * ((nb + 255) / 256) >= 256; }
 
 template <bool AX, bool BX, int EPI>
-atlasmem_status gemm(const GemmArgs& g, bool w, hipStream_t st) {
-  if (w) return gemm_launch<256, 256, 2, 2, AX, BX, EPI>(g, st);
-  return gemm_launch<128, 128, 2, 2, AX, BX, EPI>(g, st);
+atlasmem_status gemm(const GemmArgs& g, bool f32, bool w, hipStream_t st) {
+  if (f32)
+    return w ? gemm_launch<256, 256, 2, 2, AX, BX, EPI, true>(g, st) : gemm_launch<128, 128, 2, 2, AX, BX, EPI, true>(g, st);
+  return w ? gemm_launch<256, 256, 2, 2, AX, BX, EPI, false>(g, st) : gemm_launch<128, 128, 2, 2, AX, BX, EPI, false>(g, st);
 }
 
 // The inputs as the engine takes them: bf16 rows of whole, aligned 16-byte pieces.
@@ -587,10 +613,9 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   g.lda = g.ldb = p.dp;
   g.pa = s.vocab * p.dp, g.pb = s.n * p.dp;
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
-  g.products = s.bf16 ? 1 : kProducts;
   const bool w = wide(s.vocab, s.n);
   g.parts = (int)((s.vocab + (w ? 255 : 127)) / (w ? 256 : 128));
-  e = gemm<false, false, EPI_LSE>(g, w, st);
+  e = gemm<false, false, EPI_LSE>(g, !s.bf16, w, st);
   if (e != ATLASMEM_OK) return e;
   xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, X, W, s.bf16, s.n, s.d, s.vocab, labels, loss,
                                                      lse);
@@ -629,11 +654,9 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, wp, st);
   if (e != ATLASMEM_OK) return e;
   const uint16_t* wa = direct(W, s) ? (const uint16_t*)W : wp;
-  const int products = s.bf16 ? 1 : kProducts;
   for (int64_t v0 = 0; v0 < s.vocab; v0 += p.piece) {
     const int64_t nv = std::min(p.piece, s.vocab - v0), ldg = up(nv, 64);
     GemmArgs g = {};
-    g.products = products;
     // G of the piece
     g.a = wa + v0 * p.dp, g.b = direct(X, s) ? (const uint16_t*)X : xp;
     g.lda = g.ldb = p.dp;
@@ -641,27 +664,25 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     g.na = nv, g.nb = s.n, g.K = p.dp;
     g.labels = labels, g.lse = lse, g.v0 = v0, g.vocab = s.vocab;
     g.g = gp, g.ldg = ldg, g.pg = s.n * ldg, g.planes = p.planes;
-    e = gemm<false, false, EPI_GRAD>(g, wide(nv, s.n), st);
+    e = gemm<false, false, EPI_GRAD>(g, !s.bf16, wide(nv, s.n), st);
     if (e != ATLASMEM_OK) return e;
     if (dX) {
       GemmArgs x = {};
-      x.products = products;
       x.a = wa + v0 * p.dp, x.lda = p.dp, x.pa = s.vocab * p.dp, x.na = p.dp;
       x.b = gp, x.ldb = ldg, x.pb = s.n * ldg, x.nb = s.n;
       x.K = nv;
       x.splits = p.splits, x.acc = acc, x.add = v0 > 0;
-      e = gemm<true, false, EPI_ACC>(x, wide(p.dp, s.n), st);
+      e = gemm<true, false, EPI_ACC>(x, !s.bf16, wide(p.dp, s.n), st);
       if (e != ATLASMEM_OK) return e;
     }
     if (dW) {
       GemmArgs x = {};
-      x.products = products;
       x.a = xw, x.lda = p.dp, x.pa = s.n * p.dp, x.na = p.dp;
       x.scale = dloss ? largest : nullptr;
       x.b = gp, x.ldb = ldg, x.pb = s.n * ldg, x.nb = nv;
       x.K = s.n;
       x.out = (char*)dW + v0 * s.d * (s.bf16 ? 2 : 4), x.ldo = s.d, x.out_bf16 = s.bf16;
-      e = gemm<true, true, EPI_OUT>(x, wide(p.dp, nv), st);
+      e = gemm<true, true, EPI_OUT>(x, !s.bf16, wide(p.dp, nv), st);
       if (e != ATLASMEM_OK) return e;
     }
   }
