@@ -19,12 +19,9 @@ SOURCES = ["api.hip", "k_scan.hip", "k_lin.hip", "k_mlp.hip", "k_ns.hip", "k_fus
            "k_decode.hip", "k_calib.hip", "k_hsplit.hip", "k_linattn.hip", "k_groupnorm.hip", "k_xent.hip"]
 ARCH = "gfx950"
 # Packed fp32 instructions are kept out of the device code.
+# Matrix-core results go to ordinary VGPRs (fewer accumulator-register copies).
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",
-         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-# Matrix-core results go to ordinary VGPRs (fewer accumulator-register copies), but where they alone
-# fill 256 registers of a lane: those stay in the accumulator file.
-VGPR_RESULTS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-ACCUMULATOR_FILE = ["k_xent.hip"]
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form"]
 
 
 def hipcc() -> str:
@@ -36,8 +33,7 @@ def hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    results = [] if src in ACCUMULATOR_FILE else VGPR_RESULTS
-    cmd = [hipcc(), *FLAGS, *results, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -22,7 +22,6 @@ namespace am {
 namespace {
 
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
-constexpr int kStages = 4;     // steps in LDS: one in use, three on their way
 constexpr int kProducts = 6;   // of planes, fp32
 // The planes of product p, the small products first: a's 2 0 1 1 0 0, b's 0 2 1 0 1 0 (four bits each).
 __device__ __forceinline__ int plane_a(int p) { return (0x001102 >> (4 * p)) & 3; }
@@ -71,10 +70,10 @@ __device__ __forceinline__ void load_to_lds(rsrc_t rs, uint32_t voff, const uint
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(rs)
                : "memory");
 }
-template <int R, bool ACROSS>
+template <int R, bool ACROSS, int WAVES>
 struct Tile {
   static constexpr int kElems = R * kBK;
-  static constexpr int kLoads = R * kBK / 8 / 256;  // instructions of a wave
+  static constexpr int kLoads = R * kBK / 8 / 64 / WAVES;  // instructions of a wave
   uint32_t off[kLoads];
   int kc;  // along: the lane's first contraction element
 
@@ -135,7 +134,7 @@ __device__ __forceinline__ void wait_all() {
 // A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
 // through LDS, so that a row's columns leave in whole 16-byte pieces side by side.  With `rest` the
 // accumulators keep what the rounding left.
-template <int TA, int TB, int MA, int NB>
+template <int TA, int TB, int MA, int NB, int NT>
 __device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, bool rest, uint16_t* out,
                          int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr) {
   constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
@@ -161,7 +160,7 @@ __device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, in
   __syncthreads();
   const bool vec = ld % 8 == 0 && ((uintptr_t)out & 15) == 0;
 #pragma unroll 4
-  for (int id = tid; id < TB * CH; id += 256) {
+  for (int id = tid; id < TB * CH; id += NT) {
     const int r = id / CH, c = id % CH;
     const int64_t row = r0 + r, at = c0 + 8 * c;
     if (row >= nr || at >= nc) continue;
@@ -177,12 +176,12 @@ __device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, in
   }
 }
 
-template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI, bool F32>
-__global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs g) {
-  static_assert(WA * WB == 4, "four waves");
+template <int TA, int TB, int WA, int WB, int kStages, bool AX, bool BX, int EPI, bool F32>
+__global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
+  constexpr int NT = WA * WB * 64;
   constexpr int MA = TA / WA / 32, NB = TB / WB / 32;
-  using A = Tile<TA, AX>;
-  using B = Tile<TB, BX>;
+  using A = Tile<TA, AX, WA * WB>;
+  using B = Tile<TB, BX, WA * WB>;
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   constexpr int kStage = A::kElems + B::kElems;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hf = lane >> 5,
@@ -216,9 +215,9 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
       for (int n = 0; n < 16; ++n) acc[i][j][n] = 0.0f;
 
-  // Step t is computed from one of four LDS buffers while t + 1 .. t + 3 are on their way to the others;
+  // Step t is computed from one of the LDS buffers while the next steps are on their way to the others;
   // operands are read one matrix-instruction depth ahead.  One barrier a step, between its two depths:
-  // behind it step t's buffer takes t + 4's loads (a's at once, b's in the next step), and step t + 1 is
+  // behind it step t's buffer takes its next step's loads (a's at once, b's in the next step), and step t + 1 is
   // there.  Past the end loads are masked off.  The source order is the schedule: reads and loads are
   // spread over the matrix instructions, since a burst of them from all four waves fills the LDS queue
   // and holds up the matrix instructions behind it.
@@ -264,10 +263,9 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
     for (int n = 0; n < MA + NB; ++n) read(n, 0, sm, 0);
   }
+  uint16_t *s = sm, *e = sm + (kStages - 1) * kStage;
   for (int it = 0; it < iters; ++it) {
-    uint16_t* s = sm + (it & (kStages - 1)) * kStage;
-    const uint16_t* d = sm + ((it + 1) & (kStages - 1)) * kStage;
-    uint16_t* e = sm + ((it + kStages - 1) & (kStages - 1)) * kStage;
+    uint16_t* d = s == sm + (kStages - 1) * kStage ? sm : s + kStage;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (ks == 1) wait_all<(kStages - 2) * kLoads>();
@@ -288,6 +286,7 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    e = s, s = d;
   }
   // loads past the end may still be on their way to LDS
   wait_all<0>();
@@ -321,7 +320,7 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
       if (hf == 0) red[(wave % WA) * TB + wb + 32 * j + col] = float2{m, s};
     }
     __syncthreads();
-    for (int r = tid; r < TB; r += 256) {
+    for (int r = tid; r < TB; r += NT) {
       if (b0 + r >= g.nb) break;
       float m = -INFINITY, s = 0.0f;
 #pragma unroll
@@ -349,11 +348,14 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const int v = 32 * i + 8 * (n >> 2) + (n & 3);
-          const float p = __expf(acc[i][j][n] - l);
-          acc[i][j][n] = v == at ? p - 1.0f : p;
-        }
+        for (int n = 0; n < 16; ++n) acc[i][j][n] = __expf(acc[i][j][n] - l);
+      if (__any(at >= 0)) {
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (32 * i + 8 * (n >> 2) + (n & 3) == at) acc[i][j][n] -= 1.0f;
+      }
       if (!__all(kept) || a0 + TA > g.na) {
 #pragma unroll
         for (int i = 0; i < MA; ++i)
@@ -363,7 +365,7 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
       }
     }
     for (int n = 0; n < g.planes; ++n)
-      put_rows<TA, TB, MA, NB>(sm, acc, wa, wb, tid, n + 1 < g.planes, g.g + n * g.pg, g.ldg, a0, g.ldg, b0, g.nb);
+      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, n + 1 < g.planes, g.g + n * g.pg, g.ldg, a0, g.ldg, b0, g.nb);
   }
 
   if constexpr (EPI == EPI_OUT) {
@@ -375,7 +377,7 @@ __global__ __launch_bounds__(256, TA* TB >= 65536 ? 1 : 2) void xe_gemm(GemmArgs
 #pragma unroll
         for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
     if (g.out_bf16) {
-      put_rows<TA, TB, MA, NB>(sm, acc, wa, wb, tid, false, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
+      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, false, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
       return;
     }
   }
@@ -519,10 +521,10 @@ __global__ void xe_zero(void* out, int64_t count, int bf16) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 int64_t align256(int64_t b) { return up(b, 256); }
 
-template <int TA, int TB, int WA, int WB, bool AX, bool BX, int EPI, bool F32>
+template <int TA, int TB, int WA, int WB, int ST, bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
-  constexpr int lds = std::max(kStages * (TA + TB) * kBK * 2, TA * TB * 2);
-  auto kern = xe_gemm<TA, TB, WA, WB, AX, BX, EPI, F32>;
+  constexpr int lds = std::max(ST * (TA + TB) * kBK * 2, TA * TB * 2);
+  auto kern = xe_gemm<TA, TB, WA, WB, ST, AX, BX, EPI, F32>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return ATLASMEM_E_DEVICE;
@@ -530,7 +532,7 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
   g.tb = (int)((g.nb + TB - 1) / TB);
   const int64_t blocks = up((int64_t)g.ta * g.tb, 8);
   if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
-  kern<<<dim3((unsigned)blocks, EPI == EPI_ACC ? g.splits : 1), 256, lds, st>>>(g);
+  kern<<<dim3((unsigned)blocks, EPI == EPI_ACC ? g.splits : 1), WA * WB * 64, lds, st>>>(g);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -538,11 +540,13 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
 // Tiles of 256 x 256 where they fill the chip, of 128 x 128 otherwise.
 bool wide(int64_t na, int64_t nb) { return ((na + 255) / 256) * ((nb + 255) / 256) >= 256; }
 
+template <bool AX, bool BX, int EPI, bool F32>
+atlasmem_status gemm_of(const GemmArgs& g, bool w, hipStream_t st) {
+  return w ? gemm_launch<256, 256, 2, 4, 4, AX, BX, EPI, F32>(g, st) : gemm_launch<128, 128, 2, 2, 4, AX, BX, EPI, F32>(g, st);
+}
 template <bool AX, bool BX, int EPI>
 atlasmem_status gemm(const GemmArgs& g, bool f32, bool w, hipStream_t st) {
-  if (f32)
-    return w ? gemm_launch<256, 256, 2, 2, AX, BX, EPI, true>(g, st) : gemm_launch<128, 128, 2, 2, AX, BX, EPI, true>(g, st);
-  return w ? gemm_launch<256, 256, 2, 2, AX, BX, EPI, false>(g, st) : gemm_launch<128, 128, 2, 2, AX, BX, EPI, false>(g, st);
+  return f32 ? gemm_of<AX, BX, EPI, true>(g, w, st) : gemm_of<AX, BX, EPI, false>(g, w, st);
 }
 
 // The inputs as the engine takes them: bf16 rows of whole, aligned 16-byte pieces.
