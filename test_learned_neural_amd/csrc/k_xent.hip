@@ -37,7 +37,7 @@ struct GemmArgs {
   int64_t na, nb;          // rows (or, across the contraction, columns) of a and b
   int64_t K;
   int ta, tb;              // tiles of a and b
-  int splits;              // pieces of the contraction (EPI_ACC)
+  int splits;              // pieces of the contraction (ACC; else 1)
   // epilogues
   float2* part;            // LSE: [nb][parts]: (maximum, sum of exponentials)
   int parts;
@@ -188,20 +188,21 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
             col = lane & 31;
   const int wa = (wave % WA) * (TA / WA), wb = (wave / WA) * (TB / WB);
 
-  // tiles of one XCD are neighbours: eight tiles of b beside four of a at a time share its L2
-  const int total = g.ta * g.tb;
-  const int bid = blockIdx.x;
+  // The workgroups of one XCD are neighbours, and share its L2: the tiles of one piece of the contraction
+  // before the next piece's, eight tiles of b beside four of a at a time.
+  const int tiles = g.ta * g.tb, total = tiles * g.splits;
   const int per = (total + 7) / 8;
-  const int t = (bid & 7) * per + (bid >> 3);
-  if ((bid >> 3) >= per || t >= total) return;
+  const int work = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || work >= total) return;
+  const int split = work / tiles, t = work % tiles;
   const int group = t / (8 * g.ta), in = t % (8 * g.ta);
   const int width = min(8, g.tb - group * 8);
   const int64_t a0 = (int64_t)(in / width) * TA, b0 = (int64_t)(group * 8 + in % width) * TB;
 
   int64_t k0 = 0, k1 = g.K;
   if constexpr (EPI == EPI_ACC) {
-    const int64_t steps = (g.K + kBK - 1) / kBK, each = (steps + g.splits - 1) / g.splits;
-    k0 = min((int64_t)blockIdx.y * each * kBK, g.K);
+    const int64_t each = ((g.K + kBK - 1) / kBK + g.splits - 1) / g.splits;
+    k0 = min(split * each * kBK, g.K);
     k1 = min(k0 + each * kBK, g.K);
   }
   const int steps = (int)((k1 - k0 + kBK - 1) / kBK);
@@ -394,7 +395,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
           if (c >= g.na) continue;
           float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           if constexpr (EPI == EPI_ACC) {
-            float4* p = (float4*)(g.acc + ((int64_t)blockIdx.y * g.nb + r) * g.lda + c);
+            float4* p = (float4*)(g.acc + ((int64_t)split * g.nb + r) * g.lda + c);
             if (g.add) {
               const float4 o = *p;
               x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
@@ -458,8 +459,8 @@ __global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int d
 // loss, lse of a row: a wave joins the tiles' maxima and sums, and takes the row's product with its
 // label's class.
 __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, const void* X, const void* W, int in_bf16,
-                                               int64_t n, int d, int64_t vocab, const int64_t* labels, float* loss,
-                                               float* lse) {
+                                               int vec, int64_t n, int d, int64_t vocab, const int64_t* labels,
+                                               float* loss, float* lse) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (r >= n) return;
@@ -485,7 +486,19 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
     m = t;
   }
   float z = 0.0f;
-  for (int c = lane; c < d; c += 64) z += load_in(X, r * d + c, in_bf16) * load_in(W, y * d + c, in_bf16);
+  for (int c = lane * 8; c < d; c += 512) {  // one order of the sum, whatever the alignment
+    if (vec) {
+      const u32x4 a = *(const u32x4*)((const uint16_t*)X + r * d + c), b = *(const u32x4*)((const uint16_t*)W + y * d + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        z = fmaf(__uint_as_float(k & 1 ? a[k >> 1] & 0xFFFF0000u : a[k >> 1] << 16),
+                 __uint_as_float(k & 1 ? b[k >> 1] & 0xFFFF0000u : b[k >> 1] << 16), z);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < d) z = fmaf(load_in(X, r * d + c + k, in_bf16), load_in(W, y * d + c + k, in_bf16), z);
+    }
+  }
   for (int k = 32; k; k >>= 1) z += __shfl_xor(z, k);
   if (lane == 0) {
     const float l = m + logf(s), q = l - z;
@@ -494,19 +507,29 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
   }
 }
 
-// dX from the partial sums of the contraction's pieces, times the rows' weights.
+// dX from the partial sums of the contraction's pieces, times the rows' weights: four columns a thread.
 __global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int64_t* labels, int64_t vocab,
-                       const float* dloss, void* out, int out_bf16) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n * d) return;
-  const int64_t at = i / d * dp + i % d;
-  float v = 0.0f;
-  for (int s = 0; s < splits; ++s) v += acc[s * n * dp + at];
-  const int64_t y = labels[i / d];
-  if (y < 0 || y >= vocab) v = 0.0f;
-  else if (dloss) v *= dloss[i / d];
-  if (out_bf16) ((uint16_t*)out)[i] = (uint16_t)bf16_bits(v);
-  else ((float*)out)[i] = v;
+                       const float* dloss, void* out, int out_bf16, int vec) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / (dp / 4);
+  const int c = (int)(i % (dp / 4)) * 4;
+  if (r >= n || c >= d) return;
+  float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < splits; ++s) {
+    const float4 a = *(const float4*)(acc + (s * n + r) * dp + c);
+    v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+  }
+  const int64_t y = labels[r];
+  const bool kept = y >= 0 && y < vocab;
+  const float w = kept && dloss ? dloss[r] : 1.0f;
+  const float x[4] = {kept ? v.x * w : 0.0f, kept ? v.y * w : 0.0f, kept ? v.z * w : 0.0f, kept ? v.w * w : 0.0f};
+  const int64_t at = r * d + c;
+  if (vec && out_bf16) *(uint2*)((uint16_t*)out + at) = uint2{cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])};
+  else if (vec) *(float4*)((float*)out + at) = float4{x[0], x[1], x[2], x[3]};
+  else
+    for (int k = 0; k < 4 && c + k < d; ++k) {
+      if (out_bf16) ((uint16_t*)out)[at + k] = (uint16_t)bf16_bits(x[k]);
+      else ((float*)out)[at + k] = x[k];
+    }
 }
 
 __global__ void xe_zero(void* out, int64_t count, int bf16) {
@@ -530,15 +553,22 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
     return ATLASMEM_E_DEVICE;
   g.ta = (int)((g.na + TA - 1) / TA);
   g.tb = (int)((g.nb + TB - 1) / TB);
-  const int64_t blocks = up((int64_t)g.ta * g.tb, 8);
+  if (EPI != EPI_ACC) g.splits = 1;
+  const int64_t blocks = up((int64_t)g.ta * g.tb * g.splits, 8);
   if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
-  kern<<<dim3((unsigned)blocks, EPI == EPI_ACC ? g.splits : 1), WA * WB * 64, lds, st>>>(g);
+  kern<<<(unsigned)blocks, WA * WB * 64, lds, st>>>(g);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
 
-// Tiles of 256 x 256 where they fill the chip, of 128 x 128 otherwise.
-bool wide(int64_t na, int64_t nb) { return ((na + 255) / 256) * ((nb + 255) / 256) >= 256; }
+// Tiles of 256 x 256 (a workgroup a CU) or of 128 x 128 (two).  The large ones take 0.7 of the time for
+// an area (8192 x 16384 x 2048: 554 us against 790), the small ones fill the chip with less: rounds of
+// workgroups decide, or where the contraction is split to fill it (dX), the areas.
+int64_t tiles_of(int64_t na, int64_t nb, int side) { return (na + side - 1) / side * ((nb + side - 1) / side); }
+bool wide(int64_t na, int64_t nb) {
+  return (tiles_of(na, nb, 256) + 255) / 256 * 28 <= (tiles_of(na, nb, 128) + 511) / 512 * 20;
+}
+bool wide_split(int64_t na, int64_t nb) { return tiles_of(na, nb, 256) * 28 <= tiles_of(na, nb, 128) * 10; }
 
 template <bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_of(const GemmArgs& g, bool w, hipStream_t st) {
@@ -554,7 +584,7 @@ struct Plan {
   int planes, dp;
   int64_t n, vocab, piece;      // classes of a piece
   int parts, splits;
-  bool copy_w;
+  bool wide_x;                  // large tiles for dX
   int64_t x_bytes, w_bytes, part_bytes, g_bytes, acc_bytes;
 };
 
@@ -570,8 +600,9 @@ Plan plan_of(const CrossEntropy& s) {
   const int64_t pieces = (s.vocab + piece - 1) / piece;
   p.piece = up((s.vocab + pieces - 1) / pieces, 256);
   p.parts = (int)((s.vocab + 127) / 128);
-  const int64_t tiles = std::max<int64_t>((s.n + 127) / 128, 1) * ((p.dp + 127) / 128);
-  p.splits = wide(p.dp, s.n) ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(512 / tiles, p.piece / 512));
+  p.wide_x = wide_split(p.dp, s.n);
+  const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.wide_x ? 256 : 128), 1);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.wide_x ? 256 : 512) / tiles, p.piece / 512));
   p.x_bytes = align256(2 * p.planes * s.n * (int64_t)p.dp);
   p.w_bytes = align256(2 * p.planes * s.vocab * (int64_t)p.dp);
   p.part_bytes = align256(8 * s.n * (int64_t)p.parts);
@@ -621,7 +652,7 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   g.parts = (int)((s.vocab + (w ? 255 : 127)) / (w ? 256 : 128));
   e = gemm<false, false, EPI_LSE>(g, !s.bf16, w, st);
   if (e != ATLASMEM_OK) return e;
-  xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, X, W, s.bf16, s.n, s.d, s.vocab, labels, loss,
+  xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, X, W, s.bf16, direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss,
                                                      lse);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
@@ -676,7 +707,7 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
       x.b = gp, x.ldb = ldg, x.pb = s.n * ldg, x.nb = s.n;
       x.K = nv;
       x.splits = p.splits, x.acc = acc, x.add = v0 > 0;
-      e = gemm<true, false, EPI_ACC>(x, !s.bf16, wide(p.dp, s.n), st);
+      e = gemm<true, false, EPI_ACC>(x, !s.bf16, p.wide_x, st);
       if (e != ATLASMEM_OK) return e;
     }
     if (dW) {
@@ -691,8 +722,9 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     }
   }
   if (dX) {
-    xe_sum<<<(unsigned)((s.n * s.d + 255) / 256), 256, 0, st>>>(acc, p.splits, s.n, s.d, p.dp, labels, s.vocab, dloss,
-                                                              dX, s.bf16);
+    const int vec = s.d % 4 == 0 && ((uintptr_t)dX & 15) == 0;
+    xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(acc, p.splits, s.n, s.d, p.dp, labels, s.vocab,
+                                                                       dloss, dX, s.bf16, vec);
     AM_LAUNCH_CHECK();
   }
   return ATLASMEM_OK;
