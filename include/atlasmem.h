@@ -424,7 +424,7 @@ atlasmem_status atlasmem_gates(const void* U, int64_t B, int64_t T, int32_t d_mo
  * S_t = v_t k_t^T), per (b, h) and with lambda = exp(log_decay[h]):
  *   W_t = lambda W_{t-1} + v_t k_t^T,   Y[t] = scale W_t q_t
  * Calls of at most 16 tokens run the recurrence (each state read and written once); longer ones run
- * in chunks of 64 tokens on the matrix cores.
+ * in chunks of 32 tokens on the matrix cores.
  *   Q, K: [batch, heads, T, d_key], V, Y: [batch, heads, T, d_value] of `dtype`, in `layout`;
  *         d_key, d_value 1..128
  *   log_decay: fp32 [heads], <= 0 (0: nothing is forgotten; -INFINITY: only the own token is read)

@@ -6,7 +6,7 @@
 // outer loss with respect to q, k, v, W_0 and log_decay.
 //
 // One chunk kernel serves the forward and the three backward products.  With "queries" x, "keys" y,
-// "values" z and a state S [x, z] (chunks of 64 positions i, j; S_0 the state before the chunk):
+// "values" z and a state S [x, z] (chunks of 32 positions i, j; S_0 the state before the chunk):
 //   out_i = c_out (lambda^(i+1-e) S_0^T x_i + c_upd sum_{j<=i} lambda^(i-j) (x_i . y_j) z_j)
 //   S'    = lambda^r S_0 + c_upd sum_j lambda^(r-1-j+e) y_j z_j^T            (r rows in the chunk)
 //   forward   x = q,  y = k,  z = v,  e = 0: y_t, state W^T
@@ -26,8 +26,7 @@ namespace am {
 
 namespace {
 
-constexpr int kC = 64;          // tokens per chunk: two 32-row matrix-core tiles
-constexpr int kPad = 8;         // LDS row padding (elements): consecutive rows 16 bytes apart in bank order
+constexpr int kC = 32;          // tokens per chunk: one 32-row matrix-core tile
 
 struct LaRows {                 // a [B, H, T, w] tensor of either layout
   const void* p;
@@ -132,9 +131,19 @@ __device__ __forceinline__ Raw<F32> load_group(const LaRows& r, int64_t base, in
   return g;
 }
 
-// ... into an LDS tile of planes (plane stride ps elements).
-template <bool F32>
-__device__ __forceinline__ void store_group(uint16_t* s, int ps, const Raw<F32>& g) {
+// LDS tile of a chunk: 32 rows of W (64 or 128) elements, the 8-byte pieces of a row exchanged by bits of
+// its index so that both reads below touch every bank once: 32 rows at one column piece, and 4 rows at
+// 8 neighbouring pieces.
+template <int W>
+__device__ __forceinline__ constexpr int exchange(int row) {
+  return W == 128 ? ((row & 3) << 3) | ((row >> 2) & 7) : (((row >> 1) & 1) << 3) | ((row >> 2) & 7);
+}
+// Eight elements (column c, a multiple of 8) of a row into a tile of planes.
+template <int W, bool F32>
+__device__ __forceinline__ void store_group(uint16_t* s, int row, int c, const Raw<F32>& g) {
+  const int f = exchange<W>(row);
+  uint16_t* d = s + row * W + (((c >> 2) ^ (f & ~1)) << 2);
+  auto put = [&](uint16_t* p, u32x4 v) { *(u32x4*)p = f & 1 ? u32x4{v[2], v[3], v[0], v[1]} : v; };
   if constexpr (F32) {
     float v[8];
 #pragma unroll
@@ -142,32 +151,42 @@ __device__ __forceinline__ void store_group(uint16_t* s, int ps, const Raw<F32>&
     Op<3> o;
     split8(v, o);
 #pragma unroll
-    for (int n = 0; n < 3; ++n) *(u32x4*)(s + n * ps) = o.p[n];
+    for (int n = 0; n < 3; ++n) put(d + n * kC * W, o.p[n]);
   } else {
-    *(u32x4*)s = g.a[0];
+    put(d, g.a[0]);
   }
 }
 
 // A row operand: lane l takes row l % 32 and, of every 16 columns, those that an accumulator tile
-// has in its registers (4 (l / 32) + {0..3, 8..11}).
-template <int NP>
-__device__ __forceinline__ Op<NP> row_op(const uint16_t* s, int ps, int ld, int row, int k, int hf) {
+// has in its registers (4 (l / 32) + {0..3, 8..11}).  at: row_at of the lane.
+template <int W>
+__device__ __forceinline__ int row_at(int lane) {
+  return (lane & 31) * W + (((lane >> 5) ^ exchange<W>(lane & 31)) << 2);
+}
+template <int W, int NP>
+__device__ __forceinline__ Op<NP> row_op(const uint16_t* s, int at, int k) {
+  Op<NP> o;
+#pragma unroll
+  for (int n = 0; n < NP; ++n)
+    o.p[n] = cat2(*(const uint2*)(s + n * kC * W + (at ^ (16 * k))), *(const uint2*)(s + n * kC * W + (at ^ (16 * k + 8))));
+  return o;
+}
+// A column operand: lane l takes column c0 + l % 32 and the rows 16 k + .. in the same order.  at: col_at.
+template <int W>
+__device__ __forceinline__ int col_at(int lane) {
+  const int row = 4 * (lane >> 5) + ((lane & 15) >> 2);
+  return row * W + ((((lane & 16) >> 2) + (lane & 3)) ^ exchange<W>(row)) * 4;
+}
+template <int W, int NP>
+__device__ __forceinline__ Op<NP> col_op(const uint16_t* s, int at, int c0, int k) {
+  constexpr int kRow8 = exchange<W>(8), kRow16 = exchange<W>(16);
+  const int x = ((c0 >> 2) ^ (k ? kRow16 : 0)) * 4;
   Op<NP> o;
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
-    const uint16_t* q = s + n * ps + row * ld + 16 * k + 4 * hf;
-    o.p[n] = cat2(*(const uint2*)q, *(const uint2*)(q + 8));
+    const uint16_t* p = s + n * kC * W + 16 * k * W;
+    o.p[n] = cat2(lds_tr16(p + (at ^ x)), lds_tr16(p + 8 * W + (at ^ (x ^ (kRow8 * 4)))));
   }
-  return o;
-}
-// A column operand: lane l takes column c0 + l % 32 and the rows in the same order.
-template <int NP>
-__device__ __forceinline__ Op<NP> col_op(const uint16_t* s, int ps, int ld, int c0, int k, int lane) {
-  const int hf = lane >> 5;
-  const int off = (16 * k + 4 * hf + ((lane & 15) >> 2)) * ld + c0 + (lane & 16) + 4 * (lane & 3);
-  Op<NP> o;
-#pragma unroll
-  for (int n = 0; n < NP; ++n) o.p[n] = cat2(lds_tr16(s + n * ps + off), lds_tr16(s + n * ps + off + 8 * ld));
   return o;
 }
 
@@ -177,22 +196,20 @@ template <int DX, int NW, bool F32, bool OUT, bool DEC>
 __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   constexpr int NP = F32 ? 3 : 1;                    // planes of an input
   constexpr int NC = F32 || DEC ? 3 : 2;             // planes of a computed operand of the outputs
-  constexpr int LX = DX * 32 + kPad, LZ = NW * 32 + kPad;
+  constexpr int WX = DX * 32, WZ = NW * 32;
   constexpr int NT = NW * 64;
   constexpr int GX = kC * DX * 4 / NT, GZ = kC * NW * 4 / NT;  // 8-element groups per thread
-  constexpr int PSX = kC * LX, PSZ = kC * LZ;
+  constexpr int TX = NP * kC * WX, TZ = NP * kC * WZ, kBuf = (OUT ? 2 : 1) * TX + TZ;
+  constexpr int kBufs = F32 ? 1 : 2;
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
-  uint16_t* sx = sm;
-  uint16_t* sy = sx + (OUT ? NP * PSX : 0);
-  uint16_t* sz = sy + NP * PSX;
-  float* pw = (float*)(sz + NP * PSZ);               // lambda^0 .. lambda^64
+  float* pw = (float*)(sm + kBufs * kBuf);           // lambda^0 .. lambda^32
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hf = lane >> 5, col = lane & 31;
   const int nrun = OUT ? a.nseg : a.nseg - 1;        // the last segment's own sum starts nothing
   const int seg = blockIdx.x % nrun;
   const int m = blockIdx.x / nrun;
   const int b = m / a.H, h = m % a.H;
-  const int z0 = blockIdx.y * NW * 32;
+  const int z0 = blockIdx.y * WZ;
   const int zc = z0 + wave * 32;
   const int64_t len = a.len ? min((int64_t)max(a.len[b], 0), a.T) : a.T;
   const int64_t p0 = (int64_t)seg * a.lseg, p1 = min(p0 + a.lseg, a.T);
@@ -242,187 +259,182 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
       rz[i] = load_group<F32>(a.z, bz, token(p + row), z0 + c);
     }
   };
-  double dec = 0.0;
-
-  if (p0 < p1) fetch(p0);
-  for (int64_t p = p0; p < p1; p += kC) {
-    __syncthreads();
+  auto stage = [&](uint16_t* s) {
 #pragma unroll
     for (int i = 0; i < GX; ++i) {
       const int id = tid + i * NT, row = id / (DX * 4), c = (id % (DX * 4)) * 8;
-      if constexpr (OUT) store_group<F32>(sx + row * LX + c, PSX, rx[i]);
-      store_group<F32>(sy + row * LX + c, PSX, ry[i]);
+      store_group<WX, F32>(s, row, c, ry[i]);
+      if constexpr (OUT) store_group<WX, F32>(s + TX + TZ, row, c, rx[i]);
     }
 #pragma unroll
     for (int i = 0; i < GZ; ++i) {
       const int id = tid + i * NT, row = id / (NW * 4), c = (id % (NW * 4)) * 8;
-      store_group<F32>(sz + row * LZ + c, PSZ, rz[i]);
+      store_group<WZ, F32>(s + TX, row, c, rz[i]);
     }
+  };
+  double dec = 0.0;
+
+  fetch(p0);
+  __syncthreads();
+  // decay from position j (the register's) to i (the lane's), of the carried state, and to the chunk's end
+  float D[OUT ? 16 : 1], wz[16];
+  const float wi = pw[col + 1 - a.e];
+  if constexpr (OUT) {
+#pragma unroll
+    for (int n = 0; n < 16; ++n) D[n] = pw[max(col - (8 * (n >> 2) + 4 * hf + (n & 3)), 0)] * a.c_upd;
+  }
+  auto weights = [&](int r) {
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      const int j = 8 * (n >> 2) + 4 * hf + (n & 3);
+      wz[n] = j < r ? pw[r - 1 - j + a.e] * a.c_upd : 0.0f;
+    }
+  };
+  weights(kC);
+  const int rat = row_at<WX>(lane), cat = col_at<WX>(lane), zat = col_at<WZ>(lane);
+
+  int buf = 0;
+  for (int64_t p = p0; p < p1; p += kC) {
+    uint16_t* sy = sm + buf * kBuf;
+    const uint16_t *sz = sy + TX, *sx = sz + TZ;
+    if constexpr (kBufs == 1) __syncthreads();
+    stage(sy);
     __syncthreads();
     if (p + kC < p1) fetch(p + kC);
+    if constexpr (kBufs == 2) buf ^= 1;
     const int r = (int)max((int64_t)0, min((int64_t)kC, min(len, p1) - p));
 
-    Op<NP> zo[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) zo[k] = col_op<NP>(sz, PSZ, LZ, wave * 32, k, lane);
-
+    Op<NP> zo[2];
     if constexpr (OUT) {
-      f32x16 O[2], Ot[DEC ? 2 : 1], P[3];  // P: (j-tile, i-tile) = (0,0), (0,1), (1,1)
-      O[0] = O[1] = zero16();
-      if constexpr (DEC) Ot[0] = Ot[1] = zero16();
-      P[0] = P[1] = P[2] = zero16();
+      f32x16 O = zero16(), Ot = zero16(), P = zero16();
 #pragma unroll
       for (int k = 0; k < 2 * DX; ++k) {
-        const Op<NP> x0 = row_op<NP>(sx, PSX, LX, col, k, hf), x1 = row_op<NP>(sx, PSX, LX, 32 + col, k, hf);
-        const Op<NP> y0 = row_op<NP>(sy, PSX, LX, col, k, hf), y1 = row_op<NP>(sy, PSX, LX, 32 + col, k, hf);
-        P[0] = mm(y0, x0, P[0]);
-        P[1] = mm(y0, x1, P[1]);
-        P[2] = mm(y1, x1, P[2]);
+        const Op<NP> x = row_op<WX, NP>(sx, rat, k), y = row_op<WX, NP>(sy, rat, k);
+        P = mm(y, x, P);
         Op<NC> s;
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = S[k >> 1][8 * (k & 1) + i];
         split8(v, s);
-        O[0] = mm(s, x0, O[0]);
-        O[1] = mm(s, x1, O[1]);
+        O = mm(s, x, O);
         if constexpr (DEC) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = St[k >> 1][8 * (k & 1) + i];
           split8(v, s);
-          Ot[0] = mm(s, x0, Ot[0]);
-          Ot[1] = mm(s, x1, Ot[1]);
+          Ot = mm(s, x, Ot);
         }
       }
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        const int i = 32 * it + col;
-        const float w = pw[i + 1 - a.e];
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          O[it][n] *= w;
-          if constexpr (DEC) Ot[it][n] = Ot[it][n] * w + (float)(i + 1) * O[it][n];
-        }
-      }
-      // decay between rows: position i of the lane's column, j of the register
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const int i = (q ? 32 : 0) + col;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const int j = (q == 2 ? 32 : 0) + 8 * (n >> 2) + 4 * hf + (n & 3);
-          P[q][n] = i >= j ? P[q][n] * (pw[max(i - j, 0)] * a.c_upd) : 0.0f;
-        }
+      for (int n = 0; n < 16; ++n) {
+        O[n] *= wi;
+        if constexpr (DEC) Ot[n] = Ot[n] * wi + (float)(col + 1) * O[n];
+        P[n] = col >= 8 * (n >> 2) + 4 * hf + (n & 3) ? P[n] * D[n] : 0.0f;
       }
 #pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const int it = q ? 1 : 0, jt = q == 2 ? 1 : 0;
+      for (int k = 0; k < 2; ++k) {
+        zo[k] = col_op<WZ, NP>(sz, zat, wave * 32, k);
+        float v[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float v[8];
+        for (int n = 0; n < 8; ++n) v[n] = P[8 * k + n];
+        Op<NC> s;
+        split8(v, s);
+        O = mm(zo[k], s, O);
+        if constexpr (DEC) {
 #pragma unroll
-          for (int n = 0; n < 8; ++n) v[n] = P[q][8 * k + n];
-          Op<NC> s;
+          for (int n = 0; n < 8; ++n) v[n] *= (float)(col - (16 * k + 8 * (n >> 2) + 4 * hf + (n & 3)));
           split8(v, s);
-          O[it] = mm(zo[2 * jt + k], s, O[it]);
+          Ot = mm(zo[k], s, Ot);
+        }
+      }
+      // rows: the lane's position, four consecutive columns a register group
+      const int64_t pos = p + col;
+      if (pos < p1) {
+        const bool live = col < r;
+        const int64_t t = live && a.rev ? len - 1 - pos : pos;
+        const int64_t at = b * a.o.sb + h * a.o.sh + t * a.o.st;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = zc + 8 * q + 4 * hf;
+          float v[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) v[n] = live ? O[4 * q + n] * a.c_out : 0.0f;
           if constexpr (DEC) {
+            if (live) {
+              const int64_t ta = b * a.t.sb + h * a.t.sh + t * a.t.st;
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-              v[n] *= (float)(32 * it + col - (32 * jt + 16 * k + 8 * (n >> 2) + 4 * hf + (n & 3)));
-            split8(v, s);
-            Ot[it] = mm(zo[2 * jt + k], s, Ot[it]);
-          }
-        }
-      }
-      // rows: lane's position, four consecutive columns a register group
-#pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        const int64_t pos = p + 32 * it + col;
-        if (pos < p1) {
-          const bool live = pos < len;
-          const int64_t t = live ? token(pos) : pos;
-          const int64_t at = b * a.o.sb + h * a.o.sh + t * a.o.st;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = zc + 8 * q + 4 * hf;
-            float v[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) v[n] = live ? O[it][4 * q + n] * a.c_out : 0.0f;
-            if constexpr (DEC) {
-              if (live) {
-                const int64_t ta = b * a.t.sb + h * a.t.sh + t * a.t.st;
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                  if (c + n < a.z.w)
-                    dec += (double)(Ot[it][4 * q + n] * a.c_out) * load_in(a.t.p, ta + c + n, !F32);
-              }
+              for (int n = 0; n < 4; ++n)
+                if (c + n < a.z.w) dec += (double)(Ot[4 * q + n] * a.c_out) * load_in(a.t.p, ta + c + n, !F32);
             }
-            if (c >= a.z.w) continue;
-            if constexpr (F32) {
-              float* o = (float*)a.o.p + at + c;
-              if (a.o.vec) {
-                *(float4*)o = float4{v[0], v[1], v[2], v[3]};
-              } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                  if (c + n < a.z.w) o[n] = v[n];
-              }
+          }
+          if (c >= a.z.w) continue;
+          if constexpr (F32) {
+            float* o = (float*)a.o.p + at + c;
+            if (a.o.vec) {
+              *(float4*)o = float4{v[0], v[1], v[2], v[3]};
             } else {
-              uint16_t* o = (uint16_t*)a.o.p + at + c;
-              const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
-              if (a.o.vec) {
-                *(uint2*)o = w;
-              } else {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                  if (c + n < a.z.w) o[n] = (uint16_t)((n & 2 ? w.y : w.x) >> (16 * (n & 1)));
-              }
+              for (int n = 0; n < 4; ++n)
+                if (c + n < a.z.w) o[n] = v[n];
+            }
+          } else {
+            uint16_t* o = (uint16_t*)a.o.p + at + c;
+            const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+            if (a.o.vec) {
+              *(uint2*)o = w;
+            } else {
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                if (c + n < a.z.w) o[n] = (uint16_t)((n & 2 ? w.y : w.x) >> (16 * (n & 1)));
             }
           }
         }
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) zo[k] = col_op<WZ, NP>(sz, zat, wave * 32, k);
     }
 
     // state: column operands of y times the weighted z (three planes: the state is an fp32 result)
-    {
-      const float keep = pw[r];
+    if (r < kC) weights(r);
+    const float keep = pw[r];
 #pragma unroll
-      for (int xt = 0; xt < DX; ++xt)
+    for (int xt = 0; xt < DX; ++xt)
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          if constexpr (DEC) St[xt][n] = keep * (St[xt][n] + (float)r * S[xt][n]);
-          S[xt][n] *= keep;
+      for (int n = 0; n < 16; ++n) {
+        if constexpr (DEC) St[xt][n] = keep * (St[xt][n] + (float)r * S[xt][n]);
+        S[xt][n] *= keep;
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float v[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        float zv = 0.0f;
+#pragma unroll
+        for (int s = NP - 1; s >= 0; --s) {
+          const uint32_t w = zo[k].p[s][n >> 1];
+          zv += __uint_as_float(n & 1 ? w & 0xFFFF0000u : w << 16);
         }
+        v[n] = zv * wz[8 * k + n];
+      }
+      Op<3> s, st;
+      split8(v, s);
+      if constexpr (DEC) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v[8], vt[8];
+        for (int n = 0; n < 8; ++n) v[n] *= (float)max(r - 1 - (16 * k + 8 * (n >> 2) + 4 * hf + (n & 3)), 0);
+        split8(v, st);
+      }
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int j = 16 * k + 8 * (n >> 2) + 4 * hf + (n & 3);
-          float zv = 0.0f;
-#pragma unroll
-          for (int s = NP - 1; s >= 0; --s) {
-            const uint32_t w = zo[k].p[s][n >> 1];
-            zv += __uint_as_float(n & 1 ? w & 0xFFFF0000u : w << 16);
-          }
-          const int left = max(r - 1 - j, 0);
-          v[n] = j < r ? zv * (pw[left + (j < r ? a.e : 0)] * a.c_upd) : 0.0f;
-          vt[n] = v[n] * (float)left;
-        }
-        Op<3> s, st;
-        split8(v, s);
-        if constexpr (DEC) split8(vt, st);
-#pragma unroll
-        for (int xt = 0; xt < DX; ++xt) {
-          const Op<NP> yo = col_op<NP>(sy, PSX, LX, 32 * xt, k, lane);
-          S[xt] = mm(yo, s, S[xt]);
-          if constexpr (DEC) St[xt] = mm(yo, st, St[xt]);
-        }
+      for (int xt = 0; xt < DX; ++xt) {
+        const Op<NP> yo = col_op<WX, NP>(sy, cat, 32 * xt, k);
+        S[xt] = mm(yo, s, S[xt]);
+        if constexpr (DEC) St[xt] = mm(yo, st, St[xt]);
       }
     }
   }
 
   // the state out: C-layout tiles to the caller's order
-  auto put = [&](const f32x16* D, float* dst) {
+  auto put = [&](const f32x16* V, float* dst) {
     if (zc + col >= a.z.w) return;
     float* o = dst + (int64_t)(zc + col) * a.ssz;
 #pragma unroll
@@ -430,7 +442,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
-        if (x < a.x.w) o[(int64_t)x * a.ssx] = D[xt][i];
+        if (x < a.x.w) o[(int64_t)x * a.ssx] = V[xt][i];
       }
   };
   if constexpr (OUT) {
@@ -600,7 +612,7 @@ int waves(int w) { return w <= 64 ? 2 : 4; }
 template <int DX, int NW, bool F32, bool OUT, bool DEC>
 atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   constexpr int NP = F32 ? 3 : 1;
-  constexpr int lds = 2 * kC * NP * ((OUT ? 2 : 1) * (DX * 32 + kPad) + NW * 32 + kPad) + 4 * (kC + 4);
+  constexpr int lds = (F32 ? 1 : 2) * 2 * kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 4 * (kC + 4);
   auto kern = la_chunk<DX, NW, F32, OUT, DEC>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
@@ -626,11 +638,11 @@ atlasmem_status chunk_run(const LaArgs& a, bool bf16, bool dec, int64_t M, hipSt
 }
 
 // Segments of the token axis: enough workgroups to fill the chip several times where the memories
-// alone do not, none shorter than four chunks.
+// alone do not, none shorter than eight chunks.
 int segments(const LinAttn& s, int64_t& lseg) {
   const int64_t chunks = std::max<int64_t>((s.T + kC - 1) / kC, 1);
   const int64_t M = (int64_t)s.B * s.H;
-  int64_t n = std::min<int64_t>((1024 + M - 1) / M, (chunks + 3) / 4);
+  int64_t n = std::min<int64_t>((1024 + M - 1) / M, (chunks + 7) / 8);
   const int64_t per = (chunks + n - 1) / n;
   lseg = per * kC;
   return (int)((chunks + per - 1) / per);
