@@ -436,7 +436,7 @@ atlasmem_status atlasmem_gates(const void* U, int64_t B, int64_t T, int32_t d_mo
  *         (NULL where that is 0)
  * bf16 inputs enter the products as they are, fp32 ones as three bf16 planes (24 bits); states and
  * sums are fp32, Y is rounded once.  Errors: E_INVALID for bad sizes, enums, null or overlapping
- * pointers, a short workspace; E_SHAPE beyond the limits (batch * heads <= 2^20).
+ * pointers, a short workspace; E_SHAPE beyond the limits (heads <= 65536, batch * heads <= 2^20).
  * The workspace function returns -1 for sizes that the calls refuse. */
 int64_t atlasmem_linear_attention_workspace_bytes(int32_t dtype, int32_t batch, int32_t heads, int64_t T,
                                                   int32_t d_key, int32_t d_value, int32_t backward);

@@ -463,7 +463,8 @@ atlasmem_status lin_attn_of(int32_t dtype, int32_t batch, int32_t heads, int64_t
       (dtype != ATLASMEM_F32 && dtype != ATLASMEM_BF16) ||
       (layout != ATLASMEM_HEADS_FIRST && layout != ATLASMEM_TOKENS_FIRST))
     return ATLASMEM_E_INVALID;
-  if (d_key > kLinAttnMaxDim || d_value > kLinAttnMaxDim || T > INT32_MAX - 64 ||
+  // 32 rows of all heads stay below 2^30 bytes
+  if (d_key > kLinAttnMaxDim || d_value > kLinAttnMaxDim || T > INT32_MAX - 64 || heads > (1 << 16) ||
       (int64_t)batch * heads > (1 << 20))
     return ATLASMEM_E_SHAPE;
   s = {batch, heads, T, d_key, d_value, dtype == ATLASMEM_BF16, layout == ATLASMEM_TOKENS_FIRST, nullptr, nullptr};

@@ -100,6 +100,10 @@ __device__ __forceinline__ void buf_st_u16(rsrc_t r, int voff, int soff, uint32_
 __device__ __forceinline__ void buf_st(rsrc_t r, int voff, int soff, float x) {
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, voff, soff, 0);
 }
+__device__ __forceinline__ void buf_st8(rsrc_t r, int voff, int soff, uint2 x) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{x.x, x.y}, r, voff, soff, 0);
+}
 __device__ __forceinline__ void buf_st4(rsrc_t r, int voff, int soff, float4 x) {
   __builtin_amdgcn_raw_buffer_store_b128(
       u32x4{__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)}, r, voff, soff, 0);

@@ -95,37 +95,45 @@ __device__ __forceinline__ f32x16 mm(const Op<NA>& a, const Op<NB>& b, f32x16 c)
   return c;
 }
 
+// The rows of a chunk in memory: a buffer from its first token on, rows behind the sequence out of range
+// (they read as zeros).  A lane's offset of position i is row_off, less `adj` where positions run
+// backwards and the chunk is short.
+struct ChunkRows {
+  rsrc_t r;
+  uint32_t adj;
+};
+__device__ __forceinline__ ChunkRows chunk_rows(const LaRows& t, int64_t at, int64_t first, int rows, int el, int rev) {
+  const uint32_t step = (uint32_t)t.st * el;
+  ChunkRows c;
+  c.r = make_rsrc((const char*)t.p + (at + first * t.st) * el, rows > 0 ? (rows - 1) * step + (uint32_t)t.w * el : 0u);
+  c.adj = rev ? (uint32_t)(kC - rows) * step : 0u;
+  return c;
+}
+constexpr uint32_t kNoRow = 0xC0000000u;  // behind any buffer (rows of a chunk span less than 2^30 bytes)
+__device__ __forceinline__ uint32_t row_off(const LaRows& t, int row, int c, int el, int rev) {
+  return c < t.w ? (uint32_t)(rev ? kC - 1 - row : row) * (uint32_t)(t.st * el) + (uint32_t)c * el : kNoRow;
+}
+
 // Eight consecutive elements of a row as read from memory.
 template <bool F32>
 struct Raw {
   u32x4 a[F32 ? 2 : 1];
 };
-
-template <bool F32>
-__device__ __forceinline__ Raw<F32> load_group(const LaRows& r, int64_t base, int64_t t, int c0) {
+// VEC: whole, aligned pieces; else element by element, `left` of them inside the row.
+template <bool F32, bool VEC>
+__device__ __forceinline__ Raw<F32> load_group(const ChunkRows& c, uint32_t off, int left) {
   Raw<F32> g;
-  g.a[0] = u32x4{0, 0, 0, 0};
-  if constexpr (F32) g.a[1] = u32x4{0, 0, 0, 0};
-  if (t < 0 || c0 >= r.w) return g;
-  const int64_t at = base + t * r.st + c0;
-  if constexpr (F32) {
-    const float* p = (const float*)r.p + at;
-    if (r.vec) {
-      g.a[0] = *(const u32x4*)p;
-      if (c0 + 4 < r.w) g.a[1] = *(const u32x4*)(p + 4);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c0 + i < r.w) g.a[i >> 2][i & 3] = __float_as_uint(p[i]);
-    }
+  const uint32_t o = off - c.adj;
+  if constexpr (VEC) {
+    g.a[0] = buf_ld16(c.r, (int)o, 0);
+    if constexpr (F32) g.a[1] = buf_ld16(c.r, left > 4 ? (int)(o + 16) : -1, 0);
   } else {
-    const uint16_t* p = (const uint16_t*)r.p + at;
-    if (r.vec) {
-      g.a[0] = *(const u32x4*)p;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c0 + i < r.w) g.a[0][i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) g.a[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (F32) g.a[i >> 2][i & 3] = __float_as_uint(buf_ld(c.r, i < left ? (int)(o + 4 * i) : -1, 0));
+      else g.a[0][i >> 1] |= buf_ld_u16(c.r, i < left ? (int)(o + 2 * i) : -1, 0) << (16 * (i & 1));
     }
   }
   return g;
@@ -142,8 +150,11 @@ __device__ __forceinline__ constexpr int exchange(int row) {
 template <int W, bool F32>
 __device__ __forceinline__ void store_group(uint16_t* s, int row, int c, const Raw<F32>& g) {
   const int f = exchange<W>(row);
-  uint16_t* d = s + row * W + (((c >> 2) ^ (f & ~1)) << 2);
-  auto put = [&](uint16_t* p, u32x4 v) { *(u32x4*)p = f & 1 ? u32x4{v[2], v[3], v[0], v[1]} : v; };
+  uint16_t *lo = s + row * W + (((c >> 2) ^ f) << 2), *hi = s + row * W + ((((c >> 2) | 1) ^ f) << 2);
+  auto put = [&](int at, u32x4 v) {
+    *(uint2*)(lo + at) = uint2{v[0], v[1]};
+    *(uint2*)(hi + at) = uint2{v[2], v[3]};
+  };
   if constexpr (F32) {
     float v[8];
 #pragma unroll
@@ -151,9 +162,9 @@ __device__ __forceinline__ void store_group(uint16_t* s, int row, int c, const R
     Op<3> o;
     split8(v, o);
 #pragma unroll
-    for (int n = 0; n < 3; ++n) put(d + n * kC * W, o.p[n]);
+    for (int n = 0; n < 3; ++n) put(n * kC * W, o.p[n]);
   } else {
-    put(d, g.a[0]);
+    put(0, g.a[0]);
   }
 }
 
@@ -192,7 +203,7 @@ __device__ __forceinline__ Op<NP> col_op(const uint16_t* s, int at, int c0, int 
 
 // DX: 32-column tiles of x and y; NW: waves, each with 32 columns of z; OUT: outputs (else the
 // segment's own state alone); DEC: the tangent too.
-template <int DX, int NW, bool F32, bool OUT, bool DEC>
+template <int DX, int NW, bool F32, bool VEC, bool OUT, bool DEC>
 __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   constexpr int NP = F32 ? 3 : 1;                    // planes of an input
   constexpr int NC = F32 || DEC ? 3 : 2;             // planes of a computed operand of the outputs
@@ -216,9 +227,11 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   const float g = a.log_decay[h];
   for (int i = tid; i <= kC; i += NT) pw[i] = decay_pow(g, i);
 
-  const int64_t bx = b * a.x.sb + h * a.x.sh, by = b * a.y.sb + h * a.y.sh, bz = b * a.z.sb + h * a.z.sh;
-  // position -> token; -1 behind the sequence
-  auto token = [&](int64_t p) -> int64_t { return p < len && p < p1 ? (a.rev ? len - 1 - p : p) : -1; };
+  constexpr int EL = F32 ? 4 : 2;
+  // of a chunk at position p: rows inside the sequence, and its first token in memory
+  auto rows_at = [&](int64_t p) { return (int)max((int64_t)0, min((int64_t)kC, min(len, p1) - p)); };
+  auto first_at = [&](int64_t p, int r) { return a.rev ? len - p - r : p; };
+  const int64_t atx = b * a.x.sb + h * a.x.sh, atz = b * a.z.sb + h * a.z.sh;  // y lies like x, o and t like z
 
   // state tiles: column zc + col, rows 32 xt + 8 q + 4 hf + u
   f32x16 S[DX], St[DEC ? DX : 1];
@@ -245,19 +258,31 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   }
 
   Raw<F32> rx[OUT ? GX : 1], ry[GX], rz[GZ];
+  uint32_t ox[GX], oz[GZ];
+#pragma unroll
+  for (int i = 0; i < GX; ++i) {
+    const int id = tid + i * NT;
+    ox[i] = row_off(a.x, id / (DX * 4), (id % (DX * 4)) * 8, EL, a.rev);
+  }
+#pragma unroll
+  for (int i = 0; i < GZ; ++i) {
+    const int id = tid + i * NT;
+    oz[i] = row_off(a.z, id / (NW * 4), z0 + (id % (NW * 4)) * 8, EL, a.rev);
+  }
   auto fetch = [&](int64_t p) {
+    const int r = rows_at(p);
+    const int64_t t = first_at(p, r);
+    const ChunkRows cx = chunk_rows(a.x, atx, t, r, EL, a.rev), cy = chunk_rows(a.y, atx, t, r, EL, a.rev),
+                    cz = chunk_rows(a.z, atz, t, r, EL, a.rev);
 #pragma unroll
     for (int i = 0; i < GX; ++i) {
-      const int id = tid + i * NT, row = id / (DX * 4), c = (id % (DX * 4)) * 8;
-      const int64_t t = token(p + row);
-      if constexpr (OUT) rx[i] = load_group<F32>(a.x, bx, t, c);
-      ry[i] = load_group<F32>(a.y, by, t, c);
+      const int left = a.x.w - ((tid + i * NT) % (DX * 4)) * 8;
+      if constexpr (OUT) rx[i] = load_group<F32, VEC>(cx, ox[i], left);
+      ry[i] = load_group<F32, VEC>(cy, ox[i], left);
     }
 #pragma unroll
-    for (int i = 0; i < GZ; ++i) {
-      const int id = tid + i * NT, row = id / (NW * 4), c = (id % (NW * 4)) * 8;
-      rz[i] = load_group<F32>(a.z, bz, token(p + row), z0 + c);
-    }
+    for (int i = 0; i < GZ; ++i)
+      rz[i] = load_group<F32, VEC>(cz, oz[i], a.z.w - z0 - ((tid + i * NT) % (NW * 4)) * 8);
   };
   auto stage = [&](uint16_t* s) {
 #pragma unroll
@@ -278,10 +303,11 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   __syncthreads();
   // decay from position j (the register's) to i (the lane's), of the carried state, and to the chunk's end
   float D[OUT ? 16 : 1], wz[16];
-  const float wi = pw[col + 1 - a.e];
+  const float wi = pw[col + 1 - a.e] * a.c_out;
   if constexpr (OUT) {
 #pragma unroll
-    for (int n = 0; n < 16; ++n) D[n] = pw[max(col - (8 * (n >> 2) + 4 * hf + (n & 3)), 0)] * a.c_upd;
+    for (int n = 0; n < 16; ++n)
+      D[n] = pw[max(col - (8 * (n >> 2) + 4 * hf + (n & 3)), 0)] * a.c_upd * a.c_out;
   }
   auto weights = [&](int r) {
 #pragma unroll
@@ -292,6 +318,12 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   };
   weights(kC);
   const int rat = row_at<WX>(lane), cat = col_at<WX>(lane), zat = col_at<WZ>(lane);
+  const int ci = col - 4 * hf;                        // i >= j: ci >= 8 (n / 4) + n % 4
+  uint32_t oo[OUT ? 4 : 1];                           // the lane's output pieces
+  if constexpr (OUT) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) oo[q] = row_off(a.o, col, zc + 8 * q + 4 * hf, EL, a.rev);
+  }
 
   int buf = 0;
   for (int64_t p = p0; p < p1; p += kC) {
@@ -302,7 +334,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     __syncthreads();
     if (p + kC < p1) fetch(p + kC);
     if constexpr (kBufs == 2) buf ^= 1;
-    const int r = (int)max((int64_t)0, min((int64_t)kC, min(len, p1) - p));
+    const int r = rows_at(p);
 
     Op<NP> zo[2];
     if constexpr (OUT) {
@@ -328,7 +360,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
       for (int n = 0; n < 16; ++n) {
         O[n] *= wi;
         if constexpr (DEC) Ot[n] = Ot[n] * wi + (float)(col + 1) * O[n];
-        P[n] = col >= 8 * (n >> 2) + 4 * hf + (n & 3) ? P[n] * D[n] : 0.0f;
+        P[n] = ci >= 8 * (n >> 2) + (n & 3) ? P[n] * D[n] : 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -347,46 +379,51 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
         }
       }
       // rows: the lane's position, four consecutive columns a register group
-      const int64_t pos = p + col;
-      if (pos < p1) {
-        const bool live = col < r;
-        const int64_t t = live && a.rev ? len - 1 - pos : pos;
-        const int64_t at = b * a.o.sb + h * a.o.sh + t * a.o.st;
+      const ChunkRows co = chunk_rows(a.o, atz, first_at(p, r), r, EL, a.rev);
+      auto put_piece = [&](const ChunkRows& c, uint32_t off, const float* v, int left) {
+        const uint32_t o = off - c.adj;
+        if constexpr (F32) {
+          if constexpr (VEC) {
+            buf_st4(c.r, (int)o, 0, float4{v[0], v[1], v[2], v[3]});
+          } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) buf_st(c.r, n < left ? (int)(o + 4 * n) : -1, 0, v[n]);
+          }
+        } else {
+          const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+          if constexpr (VEC) {
+            buf_st8(c.r, (int)o, 0, w);
+          } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) buf_st_u16(c.r, n < left ? (int)(o + 2 * n) : -1, 0, (n & 2 ? w.y : w.x) >> (16 * (n & 1)));
+          }
+        }
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {O[4 * q], O[4 * q + 1], O[4 * q + 2], O[4 * q + 3]};
+        put_piece(co, oo[q], v, a.z.w - zc - 8 * q - 4 * hf);
+      }
+      if constexpr (DEC) {
+        const ChunkRows ct = chunk_rows(a.t, atz, first_at(p, r), r, EL, a.rev);
+        float part = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int left = a.z.w - zc - 8 * (n >> 2) - 4 * hf;
+          const int o = (n & 3) < left ? (int)(oo[n >> 2] - ct.adj + EL * (n & 3)) : -1;
+          const float t = F32 ? buf_ld(ct.r, o, 0) : bf16_value(buf_ld_u16(ct.r, o, 0));
+          part += col < r ? Ot[n] * t : 0.0f;
+        }
+        dec += part;
+      }
+      if (r < kC) {  // rows of the segment behind the sequence
+        const int64_t behind = p + r;
+        const ChunkRows ce = chunk_rows(a.o, atz, behind, (int)min((int64_t)(kC - r), p1 - behind), EL, 0);
+        const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int c = zc + 8 * q + 4 * hf;
-          float v[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) v[n] = live ? O[4 * q + n] * a.c_out : 0.0f;
-          if constexpr (DEC) {
-            if (live) {
-              const int64_t ta = b * a.t.sb + h * a.t.sh + t * a.t.st;
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                if (c + n < a.z.w) dec += (double)(Ot[4 * q + n] * a.c_out) * load_in(a.t.p, ta + c + n, !F32);
-            }
-          }
-          if (c >= a.z.w) continue;
-          if constexpr (F32) {
-            float* o = (float*)a.o.p + at + c;
-            if (a.o.vec) {
-              *(float4*)o = float4{v[0], v[1], v[2], v[3]};
-            } else {
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                if (c + n < a.z.w) o[n] = v[n];
-            }
-          } else {
-            uint16_t* o = (uint16_t*)a.o.p + at + c;
-            const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
-            if (a.o.vec) {
-              *(uint2*)o = w;
-            } else {
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                if (c + n < a.z.w) o[n] = (uint16_t)((n & 2 ? w.y : w.x) >> (16 * (n & 1)));
-            }
-          }
+          put_piece(ce, row_off(a.o, col, c, EL, 0), none, a.z.w - c);
         }
       }
     } else {
@@ -609,11 +646,11 @@ LaRows rows_of(const void* p, const LinAttn& s, int w) {
 int tiles(int w) { return w <= 64 ? 2 : 4; }
 int waves(int w) { return w <= 64 ? 2 : 4; }
 
-template <int DX, int NW, bool F32, bool OUT, bool DEC>
+template <int DX, int NW, bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   constexpr int NP = F32 ? 3 : 1;
   constexpr int lds = (F32 ? 1 : 2) * 2 * kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 4 * (kC + 4);
-  auto kern = la_chunk<DX, NW, F32, OUT, DEC>;
+  auto kern = la_chunk<DX, NW, F32, VEC, OUT, DEC>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return ATLASMEM_E_DEVICE;
@@ -623,18 +660,26 @@ atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   return ATLASMEM_OK;
 }
 
-template <bool F32, bool OUT, bool DEC>
+template <bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_pick(const LaArgs& a, int64_t blocks, hipStream_t st) {
   const int dx = tiles(a.x.w), nw = waves(a.z.w);
-  if (dx == 2) return nw == 2 ? chunk_launch<2, 2, F32, OUT, DEC>(a, blocks, st) : chunk_launch<2, 4, F32, OUT, DEC>(a, blocks, st);
-  return nw == 2 ? chunk_launch<4, 2, F32, OUT, DEC>(a, blocks, st) : chunk_launch<4, 4, F32, OUT, DEC>(a, blocks, st);
+  if (dx == 2)
+    return nw == 2 ? chunk_launch<2, 2, F32, VEC, OUT, DEC>(a, blocks, st)
+                   : chunk_launch<2, 4, F32, VEC, OUT, DEC>(a, blocks, st);
+  return nw == 2 ? chunk_launch<4, 2, F32, VEC, OUT, DEC>(a, blocks, st)
+                 : chunk_launch<4, 4, F32, VEC, OUT, DEC>(a, blocks, st);
 }
 
 template <bool OUT>
 atlasmem_status chunk_run(const LaArgs& a, bool bf16, bool dec, int64_t M, hipStream_t st) {
   const int64_t blocks = M * (OUT ? a.nseg : a.nseg - 1);
-  if (bf16) return dec ? chunk_pick<false, OUT, true>(a, blocks, st) : chunk_pick<false, OUT, false>(a, blocks, st);
-  return dec ? chunk_pick<true, OUT, true>(a, blocks, st) : chunk_pick<true, OUT, false>(a, blocks, st);
+  const bool vec = a.x.vec && a.y.vec && a.z.vec && (!OUT || (a.o.vec && (!dec || a.t.vec)));
+  if (bf16) {
+    if (vec) return dec ? chunk_pick<false, true, OUT, true>(a, blocks, st) : chunk_pick<false, true, OUT, false>(a, blocks, st);
+    return dec ? chunk_pick<false, false, OUT, true>(a, blocks, st) : chunk_pick<false, false, OUT, false>(a, blocks, st);
+  }
+  if (vec) return dec ? chunk_pick<true, true, OUT, true>(a, blocks, st) : chunk_pick<true, true, OUT, false>(a, blocks, st);
+  return dec ? chunk_pick<true, false, OUT, true>(a, blocks, st) : chunk_pick<true, false, OUT, false>(a, blocks, st);
 }
 
 // Segments of the token axis: enough workgroups to fill the chip several times where the memories
@@ -642,7 +687,7 @@ atlasmem_status chunk_run(const LaArgs& a, bool bf16, bool dec, int64_t M, hipSt
 int segments(const LinAttn& s, int64_t& lseg) {
   const int64_t chunks = std::max<int64_t>((s.T + kC - 1) / kC, 1);
   const int64_t M = (int64_t)s.B * s.H;
-  int64_t n = std::min<int64_t>((1024 + M - 1) / M, (chunks + 7) / 8);
+  int64_t n = std::min<int64_t>((512 + M - 1) / M, (chunks + 7) / 8);
   const int64_t per = (chunks + n - 1) / n;
   lseg = per * kC;
   return (int)((chunks + per - 1) / per);
