@@ -210,7 +210,9 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   constexpr int WX = DX * 32, WZ = NW * 32;
   constexpr int NT = NW * 64;
   constexpr int GX = kC * DX * 4 / NT, GZ = kC * NW * 4 / NT;  // 8-element groups per thread
-  constexpr int TX = NP * kC * WX, TZ = NP * kC * WZ, kBuf = (OUT ? 2 : 1) * TX + TZ;
+  // 16 bytes between the tiles: at whole multiples of 512 the compiler joins a read of x with one of y,
+  // and takes the results apart again with moves
+  constexpr int TX = NP * kC * WX + 8, TZ = NP * kC * WZ + 8, kBuf = (OUT ? 2 : 1) * TX + TZ;
   constexpr int kBufs = F32 ? 1 : 2;
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   float* pw = (float*)(sm + kBufs * kBuf);           // lambda^0 .. lambda^32
@@ -649,7 +651,7 @@ int waves(int w) { return w <= 64 ? 2 : 4; }
 template <int DX, int NW, bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   constexpr int NP = F32 ? 3 : 1;
-  constexpr int lds = (F32 ? 1 : 2) * 2 * kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 4 * (kC + 4);
+  constexpr int lds = (F32 ? 1 : 2) * 2 * (kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 24) + 4 * (kC + 4);
   auto kern = la_chunk<DX, NW, F32, VEC, OUT, DEC>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
