@@ -423,6 +423,8 @@ bool apart(const Range& a, const Range& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
   return x + (uint64_t)a.bytes <= y || y + (uint64_t)b.bytes <= x;
 }
+// A workspace of `need` bytes or more, aligned to 16.
+bool usable(const void* p, int64_t bytes, int64_t need) { return p && bytes >= need && ((uintptr_t)p & 15) == 0; }
 // No output overlaps an input or another output.
 bool disjoint(const Range* out, int n_out, const Range* in, int n_in) {
   for (int i = 0; i < n_out; ++i) {
@@ -841,7 +843,7 @@ atlasmem_status atlasmem_linear_attention(const void* Q, const void* K, const vo
   if (e != ATLASMEM_OK) return e;
   if (!log_decay || (T > 0 && (!Q || !K || !V || !Y))) return ATLASMEM_E_INVALID;
   const int64_t need = linear_attention_workspace_bytes(s, false);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return ATLASMEM_E_INVALID;
+  if (need > 0 && !usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
   const int64_t el = s.bf16 ? 2 : 4, M = (int64_t)batch * heads;
   const int64_t nk = M * T * d_key * el, nv = M * T * d_value * el, ns = M * d_key * d_value * 4;
   const Range out[] = {{Y, nv}, {W_T, ns}, {workspace, need}};
@@ -863,7 +865,7 @@ atlasmem_status atlasmem_linear_attention_backward(const void* Q, const void* K,
   if (e != ATLASMEM_OK) return e;
   if (!log_decay || !workspace || (T > 0 && (!Q || !K || !V || !dY || !dQ || !dK || !dV))) return ATLASMEM_E_INVALID;
   const int64_t need = linear_attention_workspace_bytes(s, true);
-  if (workspace_bytes < need) return ATLASMEM_E_INVALID;
+  if (!usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
   const int64_t el = s.bf16 ? 2 : 4, M = (int64_t)batch * heads;
   const int64_t nk = M * T * d_key * el, nv = M * T * d_value * el, ns = M * d_key * d_value * 4;
   const Range out[] = {{dQ, nk}, {dK, nk}, {dV, nv}, {dW0, ns}, {dlog_decay, heads * 4}, {workspace, need}};
@@ -892,7 +894,7 @@ atlasmem_status atlasmem_group_norm(const void* X, int32_t dtype, int64_t n, int
   if (n == 0) return ATLASMEM_OK;
   if (!X || !Y) return ATLASMEM_E_INVALID;
   const int64_t need = group_norm_workspace_bytes(s, false);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return ATLASMEM_E_INVALID;
+  if (need > 0 && !usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
   const int64_t nx = n * L * channels * (s.bf16 ? 2 : 4), ns = n * groups * 4, nc = channels * (int64_t)4;
   const Range out[] = {{Y, nx}, {mean, ns}, {rstd, ns}, {workspace, need}};
   const Range in[] = {{X == Y ? nullptr : X, nx}, {gamma, nc}, {beta, nc}};
@@ -911,7 +913,7 @@ atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int3
   if (e != ATLASMEM_OK) return e;
   if (n > 0 && (!X || !dY || !mean || !rstd || !dX)) return ATLASMEM_E_INVALID;
   const int64_t need = group_norm_workspace_bytes(s, true);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return ATLASMEM_E_INVALID;
+  if (need > 0 && !usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
   const int64_t nx = n * L * channels * (s.bf16 ? 2 : 4), ns = n * groups * 4, nc = channels * (int64_t)4;
   const Range out[] = {{dX, nx}, {dgamma, nc}, {dbeta, nc}, {workspace, need}};
   const Range in[] = {{X == dX ? nullptr : X, nx}, {dY == dX ? nullptr : dY, nx}, {mean, ns}, {rstd, ns}, {gamma, nc},
@@ -937,7 +939,7 @@ atlasmem_status atlasmem_cross_entropy(const void* X, const void* W, int32_t dty
   if (n == 0) return ATLASMEM_OK;
   if (!X || !W || !labels || !loss || !lse || !workspace) return ATLASMEM_E_INVALID;
   const int64_t need = cross_entropy_workspace_bytes(s, false);
-  if (workspace_bytes < need) return ATLASMEM_E_INVALID;
+  if (!usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
   const int64_t el = s.bf16 ? 2 : 4;
   const Range out[] = {{loss, n * 4}, {lse, n * 4}, {workspace, need}};
   const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {labels, n * 8}};
@@ -955,7 +957,7 @@ atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, in
   if (n > 0 && (!X || !W || !labels || !lse || !workspace)) return ATLASMEM_E_INVALID;
   if (!dX && !dW) return ATLASMEM_OK;
   const int64_t need = cross_entropy_workspace_bytes(s, true);
-  if (n > 0 && workspace_bytes < need) return ATLASMEM_E_INVALID;
+  if (n > 0 && !usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
   const int64_t el = s.bf16 ? 2 : 4;
   const Range out[] = {{dX, n * d * el}, {dW, vocab * d * el}, {workspace, n > 0 ? need : 0}};
   const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {labels, n * 8}, {lse, n * 4}, {dloss, n * 4}};

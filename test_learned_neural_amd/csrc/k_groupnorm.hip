@@ -147,21 +147,42 @@ __global__ __launch_bounds__(256) void gn_rows(GnArgs a) {
 #pragma unroll
     for (int k = 0; k < V; ++k) dg[i][k] = db[i][k] = 0.0f;
 
-  for (int64_t r = on ? slot : a.n; __any(r < a.n); r += a.slots) {
+  // the next sample is on its way while this one is computed
+  float nx[NI][V], nd[BWD ? NI : 1][V], nm = 0.0f, nr = 0.0f;
+  auto fetch = [&](int64_t r) {
     const bool live = r < a.n;
     const int64_t base = r * a.L * a.C + (int64_t)g * a.c;
-    float x[NI][V], d[BWD ? NI : 1][V];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[i][k] = 0.0f;
-      if (live && in[i]) ld<F32, V>(a.x, base + at[i], x[i]);
+      for (int k = 0; k < V; ++k) nx[i][k] = 0.0f;
+      if (live && in[i]) ld<F32, V>(a.x, base + at[i], nx[i]);
       if constexpr (BWD) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) d[i][k] = 0.0f;
-        if (live && in[i]) ld<F32, V>(a.dy, base + at[i], d[i]);
+        for (int k = 0; k < V; ++k) nd[i][k] = 0.0f;
+        if (live && in[i]) ld<F32, V>(a.dy, base + at[i], nd[i]);
       }
     }
+    if constexpr (BWD) {
+      nm = live ? a.mean[r * a.G + g] : 0.0f;
+      nr = live ? a.rstd[r * a.G + g] : 0.0f;
+    }
+  };
+  int64_t r = on ? slot : a.n;
+  fetch(r);
+  for (; __any(r < a.n); r += a.slots) {
+    const bool live = r < a.n;
+    const int64_t base = r * a.L * a.C + (int64_t)g * a.c;
+    float x[NI][V], d[BWD ? NI : 1][V];
+    const float mean_in = nm, rstd_in = nr;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        x[i][k] = nx[i][k];
+        if constexpr (BWD) d[i][k] = nd[i][k];
+      }
+    fetch(r + a.slots);
     if constexpr (!BWD) {
       float s = 0.0f;
 #pragma unroll
@@ -189,7 +210,7 @@ __global__ __launch_bounds__(256) void gn_rows(GnArgs a) {
         if (live && in[i]) st<F32, V>(a.out, base + at[i], x[i]);
       }
     } else {
-      const float mean = live ? a.mean[r * a.G + g] : 0.0f, rstd = live ? a.rstd[r * a.G + g] : 0.0f;
+      const float mean = mean_in, rstd = rstd_in;
       float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -230,12 +251,9 @@ __global__ __launch_bounds__(256) void gn_rows(GnArgs a) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       if (in[i] && (a.L == 1 || (i == 0 && lane < across))) {
-        float* p = a.part + (slot * 2) * a.C + g * a.c + at[i];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          p[k] = dg[i][k];
-          p[a.C + k] = db[i][k];
-        }
+        const int64_t p = (slot * 2) * a.C + g * a.c + at[i];  // channels a multiple of V: aligned like X
+        st<true, V>(a.part, p, dg[i]);
+        st<true, V>(a.part, p + a.C, db[i]);
       }
   }
 }
@@ -344,20 +362,24 @@ __global__ __launch_bounds__(256) void gn_moments(GnArgs a) {
   }
 }
 
-// mean, rstd of a (sample, group): one workgroup of a wave.
+// mean, rstd of a (sample, group): one workgroup.
 template <int V>
-__global__ __launch_bounds__(64) void gn_stats(GnArgs a, float* mean, float* rstd) {
+__global__ __launch_bounds__(256) void gn_stats(GnArgs a, float* mean, float* rstd) {
   const int64_t smp = blockIdx.x / a.G;
   const int g = blockIdx.x % a.G, per = a.c / V;
   Mom m = {0.0f, 0.0f, 0.0f};
-  for (int64_t i = threadIdx.x; i < (int64_t)a.splits * per; i += 64) {
+  __shared__ Mom sm[4];
+  for (int64_t i = threadIdx.x; i < (int64_t)a.splits * per; i += 256) {
     const int sp = (int)(i / per), cv = g * per + (int)(i % per);
     const float cnt = (float)(min(a.span, a.L - sp * a.span) * V);
     const float* p = a.part + ((smp * a.splits + sp) * (a.C / V) + cv) * 2;
     m = join(m, Mom{cnt, p[0], p[1]});
   }
   for (int s = 32; s; s >>= 1) m = join(m, Mom{__shfl_xor(m.n, s), __shfl_xor(m.mean, s), __shfl_xor(m.m2, s)});
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+  __syncthreads();
   if (threadIdx.x == 0) {
+    for (int k = 1; k < 4; ++k) m = join(m, sm[k]);
     mean[blockIdx.x] = m.mean;
     rstd[blockIdx.x] = 1.0f / sqrtf(m.m2 / m.n + a.eps);
   }
@@ -437,12 +459,12 @@ __global__ __launch_bounds__(256) void gn_sums(GnArgs a) {
 }
 
 // mean(h xh), mean(h) of a (sample, group): [n, G, 2]
-__global__ __launch_bounds__(256) void gn_group_sums(GnArgs a, float* out) {
-  __shared__ float sm[2][4];
+__global__ __launch_bounds__(1024) void gn_group_sums(GnArgs a, float* out) {
+  __shared__ float sm[2][16];
   const int64_t smp = blockIdx.x / a.G;
   const int g = blockIdx.x % a.G;
   float s2 = 0.0f, s1 = 0.0f;
-  for (int64_t i = threadIdx.x; i < (int64_t)a.splits * a.c; i += 256) {
+  for (int64_t i = threadIdx.x; i < (int64_t)a.splits * a.c; i += 1024) {
     const int ch = g * a.c + (int)(i % a.c);
     const float* p = a.part + (smp * a.splits + i / a.c) * 2 * a.C + ch;
     const float ga = a.gamma ? a.gamma[ch] : 1.0f;
@@ -453,7 +475,8 @@ __global__ __launch_bounds__(256) void gn_group_sums(GnArgs a, float* out) {
   if ((threadIdx.x & 63) == 0) sm[0][threadIdx.x >> 6] = s2, sm[1][threadIdx.x >> 6] = s1;
   __syncthreads();
   if (threadIdx.x < 2) {
-    const float t = sm[threadIdx.x][0] + sm[threadIdx.x][1] + sm[threadIdx.x][2] + sm[threadIdx.x][3];
+    float t = 0.0f;
+    for (int k = 0; k < 16; ++k) t += sm[threadIdx.x][k];
     out[(int64_t)blockIdx.x * 2 + threadIdx.x] = t / ((float)a.L * (float)a.c);
   }
 }
@@ -489,15 +512,19 @@ __global__ __launch_bounds__(256) void gn_apply_grad(GnArgs a, const float* sums
 // ------------------------------------------------------------------------------------------- host
 
 constexpr int kLanes = 64, kVecs = 4;             // a group of the one-pass form: at most 64 lanes x 4 vectors
-constexpr int64_t kSlotsMost = 512;               // samples in flight of the backward's one-pass form
+constexpr int64_t kSlotSums = 1 << 21;            // channels of all samples in flight of the backward's
+constexpr int64_t kLanesMost = 1 << 19;           // lanes in flight of the forward's: 32 waves a CU
 constexpr int64_t kRowsAtOnce = 1024;             // more rows of partial sums are first summed in pieces
 constexpr int64_t kPieces = 128;
 
-// Samples in flight: the backward writes a row of partial sums for each, so it keeps few.
-int64_t row_slots(int64_t n, bool bwd) { return bwd ? std::min(n, kSlotsMost) : n; }
+// Samples in flight, each with lanes that walk every so-manieth sample.  The backward writes two rows of
+// channel sums for each: 16 MB fill the chip (2048 channels of bf16, 16384 samples: 1024 in flight 55 us,
+// 512 72 us, 2048 70 us).
+int64_t row_slots(int64_t n, int C) { return std::min(n, std::max<int64_t>(1, kSlotSums / C)); }
+int64_t forward_slots(int64_t n, int64_t lanes) { return std::min(n, std::max<int64_t>(1, kLanesMost / lanes)); }
 
 void set_spans(GnArgs& a) {
-  const int64_t want = std::max<int64_t>(1, 2048 / std::max<int64_t>(a.n, 1));
+  const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(a.n, 1));
   const int64_t s = std::max<int64_t>(1, std::min(want, (a.L + 15) / 16));
   a.span = (a.L + s - 1) / s;
   a.splits = (int)((a.L + a.span - 1) / a.span);
@@ -527,7 +554,7 @@ atlasmem_status rows_launch(GnArgs a, hipStream_t st) {
   a.across = pow2_from(vecs);
   a.team = pow2_from(a.across * a.L);
   const int ni = a.L == 1 ? (vecs + a.team - 1) / a.team : (int)((a.L * a.across + a.team - 1) / a.team);
-  a.slots = row_slots(a.n, BWD);
+  a.slots = BWD ? row_slots(a.n, a.C) : forward_slots(a.n, (int64_t)a.G * a.team);
   const int64_t blocks = (a.slots * a.G * a.team + 255) / 256;
   if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
   if (ni == 1) gn_rows<F32, V, 1, SILU, BWD><<<(unsigned)blocks, 256, 0, st>>>(a);
@@ -546,7 +573,7 @@ atlasmem_status forward(GnArgs a, hipStream_t st) {
   if (!a.rstd) a.rstd = stats + a.n * a.G;
   gn_moments<F32, V><<<grid, 256, 0, st>>>(a);
   AM_LAUNCH_CHECK();
-  gn_stats<V><<<(unsigned)(a.n * a.G), 64, 0, st>>>(a, a.mean, a.rstd);
+  gn_stats<V><<<(unsigned)(a.n * a.G), 256, 0, st>>>(a, a.mean, a.rstd);
   AM_LAUNCH_CHECK();
   gn_apply<F32, V, SILU><<<grid, 256, 0, st>>>(a);
   AM_LAUNCH_CHECK();
@@ -576,13 +603,13 @@ atlasmem_status backward(GnArgs a, hipStream_t st) {
     const atlasmem_status e = rows_launch<F32, V, SILU, true>(a, st);
     if (e != ATLASMEM_OK) return e;
     a.part = part;
-    count = row_slots(a.n, true);
+    count = row_slots(a.n, a.C);
   } else {
     const dim3 grid((unsigned)(a.n * a.splits), (unsigned)((a.C / V + 255) / 256));
     float* sums = a.part + 2 * a.n * a.splits * (int64_t)a.C;
     gn_sums<F32, V, SILU><<<grid, 256, 0, st>>>(a);
     AM_LAUNCH_CHECK();
-    gn_group_sums<<<(unsigned)(a.n * a.G), 256, 0, st>>>(a, sums);
+    gn_group_sums<<<(unsigned)(a.n * a.G), 1024, 0, st>>>(a, sums);
     AM_LAUNCH_CHECK();
     gn_apply_grad<F32, V, SILU><<<grid, 256, 0, st>>>(a, sums);
     AM_LAUNCH_CHECK();
@@ -627,7 +654,7 @@ int64_t group_norm_workspace_bytes(const GroupNorm& s, bool backward) {
   const GnArgs a = args_of(s);
   const bool rows = one_pass(a.L, a.c, 1);  // whatever the alignment
   if (!backward) return rows ? 0 : 4 * (2 * a.n * a.splits * (int64_t)a.C + 2 * a.n * a.G);
-  const int64_t count = std::max(row_slots(a.n, true), rows ? (int64_t)0 : a.n * a.splits);
+  const int64_t count = std::max(row_slots(a.n, a.C), rows ? (int64_t)0 : a.n * a.splits);
   return 4 * (2 * count * a.C + 2 * a.n * a.G + (count > kRowsAtOnce ? 2 * kPieces * a.C : 0));
 }
 

@@ -17,6 +17,7 @@
 //   sum_i scale dy_i . (dS_i / dlog lambda)^T q_i + <dW_T, dS_T / dlog lambda>,
 // every term a product that is there: the shorter identity through sum_t (q.dq - k.dk) cancels.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "internal.h"
@@ -327,16 +328,19 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     for (int q = 0; q < 4; ++q) oo[q] = row_off(a.o, col, zc + 8 * q + 4 * hf, EL, a.rev);
   }
 
+  // One chunk; FULL: all its positions are inside the sequence (one block of code without branches, which
+  // the scheduler can fill the waits of each part of with the others).
   int buf = 0;
-  for (int64_t p = p0; p < p1; p += kC) {
+  auto chunk = [&](auto full, int64_t p) {
+    constexpr bool FULL = decltype(full)::value;
     uint16_t* sy = sm + buf * kBuf;
     const uint16_t *sz = sy + TX, *sx = sz + TZ;
     if constexpr (kBufs == 1) __syncthreads();
     stage(sy);
     __syncthreads();
-    if (p + kC < p1) fetch(p + kC);
+    fetch(p + kC);
     if constexpr (kBufs == 2) buf ^= 1;
-    const int r = rows_at(p);
+    const int r = FULL ? kC : rows_at(p);
 
     Op<NP> zo[2];
     if constexpr (OUT) {
@@ -418,7 +422,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
         }
         dec += part;
       }
-      if (r < kC) {  // rows of the segment behind the sequence
+      if constexpr (!FULL) {  // rows of the segment behind the sequence
         const int64_t behind = p + r;
         const ChunkRows ce = chunk_rows(a.o, atz, behind, (int)min((int64_t)(kC - r), p1 - behind), EL, 0);
         const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -434,7 +438,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     }
 
     // state: column operands of y times the weighted z (three planes: the state is an fp32 result)
-    if (r < kC) weights(r);
+    if constexpr (!FULL) weights(r);
     const float keep = pw[r];
 #pragma unroll
     for (int xt = 0; xt < DX; ++xt)
@@ -470,7 +474,10 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
         if constexpr (DEC) St[xt] = mm(yo, st, St[xt]);
       }
     }
-  }
+  };
+  int64_t p = p0;
+  for (; p + kC <= min(len, p1); p += kC) chunk(std::true_type{}, p);
+  for (; p < p1; p += kC) chunk(std::false_type{}, p);
 
   // the state out: C-layout tiles to the caller's order
   auto put = [&](const f32x16* V, float* dst) {
@@ -524,17 +531,27 @@ __global__ void la_scan(const float* w0, float* u, float* ut, const float* log_d
   float s = w0 ? w0[(int64_t)m * P + i] : 0.0f, t = 0.0f;
   float* p = u + (int64_t)m * nseg * P + i;
   float* pt = ut ? ut + (int64_t)m * nseg * P + i : nullptr;
-  p[0] = s;
-  if (pt) pt[0] = 0.0f;
-  for (int k = 1; k < nseg; ++k) {
-    const int64_t cnt = min(lseg, max((int64_t)0, n - (k - 1) * lseg));
-    const float keep = decay_pow(g, cnt);
-    if (pt) {
-      t = keep * (t + (float)cnt * s) + pt[(int64_t)k * P];
-      pt[(int64_t)k * P] = t;
+  constexpr int kAhead = 8;  // segments whose sums are read before the chain of products uses them
+  for (int k0 = 0; k0 < nseg; k0 += kAhead) {
+    float v[kAhead], vt[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const bool in = k0 + k > 0 && k0 + k < nseg;
+      v[k] = in ? p[(int64_t)(k0 + k) * P] : 0.0f;
+      vt[k] = in && pt ? pt[(int64_t)(k0 + k) * P] : 0.0f;
     }
-    s = keep * s + p[(int64_t)k * P];
-    p[(int64_t)k * P] = s;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k0 + k >= nseg) break;
+      if (k0 + k > 0) {
+        const int64_t cnt = min(lseg, max((int64_t)0, n - (k0 + k - 1) * lseg));
+        const float keep = decay_pow(g, cnt);
+        t = keep * (t + (float)cnt * s) + vt[k];
+        s = keep * s + v[k];
+      }
+      p[(int64_t)(k0 + k) * P] = s;
+      if (pt) pt[(int64_t)(k0 + k) * P] = t;
+    }
   }
 }
 

@@ -40,7 +40,7 @@ FAR = 1 << 36
 @pytest.mark.parametrize("kw,status", [
     (dict(X=None), am.E_INVALID), (dict(W=None), am.E_INVALID), (dict(labels=None), am.E_INVALID),
     (dict(loss=None), am.E_INVALID), (dict(lse=None), am.E_INVALID), (dict(ws=None), am.E_INVALID),
-    (dict(bytes=100), am.E_INVALID), (dict(dtype=9), am.E_INVALID), (dict(n=-1), am.E_INVALID),
+    (dict(bytes=100), am.E_INVALID), (dict(ws=6 * FAR + 8), am.E_INVALID), (dict(dtype=9), am.E_INVALID), (dict(n=-1), am.E_INVALID),
     (dict(d=0), am.E_INVALID), (dict(vocab=0), am.E_INVALID), (dict(d=16385), am.E_SHAPE),
     (dict(vocab=1 << 25), am.E_SHAPE), (dict(n=1 << 25), am.E_SHAPE),
     (dict(lse=4 * FAR), am.E_INVALID), (dict(loss=FAR + 8), am.E_INVALID), (dict(ws=2 * FAR), am.E_INVALID),

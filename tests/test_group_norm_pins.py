@@ -47,6 +47,7 @@ FAR = 1 << 32
     (dict(eps=float("nan")), am.E_INVALID), (dict(C=1 << 17, G=1), am.E_SHAPE),
     (dict(n=1 << 30, G=8), am.E_SHAPE), (dict(L=1 << 40), am.E_SHAPE),
     (dict(L=5000, ws=None), am.E_INVALID), (dict(L=5000, bytes=16), am.E_INVALID),
+    (dict(L=5000, ws=7 * FAR + 4), am.E_INVALID),        # not aligned
     (dict(Y=FAR + 32), am.E_INVALID),                    # partly over X
     (dict(mean=5 * FAR, rstd=5 * FAR), am.E_INVALID),    # two outputs in one place
     (dict(mean=2 * FAR), am.E_INVALID),                  # over Y

@@ -71,8 +71,10 @@ def call(**kw):
     (dict(layout=2), am.E_INVALID), (dict(batch=0), am.E_INVALID), (dict(heads=0), am.E_INVALID),
     (dict(T=-1), am.E_INVALID), (dict(dk=0), am.E_INVALID), (dict(dv=-3), am.E_INVALID),
     (dict(dk=129), am.E_SHAPE), (dict(dv=129), am.E_SHAPE), (dict(batch=1 << 11, heads=1 << 10), am.E_SHAPE),
+    (dict(heads=(1 << 16) + 1), am.E_SHAPE),
     (dict(T=1 << 31), am.E_SHAPE),
     (dict(T=5000, ws=None), am.E_INVALID), (dict(T=5000, bytes=100), am.E_INVALID),
+    (dict(T=5000, ws=(9 << 30) + 8), am.E_INVALID),  # not aligned
     (dict(Y=(1 << 20) + 64), am.E_INVALID),          # over Q
     (dict(Y=(3 << 20)), am.E_INVALID),               # over V
     (dict(W_T=(5 << 20) + 16), am.E_INVALID),        # W_T inside W0, but not W0 itself
