@@ -8,7 +8,8 @@
 //   dX  a = W (lanes d, rows across the contraction: read transposed from LDS), b = G
 //   dW  a = X, b = G, both across the contraction
 // An output tile has b's index in its lanes and a's, four at a time, in its registers.  bf16 inputs are
-// used as they are.  G is rounded without its weight: the label's entry, -1 + p, is the large one and in
+// used as they are.  Rows that are left out are left out of the products: the others' X is copied
+// together, and the kernels take their number from the device.  G is rounded without its weight: the label's entry, -1 + p, is the large one and in
 // bf16 nearly exact while p is small; dX's weight goes to the fp32 sums, and dW's to X, relative to the
 // largest one, so that equal weights round nothing.  fp32 inputs (and then G) as three bf16 planes, the six products of planes down to
 // 2^-16 of the leading one summed in fp32 (relative 2^-24, at the matrix cores' bf16 rate over six).
@@ -36,20 +37,23 @@ struct GemmArgs {
   int64_t pa, pb;          // elements from plane to plane
   int64_t na, nb;          // rows (or, across the contraction, columns) of a and b
   int64_t K;
+  const int* count;        // rows that count (OUT: K, else nb), or null: as given
   int ta, tb;              // tiles of a and b
   int splits;              // pieces of the contraction (ACC; else 1)
   // epilogues
   float2* part;            // LSE: [nb][parts]: (maximum, sum of exponentials)
   int parts;
   int part0;
-  const int64_t* labels;   // [nb]
+  const int64_t* labels;   // [rows of X]
   const float* lse;
+  const int* index;        // GRAD: [nb], b's rows in X
   int64_t v0, vocab;
   uint16_t* g;             // GRAD: [nb][ldg], planes of pg elements
   int64_t ldg, pg;
   int planes;
-  float* acc;              // ACC: [splits][nb][na]
-  int first, add;
+  float* acc;              // ACC: [splits][acc_rows][na]
+  int64_t acc_rows;
+  int add;
   const float* scale;      // OUT: one factor, or null
   void* out;               // [nb][ldo]
   int64_t ldo;
@@ -190,6 +194,14 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 
   // The workgroups of one XCD are neighbours, and share its L2: the tiles of one piece of the contraction
   // before the next piece's, eight tiles of b beside four of a at a time.
+  if (g.count) {
+    if constexpr (EPI == EPI_OUT) {
+      g.K = *g.count;
+    } else {
+      g.nb = *g.count;
+      g.tb = (int)((g.nb + TB - 1) / TB);
+    }
+  }
   const int tiles = g.ta * g.tb, total = tiles * g.splits;
   const int per = (total + 7) / 8;
   const int work = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -339,9 +351,10 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int64_t r = b0 + wb + 32 * j + col;
-      const int64_t y = r < g.nb ? g.labels[r] : -1;
-      const bool kept = y >= 0 && y < g.vocab;
-      const float l = kept ? g.lse[r] : 0.0f;
+      const int64_t row = r < g.nb ? g.index[r] : -1;
+      const bool kept = row >= 0;
+      const int64_t y = kept ? g.labels[row] : -1;
+      const float l = kept ? g.lse[row] : 0.0f;
       // the lane's label and the end of the vocabulary, counted from its first class
       const int64_t first = a0 + wa + 4 * hf;
       const int at = kept && y - g.v0 >= first && y - g.v0 < first + TA ? (int)(y - g.v0 - first) : -1;
@@ -395,7 +408,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
           if (c >= g.na) continue;
           float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           if constexpr (EPI == EPI_ACC) {
-            float4* p = (float4*)(g.acc + ((int64_t)split * g.nb + r) * g.lda + c);
+            float4* p = (float4*)(g.acc + ((int64_t)split * g.acc_rows + r) * g.lda + c);
             if (g.add) {
               const float4 o = *p;
               x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
@@ -413,52 +426,90 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   }
 }
 
-// The largest |dloss| of the rows that count (one workgroup), 1 without weights.
-__global__ __launch_bounds__(1024) void xe_largest(const float* dloss, const int64_t* labels, int64_t n, int64_t vocab,
-                                                   float* out) {
-  __shared__ float s[16];
+// The rows that count, those whose label is a class, in order (one workgroup): index [rows that count],
+// at [n] (a row's place among them, or -1), their number, and the largest |dloss| among them (1 without).
+__global__ __launch_bounds__(1024) void xe_rows(const int64_t* labels, const float* dloss, int64_t n, int64_t vocab,
+                                                int* index, int* at, int* count, float* largest) {
+  __shared__ int s[16];
+  __shared__ float sm[16];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int base = 0;
   float m = 0.0f;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) {
-    const float w = fabsf(dloss[i]);
-    if (labels[i] >= 0 && labels[i] < vocab) m = fmaxf(m, w <= 3.0e38f ? w : 0.0f);
+  for (int64_t i0 = 0; i0 < n; i0 += 1024) {
+    const int64_t i = i0 + threadIdx.x;
+    const int64_t y = i < n ? labels[i] : -1;
+    const bool kept = y >= 0 && y < vocab;
+    if (kept && dloss) {
+      const float w = fabsf(dloss[i]);
+      m = fmaxf(m, w <= 3.0e38f ? w : 0.0f);
+    }
+    const uint64_t mask = __ballot(kept);
+    __syncthreads();
+    if (lane == 0) s[wave] = __popcll(mask);
+    __syncthreads();
+    int before = base, all = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      before += k < wave ? s[k] : 0;
+      all += s[k];
+    }
+    const int place = before + __popcll(mask & ((1ull << lane) - 1));
+    if (i < n) at[i] = kept ? place : -1;
+    if (kept) index[place] = (int)i;
+    base += all;
   }
   for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = m;
+  if (lane == 0) sm[wave] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int k = 1; k < 16; ++k) m = fmaxf(m, s[k]);
-    *out = m > 0.0f ? m : 1.0f;
+    for (int k = 1; k < 16; ++k) m = fmaxf(m, sm[k]);
+    *count = base;
+    if (largest) *largest = m > 0.0f ? m : 1.0f;
   }
 }
 
-// Rows of an input as bf16 planes [planes][rows][dp], zero from column d on.  With labels, for dW: rows
-// that count times dloss / largest, and zeros for those whose label is no class (what they hold must
-// not reach the other rows' sums).
-__global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int dp, int planes, const int64_t* labels,
-                          int64_t vocab, const float* dloss, const float* largest, uint16_t* out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // a pair of columns
-  const int64_t per = dp / 2;
-  if (i >= rows * per) return;
+// Rows of an input as bf16 planes [planes][rows][dp], zero from column d on: all of them, or with `index`
+// those that count.  out_w: the same rows times dloss / largest.
+__global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int dp, int planes, const int* index,
+                          const int* count, const float* dloss, const float* largest, uint16_t* out, uint16_t* out_w) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // four columns
+  const int64_t per = dp / 4;
   const int64_t r = i / per;
-  const int c = (int)(i % per) * 2;
-  const bool kept = !labels || (labels[r] >= 0 && labels[r] < vocab);
-  float v0 = kept && c < d ? load_in(x, r * d + c, in_bf16) : 0.0f;
-  float v1 = kept && c + 1 < d ? load_in(x, r * d + c + 1, in_bf16) : 0.0f;
-  if (dloss && kept) {
-    const float w = dloss[r] / *largest;
-    v0 *= w, v1 *= w;
+  if (r >= (count ? *count : rows)) return;
+  const int c = (int)(i % per) * 4;
+  const int64_t row = index ? index[r] : r;
+  float v[4];
+  if (d % 4 == 0 && ((uintptr_t)x & 15) == 0 && c < d) {
+    if (in_bf16) {
+      const uint2 w = *(const uint2*)((const uint16_t*)x + row * d + c);
+      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+      const float4 w = *(const float4*)((const float*)x + row * d + c);
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = c + k < d ? load_in(x, row * d + c + k, in_bf16) : 0.0f;
   }
-  for (int n = 0; n < planes; ++n) {
-    const uint32_t w = cvt_pk_bf16(v0, v1);
-    *(uint32_t*)(out + (n * rows + r) * dp + c) = w;
-    v0 -= __uint_as_float(w << 16);
-    v1 -= __uint_as_float(w & 0xFFFF0000u);
+  auto put = [&](uint16_t* o, float a, float b, float c2, float d2) {
+    for (int n = 0; n < planes; ++n) {
+      const uint2 w = {cvt_pk_bf16(a, b), cvt_pk_bf16(c2, d2)};
+      *(uint2*)(o + (n * rows + r) * dp + c) = w;
+      a -= __uint_as_float(w.x << 16), b -= __uint_as_float(w.x & 0xFFFF0000u);
+      c2 -= __uint_as_float(w.y << 16), d2 -= __uint_as_float(w.y & 0xFFFF0000u);
+    }
+  };
+  put(out, v[0], v[1], v[2], v[3]);
+  if (out_w) {
+    const float w = dloss[row] / *largest;
+    put(out_w, v[0] * w, v[1] * w, v[2] * w, v[3] * w);
   }
 }
 
 // loss, lse of a row: a wave joins the tiles' maxima and sums, and takes the row's product with its
 // label's class.
-__global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, const void* X, const void* W, int in_bf16,
+__global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, const int* at, const void* X, const void* W, int in_bf16,
                                                int vec, int64_t n, int d, int64_t vocab, const int64_t* labels,
                                                float* loss, float* lse) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -469,7 +520,7 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
     if (lane == 0) loss[r] = 0.0f, lse[r] = 0.0f;
     return;
   }
-  const float2* p = part + r * parts;
+  const float2* p = part + (at ? at[r] : r) * parts;
   float m = -INFINITY, s = 0.0f;
   for (int i = lane; i < parts; i += 64) {
     const float2 q = p[i];
@@ -508,27 +559,26 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
 }
 
 // dX from the partial sums of the contraction's pieces, times the rows' weights: four columns a thread.
-__global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int64_t* labels, int64_t vocab,
-                       const float* dloss, void* out, int out_bf16, int vec) {
+__global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int* at, const float* dloss,
+                       void* out, int out_bf16, int vec) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / (dp / 4);
   const int c = (int)(i % (dp / 4)) * 4;
   if (r >= n || c >= d) return;
+  const int64_t place = at[r];
   float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < splits; ++s) {
-    const float4 a = *(const float4*)(acc + (s * n + r) * dp + c);
+  for (int s = 0; s < splits && place >= 0; ++s) {
+    const float4 a = *(const float4*)(acc + (s * n + place) * dp + c);
     v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
   }
-  const int64_t y = labels[r];
-  const bool kept = y >= 0 && y < vocab;
-  const float w = kept && dloss ? dloss[r] : 1.0f;
-  const float x[4] = {kept ? v.x * w : 0.0f, kept ? v.y * w : 0.0f, kept ? v.z * w : 0.0f, kept ? v.w * w : 0.0f};
-  const int64_t at = r * d + c;
-  if (vec && out_bf16) *(uint2*)((uint16_t*)out + at) = uint2{cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])};
-  else if (vec) *(float4*)((float*)out + at) = float4{x[0], x[1], x[2], x[3]};
+  const float w = place >= 0 && dloss ? dloss[r] : 1.0f;
+  const float x[4] = {v.x * w, v.y * w, v.z * w, v.w * w};
+  const int64_t o = r * d + c;
+  if (vec && out_bf16) *(uint2*)((uint16_t*)out + o) = uint2{cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])};
+  else if (vec) *(float4*)((float*)out + o) = float4{x[0], x[1], x[2], x[3]};
   else
     for (int k = 0; k < 4 && c + k < d; ++k) {
-      if (out_bf16) ((uint16_t*)out)[at + k] = (uint16_t)bf16_bits(x[k]);
-      else ((float*)out)[at + k] = x[k];
+      if (out_bf16) ((uint16_t*)out)[o + k] = (uint16_t)bf16_bits(x[k]);
+      else ((float*)out)[o + k] = x[k];
     }
 }
 
@@ -585,7 +635,6 @@ struct Plan {
   int64_t n, vocab, piece;      // classes of a piece
   int parts, splits;
   bool wide_x;                  // large tiles for dX
-  int64_t x_bytes, w_bytes, part_bytes, g_bytes, acc_bytes;
 };
 
 constexpr int64_t kPieceBytes = 256 << 20;  // of G: what the last-level cache holds
@@ -603,22 +652,62 @@ Plan plan_of(const CrossEntropy& s) {
   p.wide_x = wide_split(p.dp, s.n);
   const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.wide_x ? 256 : 128), 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.wide_x ? 256 : 512) / tiles, p.piece / 512));
-  p.x_bytes = align256(2 * p.planes * s.n * (int64_t)p.dp);
-  p.w_bytes = align256(2 * p.planes * s.vocab * (int64_t)p.dp);
-  p.part_bytes = align256(8 * s.n * (int64_t)p.parts);
-  p.g_bytes = align256(2 * p.planes * s.n * p.piece);
-  p.acc_bytes = align256(4 * (int64_t)p.splits * s.n * p.dp);
   return p;
 }
 
 bool direct(const void* p, const CrossEntropy& s) { return s.bf16 && s.d % 8 == 0 && ((uintptr_t)p & 15) == 0; }
 
-atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int64_t* labels,
-                          const float* dloss, const float* largest, uint16_t* out, hipStream_t st) {
-  const int64_t blocks = (rows * (p.dp / 2) + 255) / 256;
+// What a call finds in its workspace, one behind the other.
+struct Space {
+  int *index, *at, *count;
+  float* largest;
+  uint16_t *x, *xw, *w, *g;
+  float* acc;
+  float2* part;
+  int64_t bytes;
+};
+Space space_of(void* p, const CrossEntropy& s, const Plan& l, bool backward) {
+  Space w = {};
+  char* at = (char*)p;
+  auto take = [&](int64_t bytes) {
+    char* r = at;
+    at += align256(bytes);
+    return r;
+  };
+  const int64_t rows = 2 * l.planes * s.n * (int64_t)l.dp;
+  w.index = (int*)take(4 * s.n), w.at = (int*)take(4 * s.n);
+  w.count = (int*)take(8), w.largest = (float*)(w.count + 1);
+  w.x = (uint16_t*)take(rows);
+  w.w = (uint16_t*)take(2 * l.planes * s.vocab * (int64_t)l.dp);
+  if (backward) {
+    w.xw = (uint16_t*)take(rows);
+    w.g = (uint16_t*)take(2 * l.planes * s.n * l.piece);
+    w.acc = (float*)take(4 * (int64_t)l.splits * s.n * l.dp);
+  } else {
+    w.part = (float2*)take(8 * s.n * (int64_t)l.parts);
+  }
+  w.bytes = at - (char*)p;
+  return w;
+}
+
+// Forward calls of so many operations leave out the rows that do not count: finding and copying the others
+// takes 10 us, which the products of a tenth of the rows outweigh from here on (1.1 PFLOP/s).
+constexpr double kGatherFrom = 2e11;
+
+atlasmem_status rows_that_count(const CrossEntropy& s, const Space& w, const int64_t* labels, const float* dloss,
+                                hipStream_t st) {
+  xe_rows<<<1, 1024, 0, st>>>(labels, dloss, s.n, s.vocab, w.index, w.at, w.count, w.largest);
+  AM_LAUNCH_CHECK();
+  return ATLASMEM_OK;
+}
+
+atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int* index,
+                          const int* count, const float* dloss, const float* largest, uint16_t* out, uint16_t* out_w,
+                          hipStream_t st) {
+  const int64_t blocks = (rows * (p.dp / 4) + 255) / 256;
   if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
-  xe_planes<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, p.planes, labels, s.vocab, dloss,
-                                            largest, out);
+  xe_planes<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, p.planes, index, count, dloss, largest, out,
+                                              out_w);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -626,34 +715,36 @@ atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, i
 }  // namespace
 
 int64_t cross_entropy_workspace_bytes(const CrossEntropy& s, bool backward) {
-  const Plan p = plan_of(s);
-  const int64_t inputs = p.x_bytes + p.w_bytes;
-  return backward ? inputs + p.x_bytes + p.g_bytes + p.acc_bytes + 256 : inputs + p.part_bytes;
+  return space_of(nullptr, s, plan_of(s), backward).bytes;
 }
 
 atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* W, const int64_t* labels, float* loss,
                               float* lse, void* workspace, hipStream_t st) {
   const Plan p = plan_of(s);
-  char* ws = (char*)workspace;
-  uint16_t* xp = (uint16_t*)ws;
-  uint16_t* wp = (uint16_t*)(ws + p.x_bytes);
-  GemmArgs g = {};
-  g.part = (float2*)(ws + p.x_bytes + p.w_bytes);
+  const Space ws = space_of(workspace, s, p, false);
+  const bool gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : kProducts) >= kGatherFrom;
   atlasmem_status e = ATLASMEM_OK;
-  if (!direct(X, s)) e = planes_of(X, s, p, s.n, nullptr, nullptr, nullptr, xp, st);
-  if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, wp, st);
+  if (gather) e = rows_that_count(s, ws, labels, nullptr, st);
+  const int *index = gather ? ws.index : nullptr, *count = gather ? ws.count : nullptr;
+  if (e == ATLASMEM_OK && (gather || !direct(X, s)))
+    e = planes_of(X, s, p, s.n, index, count, nullptr, nullptr, ws.x, nullptr, st);
+  if (e == ATLASMEM_OK && !direct(W, s))
+    e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
   if (e != ATLASMEM_OK) return e;
-  g.a = direct(W, s) ? (const uint16_t*)W : wp;
-  g.b = direct(X, s) ? (const uint16_t*)X : xp;
+  GemmArgs g = {};
+  g.part = ws.part;
+  g.a = direct(W, s) ? (const uint16_t*)W : ws.w;
+  g.b = gather || !direct(X, s) ? ws.x : (const uint16_t*)X;
   g.lda = g.ldb = p.dp;
   g.pa = s.vocab * p.dp, g.pb = s.n * p.dp;
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
+  g.count = count;
   const bool w = wide(s.vocab, s.n);
   g.parts = (int)((s.vocab + (w ? 255 : 127)) / (w ? 256 : 128));
   e = gemm<false, false, EPI_LSE>(g, !s.bf16, w, st);
   if (e != ATLASMEM_OK) return e;
-  xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, X, W, s.bf16, direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss,
-                                                     lse);
+  xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, gather ? ws.at : nullptr, X, W, s.bf16,
+                                                     direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss, lse);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -670,51 +761,44 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     return ATLASMEM_OK;
   }
   const Plan p = plan_of(s);
-  char* ws = (char*)workspace;
-  uint16_t* xp = (uint16_t*)ws;
-  uint16_t* wp = (uint16_t*)(ws + p.x_bytes);
-  uint16_t* xw = (uint16_t*)(ws + p.x_bytes + p.w_bytes);  // weighted, for dW
-  uint16_t* gp = (uint16_t*)(ws + 2 * p.x_bytes + p.w_bytes);
-  float* acc = (float*)(ws + 2 * p.x_bytes + p.w_bytes + p.g_bytes);
-  float* largest = (float*)(ws + 2 * p.x_bytes + p.w_bytes + p.g_bytes + p.acc_bytes);
-  atlasmem_status e = ATLASMEM_OK;
-  if (dW) {
-    if (dloss) {
-      xe_largest<<<1, 1024, 0, st>>>(dloss, labels, s.n, s.vocab, largest);
-      AM_LAUNCH_CHECK();
-    }
-    e = planes_of(X, s, p, s.n, labels, dloss, largest, xw, st);
-  }
-  if (e == ATLASMEM_OK && !direct(X, s)) e = planes_of(X, s, p, s.n, nullptr, nullptr, nullptr, xp, st);
-  if (e == ATLASMEM_OK && !direct(W, s)) e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, wp, st);
+  const Space ws = space_of(workspace, s, p, true);
+  const bool weighted = dW && dloss;
+  atlasmem_status e = rows_that_count(s, ws, labels, dloss, st);
+  if (e == ATLASMEM_OK)
+    e = planes_of(X, s, p, s.n, ws.index, ws.count, dloss, ws.largest, ws.x, weighted ? ws.xw : nullptr, st);
+  if (e == ATLASMEM_OK && !direct(W, s))
+    e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
   if (e != ATLASMEM_OK) return e;
-  const uint16_t* wa = direct(W, s) ? (const uint16_t*)W : wp;
+  const uint16_t* wa = direct(W, s) ? (const uint16_t*)W : ws.w;
   for (int64_t v0 = 0; v0 < s.vocab; v0 += p.piece) {
     const int64_t nv = std::min(p.piece, s.vocab - v0), ldg = up(nv, 64);
-    GemmArgs g = {};
     // G of the piece
-    g.a = wa + v0 * p.dp, g.b = direct(X, s) ? (const uint16_t*)X : xp;
+    GemmArgs g = {};
+    g.count = ws.count;
+    g.a = wa + v0 * p.dp, g.b = ws.x;
     g.lda = g.ldb = p.dp;
     g.pa = s.vocab * p.dp, g.pb = s.n * p.dp;
     g.na = nv, g.nb = s.n, g.K = p.dp;
-    g.labels = labels, g.lse = lse, g.v0 = v0, g.vocab = s.vocab;
-    g.g = gp, g.ldg = ldg, g.pg = s.n * ldg, g.planes = p.planes;
+    g.labels = labels, g.lse = lse, g.index = ws.index, g.v0 = v0;
+    g.g = ws.g, g.ldg = ldg, g.pg = s.n * ldg, g.planes = p.planes;
     e = gemm<false, false, EPI_GRAD>(g, !s.bf16, wide(nv, s.n), st);
     if (e != ATLASMEM_OK) return e;
     if (dX) {
       GemmArgs x = {};
+      x.count = ws.count;
       x.a = wa + v0 * p.dp, x.lda = p.dp, x.pa = s.vocab * p.dp, x.na = p.dp;
-      x.b = gp, x.ldb = ldg, x.pb = s.n * ldg, x.nb = s.n;
+      x.b = ws.g, x.ldb = ldg, x.pb = s.n * ldg, x.nb = s.n;
       x.K = nv;
-      x.splits = p.splits, x.acc = acc, x.add = v0 > 0;
+      x.splits = p.splits, x.acc = ws.acc, x.acc_rows = s.n, x.add = v0 > 0;
       e = gemm<true, false, EPI_ACC>(x, !s.bf16, p.wide_x, st);
       if (e != ATLASMEM_OK) return e;
     }
     if (dW) {
       GemmArgs x = {};
-      x.a = xw, x.lda = p.dp, x.pa = s.n * p.dp, x.na = p.dp;
-      x.scale = dloss ? largest : nullptr;
-      x.b = gp, x.ldb = ldg, x.pb = s.n * ldg, x.nb = nv;
+      x.count = ws.count;
+      x.a = weighted ? ws.xw : ws.x, x.lda = p.dp, x.pa = s.n * p.dp, x.na = p.dp;
+      x.scale = weighted ? ws.largest : nullptr;
+      x.b = ws.g, x.ldb = ldg, x.pb = s.n * ldg, x.nb = nv;
       x.K = s.n;
       x.out = (char*)dW + v0 * s.d * (s.bf16 ? 2 : 4), x.ldo = s.d, x.out_bf16 = s.bf16;
       e = gemm<true, true, EPI_OUT>(x, !s.bf16, wide(p.dp, nv), st);
@@ -723,8 +807,8 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   }
   if (dX) {
     const int vec = s.d % 4 == 0 && ((uintptr_t)dX & 15) == 0;
-    xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(acc, p.splits, s.n, s.d, p.dp, labels, s.vocab,
-                                                                       dloss, dX, s.bf16, vec);
+    xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(ws.acc, p.splits, s.n, s.d, p.dp, ws.at, dloss, dX,
+                                                                       s.bf16, vec);
     AM_LAUNCH_CHECK();
   }
   return ATLASMEM_OK;
