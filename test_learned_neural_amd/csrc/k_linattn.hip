@@ -202,21 +202,25 @@ __device__ __forceinline__ Op<NP> col_op(const uint16_t* s, int at, int c0, int 
   return o;
 }
 
-// DX: 32-column tiles of x and y; NW: waves, each with 32 columns of z; OUT: outputs (else the
-// segment's own state alone); DEC: the tangent too.
-template <int DX, int NW, bool F32, bool VEC, bool OUT, bool DEC>
-__global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
+// DX: 32-column tiles of x and y; NW: waves side by side, each with 32 columns of z; XS: waves that share
+// those columns, each with a part of x.  Everything is linear in the parts of x (scores, state, outputs),
+// so a wave carries its own part through and only the outputs are added, a chunk later, through LDS.
+// VEC: rows are whole, aligned pieces; OUT: outputs (else the segment's own state alone); DEC: the tangent.
+template <int DX, int NW, int XS, bool F32, bool VEC, bool OUT, bool DEC>
+__global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
   constexpr int NP = F32 ? 3 : 1;                    // planes of an input
   constexpr int NC = F32 || DEC ? 3 : 2;             // planes of a computed operand of the outputs
   constexpr int WX = DX * 32, WZ = NW * 32;
-  constexpr int NT = NW * 64;
+  constexpr int NT = NW * XS * 64, DW = DX / XS;     // threads; x tiles of a wave
   constexpr int GX = kC * DX * 4 / NT, GZ = kC * NW * 4 / NT;  // 8-element groups per thread
   // 16 bytes between the tiles: at whole multiples of 512 the compiler joins a read of x with one of y,
   // and takes the results apart again with moves
   constexpr int TX = NP * kC * WX + 8, TZ = NP * kC * WZ + 8, kBuf = (OUT ? 2 : 1) * TX + TZ;
   constexpr int kBufs = F32 ? 1 : 2;
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
-  float* pw = (float*)(sm + kBufs * kBuf);           // lambda^0 .. lambda^32
+  float* parts = (float*)(sm + kBufs * kBuf);        // outputs of the other parts of x: two chunks
+  constexpr int kParts = OUT ? (XS - 1) * NW * 1024 : 0;
+  float* pw = parts + 2 * kParts;                    // lambda^0 .. lambda^32
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hf = lane >> 5, col = lane & 31;
   const int nrun = OUT ? a.nseg : a.nseg - 1;        // the last segment's own sum starts nothing
@@ -224,7 +228,8 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   const int m = blockIdx.x / nrun;
   const int b = m / a.H, h = m % a.H;
   const int z0 = blockIdx.y * WZ;
-  const int zc = z0 + wave * 32;
+  const int zw = wave % NW, xs = __builtin_amdgcn_readfirstlane(wave / NW);
+  const int zc = z0 + zw * 32;
   const int64_t len = a.len ? min((int64_t)max(a.len[b], 0), a.T) : a.T;
   const int64_t p0 = (int64_t)seg * a.lseg, p1 = min(p0 + a.lseg, a.T);
   const float g = a.log_decay[h];
@@ -236,10 +241,10 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   auto first_at = [&](int64_t p, int r) { return a.rev ? len - p - r : p; };
   const int64_t atx = b * a.x.sb + h * a.x.sh, atz = b * a.z.sb + h * a.z.sh;  // y lies like x, o and t like z
 
-  // state tiles: column zc + col, rows 32 xt + 8 q + 4 hf + u
-  f32x16 S[DX], St[DEC ? DX : 1];
+  // state tiles: column zc + col, rows 32 (xs DW + xt) + 8 q + 4 hf + u
+  f32x16 S[DW], St[DEC ? DW : 1];
 #pragma unroll
-  for (int xt = 0; xt < DX; ++xt) {
+  for (int xt = 0; xt < DW; ++xt) {
     S[xt] = zero16();
     if constexpr (DEC) St[xt] = zero16();
   }
@@ -249,10 +254,10 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
       if (!src || zc + col >= a.z.w) return;
       const float* p = src + slot * a.P + (int64_t)(zc + col) * a.ssz;
 #pragma unroll
-      for (int xt = 0; xt < DX; ++xt)
+      for (int xt = 0; xt < DW; ++xt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
+          const int x = 32 * (xs * DW + xt) + 8 * (i >> 2) + 4 * hf + (i & 3);
           if (x < a.x.w) D[xt][i] = p[(int64_t)x * a.ssx];
         }
     };
@@ -320,13 +325,70 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     }
   };
   weights(kC);
-  const int rat = row_at<WX>(lane), cat = col_at<WX>(lane), zat = col_at<WZ>(lane);
+  const int part = 32 * DW * xs;                      // the wave's first x: bits of their own in an offset
+  const int rat = row_at<WX>(lane) ^ part, cat = col_at<WX>(lane) ^ part, zat = col_at<WZ>(lane);
   const int ci = col - 4 * hf;                        // i >= j: ci >= 8 (n / 4) + n % 4
   uint32_t oo[OUT ? 4 : 1];                           // the lane's output pieces
   if constexpr (OUT) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) oo[q] = row_off(a.o, col, zc + 8 * q + 4 * hf, EL, a.rev);
   }
+
+  // The outputs of a chunk at p with r rows in the sequence: the lane's position, four consecutive columns a
+  // register group; zeros behind the sequence.
+  auto put_piece = [&](const ChunkRows& c, uint32_t off, const float* v, int left) {
+    const uint32_t o = off - c.adj;
+    if constexpr (F32) {
+      if constexpr (VEC) {
+        buf_st4(c.r, (int)o, 0, float4{v[0], v[1], v[2], v[3]});
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) buf_st(c.r, n < left ? (int)(o + 4 * n) : -1, 0, v[n]);
+      }
+    } else {
+      const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+      if constexpr (VEC) {
+        buf_st8(c.r, (int)o, 0, w);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) buf_st_u16(c.r, n < left ? (int)(o + 2 * n) : -1, 0, (n & 2 ? w.y : w.x) >> (16 * (n & 1)));
+      }
+    }
+  };
+  auto put_rows = [&](const f32x16& V, int64_t p, int r) {
+    const ChunkRows co = chunk_rows(a.o, atz, first_at(p, r), r, EL, a.rev);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float v[4] = {V[4 * q], V[4 * q + 1], V[4 * q + 2], V[4 * q + 3]};
+      put_piece(co, oo[q], v, a.z.w - zc - 8 * q - 4 * hf);
+    }
+    if (r < kC) {
+      const int64_t behind = p + r;
+      const ChunkRows ce = chunk_rows(a.o, atz, behind, (int)min((int64_t)(kC - r), p1 - behind), EL, 0);
+      const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = zc + 8 * q + 4 * hf;
+        put_piece(ce, row_off(a.o, col, c, EL, 0), none, a.z.w - c);
+      }
+    }
+  };
+  // XS > 1: the first part's outputs of the last chunk, waiting for the others'
+  f32x16 Ow = zero16();
+  int64_t pwait = -1;
+  int rwait = 0;
+  bool odd = false;                                   // which half of `parts` this chunk writes
+  auto add_parts = [&](int half) {
+    if (xs || pwait < 0) return;
+#pragma unroll
+    for (int t = 0; t < XS - 1; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 v = *(const float4*)(parts + half * kParts + q * 256 * NW * (XS - 1) + ((t * NW + zw) * 64 + lane) * 4);
+        Ow[4 * q] += v.x, Ow[4 * q + 1] += v.y, Ow[4 * q + 2] += v.z, Ow[4 * q + 3] += v.w;
+      }
+    put_rows(Ow, pwait, rwait);
+  };
 
   // One chunk; FULL: all its positions are inside the sequence (one block of code without branches, which
   // the scheduler can fill the waits of each part of with the others).
@@ -339,6 +401,10 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     stage(sy);
     __syncthreads();
     fetch(p + kC);
+    if constexpr (OUT && XS > 1) {
+      odd = !odd;
+      add_parts(odd ? 0 : 1);
+    }
     if constexpr (kBufs == 2) buf ^= 1;
     const int r = FULL ? kC : rows_at(p);
 
@@ -346,7 +412,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     if constexpr (OUT) {
       f32x16 O = zero16(), Ot = zero16(), P = zero16();
 #pragma unroll
-      for (int k = 0; k < 2 * DX; ++k) {
+      for (int k = 0; k < 2 * DW; ++k) {
         const Op<NP> x = row_op<WX, NP>(sx, rat, k), y = row_op<WX, NP>(sy, rat, k);
         P = mm(y, x, P);
         Op<NC> s;
@@ -370,7 +436,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        zo[k] = col_op<WZ, NP>(sz, zat, wave * 32, k);
+        zo[k] = col_op<WZ, NP>(sz, zat, zw * 32, k);
         float v[8];
 #pragma unroll
         for (int n = 0; n < 8; ++n) v[n] = P[8 * k + n];
@@ -384,31 +450,15 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
           Ot = mm(zo[k], s, Ot);
         }
       }
-      // rows: the lane's position, four consecutive columns a register group
-      const ChunkRows co = chunk_rows(a.o, atz, first_at(p, r), r, EL, a.rev);
-      auto put_piece = [&](const ChunkRows& c, uint32_t off, const float* v, int left) {
-        const uint32_t o = off - c.adj;
-        if constexpr (F32) {
-          if constexpr (VEC) {
-            buf_st4(c.r, (int)o, 0, float4{v[0], v[1], v[2], v[3]});
-          } else {
+      if constexpr (XS == 1) {
+        put_rows(O, p, r);
+      } else if (xs) {
+        float* d = parts + (odd ? kParts : 0) + (((xs - 1) * NW + zw) * 64 + lane) * 4;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) buf_st(c.r, n < left ? (int)(o + 4 * n) : -1, 0, v[n]);
-          }
-        } else {
-          const uint2 w = {cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
-          if constexpr (VEC) {
-            buf_st8(c.r, (int)o, 0, w);
-          } else {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) buf_st_u16(c.r, n < left ? (int)(o + 2 * n) : -1, 0, (n & 2 ? w.y : w.x) >> (16 * (n & 1)));
-          }
-        }
-      };
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v[4] = {O[4 * q], O[4 * q + 1], O[4 * q + 2], O[4 * q + 3]};
-        put_piece(co, oo[q], v, a.z.w - zc - 8 * q - 4 * hf);
+        for (int q = 0; q < 4; ++q)
+          *(float4*)(d + q * 256 * NW * (XS - 1)) = float4{O[4 * q], O[4 * q + 1], O[4 * q + 2], O[4 * q + 3]};
+      } else {
+        Ow = O, pwait = p, rwait = r;
       }
       if constexpr (DEC) {
         const ChunkRows ct = chunk_rows(a.t, atz, first_at(p, r), r, EL, a.rev);
@@ -422,26 +472,16 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
         }
         dec += part;
       }
-      if constexpr (!FULL) {  // rows of the segment behind the sequence
-        const int64_t behind = p + r;
-        const ChunkRows ce = chunk_rows(a.o, atz, behind, (int)min((int64_t)(kC - r), p1 - behind), EL, 0);
-        const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = zc + 8 * q + 4 * hf;
-          put_piece(ce, row_off(a.o, col, c, EL, 0), none, a.z.w - c);
-        }
-      }
     } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) zo[k] = col_op<WZ, NP>(sz, zat, wave * 32, k);
+      for (int k = 0; k < 2; ++k) zo[k] = col_op<WZ, NP>(sz, zat, zw * 32, k);
     }
 
     // state: column operands of y times the weighted z (three planes: the state is an fp32 result)
     if constexpr (!FULL) weights(r);
     const float keep = pw[r];
 #pragma unroll
-    for (int xt = 0; xt < DX; ++xt)
+    for (int xt = 0; xt < DW; ++xt)
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
         if constexpr (DEC) St[xt][n] = keep * (St[xt][n] + (float)r * S[xt][n]);
@@ -468,7 +508,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
         split8(v, st);
       }
 #pragma unroll
-      for (int xt = 0; xt < DX; ++xt) {
+      for (int xt = 0; xt < DW; ++xt) {
         const Op<NP> yo = col_op<WX, NP>(sy, cat, 32 * xt, k);
         S[xt] = mm(yo, s, S[xt]);
         if constexpr (DEC) St[xt] = mm(yo, st, St[xt]);
@@ -478,16 +518,20 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
   int64_t p = p0;
   for (; p + kC <= min(len, p1); p += kC) chunk(std::true_type{}, p);
   for (; p < p1; p += kC) chunk(std::false_type{}, p);
+  if constexpr (OUT && XS > 1) {
+    __syncthreads();
+    add_parts(odd ? 1 : 0);
+  }
 
   // the state out: C-layout tiles to the caller's order
   auto put = [&](const f32x16* V, float* dst) {
     if (zc + col >= a.z.w) return;
     float* o = dst + (int64_t)(zc + col) * a.ssz;
 #pragma unroll
-    for (int xt = 0; xt < DX; ++xt)
+    for (int xt = 0; xt < DW; ++xt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
+        const int x = 32 * (xs * DW + xt) + 8 * (i >> 2) + 4 * hf + (i & 3);
         if (x < a.x.w) o[(int64_t)x * a.ssx] = V[xt][i];
       }
   };
@@ -498,10 +542,10 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
         if (a.adj && zc + col < a.z.w) {
           const float* q = a.adj + (int64_t)m * a.P + (int64_t)(zc + col) * a.ssz;
 #pragma unroll
-          for (int xt = 0; xt < DX; ++xt)
+          for (int xt = 0; xt < DW; ++xt)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int x = 32 * xt + 8 * (i >> 2) + 4 * hf + (i & 3);
+              const int x = 32 * (xs * DW + xt) + 8 * (i >> 2) + 4 * hf + (i & 3);
               if (x < a.x.w) dec += (double)St[xt][i] * q[(int64_t)x * a.ssx];
             }
         }
@@ -510,7 +554,7 @@ __global__ __launch_bounds__(NW * 64) void la_chunk(LaArgs a) {
     if constexpr (DEC) {
 #pragma unroll
       for (int s = 32; s; s >>= 1) dec += __shfl_xor(dec, s);
-      if (lane == 0) a.dec[(slot * gridDim.y + blockIdx.y) * NW + wave] = dec;
+      if (lane == 0) a.dec[(slot * gridDim.y + blockIdx.y) * (NW * XS) + wave] = dec;
     }
   } else {
     put(S, a.u + (slot + 1) * a.P);
@@ -664,17 +708,22 @@ LaRows rows_of(const void* p, const LinAttn& s, int w) {
 
 int tiles(int w) { return w <= 64 ? 2 : 4; }
 int waves(int w) { return w <= 64 ? 2 : 4; }
+// A wide x over a narrow z: two waves share a column tile, so that four fill a CU's SIMDs and keep under
+// 256 registers (64 memories, 4096 tokens, 128 over 64: 60 us against 71); with the tangent they need
+// more all the same, and are faster alone (177 us against 226).
+constexpr int parts_of_x(int dx, int nw, bool tangent) { return dx == 4 && nw == 2 && !tangent ? 2 : 1; }
 
-template <int DX, int NW, bool F32, bool VEC, bool OUT, bool DEC>
+template <int DX, int NW, int XS, bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   constexpr int NP = F32 ? 3 : 1;
-  constexpr int lds = (F32 ? 1 : 2) * 2 * (kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 24) + 4 * (kC + 4);
-  auto kern = la_chunk<DX, NW, F32, VEC, OUT, DEC>;
+  constexpr int lds = (F32 ? 1 : 2) * 2 * (kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 24) + 4 * (kC + 4) +
+                      (OUT ? 8 * (XS - 1) * NW * 1024 : 0);
+  auto kern = la_chunk<DX, NW, XS, F32, VEC, OUT, DEC>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
     return ATLASMEM_E_DEVICE;
   const dim3 grid((unsigned)blocks, (unsigned)((a.z.w + NW * 32 - 1) / (NW * 32)));
-  kern<<<grid, NW * 64, lds, st>>>(a);
+  kern<<<grid, NW * XS * 64, lds, st>>>(a);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -683,10 +732,10 @@ template <bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_pick(const LaArgs& a, int64_t blocks, hipStream_t st) {
   const int dx = tiles(a.x.w), nw = waves(a.z.w);
   if (dx == 2)
-    return nw == 2 ? chunk_launch<2, 2, F32, VEC, OUT, DEC>(a, blocks, st)
-                   : chunk_launch<2, 4, F32, VEC, OUT, DEC>(a, blocks, st);
-  return nw == 2 ? chunk_launch<4, 2, F32, VEC, OUT, DEC>(a, blocks, st)
-                 : chunk_launch<4, 4, F32, VEC, OUT, DEC>(a, blocks, st);
+    return nw == 2 ? chunk_launch<2, 2, 1, F32, VEC, OUT, DEC>(a, blocks, st)
+                   : chunk_launch<2, 4, 1, F32, VEC, OUT, DEC>(a, blocks, st);
+  return nw == 2 ? chunk_launch<4, 2, parts_of_x(4, 2, OUT && DEC), F32, VEC, OUT, DEC>(a, blocks, st)
+                 : chunk_launch<4, 4, 1, F32, VEC, OUT, DEC>(a, blocks, st);
 }
 
 template <bool OUT>
@@ -808,7 +857,8 @@ atlasmem_status linear_attention_backward(const LinAttn& s, const void* Q, const
   e = chunk_run<true>(a, s.bf16, want, M, st);
   if (e != ATLASMEM_OK) return e;
   if (want) {
-    const int nw = waves(s.dk), per = a.nseg * nw * ((s.dk + nw * 32 - 1) / (nw * 32));
+    const int nw = waves(s.dk);
+    const int per = a.nseg * nw * parts_of_x(tiles(s.dv), nw, true) * ((s.dk + nw * 32 - 1) / (nw * 32));
     la_decay_sum<<<s.H, 256, 0, st>>>(dec, s.B, s.H, per, dlog_decay);
     AM_LAUNCH_CHECK();
   }
