@@ -435,7 +435,8 @@ atlasmem_status atlasmem_gates(const void* U, int64_t B, int64_t T, int32_t d_mo
  *   workspace: atlasmem_linear_attention_workspace_bytes(..., backward = 0) bytes, 16-byte aligned
  *         (NULL where that is 0)
  * bf16 inputs enter the products as they are, fp32 ones as three bf16 planes (24 bits); states and
- * sums are fp32, Y is rounded once.  Errors: E_INVALID for bad sizes, enums, null or overlapping
+ * sums are fp32, Y is rounded once.  Values should be finite: in the chunks a NaN or infinity of V
+ * reaches, besides the tokens behind it, the up to 31 before it in its chunk (zeros times it).  Errors: E_INVALID for bad sizes, enums, null or overlapping
  * pointers, a short workspace; E_SHAPE beyond the limits (heads <= 65536, batch * heads <= 2^20).
  * The workspace function returns -1 for sizes that the calls refuse. */
 int64_t atlasmem_linear_attention_workspace_bytes(int32_t dtype, int32_t batch, int32_t heads, int64_t T,
@@ -496,7 +497,8 @@ atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int3
 /* Softmax cross entropy of n rows over `vocab` classes, the outer loss of a model whose last product is
  * z = X W^T, without keeping the logits z:
  *   lse_i = log sum_v exp(z_iv),   loss_i = lse_i - z_i,label_i
- *   X: [n, d], W: [vocab, d] of `dtype`; d <= 16384, n and vocab <= 2^24
+ *   X: [n, d], W: [vocab, d] of `dtype`; d <= 16384, n and vocab <= 2^24, n * d and vocab * d <= 2^33,
+ *         n * vocab <= 2^38
  *   labels: int64 [n]; a row whose label is no class (negative, or >= vocab) is left out: its loss, lse
  *         and gradient are zero, whatever its X holds
  *   loss, lse: fp32 [n]

@@ -316,72 +316,79 @@ __global__ __launch_bounds__(256) void gn_moments(GnArgs a) {
   constexpr int B = 4;
   __shared__ Mom sm[256];
   const Lanes<V> w(a);
-  const int64_t smp = blockIdx.x / a.splits;
-  const int64_t l0 = (blockIdx.x % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
-  Mom m = {0.0f, 0.0f, 0.0f};
-  if (w.on) {
-    const int64_t base = smp * a.L * a.C + (int64_t)w.cv * V;
-    for (int64_t l = l0 + w.rr; l < l1; l += (int64_t)w.rt * B) {
-      float v[B][V];
-      int cnt = 0;
-      float s = 0.0f;
+  for (int64_t blk = blockIdx.x; blk < a.n * a.splits; blk += gridDim.x) {
+    const int64_t smp = blk / a.splits;
+    const int64_t l0 = (blk % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
+    Mom m = {0.0f, 0.0f, 0.0f};
+    if (w.on) {
+      const int64_t base = smp * a.L * a.C + (int64_t)w.cv * V;
+      for (int64_t l = l0 + w.rr; l < l1; l += (int64_t)w.rt * B) {
+        float v[B][V];
+        int cnt = 0;
+        float s = 0.0f;
 #pragma unroll
-      for (int k = 0; k < B; ++k)
-        if (l + k * w.rt < l1) {
-          ld<F32, V>(a.x, base + (l + k * w.rt) * a.C, v[k]);
-          ++cnt;
-        } else {
+        for (int k = 0; k < B; ++k)
+          if (l + k * w.rt < l1) {
+            ld<F32, V>(a.x, base + (l + k * w.rt) * a.C, v[k]);
+            ++cnt;
+          } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
-        }
+            for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
+          }
 #pragma unroll
-      for (int k = 0; k < B; ++k)
+        for (int k = 0; k < B; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += v[k][i];
-      Mom b = {(float)(cnt * V), 0.0f, 0.0f};
-      b.mean = s / b.n;
+          for (int i = 0; i < V; ++i) s += v[k][i];
+        Mom b = {(float)(cnt * V), 0.0f, 0.0f};
+        b.mean = s / b.n;
 #pragma unroll
-      for (int k = 0; k < B; ++k)
-        if (k < cnt) {
+        for (int k = 0; k < B; ++k)
+          if (k < cnt) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) b.m2 += (v[k][i] - b.mean) * (v[k][i] - b.mean);
-        }
-      m = join(m, b);
+            for (int i = 0; i < V; ++i) b.m2 += (v[k][i] - b.mean) * (v[k][i] - b.mean);
+          }
+        m = join(m, b);
+      }
     }
-  }
-  if (w.rt > 1) {
-    sm[threadIdx.x] = m;
+    if (w.rt > 1) {
+      sm[threadIdx.x] = m;
+      __syncthreads();
+      if (w.on && w.rr == 0)
+        for (int k = 1; k < w.rt; ++k) m = join(m, sm[threadIdx.x + k * (a.C / V)]);
+    }
+    if (w.on && w.rr == 0) {
+      float* p = a.part + (blk * (a.C / V) + w.cv) * 2;
+      p[0] = m.mean;
+      p[1] = m.m2;
+    }
     __syncthreads();
-    if (w.on && w.rr == 0)
-      for (int k = 1; k < w.rt; ++k) m = join(m, sm[threadIdx.x + k * (a.C / V)]);
-  }
-  if (w.on && w.rr == 0) {
-    float* p = a.part + ((int64_t)blockIdx.x * (a.C / V) + w.cv) * 2;
-    p[0] = m.mean;
-    p[1] = m.m2;
   }
 }
 
 // mean, rstd of a (sample, group): one workgroup.
 template <int V>
 __global__ __launch_bounds__(256) void gn_stats(GnArgs a, float* mean, float* rstd) {
-  const int64_t smp = blockIdx.x / a.G;
-  const int g = blockIdx.x % a.G, per = a.c / V;
-  Mom m = {0.0f, 0.0f, 0.0f};
   __shared__ Mom sm[4];
-  for (int64_t i = threadIdx.x; i < (int64_t)a.splits * per; i += 256) {
-    const int sp = (int)(i / per), cv = g * per + (int)(i % per);
-    const float cnt = (float)(min(a.span, a.L - sp * a.span) * V);
-    const float* p = a.part + ((smp * a.splits + sp) * (a.C / V) + cv) * 2;
-    m = join(m, Mom{cnt, p[0], p[1]});
-  }
-  for (int s = 32; s; s >>= 1) m = join(m, Mom{__shfl_xor(m.n, s), __shfl_xor(m.mean, s), __shfl_xor(m.m2, s)});
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < 4; ++k) m = join(m, sm[k]);
-    mean[blockIdx.x] = m.mean;
-    rstd[blockIdx.x] = 1.0f / sqrtf(m.m2 / m.n + a.eps);
+  const int per = a.c / V;
+  for (int64_t grp = blockIdx.x; grp < a.n * a.G; grp += gridDim.x) {
+    const int64_t smp = grp / a.G;
+    const int g = (int)(grp % a.G);
+    Mom m = {0.0f, 0.0f, 0.0f};
+    for (int64_t i = threadIdx.x; i < (int64_t)a.splits * per; i += 256) {
+      const int sp = (int)(i / per), cv = g * per + (int)(i % per);
+      const float cnt = (float)(min(a.span, a.L - sp * a.span) * V);
+      const float* p = a.part + ((smp * a.splits + sp) * (a.C / V) + cv) * 2;
+      m = join(m, Mom{cnt, p[0], p[1]});
+    }
+    for (int s = 32; s; s >>= 1) m = join(m, Mom{__shfl_xor(m.n, s), __shfl_xor(m.mean, s), __shfl_xor(m.m2, s)});
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int k = 1; k < 4; ++k) m = join(m, sm[k]);
+      mean[grp] = m.mean;
+      rstd[grp] = 1.0f / sqrtf(m.m2 / m.n + a.eps);
+    }
+    __syncthreads();
   }
 }
 
@@ -389,21 +396,23 @@ template <bool F32, int V, bool SILU>
 __global__ __launch_bounds__(256) void gn_apply(GnArgs a) {
   const Lanes<V> w(a);
   if (!w.on) return;
-  const int64_t smp = blockIdx.x / a.splits;
-  const int64_t l0 = (blockIdx.x % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
-  const int c = w.cv * V, g = c / a.c;
-  float ga[V], be[V];
-  ldp<V>(a.gamma, c, 1.0f, ga);
-  ldp<V>(a.beta, c, 0.0f, be);
-  const float mean = a.mean[smp * a.G + g], rstd = a.rstd[smp * a.G + g];
-  const int64_t base = smp * a.L * a.C + c;
+  for (int64_t blk = blockIdx.x; blk < a.n * a.splits; blk += gridDim.x) {
+    const int64_t smp = blk / a.splits;
+    const int64_t l0 = (blk % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
+    const int c = w.cv * V, g = c / a.c;
+    float ga[V], be[V];
+    ldp<V>(a.gamma, c, 1.0f, ga);
+    ldp<V>(a.beta, c, 0.0f, be);
+    const float mean = a.mean[smp * a.G + g], rstd = a.rstd[smp * a.G + g];
+    const int64_t base = smp * a.L * a.C + c;
 #pragma unroll 4
-  for (int64_t l = l0 + w.rr; l < l1; l += w.rt) {
-    float v[V];
-    ld<F32, V>(a.x, base + l * a.C, v);
+    for (int64_t l = l0 + w.rr; l < l1; l += w.rt) {
+      float v[V];
+      ld<F32, V>(a.x, base + l * a.C, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = act_of<SILU>((v[i] - mean) * rstd * ga[i] + be[i]);
-    st<F32, V>(a.out, base + l * a.C, v);
+      for (int i = 0; i < V; ++i) v[i] = act_of<SILU>((v[i] - mean) * rstd * ga[i] + be[i]);
+      st<F32, V>(a.out, base + l * a.C, v);
+    }
   }
 }
 
@@ -412,18 +421,94 @@ template <bool F32, int V, bool SILU>
 __global__ __launch_bounds__(256) void gn_sums(GnArgs a) {
   __shared__ float sm[2][256][V];
   const Lanes<V> w(a);
-  const int64_t smp = blockIdx.x / a.splits;
-  const int64_t l0 = (blockIdx.x % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
   const int c = w.cv * V;
-  float dg[V], db[V];
+  for (int64_t blk = blockIdx.x; blk < a.n * a.splits; blk += gridDim.x) {
+    const int64_t smp = blk / a.splits;
+    const int64_t l0 = (blk % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
+    float dg[V], db[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
-  if (w.on) {
-    const int g = c / a.c;
+    for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
+    if (w.on) {
+      const int g = c / a.c;
+      float ga[V], be[V];
+      ldp<V>(a.gamma, c, 1.0f, ga);
+      ldp<V>(a.beta, c, 0.0f, be);
+      const float mean = a.mean[smp * a.G + g], rstd = a.rstd[smp * a.G + g];
+      const int64_t base = smp * a.L * a.C + c;
+#pragma unroll 4
+      for (int64_t l = l0 + w.rr; l < l1; l += w.rt) {
+        float v[V], d[V];
+        ld<F32, V>(a.x, base + l * a.C, v);
+        ld<F32, V>(a.dy, base + l * a.C, d);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (v[i] - mean) * rstd;
+          const float dz = d[i] * act_slope<SILU>(xh * ga[i] + be[i]);
+          dg[i] += dz * xh;
+          db[i] += dz;
+        }
+      }
+    }
+    if (w.rt > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sm[0][threadIdx.x][i] = dg[i], sm[1][threadIdx.x][i] = db[i];
+      __syncthreads();
+      if (w.on && w.rr == 0)
+        for (int k = 1; k < w.rt; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            dg[i] += sm[0][threadIdx.x + k * (a.C / V)][i];
+            db[i] += sm[1][threadIdx.x + k * (a.C / V)][i];
+          }
+    }
+    if (w.on && w.rr == 0) {
+      float* p = a.part + blk * 2 * a.C + c;
+#pragma unroll
+      for (int i = 0; i < V; ++i) p[i] = dg[i], p[a.C + i] = db[i];
+    }
+    __syncthreads();
+  }
+}
+
+// mean(h xh), mean(h) of a (sample, group): [n, G, 2]
+__global__ __launch_bounds__(1024) void gn_group_sums(GnArgs a, float* out) {
+  __shared__ float sm[2][16];
+  for (int64_t grp = blockIdx.x; grp < a.n * a.G; grp += gridDim.x) {
+    const int64_t smp = grp / a.G;
+    const int g = (int)(grp % a.G);
+    float s2 = 0.0f, s1 = 0.0f;
+    for (int64_t i = threadIdx.x; i < (int64_t)a.splits * a.c; i += blockDim.x) {
+      const int ch = g * a.c + (int)(i % a.c);
+      const float* p = a.part + (smp * a.splits + i / a.c) * 2 * a.C + ch;
+      const float ga = a.gamma ? a.gamma[ch] : 1.0f;
+      s2 += ga * p[0];
+      s1 += ga * p[a.C];
+    }
+    s2 = team_sum(s2, 64), s1 = team_sum(s1, 64);
+    if ((threadIdx.x & 63) == 0) sm[0][threadIdx.x >> 6] = s2, sm[1][threadIdx.x >> 6] = s1;
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      float t = 0.0f;
+      for (int k = 0; k < (int)blockDim.x / 64; ++k) t += sm[threadIdx.x][k];
+      out[grp * 2 + threadIdx.x] = t / ((float)a.L * (float)a.c);
+    }
+    __syncthreads();
+  }
+}
+
+template <bool F32, int V, bool SILU>
+__global__ __launch_bounds__(256) void gn_apply_grad(GnArgs a, const float* sums) {
+  const Lanes<V> w(a);
+  if (!w.on) return;
+  for (int64_t blk = blockIdx.x; blk < a.n * a.splits; blk += gridDim.x) {
+    const int64_t smp = blk / a.splits;
+    const int64_t l0 = (blk % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
+    const int c = w.cv * V, g = c / a.c;
     float ga[V], be[V];
     ldp<V>(a.gamma, c, 1.0f, ga);
     ldp<V>(a.beta, c, 0.0f, be);
     const float mean = a.mean[smp * a.G + g], rstd = a.rstd[smp * a.G + g];
+    const float s2 = sums[(smp * a.G + g) * 2], s1 = sums[(smp * a.G + g) * 2 + 1];
     const int64_t base = smp * a.L * a.C + c;
 #pragma unroll 4
     for (int64_t l = l0 + w.rr; l < l1; l += w.rt) {
@@ -433,79 +518,11 @@ __global__ __launch_bounds__(256) void gn_sums(GnArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float xh = (v[i] - mean) * rstd;
-        const float dz = d[i] * act_slope<SILU>(xh * ga[i] + be[i]);
-        dg[i] += dz * xh;
-        db[i] += dz;
+        const float h = d[i] * act_slope<SILU>(xh * ga[i] + be[i]) * ga[i];
+        v[i] = rstd * (h - s1 - xh * s2);
       }
+      st<F32, V>(a.out, base + l * a.C, v);
     }
-  }
-  if (w.rt > 1) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) sm[0][threadIdx.x][i] = dg[i], sm[1][threadIdx.x][i] = db[i];
-    __syncthreads();
-    if (w.on && w.rr == 0)
-      for (int k = 1; k < w.rt; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          dg[i] += sm[0][threadIdx.x + k * (a.C / V)][i];
-          db[i] += sm[1][threadIdx.x + k * (a.C / V)][i];
-        }
-  }
-  if (w.on && w.rr == 0) {
-    float* p = a.part + (int64_t)blockIdx.x * 2 * a.C + c;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = dg[i], p[a.C + i] = db[i];
-  }
-}
-
-// mean(h xh), mean(h) of a (sample, group): [n, G, 2]
-__global__ __launch_bounds__(1024) void gn_group_sums(GnArgs a, float* out) {
-  __shared__ float sm[2][16];
-  const int64_t smp = blockIdx.x / a.G;
-  const int g = blockIdx.x % a.G;
-  float s2 = 0.0f, s1 = 0.0f;
-  for (int64_t i = threadIdx.x; i < (int64_t)a.splits * a.c; i += 1024) {
-    const int ch = g * a.c + (int)(i % a.c);
-    const float* p = a.part + (smp * a.splits + i / a.c) * 2 * a.C + ch;
-    const float ga = a.gamma ? a.gamma[ch] : 1.0f;
-    s2 += ga * p[0];
-    s1 += ga * p[a.C];
-  }
-  s2 = team_sum(s2, 64), s1 = team_sum(s1, 64);
-  if ((threadIdx.x & 63) == 0) sm[0][threadIdx.x >> 6] = s2, sm[1][threadIdx.x >> 6] = s1;
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    float t = 0.0f;
-    for (int k = 0; k < 16; ++k) t += sm[threadIdx.x][k];
-    out[(int64_t)blockIdx.x * 2 + threadIdx.x] = t / ((float)a.L * (float)a.c);
-  }
-}
-
-template <bool F32, int V, bool SILU>
-__global__ __launch_bounds__(256) void gn_apply_grad(GnArgs a, const float* sums) {
-  const Lanes<V> w(a);
-  if (!w.on) return;
-  const int64_t smp = blockIdx.x / a.splits;
-  const int64_t l0 = (blockIdx.x % a.splits) * a.span, l1 = min(l0 + a.span, a.L);
-  const int c = w.cv * V, g = c / a.c;
-  float ga[V], be[V];
-  ldp<V>(a.gamma, c, 1.0f, ga);
-  ldp<V>(a.beta, c, 0.0f, be);
-  const float mean = a.mean[smp * a.G + g], rstd = a.rstd[smp * a.G + g];
-  const float s2 = sums[(smp * a.G + g) * 2], s1 = sums[(smp * a.G + g) * 2 + 1];
-  const int64_t base = smp * a.L * a.C + c;
-#pragma unroll 4
-  for (int64_t l = l0 + w.rr; l < l1; l += w.rt) {
-    float v[V], d[V];
-    ld<F32, V>(a.x, base + l * a.C, v);
-    ld<F32, V>(a.dy, base + l * a.C, d);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float xh = (v[i] - mean) * rstd;
-      const float h = d[i] * act_slope<SILU>(xh * ga[i] + be[i]) * ga[i];
-      v[i] = rstd * (h - s1 - xh * s2);
-    }
-    st<F32, V>(a.out, base + l * a.C, v);
   }
 }
 
@@ -538,6 +555,9 @@ int vec_of(int c, const GnArgs& a, bool f32) {
   return 1;
 }
 
+// Workgroups of a two-pass kernel; beyond, each takes every so-manieth piece of the work.
+unsigned blocks_of(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 20); }
+
 int pow2_from(int64_t n) {
   int p = 1;
   while (p < n && p < kLanes) p <<= 1;
@@ -567,13 +587,13 @@ atlasmem_status rows_launch(GnArgs a, hipStream_t st) {
 template <bool F32, int V, bool SILU>
 atlasmem_status forward(GnArgs a, hipStream_t st) {
   if (one_pass(a.L, a.c, V)) return rows_launch<F32, V, SILU, false>(a, st);
-  const dim3 grid((unsigned)(a.n * a.splits), (unsigned)((a.C / V + 255) / 256));
+  const dim3 grid(blocks_of(a.n * a.splits), (unsigned)((a.C / V + 255) / 256));
   float* stats = a.part + 2 * a.n * a.splits * (int64_t)a.C;
   if (!a.mean) a.mean = stats;
   if (!a.rstd) a.rstd = stats + a.n * a.G;
   gn_moments<F32, V><<<grid, 256, 0, st>>>(a);
   AM_LAUNCH_CHECK();
-  gn_stats<V><<<(unsigned)(a.n * a.G), 256, 0, st>>>(a, a.mean, a.rstd);
+  gn_stats<V><<<blocks_of(a.n * a.G), 256, 0, st>>>(a, a.mean, a.rstd);
   AM_LAUNCH_CHECK();
   gn_apply<F32, V, SILU><<<grid, 256, 0, st>>>(a);
   AM_LAUNCH_CHECK();
@@ -605,11 +625,11 @@ atlasmem_status backward(GnArgs a, hipStream_t st) {
     a.part = part;
     count = row_slots(a.n, a.C);
   } else {
-    const dim3 grid((unsigned)(a.n * a.splits), (unsigned)((a.C / V + 255) / 256));
+    const dim3 grid(blocks_of(a.n * a.splits), (unsigned)((a.C / V + 255) / 256));
     float* sums = a.part + 2 * a.n * a.splits * (int64_t)a.C;
     gn_sums<F32, V, SILU><<<grid, 256, 0, st>>>(a);
     AM_LAUNCH_CHECK();
-    gn_group_sums<<<(unsigned)(a.n * a.G), 1024, 0, st>>>(a, sums);
+    gn_group_sums<<<blocks_of(a.n * a.G), (int64_t)a.splits * a.c > 1024 ? 1024 : 128, 0, st>>>(a, sums);
     AM_LAUNCH_CHECK();
     gn_apply_grad<F32, V, SILU><<<grid, 256, 0, st>>>(a, sums);
     AM_LAUNCH_CHECK();

@@ -33,7 +33,7 @@ struct LaRows {                 // a [B, H, T, w] tensor of either layout
   const void* p;
   int64_t sb, sh, st;           // element strides of b, h, t
   int w;
-  int vec;                      // rows are whole, aligned 16-byte pieces
+  int vec, vec4;                // rows are whole, aligned pieces of 16 bytes; of four elements
 };
 
 struct LaArgs {
@@ -179,8 +179,10 @@ template <int W, int NP>
 __device__ __forceinline__ Op<NP> row_op(const uint16_t* s, int at, int k) {
   Op<NP> o;
 #pragma unroll
-  for (int n = 0; n < NP; ++n)
-    o.p[n] = cat2(*(const uint2*)(s + n * kC * W + (at ^ (16 * k))), *(const uint2*)(s + n * kC * W + (at ^ (16 * k + 8))));
+  for (int n = 0; n < NP; ++n) {
+    const uint16_t* p = s + n * kC * W;
+    o.p[n] = cat2(*(const uint2*)(p + (at ^ (16 * k))), *(const uint2*)(p + (at ^ (16 * k + 8))));
+  }
   return o;
 }
 // A column operand: lane l takes column c0 + l % 32 and the rows 16 k + .. in the same order.  at: col_at.
@@ -351,7 +353,8 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
         buf_st8(c.r, (int)o, 0, w);
       } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) buf_st_u16(c.r, n < left ? (int)(o + 2 * n) : -1, 0, (n & 2 ? w.y : w.x) >> (16 * (n & 1)));
+        for (int n = 0; n < 4; ++n)
+          buf_st_u16(c.r, n < left ? (int)(o + 2 * n) : -1, 0, (n & 2 ? w.y : w.x) >> (16 * (n & 1)));
       }
     }
   };
@@ -384,7 +387,8 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
     for (int t = 0; t < XS - 1; ++t)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float4 v = *(const float4*)(parts + half * kParts + q * 256 * NW * (XS - 1) + ((t * NW + zw) * 64 + lane) * 4);
+        const float4 v = *(const float4*)(parts + half * kParts + q * 256 * NW * (XS - 1) +
+                                          ((t * NW + zw) * 64 + lane) * 4);
         Ow[4 * q] += v.x, Ow[4 * q + 1] += v.y, Ow[4 * q + 2] += v.z, Ow[4 * q + 3] += v.w;
       }
     put_rows(Ow, pwait, rwait);
@@ -622,7 +626,6 @@ __global__ __launch_bounds__(256) void la_step(LaArgs a) {
   const int lr = threadIdx.x % LPR, r0 = blockIdx.y * RPB + threadIdx.x / LPR;
   const int dk = a.x.w, dv = a.z.w, c = 4 * lr;
   const int len = a.len ? min(max(a.len[b], 0), (int)a.T) : (int)a.T;
-  const float g = a.log_decay[h], lam = decay_pow(g, 1);
   const bool vec = a.svec;
   float W[RPT][4];
 #pragma unroll
@@ -642,27 +645,61 @@ __global__ __launch_bounds__(256) void la_step(LaArgs a) {
       }
     }
   }
+  // a token's elements: the next ones are on their way while these are used
+  const bool whole = dk % 4 == 0 && a.x.vec4 && a.y.vec4;
+  float nq[4], nk[4], nv[RPT];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) nq[n] = nk[n] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) nv[i] = 0.0f;
+    if (t >= len) return;
+    const int64_t aq = b * a.x.sb + h * a.x.sh + t * a.x.st + c, ak = b * a.y.sb + h * a.y.sh + t * a.y.st + c;
+    const int64_t av = b * a.z.sb + h * a.z.sh + t * a.z.st;
+    if (c < dk) {
+      if (whole && F32) {
+        const float4 q = *(const float4*)((const float*)a.x.p + aq), k = *(const float4*)((const float*)a.y.p + ak);
+        nq[0] = q.x, nq[1] = q.y, nq[2] = q.z, nq[3] = q.w;
+        nk[0] = k.x, nk[1] = k.y, nk[2] = k.z, nk[3] = k.w;
+      } else if (whole) {
+        const uint2 q = *(const uint2*)((const uint16_t*)a.x.p + aq), k = *(const uint2*)((const uint16_t*)a.y.p + ak);
+        nq[0] = bf16_value(q.x & 0xFFFFu), nq[1] = __uint_as_float(q.x & 0xFFFF0000u);
+        nq[2] = bf16_value(q.y & 0xFFFFu), nq[3] = __uint_as_float(q.y & 0xFFFF0000u);
+        nk[0] = bf16_value(k.x & 0xFFFFu), nk[1] = __uint_as_float(k.x & 0xFFFF0000u);
+        nk[2] = bf16_value(k.y & 0xFFFFu), nk[3] = __uint_as_float(k.y & 0xFFFF0000u);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (c + n < dk) {
+            nq[n] = load_in(a.x.p, aq + n, !F32);
+            nk[n] = load_in(a.y.p, ak + n, !F32);
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int row = r0 + i * (256 / LPR);
+      if (row < dv) nv[i] = load_in(a.z.p, av + row, !F32);
+    }
+  };
+  fetch(0);
+  const float lam = decay_pow(a.log_decay[h], 1);
   for (int t = 0; t < (int)a.T; ++t) {
     const bool live = t < len;
-    float q[4] = {0, 0, 0, 0}, k[4] = {0, 0, 0, 0};
-    if (live) {
-      const int64_t aq = b * a.x.sb + h * a.x.sh + t * a.x.st + c, ak = b * a.y.sb + h * a.y.sh + t * a.y.st + c;
+    float q[4], k[4], vs[RPT];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (c + n < dk) {
-          q[n] = load_in(a.x.p, aq + n, !F32);
-          k[n] = load_in(a.y.p, ak + n, !F32);
-        }
-    }
+    for (int n = 0; n < 4; ++n) q[n] = nq[n], k[n] = nk[n];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) vs[i] = nv[i];
+    if (t + 1 < (int)a.T) fetch(t + 1);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int row = r0 + i * (256 / LPR);
       float y = 0.0f;
       if (live) {
-        const float v = row < dv ? load_in(a.z.p, b * a.z.sb + h * a.z.sh + t * a.z.st + row, !F32) : 0.0f;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          W[i][n] = lam * W[i][n] + v * k[n];
+          W[i][n] = lam * W[i][n] + vs[i] * k[n];
           y += W[i][n] * q[n];
         }
       }
@@ -703,6 +740,7 @@ LaRows rows_of(const void* p, const LinAttn& s, int w) {
     r.sb = s.H * s.T * (int64_t)w, r.sh = s.T * (int64_t)w, r.st = w;
   }
   r.vec = ((uintptr_t)p & 15) == 0 && w % (s.bf16 ? 8 : 4) == 0;
+  r.vec4 = ((uintptr_t)p & (s.bf16 ? 7 : 15)) == 0 && w % 4 == 0;
   return r;
 }
 

@@ -7,12 +7,17 @@
 //   z   a = W (lanes v), b = X (lanes i): both rows along the contraction
 //   dX  a = W (lanes d, rows across the contraction: read transposed from LDS), b = G
 //   dW  a = X, b = G, both across the contraction
-// An output tile has b's index in its lanes and a's, four at a time, in its registers.  bf16 inputs are
-// used as they are.  Rows that are left out are left out of the products: the others' X is copied
-// together, and the kernels take their number from the device.  G is rounded without its weight: the label's entry, -1 + p, is the large one and in
-// bf16 nearly exact while p is small; dX's weight goes to the fp32 sums, and dW's to X, relative to the
-// largest one, so that equal weights round nothing.  fp32 inputs (and then G) as three bf16 planes, the six products of planes down to
-// 2^-16 of the leading one summed in fp32 (relative 2^-24, at the matrix cores' bf16 rate over six).
+// An output tile has b's index in its lanes and a's, four at a time, in its registers.
+//
+// Types.  bf16 inputs are used as they are; fp32 ones (and then G) as three bf16 planes, the six products
+// of planes down to 2^-16 of the leading one summed in fp32 (relative 2^-24, at a sixth of the bf16 rate).
+// In bf16 G is rounded without its weight: the label's entry, -1 + p, is the large one and nearly exact
+// while p is small, where dloss (-1 + p) has one rounding error for all rows of equal weight (dX 3.7e-3 off
+// instead of 1.7e-3).  dX takes its rows' weights in the fp32 sums; dW takes them on X, relative to the
+// largest one, so that equal weights round nothing.
+//
+// Rows that are left out are left out of the products: the others' X is copied together, and the kernels
+// take their number from the device.
 #include <algorithm>
 
 #include "common.h"
@@ -322,13 +327,12 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
         for (int n = 0; n < 16; ++n) m = fmaxf(m, acc[i][j][n]);
       m = fmaxf(m, __shfl_xor(m, 32));
+      const float from = m > -INFINITY ? m : 0.0f;  // a row of NaN has no maximum, and its sum stays NaN
       float s = 0.0f;
-      if (m > -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < MA; ++i)
+      for (int i = 0; i < MA; ++i)
 #pragma unroll
-          for (int n = 0; n < 16; ++n) s += __expf(acc[i][j][n] - m);
-      }
+        for (int n = 0; n < 16; ++n) s += __expf(acc[i][j][n] - from);
       s += __shfl_xor(s, 32);
       if (hf == 0) red[(wave % WA) * TB + wb + 32 * j + col] = float2{m, s};
     }
@@ -509,9 +513,9 @@ __global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int d
 
 // loss, lse of a row: a wave joins the tiles' maxima and sums, and takes the row's product with its
 // label's class.
-__global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, const int* at, const void* X, const void* W, int in_bf16,
-                                               int vec, int64_t n, int d, int64_t vocab, const int64_t* labels,
-                                               float* loss, float* lse) {
+__global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, const int* at, const void* X,
+                                               const void* W, int in_bf16, int vec, int64_t n, int d, int64_t vocab,
+                                               const int64_t* labels, float* loss, float* lse) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (r >= n) return;
@@ -539,7 +543,8 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
   float z = 0.0f;
   for (int c = lane * 8; c < d; c += 512) {  // one order of the sum, whatever the alignment
     if (vec) {
-      const u32x4 a = *(const u32x4*)((const uint16_t*)X + r * d + c), b = *(const u32x4*)((const uint16_t*)W + y * d + c);
+      const u32x4 a = *(const u32x4*)((const uint16_t*)X + r * d + c);
+      const u32x4 b = *(const u32x4*)((const uint16_t*)W + y * d + c);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         z = fmaf(__uint_as_float(k & 1 ? a[k >> 1] & 0xFFFF0000u : a[k >> 1] << 16),
@@ -583,10 +588,10 @@ __global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, c
 }
 
 __global__ void xe_zero(void* out, int64_t count, int bf16) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= count) return;
-  if (bf16) ((uint16_t*)out)[i] = 0;
-  else ((float*)out)[i] = 0.0f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+    if (bf16) ((uint16_t*)out)[i] = 0;
+    else ((float*)out)[i] = 0.0f;
+  }
 }
 
 // ------------------------------------------------------------------------------------------- host
@@ -605,7 +610,6 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
   g.tb = (int)((g.nb + TB - 1) / TB);
   if (EPI != EPI_ACC) g.splits = 1;
   const int64_t blocks = up((int64_t)g.ta * g.tb * g.splits, 8);
-  if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
   kern<<<(unsigned)blocks, WA * WB * 64, lds, st>>>(g);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
@@ -622,7 +626,8 @@ bool wide_split(int64_t na, int64_t nb) { return tiles_of(na, nb, 256) * 28 <= t
 
 template <bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_of(const GemmArgs& g, bool w, hipStream_t st) {
-  return w ? gemm_launch<256, 256, 2, 4, 4, AX, BX, EPI, F32>(g, st) : gemm_launch<128, 128, 2, 2, 4, AX, BX, EPI, F32>(g, st);
+  return w ? gemm_launch<256, 256, 2, 4, 4, AX, BX, EPI, F32>(g, st)
+           : gemm_launch<128, 128, 2, 2, 4, AX, BX, EPI, F32>(g, st);
 }
 template <bool AX, bool BX, int EPI>
 atlasmem_status gemm(const GemmArgs& g, bool f32, bool w, hipStream_t st) {
@@ -705,7 +710,6 @@ atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, i
                           const int* count, const float* dloss, const float* largest, uint16_t* out, uint16_t* out_w,
                           hipStream_t st) {
   const int64_t blocks = (rows * (p.dp / 4) + 255) / 256;
-  if (blocks > INT32_MAX) return ATLASMEM_E_SHAPE;
   xe_planes<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, p.planes, index, count, dloss, largest, out,
                                               out_w);
   AM_LAUNCH_CHECK();
@@ -744,7 +748,8 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   e = gemm<false, false, EPI_LSE>(g, !s.bf16, w, st);
   if (e != ATLASMEM_OK) return e;
   xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, gather ? ws.at : nullptr, X, W, s.bf16,
-                                                     direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss, lse);
+                                                     direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss,
+                                                     lse);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -755,7 +760,7 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   if (s.n == 0) {
     if (dW) {
       const int64_t count = s.vocab * (int64_t)s.d;
-      xe_zero<<<(unsigned)((count + 255) / 256), 256, 0, st>>>(dW, count, s.bf16);
+      xe_zero<<<(unsigned)std::min<int64_t>((count + 255) / 256, 1 << 16), 256, 0, st>>>(dW, count, s.bf16);
       AM_LAUNCH_CHECK();
     }
     return ATLASMEM_OK;
@@ -807,8 +812,8 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   }
   if (dX) {
     const int vec = s.d % 4 == 0 && ((uintptr_t)dX & 15) == 0;
-    xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(ws.acc, p.splits, s.n, s.d, p.dp, ws.at, dloss, dX,
-                                                                       s.bf16, vec);
+    xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(ws.acc, p.splits, s.n, s.d, p.dp, ws.at, dloss,
+                                                                       dX, s.bf16, vec);
     AM_LAUNCH_CHECK();
   }
   return ATLASMEM_OK;
