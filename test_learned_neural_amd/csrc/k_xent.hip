@@ -9,8 +9,9 @@
 //   dW  a = X, b = G, both across the contraction
 // An output tile has b's index in its lanes and a's, four at a time, in its registers.
 //
-// Types.  bf16 inputs are used as they are; fp32 ones (and then G) as three bf16 planes, the six products
-// of planes down to 2^-16 of the leading one summed in fp32 (relative 2^-24, at a sixth of the bf16 rate).
+// Types.  bf16 inputs are used as they are.  fp32 ones (and then G) go to LDS as they are and are split in
+// registers into three bf16 planes, whose six products down to 2^-16 of the leading one are summed in fp32
+// (relative 2^-24, at a sixth of the bf16 rate).
 // In bf16 G is rounded without its weight: the label's entry, -1 + p, is the large one and nearly exact
 // while p is small, where dloss (-1 + p) has one rounding error for all rows of equal weight (dX 3.7e-3 off
 // instead of 1.7e-3).  dX takes its rows' weights in the fp32 sums; dW takes them on X, relative to the
@@ -19,6 +20,7 @@
 // Rows that are left out are left out of the products: the others' X is copied together, and the kernels
 // take their number from the device.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "internal.h"
@@ -28,18 +30,12 @@ namespace am {
 namespace {
 
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
-constexpr int kProducts = 6;   // of planes, fp32
-// The planes of product p, the small products first: a's 2 0 1 1 0 0, b's 0 2 1 0 1 0 (four bits each).
-__device__ __forceinline__ int plane_a(int p) { return (0x001102 >> (4 * p)) & 3; }
-__device__ __forceinline__ int plane_b(int p) { return (0x010120 >> (4 * p)) & 3; }
-
 enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT };
 
 struct GemmArgs {
-  const uint16_t* a;
-  const uint16_t* b;
+  const void* a;
+  const void* b;
   int64_t lda, ldb;        // elements of a row
-  int64_t pa, pb;          // elements from plane to plane
   int64_t na, nb;          // rows (or, across the contraction, columns) of a and b
   int64_t K;
   const int* count;        // rows that count (OUT: K, else nb), or null: as given
@@ -53,28 +49,26 @@ struct GemmArgs {
   const float* lse;
   const int* index;        // GRAD: [nb], b's rows in X
   int64_t v0, vocab;
-  uint16_t* g;             // GRAD: [nb][ldg], planes of pg elements
-  int64_t ldg, pg;
-  int planes;
+  void* g;                 // GRAD: [nb][ldg]
+  int64_t ldg;
   float* acc;              // ACC: [splits][acc_rows][na]
   int64_t acc_rows;
   int add;
   const float* scale;      // OUT: one factor, or null
   void* out;               // [nb][ldo]
   int64_t ldo;
-  int out_bf16;
 };
 
 // One operand's step in LDS.  Along the contraction: [R][32], the 16-byte pieces of four rows (256 bytes,
-// all banks) exchanged by the four's index; across: [32][R], pairs of 32-byte pieces exchanged by the
-// contraction index's low bits.  Either way the lanes that are served together lie on distinct banks.
+// all banks) exchanged by the four's index; across: [32][R], pairs of 32-byte pieces exchanged by those
+// low bits of the contraction index that 256 bytes do not hold.  Either way the lanes that are served together lie on distinct banks.
 // Loads go straight to LDS, 64 pieces of 16 bytes an instruction, in LDS order: the exchange is in the
 // lanes' global offsets.  Those outside the matrix have the top bit, and the range check writes zeros.
 //
 // The load is written out because the compiler, knowing it, waits for all of them before every
 // transposing read.  It has no result register: its address is read when it is issued, and what it
 // writes, LDS, is waited for by wait_all alone.  m0 has no other use in these kernels.
-__device__ __forceinline__ void load_to_lds(rsrc_t rs, uint32_t voff, const uint16_t* lds) {
+__device__ __forceinline__ void load_to_lds(rsrc_t rs, uint32_t voff, const void* lds) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(rs)
                : "memory");
@@ -86,6 +80,8 @@ struct Tile {
   uint32_t off[kLoads];
   int kc;  // along: the lane's first contraction element
 
+  __device__ static constexpr int exchange(int k) { return R == 64 ? k & 2 : (k & 3) << 1; }
+
   __device__ void init(int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
     kc = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
 #pragma unroll
@@ -93,7 +89,7 @@ struct Tile {
       const int id = (wave * kLoads + i) * 64 + lane;  // piece in LDS order
       if constexpr (ACROSS) {
         const int k = id / (R / 8), at = id % (R / 8);
-        const int c = ((((at >> 1) ^ ((k & 3) << 1)) << 1) | (at & 1)) * 8;
+        const int c = ((((at >> 1) ^ exchange(k)) << 1) | (at & 1)) * 8;
         off[i] = c < rows - r0 ? (uint32_t)((k * ld + c) * 2) : 0x80000000u;
       } else {
         const int r = id >> 2;
@@ -120,7 +116,7 @@ struct Tile {
     if constexpr (ACROSS) {
       const int e = (lane & 15) >> 2;
       const int k = 16 * ks + 8 * hf + e;
-      const int c = (((r0 + (lane & 16)) >> 4) ^ (e << 1)) * 16 + 4 * (lane & 3);
+      const int c = (((r0 + (lane & 16)) >> 4) ^ exchange(e)) * 16 + 4 * (lane & 3);
       typedef short v4i16 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) v4i16* lds4;
       const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(s + k * R + c)));
@@ -133,6 +129,73 @@ struct Tile {
   }
 };
 
+// The same for fp32, whose operands are read as eight floats.  Along: [R][32], the pieces of a pair of rows
+// exchanged by the pair's index; across: [32][R], halves of 64 columns exchanged by the contraction index's
+// eights, so that the two halves of a wave read different banks.
+template <int R, bool ACROSS, int WAVES>
+struct Tile32 {
+  static constexpr int kElems = R * kBK;
+  static constexpr int kLoads = R * kBK / 4 / 64 / WAVES;
+  uint32_t off[kLoads];
+  int kc[kLoads];
+
+  __device__ void init(int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int id = (wave * kLoads + i) * 64 + lane;
+      if constexpr (ACROSS) {
+        const int k = id / (R / 4), c = (id % (R / 4) ^ ((k >> 3 & 1) << 3)) * 4;
+        kc[i] = 0;
+        off[i] = c < rows - r0 ? (uint32_t)((k * ld + c) * 4) : 0x80000000u;
+      } else {
+        const int r = id >> 3;
+        kc[i] = ((id & 7) ^ ((r >> 1) & 7)) * 4;
+        off[i] = r < rows - r0 ? (uint32_t)((r * ld + kc[i]) * 4) : 0x80000000u;
+      }
+    }
+  }
+  __device__ void load(int i, float* s, const float* p, int left, int64_t ld, int64_t room, int wave) const {
+    const float* d = s + (wave * kLoads + i) * 256;
+    if constexpr (ACROSS) {
+      const int n = left < kBK ? left : kBK;
+      const rsrc_t rs = make_rsrc(p, n > 0 ? (uint32_t)(((n - 1) * ld + room) * 4) : 0u);
+      load_to_lds(rs, off[i], d);
+    } else {
+      const rsrc_t rs = make_rsrc(p, 0x7fffffffu);
+      load_to_lds(rs, off[i] | (kc[i] < left ? 0u : 0x80000000u), d);
+    }
+  }
+  __device__ static void op(const float* s, int r0, int ks, int lane, float* v) {
+    const int hf = lane >> 5;
+    if constexpr (ACROSS) {
+      const float* p = s + (16 * ks + 8 * hf) * R + ((r0 ^ (hf << 5)) + (lane & 31));
+#pragma unroll
+      for (int n = 0; n < 8; ++n) v[n] = p[n * R];
+    } else {
+      const int r = r0 + (lane & 31), c = 4 * ks + 2 * hf, x = (r >> 1) & 7;
+      const float4 a = *(const float4*)(s + r * kBK + ((c ^ x) << 2));
+      const float4 b = *(const float4*)(s + r * kBK + (((c | 1) ^ x) << 2));
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  }
+};
+
+// Eight floats as three bf16 planes, v = p[0] + p[1] + p[2].
+__device__ __forceinline__ void split_planes(float* v, u32x4* p) {
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = cvt_pk_bf16(v[2 * i], v[2 * i + 1]);
+      p[n][i] = w;
+      if (n < 2) {
+        v[2 * i] -= __uint_as_float(w << 16);
+        v[2 * i + 1] -= __uint_as_float(w & 0xFFFF0000u);
+      }
+    }
+}
+
 // Waits until at most N of the wave's loads are on their way and its LDS reads are done, then for the
 // other waves: what was loaded before is in LDS, and what was read before may be overwritten.
 template <int N>
@@ -141,10 +204,9 @@ __device__ __forceinline__ void wait_all() {
 }
 
 // A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
-// through LDS, so that a row's columns leave in whole 16-byte pieces side by side.  With `rest` the
-// accumulators keep what the rounding left.
+// through LDS, so that a row's columns leave in whole 16-byte pieces side by side.
 template <int TA, int TB, int MA, int NB, int NT>
-__device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, bool rest, uint16_t* out,
+__device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, uint16_t* out,
                          int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr) {
   constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
   const int lane = tid & 63, hf = lane >> 5, col = lane & 31;
@@ -156,14 +218,10 @@ __device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, in
     for (int i = 0; i < MA; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        f32x16& x = acc[i][j];
+        const f32x16& x = acc[i][j];
         const uint2 o = {cvt_pk_bf16(x[4 * q], x[4 * q + 1]), cvt_pk_bf16(x[4 * q + 2], x[4 * q + 3])};
         const int c = (wa + 32 * i + 8 * q) >> 3;
         *(uint2*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3) + 4 * hf) = o;
-        if (rest) {
-          x[4 * q] -= __uint_as_float(o.x << 16), x[4 * q + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
-          x[4 * q + 2] -= __uint_as_float(o.y << 16), x[4 * q + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
-        }
       }
   }
   __syncthreads();
@@ -189,9 +247,11 @@ template <int TA, int TB, int WA, int WB, int kStages, bool AX, bool BX, int EPI
 __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   constexpr int NT = WA * WB * 64;
   constexpr int MA = TA / WA / 32, NB = TB / WB / 32;
-  using A = Tile<TA, AX, WA * WB>;
-  using B = Tile<TB, BX, WA * WB>;
-  extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
+  using E = std::conditional_t<F32, float, uint16_t>;
+  using A = std::conditional_t<F32, Tile32<TA, AX, WA * WB>, Tile<TA, AX, WA * WB>>;
+  using B = std::conditional_t<F32, Tile32<TB, BX, WA * WB>, Tile<TB, BX, WA * WB>>;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  E* sm = (E*)smem;
   constexpr int kStage = A::kElems + B::kElems;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hf = lane >> 5,
             col = lane & 31;
@@ -222,8 +282,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     k0 = min(split * each * kBK, g.K);
     k1 = min(k0 + each * kBK, g.K);
   }
-  const int steps = (int)((k1 - k0 + kBK - 1) / kBK);
-  const int iters = steps * (F32 ? kProducts : 1);
+  const int iters = (int)((k1 - k0 + kBK - 1) / kBK);
 
   f32x16 acc[MA][NB];
 #pragma unroll
@@ -234,83 +293,126 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int n = 0; n < 16; ++n) acc[i][j][n] = 0.0f;
 
   // Step t is computed from one of the LDS buffers while the next steps are on their way to the others;
-  // operands are read one matrix-instruction depth ahead.  One barrier a step, between its two depths:
-  // behind it step t's buffer takes its next step's loads (a's at once, b's in the next step), and step t + 1 is
-  // there.  Past the end loads are masked off.  The source order is the schedule: reads and loads are
-  // spread over the matrix instructions, since a burst of them from all four waves fills the LDS queue
-  // and holds up the matrix instructions behind it.
+  // operands are read one matrix-instruction depth (16) ahead.  One barrier a step, between its two
+  // depths: behind it step t's buffer is free for its next step's loads, and step t + 1 is there.  Past
+  // the end loads are masked off.
   A ta;
   B tb;
   ta.init(g.lda, a0, g.na, wave, lane);
   tb.init(g.ldb, b0, g.nb, wave, lane);
   const int64_t step_a = AX ? kBK * g.lda : kBK, step_b = BX ? kBK * g.ldb : kBK;
-  const int64_t start_a = AX ? k0 * g.lda + a0 : a0 * g.lda + k0, start_b = BX ? k0 * g.ldb + b0 : b0 * g.ldb + k0;
-  int q = F32 ? 0 : kProducts - 1;
-  const uint16_t *pa = g.a + plane_a(q) * g.pa + start_a, *pb = g.b + plane_b(q) * g.pb + start_b;
+  const E* pa = (const E*)g.a + (AX ? k0 * g.lda + a0 : a0 * g.lda + k0);
+  const E* pb = (const E*)g.b + (BX ? k0 * g.ldb + b0 : b0 * g.ldb + k0);
   int left = (int)(k1 - k0);
-  auto load_a = [&](int n, uint16_t* d) { ta.load(n, d, pa, left, g.lda, g.lda - a0, wave); };
-  auto load_b = [&](int n, uint16_t* d) { tb.load(n, d + A::kElems, pb, left, g.ldb, g.ldb - b0, wave); };
+  auto load_a = [&](int n, E* d) { ta.load(n, d, pa, left, g.lda, g.lda - a0, wave); };
+  auto load_b = [&](int n, E* d) { tb.load(n, d + A::kElems, pb, left, g.ldb, g.ldb - b0, wave); };
   auto next = [&]() {
     left -= kBK;
     pa += step_a, pb += step_b;
-    if (F32 && left <= 0 && q + 1 < kProducts) {
-      ++q;
-      left = (int)(k1 - k0);
-      pa = g.a + plane_a(q) * g.pa + start_a, pb = g.b + plane_b(q) * g.pb + start_b;
-    }
   };
   constexpr int kLoads = A::kLoads + B::kLoads;
-  u32x4 ao[2][MA], bo[2][NB];
-  // operands in the order in which the products need them: a 0, b 0.., a 1..
-  auto read = [&](int n, int set, const uint16_t* s, int ks) {
-    if (n == 0) ao[set][0] = A::op(s, wa, ks, lane);
-    else if (n <= NB) bo[set][n - 1] = B::op(s + A::kElems, wb + 32 * (n - 1), ks, lane);
-    else ao[set][n - NB] = A::op(s, wa + 32 * (n - NB), ks, lane);
-  };
-  if (iters > 0) {
+  if constexpr (F32) {
+    static_assert(kStages == 2, "a step in use, a step on its way");
+    float ra[MA][8], rb[NB][8];
+    auto load = [&](E* d) {
 #pragma unroll
-    for (int t = 0; t < kStages; ++t) {
+      for (int n = 0; n < A::kLoads; ++n) load_a(n, d);
 #pragma unroll
-      for (int n = 0; n < A::kLoads; ++n) load_a(n, sm + t * kStage);
-      if (t + 1 == kStages) break;
-#pragma unroll
-      for (int n = 0; n < B::kLoads; ++n) load_b(n, sm + t * kStage);
+      for (int n = 0; n < B::kLoads; ++n) load_b(n, d);
       next();
+    };
+    auto read = [&](const E* s, int ks) {
+#pragma unroll
+      for (int i = 0; i < MA; ++i) A::op(s, wa + 32 * i, ks, lane, ra[i]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) B::op(s + A::kElems, wb + 32 * j, ks, lane, rb[j]);
+    };
+    if (iters > 0) {
+      load(sm);
+      load(sm + kStage);
+      wait_all<kLoads>();
+      read(sm, 0);
     }
-    wait_all<(kStages - 1) * kLoads - B::kLoads>();
+    for (int it = 0; it < iters; ++it) {
+      E *s = sm + (it & 1) * kStage, *d = sm + (~it & 1) * kStage;
 #pragma unroll
-    for (int n = 0; n < MA + NB; ++n) read(n, 0, sm, 0);
-  }
-  uint16_t *s = sm, *e = sm + (kStages - 1) * kStage;
-  for (int it = 0; it < iters; ++it) {
-    uint16_t* d = s == sm + (kStages - 1) * kStage ? sm : s + kStage;
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4 ap[MA][3], bp[NB][3];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (ks == 1) wait_all<(kStages - 2) * kLoads>();
-      constexpr int kM = MA * NB, kR = MA + NB;
+        for (int i = 0; i < MA; ++i) split_planes(ra[i], ap[i]);
 #pragma unroll
-      for (int n = 0; n < kM; ++n) {
-        acc[n / NB][n % NB] = mfma32(ao[ks][n / NB], bo[ks][n % NB], acc[n / NB][n % NB]);
-#pragma unroll
-        for (int r = n * kR / kM; r < (n + 1) * kR / kM; ++r) read(r, ks ^ 1, ks ? d : s, ks ^ 1);
-        if (ks == 0) {
-#pragma unroll
-          for (int r = n * B::kLoads / kM; r < (n + 1) * B::kLoads / kM; ++r) load_b(r, e);
-        } else {
-          if (n == 0) next();
-#pragma unroll
-          for (int r = n * A::kLoads / kM; r < (n + 1) * A::kLoads / kM; ++r) load_a(r, s);
+        for (int j = 0; j < NB; ++j) split_planes(rb[j], bp[j]);
+        if (ks == 1) {
+          wait_all<0>();
+          load(s);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        read(ks ? d : s, ks ^ 1);
+        // the small products first
+        constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+        for (int q = 0; q < 6; ++q)
+#pragma unroll
+          for (int i = 0; i < MA; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ap[i][kA[q]], bp[j][kB[q]], acc[i][j]);
       }
     }
-    e = s, s = d;
+  } else {
+    u32x4 ao[2][MA], bo[2][NB];
+    // operands in the order in which the products need them: a 0, b 0.., a 1..
+    auto read = [&](int n, int set, const E* s, int ks) {
+      if (n == 0) ao[set][0] = A::op(s, wa, ks, lane);
+      else if (n <= NB) bo[set][n - 1] = B::op(s + A::kElems, wb + 32 * (n - 1), ks, lane);
+      else ao[set][n - NB] = A::op(s, wa + 32 * (n - NB), ks, lane);
+    };
+    if (iters > 0) {
+#pragma unroll
+      for (int t = 0; t < kStages; ++t) {
+#pragma unroll
+        for (int n = 0; n < A::kLoads; ++n) load_a(n, sm + t * kStage);
+        if (t + 1 == kStages) break;
+#pragma unroll
+        for (int n = 0; n < B::kLoads; ++n) load_b(n, sm + t * kStage);
+        next();
+      }
+      wait_all<(kStages - 1) * kLoads - B::kLoads>();
+#pragma unroll
+      for (int n = 0; n < MA + NB; ++n) read(n, 0, sm, 0);
+    }
+    // Behind the barrier a buffer takes a's loads, b's in the next step's first depth.  The source order is
+    // the schedule: reads and loads are spread over the matrix instructions, since a burst of them from
+    // all waves fills the LDS queue and holds up the matrix instructions behind it.
+    E *s = sm, *e = sm + (kStages - 1) * kStage;
+    for (int it = 0; it < iters; ++it) {
+      E* d = s == sm + (kStages - 1) * kStage ? sm : s + kStage;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if (ks == 1) wait_all<(kStages - 2) * kLoads>();
+        constexpr int kM = MA * NB, kR = MA + NB;
+#pragma unroll
+        for (int n = 0; n < kM; ++n) {
+          acc[n / NB][n % NB] = mfma32(ao[ks][n / NB], bo[ks][n % NB], acc[n / NB][n % NB]);
+#pragma unroll
+          for (int r = n * kR / kM; r < (n + 1) * kR / kM; ++r) read(r, ks ^ 1, ks ? d : s, ks ^ 1);
+          if (ks == 0) {
+#pragma unroll
+            for (int r = n * B::kLoads / kM; r < (n + 1) * B::kLoads / kM; ++r) load_b(r, e);
+          } else {
+            if (n == 0) next();
+#pragma unroll
+            for (int r = n * A::kLoads / kM; r < (n + 1) * A::kLoads / kM; ++r) load_a(r, s);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      e = s, s = d;
+    }
   }
   // loads past the end may still be on their way to LDS
   wait_all<0>();
 
   if constexpr (EPI == EPI_LSE) {
-    float2* red = (float2*)sm;  // [WA][TB]
+    float2* red = (float2*)smem;  // [WA][TB]
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       if (a0 + TA > g.na) {
@@ -382,8 +484,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
             if (!kept || 32 * i + 8 * (n >> 2) + (n & 3) >= end) acc[i][j][n] = 0.0f;
       }
     }
-    for (int n = 0; n < g.planes; ++n)
-      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, n + 1 < g.planes, g.g + n * g.pg, g.ldg, a0, g.ldg, b0, g.nb);
+    if constexpr (!F32)
+      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb);
   }
 
   if constexpr (EPI == EPI_OUT) {
@@ -394,12 +496,14 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
-    if (g.out_bf16) {
-      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, false, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
-      return;
-    }
+    if constexpr (!F32) put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
   }
-  if constexpr (EPI == EPI_ACC || EPI == EPI_OUT) {
+
+  // fp32 outputs: four columns a lane
+  if constexpr (EPI == EPI_ACC || (F32 && EPI != EPI_LSE)) {
+    float* out = EPI == EPI_ACC ? g.acc + (int64_t)split * g.acc_rows * g.lda : (float*)(EPI == EPI_GRAD ? g.g : g.out);
+    const int64_t ld = EPI == EPI_ACC ? g.lda : EPI == EPI_GRAD ? g.ldg : g.ldo;
+    const bool vec = ld % 4 == 0 && ((uintptr_t)out & 15) == 0;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int64_t r = b0 + wb + 32 * j + col;
@@ -409,21 +513,20 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int64_t c = a0 + wa + 32 * i + 8 * q + 4 * hf;
-          if (c >= g.na) continue;
+          if (c >= ld) continue;
           float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          if constexpr (EPI == EPI_ACC) {
-            float4* p = (float4*)(g.acc + ((int64_t)split * g.acc_rows + r) * g.lda + c);
-            if (g.add) {
-              const float4 o = *p;
-              x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
-            }
-            *p = x;
+          float* p = out + r * ld + c;
+          if (EPI == EPI_ACC && g.add) {
+            const float4 o = *(const float4*)p;
+            x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
+          }
+          if (vec) {
+            *(float4*)p = x;
           } else {
-            float* p = (float*)g.out + r * g.ldo + c;
-            if (c + 0 < g.ldo) p[0] = x.x;
-            if (c + 1 < g.ldo) p[1] = x.y;
-            if (c + 2 < g.ldo) p[2] = x.z;
-            if (c + 3 < g.ldo) p[3] = x.w;
+            if (c + 0 < ld) p[0] = x.x;
+            if (c + 1 < ld) p[1] = x.y;
+            if (c + 2 < ld) p[2] = x.z;
+            if (c + 3 < ld) p[3] = x.w;
           }
         }
     }
@@ -472,10 +575,10 @@ __global__ __launch_bounds__(1024) void xe_rows(const int64_t* labels, const flo
   }
 }
 
-// Rows of an input as bf16 planes [planes][rows][dp], zero from column d on: all of them, or with `index`
-// those that count.  out_w: the same rows times dloss / largest.
-__global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int dp, int planes, const int* index,
-                          const int* count, const float* dloss, const float* largest, uint16_t* out, uint16_t* out_w) {
+// Rows of an input as the products take them, [rows][dp], zero from column d on: all of them, or with
+// `index` those that count.  out_w: the same rows times dloss / largest.
+__global__ void xe_copy(const void* x, int bf16, int64_t rows, int d, int dp, const int* index, const int* count,
+                        const float* dloss, const float* largest, void* out, void* out_w) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // four columns
   const int64_t per = dp / 4;
   const int64_t r = i / per;
@@ -484,7 +587,7 @@ __global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int d
   const int64_t row = index ? index[r] : r;
   float v[4];
   if (d % 4 == 0 && ((uintptr_t)x & 15) == 0 && c < d) {
-    if (in_bf16) {
+    if (bf16) {
       const uint2 w = *(const uint2*)((const uint16_t*)x + row * d + c);
       v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
       v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
@@ -494,21 +597,15 @@ __global__ void xe_planes(const void* x, int in_bf16, int64_t rows, int d, int d
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = c + k < d ? load_in(x, row * d + c + k, in_bf16) : 0.0f;
+    for (int k = 0; k < 4; ++k) v[k] = c + k < d ? load_in(x, row * d + c + k, bf16) : 0.0f;
   }
-  auto put = [&](uint16_t* o, float a, float b, float c2, float d2) {
-    for (int n = 0; n < planes; ++n) {
-      const uint2 w = {cvt_pk_bf16(a, b), cvt_pk_bf16(c2, d2)};
-      *(uint2*)(o + (n * rows + r) * dp + c) = w;
-      a -= __uint_as_float(w.x << 16), b -= __uint_as_float(w.x & 0xFFFF0000u);
-      c2 -= __uint_as_float(w.y << 16), d2 -= __uint_as_float(w.y & 0xFFFF0000u);
-    }
+  auto put = [&](void* o, float w) {
+    const int64_t at = r * dp + c;
+    if (bf16) *(uint2*)((uint16_t*)o + at) = uint2{cvt_pk_bf16(v[0] * w, v[1] * w), cvt_pk_bf16(v[2] * w, v[3] * w)};
+    else *(float4*)((float*)o + at) = float4{v[0] * w, v[1] * w, v[2] * w, v[3] * w};
   };
-  put(out, v[0], v[1], v[2], v[3]);
-  if (out_w) {
-    const float w = dloss[row] / *largest;
-    put(out_w, v[0] * w, v[1] * w, v[2] * w, v[3] * w);
-  }
+  if (out) put(out, 1.0f);
+  if (out_w) put(out_w, dloss[row] / *largest);
 }
 
 // loss, lse of a row: a wave joins the tiles' maxima and sums, and takes the row's product with its
@@ -542,13 +639,21 @@ __global__ __launch_bounds__(256) void xe_join(const float2* part, int parts, co
   }
   float z = 0.0f;
   for (int c = lane * 8; c < d; c += 512) {  // one order of the sum, whatever the alignment
-    if (vec) {
+    if (vec && in_bf16) {
       const u32x4 a = *(const u32x4*)((const uint16_t*)X + r * d + c);
       const u32x4 b = *(const u32x4*)((const uint16_t*)W + y * d + c);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         z = fmaf(__uint_as_float(k & 1 ? a[k >> 1] & 0xFFFF0000u : a[k >> 1] << 16),
                  __uint_as_float(k & 1 ? b[k >> 1] & 0xFFFF0000u : b[k >> 1] << 16), z);
+    } else if (vec) {
+      const float *a = (const float*)X + r * d + c, *b = (const float*)W + y * d + c;
+#pragma unroll
+      for (int h = 0; h < 8; h += 4) {
+        if (c + h >= d) break;
+        const float4 u = *(const float4*)(a + h), v = *(const float4*)(b + h);
+        z = fmaf(u.w, v.w, fmaf(u.z, v.z, fmaf(u.y, v.y, fmaf(u.x, v.x, z))));
+      }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -601,7 +706,7 @@ int64_t align256(int64_t b) { return up(b, 256); }
 
 template <int TA, int TB, int WA, int WB, int ST, bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
-  constexpr int lds = std::max(ST * (TA + TB) * kBK * 2, TA * TB * 2);
+  constexpr int lds = F32 ? ST * (TA + TB) * kBK * 4 : std::max(ST * (TA + TB) * kBK * 2, TA * TB * 2);
   auto kern = xe_gemm<TA, TB, WA, WB, ST, AX, BX, EPI, F32>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
@@ -615,58 +720,68 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
   return ATLASMEM_OK;
 }
 
-// Tiles of 256 x 256 (a workgroup a CU) or of 128 x 128 (two).  The large ones take 0.7 of the time for
-// an area (8192 x 16384 x 2048: 554 us against 790), the small ones fill the chip with less: rounds of
-// workgroups decide, or where the contraction is split to fill it (dX), the areas.
+// Sides of the tiles.  256 (a workgroup a CU) take 0.7 of the time of 128 (two a CU) for an area (8192 x
+// 16384 x 2048: 554 us against 790); the smaller ones fill the chip with less: rounds of workgroups decide,
+// or where the contraction is split to fill it (dX), the areas.  Where 128 leave more than half of the chip
+// idle, 64: a step of theirs takes a third of the time.  fp32 has no 256: planes and accumulators of two
+// workgroups of 128 fill a CU's registers.
 int64_t tiles_of(int64_t na, int64_t nb, int side) { return (na + side - 1) / side * ((nb + side - 1) / side); }
-bool wide(int64_t na, int64_t nb) {
-  return (tiles_of(na, nb, 256) + 255) / 256 * 28 <= (tiles_of(na, nb, 128) + 511) / 512 * 20;
+int side_of(int64_t na, int64_t nb, bool bf16) {
+  const int64_t t = tiles_of(na, nb, 128);
+  if (t <= 128) return 64;
+  return bf16 && (tiles_of(na, nb, 256) + 255) / 256 * 28 <= (t + 511) / 512 * 20 ? 256 : 128;
 }
-bool wide_split(int64_t na, int64_t nb) { return tiles_of(na, nb, 256) * 28 <= tiles_of(na, nb, 128) * 10; }
+int side_split(int64_t na, int64_t nb, bool bf16) {
+  return bf16 && tiles_of(na, nb, 256) * 28 <= tiles_of(na, nb, 128) * 10 ? 256 : 128;
+}
 
-template <bool AX, bool BX, int EPI, bool F32>
-atlasmem_status gemm_of(const GemmArgs& g, bool w, hipStream_t st) {
-  return w ? gemm_launch<256, 256, 2, 4, 4, AX, BX, EPI, F32>(g, st)
-           : gemm_launch<128, 128, 2, 2, 4, AX, BX, EPI, F32>(g, st);
-}
 template <bool AX, bool BX, int EPI>
-atlasmem_status gemm(const GemmArgs& g, bool f32, bool w, hipStream_t st) {
-  return f32 ? gemm_of<AX, BX, EPI, true>(g, w, st) : gemm_of<AX, BX, EPI, false>(g, w, st);
+atlasmem_status gemm(const GemmArgs& g, bool bf16, int side, hipStream_t st) {
+  if (bf16) {
+    if (side == 256) return gemm_launch<256, 256, 2, 4, 4, AX, BX, EPI, false>(g, st);
+    if (side == 128) return gemm_launch<128, 128, 2, 2, 4, AX, BX, EPI, false>(g, st);
+    return gemm_launch<64, 64, 2, 2, 4, AX, BX, EPI, false>(g, st);
+  }
+  if (side == 128) return gemm_launch<128, 128, 2, 2, 2, AX, BX, EPI, true>(g, st);
+  return gemm_launch<64, 64, 2, 2, 2, AX, BX, EPI, true>(g, st);
 }
 
 // The inputs as the engine takes them: bf16 rows of whole, aligned 16-byte pieces.
 struct Plan {
-  int planes, dp;
+  int el, dp;                   // bytes of an element, elements of a copied row
   int64_t n, vocab, piece;      // classes of a piece
   int parts, splits;
-  bool wide_x;                  // large tiles for dX
+  int side_x;                   // of dX's tiles
 };
 
 constexpr int64_t kPieceBytes = 256 << 20;  // of G: what the last-level cache holds
 
 Plan plan_of(const CrossEntropy& s) {
   Plan p = {};
-  p.planes = s.bf16 ? 1 : 3;
-  p.dp = (int)up(s.d, 8);
+  p.el = s.bf16 ? 2 : 4;
+  p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
   p.n = s.n, p.vocab = s.vocab;
-  int64_t piece = kPieceBytes / std::max<int64_t>(s.n * 2 * p.planes, 1) / 256 * 256;
+  int64_t piece = kPieceBytes / std::max<int64_t>(s.n * p.el, 1) / 256 * 256;
   piece = std::max<int64_t>(piece, 2048);
   const int64_t pieces = (s.vocab + piece - 1) / piece;
   p.piece = up((s.vocab + pieces - 1) / pieces, 256);
-  p.parts = (int)((s.vocab + 127) / 128);
-  p.wide_x = wide_split(p.dp, s.n);
-  const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.wide_x ? 256 : 128), 1);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.wide_x ? 256 : 512) / tiles, p.piece / 512));
+  p.parts = (int)((s.vocab + 63) / 64);
+  p.side_x = side_split(p.dp, s.n, s.bf16);
+  const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.side_x), 1);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.side_x == 256 ? 256 : 512) / tiles, p.piece / 512));
+  if (tiles * p.splits <= 128) p.side_x = 64;
   return p;
 }
 
-bool direct(const void* p, const CrossEntropy& s) { return s.bf16 && s.d % 8 == 0 && ((uintptr_t)p & 15) == 0; }
+bool direct(const void* p, const CrossEntropy& s) {
+  return s.d % (s.bf16 ? 8 : 4) == 0 && ((uintptr_t)p & 15) == 0;
+}
 
 // What a call finds in its workspace, one behind the other.
 struct Space {
   int *index, *at, *count;
   float* largest;
-  uint16_t *x, *xw, *w, *g;
+  char *x, *xw, *w, *g;
   float* acc;
   float2* part;
   int64_t bytes;
@@ -679,14 +794,14 @@ Space space_of(void* p, const CrossEntropy& s, const Plan& l, bool backward) {
     at += align256(bytes);
     return r;
   };
-  const int64_t rows = 2 * l.planes * s.n * (int64_t)l.dp;
+  const int64_t rows = l.el * s.n * (int64_t)l.dp;
   w.index = (int*)take(4 * s.n), w.at = (int*)take(4 * s.n);
   w.count = (int*)take(8), w.largest = (float*)(w.count + 1);
-  w.x = (uint16_t*)take(rows);
-  w.w = (uint16_t*)take(2 * l.planes * s.vocab * (int64_t)l.dp);
+  w.x = take(rows);
+  w.w = take(l.el * s.vocab * (int64_t)l.dp);
   if (backward) {
-    w.xw = (uint16_t*)take(rows);
-    w.g = (uint16_t*)take(2 * l.planes * s.n * l.piece);
+    w.xw = take(rows);
+    w.g = take(l.el * s.n * l.piece);
     w.acc = (float*)take(4 * (int64_t)l.splits * s.n * l.dp);
   } else {
     w.part = (float2*)take(8 * s.n * (int64_t)l.parts);
@@ -706,12 +821,11 @@ atlasmem_status rows_that_count(const CrossEntropy& s, const Space& w, const int
   return ATLASMEM_OK;
 }
 
-atlasmem_status planes_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int* index,
-                          const int* count, const float* dloss, const float* largest, uint16_t* out, uint16_t* out_w,
-                          hipStream_t st) {
+atlasmem_status copy_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int* index,
+                        const int* count, const float* dloss, const float* largest, void* out, void* out_w,
+                        hipStream_t st) {
   const int64_t blocks = (rows * (p.dp / 4) + 255) / 256;
-  xe_planes<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, p.planes, index, count, dloss, largest, out,
-                                              out_w);
+  xe_copy<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, index, count, dloss, largest, out, out_w);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -726,26 +840,25 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
                               float* lse, void* workspace, hipStream_t st) {
   const Plan p = plan_of(s);
   const Space ws = space_of(workspace, s, p, false);
-  const bool gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : kProducts) >= kGatherFrom;
+  const bool gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) >= kGatherFrom;
   atlasmem_status e = ATLASMEM_OK;
   if (gather) e = rows_that_count(s, ws, labels, nullptr, st);
   const int *index = gather ? ws.index : nullptr, *count = gather ? ws.count : nullptr;
   if (e == ATLASMEM_OK && (gather || !direct(X, s)))
-    e = planes_of(X, s, p, s.n, index, count, nullptr, nullptr, ws.x, nullptr, st);
+    e = copy_of(X, s, p, s.n, index, count, nullptr, nullptr, ws.x, nullptr, st);
   if (e == ATLASMEM_OK && !direct(W, s))
-    e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
+    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
   if (e != ATLASMEM_OK) return e;
   GemmArgs g = {};
   g.part = ws.part;
-  g.a = direct(W, s) ? (const uint16_t*)W : ws.w;
-  g.b = gather || !direct(X, s) ? ws.x : (const uint16_t*)X;
+  g.a = direct(W, s) ? W : ws.w;
+  g.b = gather || !direct(X, s) ? ws.x : X;
   g.lda = g.ldb = p.dp;
-  g.pa = s.vocab * p.dp, g.pb = s.n * p.dp;
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
   g.count = count;
-  const bool w = wide(s.vocab, s.n);
-  g.parts = (int)((s.vocab + (w ? 255 : 127)) / (w ? 256 : 128));
-  e = gemm<false, false, EPI_LSE>(g, !s.bf16, w, st);
+  const int side = side_of(s.vocab, s.n, s.bf16);
+  g.parts = (int)((s.vocab + side - 1) / side);
+  e = gemm<false, false, EPI_LSE>(g, s.bf16, side, st);
   if (e != ATLASMEM_OK) return e;
   xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, gather ? ws.at : nullptr, X, W, s.bf16,
                                                      direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss,
@@ -770,43 +883,42 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   const bool weighted = dW && dloss;
   atlasmem_status e = rows_that_count(s, ws, labels, dloss, st);
   if (e == ATLASMEM_OK)
-    e = planes_of(X, s, p, s.n, ws.index, ws.count, dloss, ws.largest, ws.x, weighted ? ws.xw : nullptr, st);
+    e = copy_of(X, s, p, s.n, ws.index, ws.count, dloss, ws.largest, ws.x, weighted ? ws.xw : nullptr, st);
   if (e == ATLASMEM_OK && !direct(W, s))
-    e = planes_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
+    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
   if (e != ATLASMEM_OK) return e;
-  const uint16_t* wa = direct(W, s) ? (const uint16_t*)W : ws.w;
+  const char* wa = direct(W, s) ? (const char*)W : ws.w;
   for (int64_t v0 = 0; v0 < s.vocab; v0 += p.piece) {
     const int64_t nv = std::min(p.piece, s.vocab - v0), ldg = up(nv, 64);
     // G of the piece
     GemmArgs g = {};
     g.count = ws.count;
-    g.a = wa + v0 * p.dp, g.b = ws.x;
+    g.a = wa + v0 * p.dp * p.el, g.b = ws.x;
     g.lda = g.ldb = p.dp;
-    g.pa = s.vocab * p.dp, g.pb = s.n * p.dp;
     g.na = nv, g.nb = s.n, g.K = p.dp;
     g.labels = labels, g.lse = lse, g.index = ws.index, g.v0 = v0;
-    g.g = ws.g, g.ldg = ldg, g.pg = s.n * ldg, g.planes = p.planes;
-    e = gemm<false, false, EPI_GRAD>(g, !s.bf16, wide(nv, s.n), st);
+    g.g = ws.g, g.ldg = ldg;
+    e = gemm<false, false, EPI_GRAD>(g, s.bf16, side_of(nv, s.n, s.bf16), st);
     if (e != ATLASMEM_OK) return e;
     if (dX) {
       GemmArgs x = {};
       x.count = ws.count;
-      x.a = wa + v0 * p.dp, x.lda = p.dp, x.pa = s.vocab * p.dp, x.na = p.dp;
-      x.b = ws.g, x.ldb = ldg, x.pb = s.n * ldg, x.nb = s.n;
+      x.a = wa + v0 * p.dp * p.el, x.lda = p.dp, x.na = p.dp;
+      x.b = ws.g, x.ldb = ldg, x.nb = s.n;
       x.K = nv;
       x.splits = p.splits, x.acc = ws.acc, x.acc_rows = s.n, x.add = v0 > 0;
-      e = gemm<true, false, EPI_ACC>(x, !s.bf16, p.wide_x, st);
+      e = gemm<true, false, EPI_ACC>(x, s.bf16, p.side_x, st);
       if (e != ATLASMEM_OK) return e;
     }
     if (dW) {
       GemmArgs x = {};
       x.count = ws.count;
-      x.a = weighted ? ws.xw : ws.x, x.lda = p.dp, x.pa = s.n * p.dp, x.na = p.dp;
+      x.a = weighted ? ws.xw : ws.x, x.lda = p.dp, x.na = p.dp;
       x.scale = weighted ? ws.largest : nullptr;
-      x.b = ws.g, x.ldb = ldg, x.pb = s.n * ldg, x.nb = nv;
+      x.b = ws.g, x.ldb = ldg, x.nb = nv;
       x.K = s.n;
-      x.out = (char*)dW + v0 * s.d * (s.bf16 ? 2 : 4), x.ldo = s.d, x.out_bf16 = s.bf16;
-      e = gemm<true, true, EPI_OUT>(x, !s.bf16, wide(p.dp, nv), st);
+      x.out = (char*)dW + v0 * s.d * p.el, x.ldo = s.d;
+      e = gemm<true, true, EPI_OUT>(x, s.bf16, side_of(p.dp, nv, s.bf16), st);
       if (e != ATLASMEM_OK) return e;
     }
   }
