@@ -436,9 +436,10 @@ atlasmem_status atlasmem_gates(const void* U, int64_t B, int64_t T, int32_t d_mo
  *         (NULL where that is 0)
  * bf16 inputs enter the products as they are, fp32 ones as three bf16 planes (24 bits); states and
  * sums are fp32, Y is rounded once.  Values should be finite: in the chunks a NaN or infinity of V
- * reaches, besides the tokens behind it, the up to 31 before it in its chunk (zeros times it).  Errors: E_INVALID for bad sizes, enums, null or overlapping
- * pointers, a short workspace; E_SHAPE beyond the limits (heads <= 65536, batch * heads <= 2^20).
- * The workspace function returns -1 for sizes that the calls refuse. */
+ * reaches, besides the tokens behind it, the up to 31 before it in its chunk (zeros times it).
+ * Errors: E_INVALID for bad sizes, enums, null or overlapping pointers, a short workspace; E_SHAPE
+ * beyond the limits (heads <= 65536, batch * heads <= 2^20).  The workspace function returns -1 for
+ * sizes that the calls refuse. */
 int64_t atlasmem_linear_attention_workspace_bytes(int32_t dtype, int32_t batch, int32_t heads, int64_t T,
                                                   int32_t d_key, int32_t d_value, int32_t backward);
 atlasmem_status atlasmem_linear_attention(const void* Q, const void* K, const void* V, int32_t dtype, int32_t batch,
@@ -498,7 +499,7 @@ atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int3
  * z = X W^T, without keeping the logits z:
  *   lse_i = log sum_v exp(z_iv),   loss_i = lse_i - z_i,label_i
  *   X: [n, d], W: [vocab, d] of `dtype`; d <= 16384, n and vocab <= 2^24, n * d and vocab * d <= 2^33,
- *         n * vocab <= 2^38
+ *         n * vocab <= 2^38 (fp32: 2^37)
  *   labels: int64 [n]; a row whose label is no class (negative, or >= vocab) is left out: its loss, lse
  *         and gradient are zero, whatever its X holds
  *   loss, lse: fp32 [n]
@@ -514,7 +515,7 @@ atlasmem_status atlasmem_cross_entropy(const void* X, const void* W, int32_t dty
 
 /* Its gradients: with G_iv = dloss_i (exp(z_iv - lse_i) - [v = label_i]), dX = G W and dW = G^T X.  The
  * logits are computed again, a piece of the vocabulary at a time; G's pieces pass through the workspace
- * in bf16 (fp32 calls: in three planes).
+ * in the type of X, without their weight dloss (what rounding there is, is of exp(..) - [..]).
  *   lse: the forward's;  dloss: fp32 [n], or NULL (one each)
  *   dX: [n, d], dW: [vocab, d] of `dtype`, written, not added to; either may be NULL (not computed)
  *   workspace: atlasmem_cross_entropy_workspace_bytes(..., backward = 1) bytes

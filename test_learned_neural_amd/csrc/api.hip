@@ -440,9 +440,9 @@ bool disjoint(const Range* out, int n_out, const Range* in, int n_in) {
 atlasmem_status cross_entropy_of(int32_t dtype, int64_t n, int32_t d, int64_t vocab, CrossEntropy& s) {
   if (n < 0 || d < 1 || vocab < 1 || (dtype != ATLASMEM_F32 && dtype != ATLASMEM_BF16)) return ATLASMEM_E_INVALID;
   // grids and their work items stay below 2^32: a lane of the copies takes four elements, a workgroup of
-  // 512 lanes 256 x 256 logits (or, in smaller calls, 256 lanes 128 x 128)
+  // 512 lanes 256 x 256 logits, of 256 lanes (smaller calls, and fp32) 128 x 128
   if (d > (1 << 14) || n > (1 << 24) || vocab > (1 << 24) || n * d > (INT64_C(1) << 33) ||
-      vocab * d > (INT64_C(1) << 33) || n * vocab > (INT64_C(1) << 38))
+      vocab * d > (INT64_C(1) << 33) || n * vocab > (INT64_C(1) << (dtype == ATLASMEM_BF16 ? 38 : 37)))
     return ATLASMEM_E_SHAPE;
   s = {n, vocab, d, dtype == ATLASMEM_BF16};
   return ATLASMEM_OK;

@@ -43,6 +43,7 @@ FAR = 1 << 36
     (dict(bytes=100), am.E_INVALID), (dict(ws=6 * FAR + 8), am.E_INVALID), (dict(dtype=9), am.E_INVALID), (dict(n=-1), am.E_INVALID),
     (dict(d=0), am.E_INVALID), (dict(vocab=0), am.E_INVALID), (dict(d=16385), am.E_SHAPE),
     (dict(vocab=1 << 25), am.E_SHAPE), (dict(n=1 << 25), am.E_SHAPE),
+    (dict(n=1 << 24, d=1, vocab=1 << 14), am.E_SHAPE), (dict(n=1 << 23, d=1, vocab=(1 << 14) + 1), am.E_SHAPE),
     (dict(n=1 << 20, vocab=1 << 19), am.E_SHAPE), (dict(d=1 << 14, vocab=1 << 20), am.E_SHAPE),
     (dict(lse=4 * FAR), am.E_INVALID), (dict(loss=FAR + 8), am.E_INVALID), (dict(ws=2 * FAR), am.E_INVALID),
     (dict(n=0), am.OK), (dict(n=0, X=None, W=None, labels=None, loss=None, lse=None, ws=None), am.OK),
