@@ -7,6 +7,12 @@
 // group, one pass over memory.  Otherwise: partial sums over spans of positions, a small
 // reduction, and a second pass that applies them.  Variances come from differences to a mean, never
 // from a difference of sums; fp32 throughout, one rounding at the end; sums run in one order.
+//
+// Bound by memory.  bf16 16384 rows x 16 groups of 128: forward 26.7 us (134 MB at 5.0 TB/s; 34 us before
+// the next row's loads were in flight while one is computed), backward 58.7 us (201 MB and the partial
+// sums at 3.6 TB/s) and gamma's and beta's sums 9 us.  fp32 3 x 16385 x 512 with 32 groups: moments 17.5,
+// apply 32, sums 36, gradient 53 us (101 MB a tensor, which the last-level cache holds: 5.7 to 6.3 TB/s),
+// the small reductions 5 to 9 us each.  One token: 3 us, a launch.
 #include <algorithm>
 
 #include "common.h"

@@ -16,6 +16,22 @@
 // and d log_decay is the tangent state's share (dS/dlog lambda, carried beside S) of the outputs:
 //   sum_i scale dy_i . (dS_i / dlog lambda)^T q_i + <dW_T, dS_T / dlog lambda>,
 // every term a product that is there: the shorter identity through sum_t (q.dq - k.dk) cancels.
+//
+// Layout.  A wave keeps 32 columns of the state in its accumulators, where they are already the operand of
+// S_0^T x (the contraction's order inside 16 is the accumulators' own, and x and y are read in it); scores
+// are computed as y x^T, whose accumulators are the operand of the product with z.  Only x, y, z pass
+// through LDS, y and z once more by transposing reads.  Computed operands are split into two bf16 planes
+// where they end in a bf16 output and into three where they end in an fp32 one (state, log_decay).
+// Chunks of 32 tokens: the scores of longer ones take more registers than two waves a SIMD have.
+// Few memories: the token axis is cut into segments whose own sums (state pass: y and z once more) are
+// scanned into start states, so that 512 workgroups fill the chip: two passes over memory, not one.
+//
+// Measured, bf16, 128 memories x 8192 tokens x 128 x 128: state pass 161 us, scan 22 us, outputs 366 us
+// (332 at the least; the clock falls to 1.7 GHz under matrix instructions): 1.07 GB at 2.9 TB/s, vector
+// instructions 53% and matrix instructions 33% of a SIMD's cycles: issue-bound, the splits and masks
+// first.  A call 465 us.
+// Training, 64 memories x 4096 x 64 x 128: 482 us, of which the tangent's kernel takes 165.
+// One token, 1024 memories x 128 x 128: 29 us, 135 MB at 4.7 TB/s (a copy reaches 4.9).
 #include <algorithm>
 #include <type_traits>
 
@@ -781,10 +797,14 @@ atlasmem_status chunk_run(const LaArgs& a, bool bf16, bool dec, int64_t M, hipSt
   const int64_t blocks = M * (OUT ? a.nseg : a.nseg - 1);
   const bool vec = a.x.vec && a.y.vec && a.z.vec && (!OUT || (a.o.vec && (!dec || a.t.vec)));
   if (bf16) {
-    if (vec) return dec ? chunk_pick<false, true, OUT, true>(a, blocks, st) : chunk_pick<false, true, OUT, false>(a, blocks, st);
-    return dec ? chunk_pick<false, false, OUT, true>(a, blocks, st) : chunk_pick<false, false, OUT, false>(a, blocks, st);
+    if (vec)
+      return dec ? chunk_pick<false, true, OUT, true>(a, blocks, st)
+                 : chunk_pick<false, true, OUT, false>(a, blocks, st);
+    return dec ? chunk_pick<false, false, OUT, true>(a, blocks, st)
+               : chunk_pick<false, false, OUT, false>(a, blocks, st);
   }
-  if (vec) return dec ? chunk_pick<true, true, OUT, true>(a, blocks, st) : chunk_pick<true, true, OUT, false>(a, blocks, st);
+  if (vec)
+    return dec ? chunk_pick<true, true, OUT, true>(a, blocks, st) : chunk_pick<true, true, OUT, false>(a, blocks, st);
   return dec ? chunk_pick<true, false, OUT, true>(a, blocks, st) : chunk_pick<true, false, OUT, false>(a, blocks, st);
 }
 
@@ -812,7 +832,8 @@ LaArgs base_args(const LinAttn& s) {
 }
 
 atlasmem_status run_scan(const LaArgs& a, const float* w0, float* u, float* ut, int64_t M, hipStream_t st) {
-  la_scan<<<(unsigned)(M * ((a.P + 255) / 256)), 256, 0, st>>>(w0, u, ut, a.log_decay, a.len, a.H, a.T, a.lseg, a.nseg, a.P);
+  la_scan<<<(unsigned)(M * ((a.P + 255) / 256)), 256, 0, st>>>(w0, u, ut, a.log_decay, a.len, a.H, a.T, a.lseg,
+                                                               a.nseg, a.P);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }

@@ -19,6 +19,12 @@
 //
 // Rows that are left out are left out of the products: the others' X is copied together, and the kernels
 // take their number from the device.
+//
+// Measured, bf16, 8192 rows (7373 count) x 2048 x 65536: logits 1.69 ms (1.17 PFLOP/s), then for each of
+// four pieces G 487 us (1.02; of that 70 us are its stores), dX 434 us (1.14), dW 393 us (1.26): 6.9 ms a
+// training pass.  A library's plain product of these sizes reaches 1.2 (logits, written out) to 1.5
+// PFLOP/s; both run at 1.65 GHz, the power limit, with the matrix cores 75% (the library 85%) busy.
+// One row x 1024 x 50257: 18 to 21 us for W's 103 MB (4.9 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -61,7 +67,8 @@ struct GemmArgs {
 
 // One operand's step in LDS.  Along the contraction: [R][32], the 16-byte pieces of four rows (256 bytes,
 // all banks) exchanged by the four's index; across: [32][R], pairs of 32-byte pieces exchanged by those
-// low bits of the contraction index that 256 bytes do not hold.  Either way the lanes that are served together lie on distinct banks.
+// low bits of the contraction index that 256 bytes do not hold.  Either way the lanes that are served
+// together lie on distinct banks.
 // Loads go straight to LDS, 64 pieces of 16 bytes an instruction, in LDS order: the exchange is in the
 // lanes' global offsets.  Those outside the matrix have the top bit, and the range check writes zeros.
 //
@@ -496,7 +503,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
-    if constexpr (!F32) put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
+    if constexpr (!F32)
+      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
   }
 
   // fp32 outputs: four columns a lane

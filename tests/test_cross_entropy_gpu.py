@@ -127,6 +127,8 @@ CASES = [
     ("large_tiles", dict(dtype=am.BF16, n=1100, d=72, vocab=16003)),
     ("large_tiles_f32", dict(dtype=am.F32, n=1500, d=40, vocab=12000)),
     ("large_tiles_wide_rows", dict(dtype=am.BF16, n=4300, d=4096, vocab=520)),
+    ("middle_tiles", dict(dtype=am.BF16, n=700, d=904, vocab=4000)),
+    ("middle_tiles_narrow_rows", dict(dtype=am.BF16, n=1500, d=100, vocab=12000)),
     ("pieces", dict(dtype=am.F32, n=22000, d=16, vocab=4200)),
 ]
 

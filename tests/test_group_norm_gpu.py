@@ -141,6 +141,8 @@ CASES = [
     ("positions_odd", dict(dtype=am.BF16, n=2, L=333, C=21, G=3, silu=True)),
     ("positions_wide", dict(dtype=am.F32, n=2, L=50, C=4096, G=2, silu=True)),
     ("many_samples", dict(dtype=am.F32, n=3000, L=40, C=24, G=2, silu=False)),
+    ("heads_walked", dict(dtype=am.BF16, n=9001, L=1, C=1024, G=8, silu=True)),
+    ("few_positions_walked", dict(dtype=am.F32, n=9001, L=2, C=512, G=8, silu=False)),
     ("no_affine", dict(dtype=am.BF16, n=50, L=1, C=256, G=2, silu=True, affine=False)),
     ("no_affine_positions", dict(dtype=am.F32, n=2, L=500, C=32, G=2, silu=True, affine=False)),
     ("far_from_zero", dict(dtype=am.F32, n=20, L=1, C=128, G=2, silu=False, offset=500.0, std=0.5)),
@@ -151,6 +153,31 @@ CASES = [
 @pytest.mark.parametrize("kw", [c[1] for c in CASES], ids=[c[0] for c in CASES])
 def test_parity(kw):
     check(Case(**kw))
+
+
+@pytest.mark.parametrize("L", [1, 300])
+def test_gamma_alone_and_gradients_that_are_not_asked_for(L):
+    import torch
+    c = Case(am.F32, 6, L, 64, 4, True)
+    X, dY, (ga, be) = c.X.to(DEV), c.dY.to(DEV), c.affine()
+    for g, b, none in ((ga, None, torch.zeros_like(be)), (None, be, torch.ones_like(ga))):
+        full = (ga, none) if b is None else (none, be)
+        got = []
+        for g_, b_ in ((g, b), full):
+            Y, dX = torch.empty_like(X), torch.empty_like(X)
+            mean, rstd = torch.empty((2, c.n, c.G), device=DEV)
+            am.group_norm(X, *c.size(), g_, b_, EPS, c.act(), Y, mean=mean, rstd=rstd, workspace=c.workspace(False))
+            Y2 = torch.empty_like(X)
+            am.group_norm(X, *c.size(), g_, b_, EPS, c.act(), Y2, workspace=c.workspace(False))
+            dga, dbe = torch.empty((2, c.C), device=DEV)
+            dX2, dX3, dga2 = torch.empty_like(X), torch.empty_like(X), torch.empty_like(dga)
+            back = (X, dY, *c.size(), g_, b_, mean, rstd, c.act())
+            am.group_norm_backward(*back, dX, dgamma=dga, dbeta=dbe, workspace=c.workspace(True))
+            am.group_norm_backward(*back, dX2, workspace=c.workspace(True))
+            am.group_norm_backward(*back, dX3, dgamma=dga2, workspace=c.workspace(True))
+            assert torch.equal(Y, Y2) and torch.equal(dX, dX2) and torch.equal(dX, dX3) and torch.equal(dga, dga2)
+            got.append((Y, mean, rstd, dX, dga, dbe))
+        assert all(torch.equal(p, q) for p, q in zip(*got))
 
 
 def test_equal_values_give_beta():

@@ -163,6 +163,10 @@ CASES = [
     ("odd_widths_f32", dict(dtype=am.F32, B=1, H=3, T=150, dk=101, dv=66, layout=am.TOKENS_FIRST)),
     ("wide_narrow", dict(dtype=am.BF16, B=1, H=2, T=200, dk=128, dv=24)),
     ("narrow_wide", dict(dtype=am.BF16, B=1, H=2, T=200, dk=24, dv=128)),
+    ("wide_narrow_padded", dict(dtype=am.BF16, B=3, H=2, T=600, dk=96, dv=40, lengths=[600, 0, 333],
+                                layout=am.TOKENS_FIRST)),
+    ("wide_narrow_odd_f32", dict(dtype=am.F32, B=1, H=3, T=555, dk=73, dv=33)),
+    ("narrow_wide_segments", dict(dtype=am.BF16, B=2, H=1, T=1000, dk=36, dv=100, lengths=[999, 37])),
     ("segments", dict(dtype=am.BF16, B=1, H=3, T=1500, dk=64, dv=64, layout=am.TOKENS_FIRST)),
     ("segments_f32", dict(dtype=am.F32, B=1, H=2, T=900, dk=128, dv=128)),
     ("padded", dict(dtype=am.BF16, B=5, H=2, T=330, dk=64, dv=64, lengths=[330, 0, 1, 64, 257])),
@@ -254,6 +258,24 @@ def test_state_in_place_and_cut_into_calls(T):
         assert n == 0 or float((Yp - Y[:, :, at:at + n]).abs().max()) <= 1e-4 * float(Y.abs().max())
         at += n
     assert float((W - W_T).abs().max()) <= 1e-5 * float(W_T.abs().max())
+
+
+@pytest.mark.parametrize("T,dv", [(70, 64), (900, 128), (900, 24)])
+def test_gradients_that_are_not_asked_for_and_a_state_adjoint_in_place(T, dv):
+    import torch
+    c = Case(am.BF16, 1, 3, T, 72, dv)
+    d, o = c.tensors(), c.outputs()
+    c.backward(d, o, c.workspace(True))
+    some = c.outputs()
+    c.backward(d, dict(some, dW0=None, dlog_decay=None), c.workspace(True))
+    for n in ("dQ", "dK", "dV"):
+        assert float((some[n].float() - o[n].float()).abs().max()) <= 2 ** -7 * float(o[n].float().abs().max())
+    A = d["dW"].clone()
+    here = c.outputs()
+    c.backward(dict(d, dW=A), dict(here, dW0=A), c.workspace(True))
+    assert torch.equal(A, o["dW0"]) and torch.equal(here["dlog_decay"], o["dlog_decay"])
+    for n in ("dQ", "dK", "dV"):
+        assert torch.equal(here[n], o[n])
 
 
 def test_unaligned_rows_equal_aligned_ones():
