@@ -15,6 +15,8 @@
 //             (A_T = dW_T):  dk_t = A_t^T v_t (x = v, y = dy, z = q), dv_t = A_t k_t (x = k, y = q, z = dy)
 // and d log_decay is the tangent state's share (dS/dlog lambda, carried beside S) of the outputs:
 //   sum_i scale dy_i . (dS_i / dlog lambda)^T q_i + <dW_T, dS_T / dlog lambda>,
+// in the dq kernel (t = q, O_i the output's part from before the chunk, P the masked scores, St the tangent):
+//   sum_i [(i+1) t_i . O_i + sum_j (i-j) P_ij z_j . t_i] + <St, c_out sum_i lambda^(i+1) x_i t_i^T>,
 // every term a product that is there: the shorter identity through sum_t (q.dq - k.dk) cancels.
 //
 // Layout.  A wave keeps 32 columns of the state in its accumulators, where they are already the operand of
@@ -30,7 +32,8 @@
 // (332 at the least; the clock falls to 1.7 GHz under matrix instructions): 1.07 GB at 2.9 TB/s, vector
 // instructions 53% and matrix instructions 33% of a SIMD's cycles: issue-bound, the splits and masks
 // first.  A call 465 us.
-// Training, 64 memories x 4096 x 64 x 128: 482 us, of which the tangent's kernel takes 165.
+// Training, 64 memories x 4096 x 64 x 128: 450 us, of which the tangent's kernel takes 145 (the outputs'
+// tangents as rows of their own, St split into planes: 165).
 // One token, 1024 memories x 128 x 128: 29 us, 135 MB at 4.7 TB/s (a copy reaches 4.9).
 #include <algorithm>
 #include <type_traits>
@@ -99,6 +102,19 @@ __device__ __forceinline__ void split8(const float* v, Op<N>& o) {
         r[2 * i + 1] -= __uint_as_float(w & 0xFFFF0000u);
       }
     }
+}
+
+template <int N>
+__device__ __forceinline__ void join8(const Op<N>& o, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = 0.0f;
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) {
+      const uint32_t w = o.p[n][i >> 1];
+      v[i] += __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+  }
 }
 
 // Products of planes down to 2^-16 of the leading one: the rest is below fp32's rounding.
@@ -224,8 +240,9 @@ __device__ __forceinline__ Op<NP> col_op(const uint16_t* s, int at, int c0, int 
 // those columns, each with a part of x.  Everything is linear in the parts of x (scores, state, outputs),
 // so a wave carries its own part through and only the outputs are added, a chunk later, through LDS.
 // VEC: rows are whole, aligned pieces; OUT: outputs (else the segment's own state alone); DEC: the tangent.
+// Two waves a SIMD where their registers suffice (prompt kernel, 128 x 128: 325 us against 383).
 template <int DX, int NW, int XS, bool F32, bool VEC, bool OUT, bool DEC>
-__global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
+__global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_chunk(LaArgs a) {
   constexpr int NP = F32 ? 3 : 1;                    // planes of an input
   constexpr int NC = F32 || DEC ? 3 : 2;             // planes of a computed operand of the outputs
   constexpr int WX = DX * 32, WZ = NW * 32;
@@ -233,7 +250,9 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
   constexpr int GX = kC * DX * 4 / NT, GZ = kC * NW * 4 / NT;  // 8-element groups per thread
   // 16 bytes between the tiles: at whole multiples of 512 the compiler joins a read of x with one of y,
   // and takes the results apart again with moves
-  constexpr int TX = NP * kC * WX + 8, TZ = NP * kC * WZ + 8, kBuf = (OUT ? 2 : 1) * TX + TZ;
+  constexpr int TX = NP * kC * WX + 8, TZ = NP * kC * WZ + 8;
+  constexpr bool TAN = OUT && DEC;                   // the tangent's sums: t's rows too
+  constexpr int kBuf = (OUT ? 2 : 1) * TX + (TAN ? 2 : 1) * TZ;
   constexpr int kBufs = F32 ? 1 : 2;
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   float* parts = (float*)(sm + kBufs * kBuf);        // outputs of the other parts of x: two chunks
@@ -283,7 +302,7 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
     if constexpr (DEC) get(St, a.t0);
   }
 
-  Raw<F32> rx[OUT ? GX : 1], ry[GX], rz[GZ];
+  Raw<F32> rx[OUT ? GX : 1], ry[GX], rz[GZ], rt[TAN ? GZ : 1];
   uint32_t ox[GX], oz[GZ];
 #pragma unroll
   for (int i = 0; i < GX; ++i) {
@@ -309,6 +328,12 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
 #pragma unroll
     for (int i = 0; i < GZ; ++i)
       rz[i] = load_group<F32, VEC>(cz, oz[i], a.z.w - z0 - ((tid + i * NT) % (NW * 4)) * 8);
+    if constexpr (TAN) {
+      const ChunkRows ct = chunk_rows(a.t, atz, t, r, EL, a.rev);
+#pragma unroll
+      for (int i = 0; i < GZ; ++i)
+        rt[i] = load_group<F32, VEC>(ct, oz[i], a.z.w - z0 - ((tid + i * NT) % (NW * 4)) * 8);
+    }
   };
   auto stage = [&](uint16_t* s) {
 #pragma unroll
@@ -321,6 +346,7 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
     for (int i = 0; i < GZ; ++i) {
       const int id = tid + i * NT, row = id / (NW * 4), c = (id % (NW * 4)) * 8;
       store_group<WZ, F32>(s + TX, row, c, rz[i]);
+      if constexpr (TAN) store_group<WZ, F32>(s + 2 * TX + TZ, row, c, rt[i]);
     }
   };
   double dec = 0.0;
@@ -328,9 +354,9 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
   fetch(p0);
   __syncthreads();
   // decay from position j (the register's) to i (the lane's), of the carried state, and to the chunk's end
-  float D[OUT ? 16 : 1], wz[16];
+  float D[OUT && !TAN ? 16 : 1], wz[16];
   const float wi = pw[col + 1 - a.e] * a.c_out;
-  if constexpr (OUT) {
+  if constexpr (OUT && !TAN) {
 #pragma unroll
     for (int n = 0; n < 16; ++n)
       D[n] = pw[max(col - (8 * (n >> 2) + 4 * hf + (n & 3)), 0)] * a.c_upd * a.c_out;
@@ -342,9 +368,10 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
       wz[n] = j < r ? pw[r - 1 - j + a.e] * a.c_upd : 0.0f;
     }
   };
-  weights(kC);
+  if constexpr (!TAN) weights(kC);
   const int part = 32 * DW * xs;                      // the wave's first x: bits of their own in an offset
   const int rat = row_at<WX>(lane) ^ part, cat = col_at<WX>(lane) ^ part, zat = col_at<WZ>(lane);
+  const int tat = row_at<WZ>(lane) ^ (zw * 32);
   const int ci = col - 4 * hf;                        // i >= j: ci >= 8 (n / 4) + n % 4
   uint32_t oo[OUT ? 4 : 1];                           // the lane's output pieces
   if constexpr (OUT) {
@@ -412,11 +439,14 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
 
   // One chunk; FULL: all its positions are inside the sequence (one block of code without branches, which
   // the scheduler can fill the waits of each part of with the others).
-  int buf = 0;
-  auto chunk = [&](auto full, int64_t p) {
+  // With the tangent the scheduler would move so much ahead that registers run out.
+  auto hold = [&]() {
+    if constexpr (TAN) __builtin_amdgcn_sched_barrier(0);
+  };
+  auto chunk = [&](auto full, int buf, int64_t p) {
     constexpr bool FULL = decltype(full)::value;
     uint16_t* sy = sm + buf * kBuf;
-    const uint16_t *sz = sy + TX, *sx = sz + TZ;
+    const uint16_t *sz = sy + TX, *sx = sz + TZ, *st = sx + TX;
     if constexpr (kBufs == 1) __syncthreads();
     stage(sy);
     __syncthreads();
@@ -425,12 +455,11 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
       odd = !odd;
       add_parts(odd ? 0 : 1);
     }
-    if constexpr (kBufs == 2) buf ^= 1;
     const int r = FULL ? kC : rows_at(p);
 
     Op<NP> zo[2];
     if constexpr (OUT) {
-      f32x16 O = zero16(), Ot = zero16(), P = zero16();
+      f32x16 O = zero16(), P = zero16();
 #pragma unroll
       for (int k = 0; k < 2 * DW; ++k) {
         const Op<NP> x = row_op<WX, NP>(sx, rat, k), y = row_op<WX, NP>(sy, rat, k);
@@ -441,18 +470,56 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
         for (int i = 0; i < 8; ++i) v[i] = S[k >> 1][8 * (k & 1) + i];
         split8(v, s);
         O = mm(s, x, O);
-        if constexpr (DEC) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = St[k >> 1][8 * (k & 1) + i];
-          split8(v, s);
-          Ot = mm(s, x, Ot);
-        }
+        hold();
       }
+      int cj = ci;
+      if constexpr (TAN) asm volatile("" : "+v"(cj));  // else the loop keeps 16 registers of counts
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
         O[n] *= wi;
-        if constexpr (DEC) Ot[n] = Ot[n] * wi + (float)(col + 1) * O[n];
-        P[n] = ci >= 8 * (n >> 2) + (n & 3) ? P[n] * D[n] : 0.0f;
+        const int ij = cj - (8 * (n >> 2) + (n & 3));
+        P[n] = ij >= 0 ? P[n] * (TAN ? pw[max(ij, 0)] * a.c_upd * a.c_out : D[n]) : 0.0f;
+      }
+      if constexpr (DEC) {
+        // t_i . (dO_i / dlog lambda), summed over i: (i + 1) t_i . O_i of the state before the chunk,
+        // sum_j (i - j) P_ij z_j . t_i, and <St, sum_i lambda^(i+1) x_i t_i^T>
+        float inter = 0.0f, rest = 0.0f;
+        f32x16 R = zero16();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const Op<NP> to = row_op<WZ, NP>(st, tat, k);
+          R = mm(row_op<WZ, NP>(sz, tat, k), to, R);
+          float v[8];
+          join8(to, v);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) inter += v[n] * O[8 * k + n];
+          hold();
+        }
+#pragma unroll
+        for (int n = 0; n < 16; ++n) rest += (float)(cj - (8 * (n >> 2) + (n & 3))) * P[n] * R[n];
+        rest += (float)(col + 1) * inter;
+        hold();
+        Op<3> wt[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v[8];
+          join8(col_op<WZ, NP>(st, zat, zw * 32, k), v);
+#pragma unroll
+          for (int n = 0; n < 8; ++n)  // lambda^(i+1) of the register's position
+            v[n] *= pw[16 * k + 8 * (n >> 2) + 4 * hf + (n & 3) + 1 - a.e] * a.c_out;
+          split8(v, wt[k]);
+        }
+        hold();
+#pragma unroll
+        for (int xt = 0; xt < DW; ++xt) {
+          f32x16 X = zero16();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) X = mm(col_op<WX, NP>(sx, cat, 32 * xt, k), wt[k], X);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) rest += St[xt][n] * X[n];
+          hold();
+        }
+        dec += rest;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -463,12 +530,7 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
         Op<NC> s;
         split8(v, s);
         O = mm(zo[k], s, O);
-        if constexpr (DEC) {
-#pragma unroll
-          for (int n = 0; n < 8; ++n) v[n] *= (float)(col - (16 * k + 8 * (n >> 2) + 4 * hf + (n & 3)));
-          split8(v, s);
-          Ot = mm(zo[k], s, Ot);
-        }
+        hold();
       }
       if constexpr (XS == 1) {
         put_rows(O, p, r);
@@ -480,25 +542,15 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
       } else {
         Ow = O, pwait = p, rwait = r;
       }
-      if constexpr (DEC) {
-        const ChunkRows ct = chunk_rows(a.t, atz, first_at(p, r), r, EL, a.rev);
-        float part = 0.0f;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const int left = a.z.w - zc - 8 * (n >> 2) - 4 * hf;
-          const int o = (n & 3) < left ? (int)(oo[n >> 2] - ct.adj + EL * (n & 3)) : -1;
-          const float t = F32 ? buf_ld(ct.r, o, 0) : bf16_value(buf_ld_u16(ct.r, o, 0));
-          part += col < r ? Ot[n] * t : 0.0f;
-        }
-        dec += part;
-      }
     } else {
 #pragma unroll
       for (int k = 0; k < 2; ++k) zo[k] = col_op<WZ, NP>(sz, zat, zw * 32, k);
     }
 
     // state: column operands of y times the weighted z (three planes: the state is an fp32 result)
-    if constexpr (!FULL) weights(r);
+    if constexpr (!FULL || TAN) weights(r);
+    int rj = r - 1 - 4 * hf;
+    if constexpr (TAN) asm volatile("" : "+v"(rj));
     const float keep = pw[r];
 #pragma unroll
     for (int xt = 0; xt < DW; ++xt)
@@ -510,34 +562,36 @@ __global__ __launch_bounds__(NW * XS * 64) void la_chunk(LaArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float v[8];
+      join8(zo[k], v);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        float zv = 0.0f;
-#pragma unroll
-        for (int s = NP - 1; s >= 0; --s) {
-          const uint32_t w = zo[k].p[s][n >> 1];
-          zv += __uint_as_float(n & 1 ? w & 0xFFFF0000u : w << 16);
-        }
-        v[n] = zv * wz[8 * k + n];
-      }
-      Op<3> s, st;
+      for (int n = 0; n < 8; ++n) v[n] *= wz[8 * k + n];
+      Op<3> s, sd;
       split8(v, s);
       if constexpr (DEC) {
 #pragma unroll
-        for (int n = 0; n < 8; ++n) v[n] *= (float)max(r - 1 - (16 * k + 8 * (n >> 2) + 4 * hf + (n & 3)), 0);
-        split8(v, st);
+        for (int n = 0; n < 8; ++n) v[n] *= (float)max(rj - (16 * k + 8 * (n >> 2) + (n & 3)), 0);
+        split8(v, sd);
       }
 #pragma unroll
       for (int xt = 0; xt < DW; ++xt) {
         const Op<NP> yo = col_op<WX, NP>(sy, cat, 32 * xt, k);
+        hold();
         S[xt] = mm(yo, s, S[xt]);
-        if constexpr (DEC) St[xt] = mm(yo, st, St[xt]);
+        if constexpr (DEC) St[xt] = mm(yo, sd, St[xt]);
       }
     }
   };
   int64_t p = p0;
-  for (; p + kC <= min(len, p1); p += kC) chunk(std::true_type{}, p);
-  for (; p < p1; p += kC) chunk(std::false_type{}, p);
+  int buf = 0;
+  if constexpr (DEC || F32 || !VEC) {
+    for (; p + kC <= min(len, p1); p += kC, buf ^= kBufs - 1) chunk(std::true_type{}, buf, p);
+  } else {
+    for (; p + 2 * kC <= min(len, p1); p += 2 * kC) {  // two, so that the buffers' addresses are constants
+      chunk(std::true_type{}, 0, p);
+      chunk(std::true_type{}, 1, p + kC);
+    }
+  }
+  for (; p < p1; p += kC, buf ^= kBufs - 1) chunk(std::false_type{}, buf, p);
   if constexpr (OUT && XS > 1) {
     __syncthreads();
     add_parts(odd ? 1 : 0);
@@ -764,14 +818,14 @@ int tiles(int w) { return w <= 64 ? 2 : 4; }
 int waves(int w) { return w <= 64 ? 2 : 4; }
 // A wide x over a narrow z: two waves share a column tile, so that four fill a CU's SIMDs and keep under
 // 256 registers (64 memories, 4096 tokens, 128 over 64: 60 us against 71); with the tangent they need
-// more all the same, and are faster alone (177 us against 226).
+// more all the same, and are faster alone (143 us against 246).
 constexpr int parts_of_x(int dx, int nw, bool tangent) { return dx == 4 && nw == 2 && !tangent ? 2 : 1; }
 
 template <int DX, int NW, int XS, bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   constexpr int NP = F32 ? 3 : 1;
-  constexpr int lds = (F32 ? 1 : 2) * 2 * (kC * NP * ((OUT ? 2 : 1) * DX * 32 + NW * 32) + 24) + 4 * (kC + 4) +
-                      (OUT ? 8 * (XS - 1) * NW * 1024 : 0);
+  constexpr int lds = (F32 ? 1 : 2) * 2 * (kC * NP * ((OUT ? 2 : 1) * DX * 32 + (OUT && DEC ? 2 : 1) * NW * 32) + 32) +
+                      4 * (kC + 4) + (OUT ? 8 * (XS - 1) * NW * 1024 : 0);
   auto kern = la_chunk<DX, NW, XS, F32, VEC, OUT, DEC>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
@@ -789,7 +843,7 @@ atlasmem_status chunk_pick(const LaArgs& a, int64_t blocks, hipStream_t st) {
     return nw == 2 ? chunk_launch<2, 2, 1, F32, VEC, OUT, DEC>(a, blocks, st)
                    : chunk_launch<2, 4, 1, F32, VEC, OUT, DEC>(a, blocks, st);
   return nw == 2 ? chunk_launch<4, 2, parts_of_x(4, 2, OUT && DEC), F32, VEC, OUT, DEC>(a, blocks, st)
-                 : chunk_launch<4, 4, 1, F32, VEC, OUT, DEC>(a, blocks, st);
+                 : chunk_launch<4, 4, parts_of_x(4, 4, OUT && DEC), F32, VEC, OUT, DEC>(a, blocks, st);
 }
 
 template <bool OUT>
