@@ -28,11 +28,11 @@
 // Few memories: the token axis is cut into segments whose own sums (state pass: y and z once more) are
 // scanned into start states, so that 512 workgroups fill the chip: two passes over memory, not one.
 //
-// Measured, bf16, 128 memories x 8192 tokens x 128 x 128: state pass 161 us, scan 22 us, outputs 366 us
-// (332 at the least; the clock falls to 1.7 GHz under matrix instructions): 1.07 GB at 2.9 TB/s, vector
+// Measured, bf16, 128 memories x 8192 tokens x 128 x 128: state pass 152 us, scan 21 us, outputs 355 us
+// (310 at the least; the clock falls to 1.7 GHz under matrix instructions): 1.07 GB at 3.0 TB/s, vector
 // instructions 53% and matrix instructions 33% of a SIMD's cycles: issue-bound, the splits and masks
-// first.  A call 465 us.
-// Training, 64 memories x 4096 x 64 x 128: 450 us, of which the tangent's kernel takes 145 (the outputs'
+// first.  A call 444 us.
+// Training, 64 memories x 4096 x 64 x 128: 430 us, of which the tangent's kernel takes 150 (the outputs'
 // tangents as rows of their own, St split into planes: 165).
 // One token, 1024 memories x 128 x 128: 29 us, 135 MB at 4.7 TB/s (a copy reaches 4.9).
 #include <algorithm>
@@ -290,6 +290,18 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
     auto get = [&](f32x16* D, const float* src) {
       if (!src || zc + col >= a.z.w) return;
       const float* p = src + slot * a.P + (int64_t)(zc + col) * a.ssz;
+      if (a.svec && a.ssx == 1) {
+#pragma unroll
+        for (int xt = 0; xt < DW; ++xt)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int x = 32 * (xs * DW + xt) + 8 * q + 4 * hf;
+            if (x >= a.x.w) continue;
+            const float4 f = *(const float4*)(p + x);
+            D[xt][4 * q] = f.x, D[xt][4 * q + 1] = f.y, D[xt][4 * q + 2] = f.z, D[xt][4 * q + 3] = f.w;
+          }
+        return;
+      }
 #pragma unroll
       for (int xt = 0; xt < DW; ++xt)
 #pragma unroll
@@ -601,6 +613,17 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
   auto put = [&](const f32x16* V, float* dst) {
     if (zc + col >= a.z.w) return;
     float* o = dst + (int64_t)(zc + col) * a.ssz;
+    if (a.svec && a.ssx == 1) {
+#pragma unroll
+      for (int xt = 0; xt < DW; ++xt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int x = 32 * (xs * DW + xt) + 8 * q + 4 * hf;
+          if (x < a.x.w)
+            *(float4*)(o + x) = float4{V[xt][4 * q], V[xt][4 * q + 1], V[xt][4 * q + 2], V[xt][4 * q + 3]};
+        }
+      return;
+    }
 #pragma unroll
     for (int xt = 0; xt < DW; ++xt)
 #pragma unroll
@@ -863,9 +886,9 @@ atlasmem_status chunk_run(const LaArgs& a, bool bf16, bool dec, int64_t M, hipSt
 }
 
 // Segments of the token axis: enough workgroups to fill the chip several times where the memories
-// alone do not, none shorter than two chunks (a segment's own time is 20 us and 1 to 2 us a chunk, a state of
-// the scan less: 1 x 1 x 1000 x 128 in fp32 forward 43 us, 56 at four chunks, 84 at eight; 24 memories x 1999
-// tokens x 64 in fp32 49, 53, 62; 64 x 1024 x 64 x 128 is the other way round, 49, 49, 42).
+// alone do not, none shorter than two chunks (1 x 1 x 1000 x 128 in fp32 forward 43 us, 56 at four chunks, 84
+// at eight; 24 memories x 1999 tokens x 64 in fp32 49, 53, 62; 64 x 1024 x 64 x 128 in bf16 49, 49, 42; each
+// 5 to 10 us less since states whose rows are consecutive move in 16-byte pieces).
 int segments(const LinAttn& s, int64_t& lseg) {
   const int64_t chunks = std::max<int64_t>((s.T + kC - 1) / kC, 1);
   const int64_t M = (int64_t)s.B * s.H;
@@ -996,6 +1019,7 @@ atlasmem_status linear_attention_backward(const LinAttn& s, const void* Q, const
   a.x = rows_of(K, s, s.dk), a.y = rows_of(Q, s, s.dk), a.z = rows_of(dY, s, s.dv), a.o = rows_of(dV, s, s.dv);
   a.ssx = 1, a.ssz = s.dk;
   a.sT = dW0;
+  a.svec = s.dk % 4 == 0 && (((uintptr_t)dWT | (uintptr_t)dW0) & 15) == 0;
   return chunk_run<true>(a, s.bf16, false, M, st);
 }
 
