@@ -504,8 +504,11 @@ atlasmem_status atlasmem_group_norm_backward(const void* X, const void* dY, int3
  *         and gradient are zero, whatever its X holds
  *   loss, lse: fp32 [n]
  *   workspace: atlasmem_cross_entropy_workspace_bytes(..., backward = 0) bytes, 16-byte aligned
- * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits); sums are
- * fp32.  n = 0 is valid.  Errors: E_INVALID for bad sizes, enums, null or overlapping pointers, a short
+ * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits), or in sums
+ * that an infinity or a float beyond bf16's largest enters as they are; sums are fp32.  A class can be
+ * masked by a column of ones in X and minus infinity or the lowest float in its row of W: its probability
+ * is zero and the loss finite (minus infinity makes dX's column of ones NaN: zero times it).
+ * n = 0 is valid.  Errors: E_INVALID for bad sizes, enums, null or overlapping pointers, a short
  * workspace; E_SHAPE beyond the limits.  The workspace function returns -1 for sizes that are refused. */
 int64_t atlasmem_cross_entropy_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab,
                                                int32_t backward);

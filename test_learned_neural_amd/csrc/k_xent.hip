@@ -11,7 +11,9 @@
 //
 // Types.  bf16 inputs are used as they are.  fp32 ones (and then G) go to LDS as they are and are split in
 // registers into three bf16 planes, whose six products down to 2^-16 of the leading one are summed in fp32
-// (relative 2^-24, at a sixth of the bf16 rate).
+// (relative 2^-24, at a sixth of the bf16 rate).  Sums that planes cannot hold (infinities, the lowest float: a
+// masked class) come out NaN and are taken from a second pass of the tile by fp32 matrix instructions; the
+// check alone costs 1% of a training pass (777 x 384 x 16001: 264 -> 268 us).
 // In bf16 G is rounded without its weight: the label's entry, -1 + p, is the large one and nearly exact
 // while p is small, where dloss (-1 + p) has one rounding error for all rows of equal weight (dX 3.7e-3 off
 // instead of 1.7e-3).  dX takes its rows' weights in the fp32 sums; dW takes them on X, relative to the
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   constexpr int kLoads = A::kLoads + B::kLoads;
   if constexpr (F32) {
     static_assert(kStages == 2, "a step in use, a step on its way");
-    float ra[MA][8], rb[NB][8];
+    const E *pa0 = pa, *pb0 = pb;
     auto load = [&](E* d) {
 #pragma unroll
       for (int n = 0; n < A::kLoads; ++n) load_a(n, d);
@@ -328,41 +330,96 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int n = 0; n < B::kLoads; ++n) load_b(n, d);
       next();
     };
-    auto read = [&](const E* s, int ks) {
+    // PLANES: operands split into three bf16 planes, six products; else fp32 matrix instructions
+    auto product = [&](auto planes, f32x16(&acc)[MA][NB]) {
+      constexpr bool PLANES = decltype(planes)::value;
+      float ra[MA][8], rb[NB][8];
+      auto read = [&](const E* s, int ks) {
 #pragma unroll
-      for (int i = 0; i < MA; ++i) A::op(s, wa + 32 * i, ks, lane, ra[i]);
+        for (int i = 0; i < MA; ++i) A::op(s, wa + 32 * i, ks, lane, ra[i]);
 #pragma unroll
-      for (int j = 0; j < NB; ++j) B::op(s + A::kElems, wb + 32 * j, ks, lane, rb[j]);
-    };
-    if (iters > 0) {
-      load(sm);
-      load(sm + kStage);
-      wait_all<kLoads>();
-      read(sm, 0);
-    }
-    for (int it = 0; it < iters; ++it) {
-      E *s = sm + (it & 1) * kStage, *d = sm + (~it & 1) * kStage;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        u32x4 ap[MA][3], bp[NB][3];
-#pragma unroll
-        for (int i = 0; i < MA; ++i) split_planes(ra[i], ap[i]);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) split_planes(rb[j], bp[j]);
-        if (ks == 1) {
-          wait_all<0>();
-          load(s);
-        }
-        read(ks ? d : s, ks ^ 1);
-        // the small products first
-        constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
-#pragma unroll
-        for (int q = 0; q < 6; ++q)
-#pragma unroll
-          for (int i = 0; i < MA; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ap[i][kA[q]], bp[j][kB[q]], acc[i][j]);
+        for (int j = 0; j < NB; ++j) B::op(s + A::kElems, wb + 32 * j, ks, lane, rb[j]);
+      };
+      if (iters > 0) {
+        load(sm);
+        load(sm + kStage);
+        wait_all<kLoads>();
+        read(sm, 0);
       }
+      for (int it = 0; it < iters; ++it) {
+        E *s = sm + (it & 1) * kStage, *d = sm + (~it & 1) * kStage;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          u32x4 ap[MA][3], bp[NB][3];
+          if constexpr (PLANES) {
+#pragma unroll
+            for (int i = 0; i < MA; ++i) split_planes(ra[i], ap[i]);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) split_planes(rb[j], bp[j]);
+          } else {
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+              for (int i = 0; i < MA; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                  acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(ra[i][n], rb[j][n], acc[i][j], 0, 0, 0);
+          }
+          if (ks == 1) {
+            wait_all<0>();
+            load(s);
+          }
+          read(ks ? d : s, ks ^ 1);
+          if constexpr (PLANES) {
+            // the small products first
+            constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+            for (int q = 0; q < 6; ++q)
+#pragma unroll
+              for (int i = 0; i < MA; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ap[i][kA[q]], bp[j][kB[q]], acc[i][j]);
+          }
+        }
+      }
+      // loads past the end may still be on their way to LDS
+      wait_all<0>();
+    };
+    product(std::true_type{}, acc);
+    // Planes have no infinity (inf - inf, and zero planes times it) and no float beyond bf16's largest: every
+    // sum that one enters is NaN.  Such sums (masked classes; or NaN in the inputs) are computed again as
+    // the definition has them; the tile's others stay, whatever their neighbours hold.
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) nan |= acc[i][j][n] != acc[i][j][n];
+    int* again = (int*)smem;
+    if (tid == 0) *again = 0;
+    __syncthreads();
+    if (nan) *again = 1;
+    __syncthreads();
+    const bool redo = __builtin_amdgcn_readfirstlane(*again);
+    __syncthreads();
+    if (redo) {
+      pa = pa0, pb = pb0, left = (int)(k1 - k0);
+      f32x16 exact[MA][NB];
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) exact[i][j][n] = 0.0f;
+      product(std::false_type{}, exact);
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            acc[i][j][n] = acc[i][j][n] == acc[i][j][n] ? acc[i][j][n] : exact[i][j][n];
     }
   } else {
     u32x4 ao[2][MA], bo[2][NB];
@@ -414,9 +471,9 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       }
       e = s, s = d;
     }
+    // loads past the end may still be on their way to LDS
+    wait_all<0>();
   }
-  // loads past the end may still be on their way to LDS
-  wait_all<0>();
 
   if constexpr (EPI == EPI_LSE) {
     float2* red = (float2*)smem;  // [WA][TB]
