@@ -86,8 +86,11 @@ struct Op {
   u32x4 p[N];
 };
 
-template <int N>
+// WIDE: of fp32 values, whose largest ones would round to an infinity: the first plane stops at bf16's largest,
+// and the others take the rest (a NaN stays in them).
+template <bool WIDE, int N>
 __device__ __forceinline__ void split8(const float* v, Op<N>& o) {
+  constexpr float kMost = 0x1.FEp127f;
   float r[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) r[i] = v[i];
@@ -95,7 +98,10 @@ __device__ __forceinline__ void split8(const float* v, Op<N>& o) {
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w = cvt_pk_bf16(r[2 * i], r[2 * i + 1]);
+      const bool stop = WIDE && n == 0;
+      const float a = stop ? __builtin_amdgcn_fmed3f(r[2 * i], -kMost, kMost) : r[2 * i];
+      const float b = stop ? __builtin_amdgcn_fmed3f(r[2 * i + 1], -kMost, kMost) : r[2 * i + 1];
+      const uint32_t w = cvt_pk_bf16(a, b);
       o.p[n][i] = w;
       if (n + 1 < N) {
         r[2 * i] -= __uint_as_float(w << 16);
@@ -193,7 +199,7 @@ __device__ __forceinline__ void store_group(uint16_t* s, int row, int c, const R
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(g.a[i >> 2][i & 3]);
     Op<3> o;
-    split8(v, o);
+    split8<F32>(v, o);
 #pragma unroll
     for (int n = 0; n < 3; ++n) put(n * kC * W, o.p[n]);
   } else {
@@ -480,7 +486,7 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = S[k >> 1][8 * (k & 1) + i];
-        split8(v, s);
+        split8<F32>(v, s);
         O = mm(s, x, O);
         hold();
       }
@@ -519,7 +525,7 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
 #pragma unroll
           for (int n = 0; n < 8; ++n)  // lambda^(i+1) of the register's position
             v[n] *= pw[16 * k + 8 * (n >> 2) + 4 * hf + (n & 3) + 1 - a.e] * a.c_out;
-          split8(v, wt[k]);
+          split8<F32>(v, wt[k]);
         }
         hold();
 #pragma unroll
@@ -540,7 +546,7 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
 #pragma unroll
         for (int n = 0; n < 8; ++n) v[n] = P[8 * k + n];
         Op<NC> s;
-        split8(v, s);
+        split8<F32>(v, s);
         O = mm(zo[k], s, O);
         hold();
       }
@@ -578,11 +584,11 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
 #pragma unroll
       for (int n = 0; n < 8; ++n) v[n] *= wz[8 * k + n];
       Op<3> s, sd;
-      split8(v, s);
+      split8<F32>(v, s);
       if constexpr (DEC) {
 #pragma unroll
         for (int n = 0; n < 8; ++n) v[n] *= (float)max(rj - (16 * k + 8 * (n >> 2) + (n & 3)), 0);
-        split8(v, sd);
+        split8<F32>(v, sd);
       }
 #pragma unroll
       for (int xt = 0; xt < DW; ++xt) {
