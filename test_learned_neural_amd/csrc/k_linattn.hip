@@ -178,6 +178,22 @@ __device__ __forceinline__ Raw<F32> load_group(const ChunkRows& c, uint32_t off,
   return g;
 }
 
+// Whether a group holds a NaN or an infinity.
+template <bool F32>
+__device__ __forceinline__ bool any_unbounded(const Raw<F32>& g) {
+  if constexpr (F32) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += 0.0f * __uint_as_float(g.a[i >> 2][i & 3]);
+    return t != t;
+  } else {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 t = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, g.a[0][i] | 0x80008000u));
+    return t[0] >= 0xFF80u || t[1] >= 0xFF80u;
+  }
+}
 // LDS tile of a chunk: 32 rows of W (64 or 128) elements, the 8-byte pieces of a row exchanged by bits of
 // its index so that both reads below touch every bank once: 32 rows at one column piece, and 4 rows at
 // 8 neighbouring pieces.
@@ -204,6 +220,21 @@ __device__ __forceinline__ void store_group(uint16_t* s, int row, int c, const R
     for (int n = 0; n < 3; ++n) put(n * kC * W, o.p[n]);
   } else {
     put(0, g.a[0]);
+  }
+}
+
+// Takes a group's elements that are no finite numbers out of a tile (they show in its last plane), and notes the
+// smallest position of each column's, and that there is one.
+template <int W, int NP>
+__device__ __forceinline__ void note_unbounded(uint16_t* s, int row, int c, int* from, int* any, int position) {
+  *any = 1;
+  const int f = exchange<W>(row);
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    uint16_t* e = s + row * W + ((((c + i) >> 2) ^ f) << 2) + (i & 3);
+    if ((e[(NP - 1) * kC * W] & 0x7F80) != 0x7F80) continue;
+    for (int n = 0; n < NP; ++n) e[n * kC * W] = 0;
+    atomicMin(from + c + i, position);
   }
 }
 
@@ -260,10 +291,14 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
   constexpr bool TAN = OUT && DEC;                   // the tangent's sums: t's rows too
   constexpr int kBuf = (OUT ? 2 : 1) * TX + (TAN ? 2 : 1) * TZ;
   constexpr int kBufs = F32 ? 1 : 2;
+  constexpr bool kAhead = !TAN || (VEC && !F32);     // the next chunk's rows wait in registers, where they have room
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   float* parts = (float*)(sm + kBufs * kBuf);        // outputs of the other parts of x: two chunks
   constexpr int kParts = OUT ? (XS - 1) * NW * 1024 : 0;
   float* pw = parts + 2 * kParts;                    // lambda^0 .. lambda^32
+  // Outputs: a NaN or infinity of z would reach the positions before it in its chunk, through zeros of the
+  // scores.  It does not enter the tiles: its column is NaN from its position on, the first of which is kept here.
+  int* from = (int*)(pw + kC + 4);                   // [WZ], and whether there is one
 
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hf = lane >> 5, col = lane & 31;
   const int nrun = OUT ? a.nseg : a.nseg - 1;        // the last segment's own sum starts nothing
@@ -277,6 +312,9 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
   const int64_t p0 = (int64_t)seg * a.lseg, p1 = min(p0 + a.lseg, a.T);
   const float g = a.log_decay[h];
   for (int i = tid; i <= kC; i += NT) pw[i] = decay_pow(g, i);
+  if constexpr (OUT) {
+    for (int i = tid; i <= WZ; i += NT) from[i] = i < WZ ? INT32_MAX : 0;
+  }
 
   constexpr int EL = F32 ? 4 : 2;
   // of a chunk at position p: rows inside the sequence, and its first token in memory
@@ -369,7 +407,7 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
   };
   double dec = 0.0;
 
-  fetch(p0);
+  if constexpr (kAhead) fetch(p0);
   __syncthreads();
   // decay from position j (the register's) to i (the lane's), of the carried state, and to the chunk's end
   float D[OUT && !TAN ? 16 : 1], wz[16];
@@ -465,10 +503,19 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
     constexpr bool FULL = decltype(full)::value;
     uint16_t* sy = sm + buf * kBuf;
     const uint16_t *sz = sy + TX, *sx = sz + TZ, *st = sx + TX;
+    if constexpr (!kAhead) fetch(p);
     if constexpr (kBufs == 1) __syncthreads();
     stage(sy);
+    if constexpr (OUT) {
+#pragma unroll
+      for (int i = 0; i < GZ; ++i) {
+        const int id = tid + i * NT, row = id / (NW * 4);
+        if (any_unbounded(rz[i]))
+          note_unbounded<WZ, NP>(sy + TX, row, (id % (NW * 4)) * 8, from, from + WZ, (int)(p - p0) + row);
+      }
+    }
     __syncthreads();
-    fetch(p + kC);
+    if constexpr (kAhead) fetch(p + kC);
     if constexpr (OUT && XS > 1) {
       odd = !odd;
       add_parts(odd ? 0 : 1);
@@ -550,6 +597,11 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
         O = mm(zo[k], s, O);
         hold();
       }
+      if (__builtin_amdgcn_readfirstlane(from[WZ])) {
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          if ((int)(p - p0) + col >= from[zw * 32 + 8 * (n >> 2) + 4 * hf + (n & 3)]) O[n] = __builtin_nanf("");
+      }
       if constexpr (XS == 1) {
         put_rows(O, p, r);
       } else if (xs) {
@@ -613,6 +665,20 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
   if constexpr (OUT && XS > 1) {
     __syncthreads();
     add_parts(odd ? 1 : 0);
+  }
+
+  if constexpr (OUT) {
+    __syncthreads();  // every chunk is staged
+    if (from[zw * 32 + col] != INT32_MAX) {
+#pragma unroll
+      for (int xt = 0; xt < DW; ++xt)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          S[xt][n] = __builtin_nanf("");
+          if constexpr (DEC) St[xt][n] = __builtin_nanf("");
+        }
+    }
+    if (DEC && from[WZ]) dec = __builtin_nan("");
   }
 
   // the state out: C-layout tiles to the caller's order
@@ -854,7 +920,7 @@ template <int DX, int NW, int XS, bool F32, bool VEC, bool OUT, bool DEC>
 atlasmem_status chunk_launch(const LaArgs& a, int64_t blocks, hipStream_t st) {
   constexpr int NP = F32 ? 3 : 1;
   constexpr int lds = (F32 ? 1 : 2) * 2 * (kC * NP * ((OUT ? 2 : 1) * DX * 32 + (OUT && DEC ? 2 : 1) * NW * 32) + 32) +
-                      4 * (kC + 4) + (OUT ? 8 * (XS - 1) * NW * 1024 : 0);
+                      4 * (kC + 4) + (OUT ? 4 * (NW * 32 + 4) + 8 * (XS - 1) * NW * 1024 : 0);
   auto kern = la_chunk<DX, NW, XS, F32, VEC, OUT, DEC>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
