@@ -14,10 +14,14 @@
 // (relative 2^-24, at a sixth of the bf16 rate).  Sums that planes cannot hold (infinities, the lowest float: a
 // masked class) come out NaN and are taken from a second pass of the tile by fp32 matrix instructions; the
 // check alone costs 1% of a training pass (777 x 384 x 16001: 264 -> 268 us).
-// In bf16 G is rounded without its weight: the label's entry, -1 + p, is the large one and nearly exact
-// while p is small, where dloss (-1 + p) has one rounding error for all rows of equal weight (dX 3.7e-3 off
-// instead of 1.7e-3).  dX takes its rows' weights in the fp32 sums; dW takes them on X, relative to the
-// largest one, so that equal weights round nothing.
+// In bf16 G is rounded, once: kept in fp32 its two products would take twice the matrix instructions.  dX's G is
+// rounded without its weight: the label's entry, -1 + p, is the large one and nearly exact while p is small,
+// where dloss (-1 + p) has one rounding error for all rows of equal weight (dX 3.7e-3 off instead of
+// 1.7e-3); dX takes its rows' weights in the fp32 sums.  dW sums over the rows, and its G is rounded with their
+// weights (over the largest one), X as it is.  Where all weights are one value the two are the same,
+// and that value is a factor of dW's fp32 sums (8192 x 2048 x 65536, all rows, gradients 5.60 ms; unequal weights, with
+// a second G to write, 5.86 ms.  Weights on X instead, a second rounding, took 5.58 ms; 1024 x 256 x 16384: dW
+// 2.36e-3 off instead of 2.19e-3, its rows of classes that are no label 2.65e-3 instead of 2.32e-3).
 //
 // Rows that are left out are left out of the products: the others' X is copied together, and the kernels
 // take their number from the device.
@@ -58,11 +62,15 @@ struct GemmArgs {
   const int* index;        // GRAD: [nb], b's rows in X
   int64_t v0, vocab;
   void* g;                 // GRAD: [nb][ldg]
+  void* gw;                // ... and times weight / *scale, or null; OUT: what b is then
+  const int* equal;        // ... where the weights are not all one value
+  int both;                // ... beside g, not in its place
+  const float* weight;     // GRAD: [rows of X]
   int64_t ldg;
   float* acc;              // ACC: [splits][acc_rows][na]
   int64_t acc_rows;
   int add;
-  const float* scale;      // OUT: one factor, or null
+  const float* scale;      // GRAD: see gw; OUT: one factor, or null
   void* out;               // [nb][ldo]
   int64_t ldo;
 };
@@ -215,7 +223,7 @@ __device__ __forceinline__ void wait_all() {
 // A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
 // through LDS, so that a row's columns leave in whole 16-byte pieces side by side.
 template <int TA, int TB, int MA, int NB, int NT>
-__device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, uint16_t* out,
+__device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, uint16_t* out,
                          int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr) {
   constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
   const int lane = tid & 63, hf = lane >> 5, col = lane & 31;
@@ -252,6 +260,40 @@ __device__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, in
   }
 }
 
+// The same in fp32, four columns a lane; added to what is there (rows of whole 16-byte pieces), or not.
+template <int MA, int NB>
+__device__ __forceinline__ void put_rows32(f32x16 (&acc)[MA][NB], int wa, int wb, int lane, float* out, int64_t ld,
+                                           int64_t c0, int64_t r0, int64_t nr, int add) {
+  const int hf = lane >> 5, col = lane & 31;
+  const bool vec = ld % 4 == 0 && ((uintptr_t)out & 15) == 0;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int64_t r = r0 + wb + 32 * j + col;
+    if (r >= nr) continue;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t c = c0 + wa + 32 * i + 8 * q + 4 * hf;
+        if (c >= ld) continue;
+        float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        float* p = out + r * ld + c;
+        if (add) {
+          const float4 o = *(const float4*)p;
+          x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
+        }
+        if (vec) {
+          *(float4*)p = x;
+        } else {
+          if (c + 0 < ld) p[0] = x.x;
+          if (c + 1 < ld) p[1] = x.y;
+          if (c + 2 < ld) p[2] = x.z;
+          if (c + 3 < ld) p[3] = x.w;
+        }
+      }
+  }
+}
+
 template <int TA, int TB, int WA, int WB, int kStages, bool AX, bool BX, int EPI, bool F32>
 __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   constexpr int NT = WA * WB * 64;
@@ -271,6 +313,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   if (g.count) {
     if constexpr (EPI == EPI_OUT) {
       g.K = *g.count;
+      if (g.gw && !*g.equal) g.b = g.gw;
     } else {
       g.nb = *g.count;
       g.tb = (int)((g.nb + TB - 1) / TB);
@@ -548,8 +591,24 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
             if (!kept || 32 * i + 8 * (n >> 2) + (n & 3) >= end) acc[i][j][n] = 0.0f;
       }
     }
-    if constexpr (!F32)
-      put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb);
+    const bool weighted = g.gw && !*g.equal;
+    auto put = [&](void* out) __attribute__((always_inline)) {
+      if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)out, g.ldg, a0, b0, g.nb, 0);
+      else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)out, g.ldg, a0, g.ldg, b0, g.nb);
+    };
+    if (g.both || !weighted) put(g.g);
+    if (weighted) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int64_t r = b0 + wb + 32 * j + col;
+        const float w = r < g.nb ? g.weight[g.index[r]] / *g.scale : 0.0f;
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
+      }
+      put(g.gw);
+    }
   }
 
   if constexpr (EPI == EPI_OUT) {
@@ -564,56 +623,32 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
   }
 
-  // fp32 outputs: four columns a lane
-  if constexpr (EPI == EPI_ACC || (F32 && EPI != EPI_LSE)) {
-    float* out = EPI == EPI_ACC ? g.acc + (int64_t)split * g.acc_rows * g.lda : (float*)(EPI == EPI_GRAD ? g.g : g.out);
-    const int64_t ld = EPI == EPI_ACC ? g.lda : EPI == EPI_GRAD ? g.ldg : g.ldo;
-    const bool vec = ld % 4 == 0 && ((uintptr_t)out & 15) == 0;
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int64_t r = b0 + wb + 32 * j + col;
-      if (r >= g.nb) continue;
-#pragma unroll
-      for (int i = 0; i < MA; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t c = a0 + wa + 32 * i + 8 * q + 4 * hf;
-          if (c >= ld) continue;
-          float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          float* p = out + r * ld + c;
-          if (EPI == EPI_ACC && g.add) {
-            const float4 o = *(const float4*)p;
-            x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
-          }
-          if (vec) {
-            *(float4*)p = x;
-          } else {
-            if (c + 0 < ld) p[0] = x.x;
-            if (c + 1 < ld) p[1] = x.y;
-            if (c + 2 < ld) p[2] = x.z;
-            if (c + 3 < ld) p[3] = x.w;
-          }
-        }
-    }
-  }
+  if constexpr (EPI == EPI_ACC)
+    put_rows32<MA, NB>(acc, wa, wb, lane, g.acc + (int64_t)split * g.acc_rows * g.lda, g.lda, a0, b0, g.nb, g.add);
+  if constexpr (F32 && EPI == EPI_OUT)
+    put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.out, g.ldo, a0, b0, g.nb, 0);
 }
 
 // The rows that count, those whose label is a class, in order (one workgroup): index [rows that count],
-// at [n] (a row's place among them, or -1), their number, and the largest |dloss| among them (1 without).
+// at [n] (a row's place among them, or -1), their number; and of their dloss the value that all have, or the
+// largest finite magnitude (1 without), and which.
 __global__ __launch_bounds__(1024) void xe_rows(const int64_t* labels, const float* dloss, int64_t n, int64_t vocab,
-                                                int* index, int* at, int* count, float* largest) {
+                                                int* index, int* at, int* count, float* scale, int* equal) {
   __shared__ int s[16];
-  __shared__ float sm[16];
+  __shared__ float sm[16], from[16], to[16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int base = 0;
-  float m = 0.0f;
+  float m = 0.0f, lo = INFINITY, hi = -INFINITY;
+  bool nan = false;
   for (int64_t i0 = 0; i0 < n; i0 += 1024) {
     const int64_t i = i0 + threadIdx.x;
     const int64_t y = i < n ? labels[i] : -1;
     const bool kept = y >= 0 && y < vocab;
     if (kept && dloss) {
-      const float w = fabsf(dloss[i]);
-      m = fmaxf(m, w <= 3.0e38f ? w : 0.0f);
+      const float w = dloss[i];
+      m = fmaxf(m, fabsf(w) <= 3.0e38f ? fabsf(w) : 0.0f);
+      lo = fminf(lo, w), hi = fmaxf(hi, w);
+      nan |= w != w;
     }
     const uint64_t mask = __ballot(kept);
     __syncthreads();
@@ -630,20 +665,25 @@ __global__ __launch_bounds__(1024) void xe_rows(const int64_t* labels, const flo
     if (kept) index[place] = (int)i;
     base += all;
   }
-  for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
-  if (lane == 0) sm[wave] = m;
+  if (nan) lo = -INFINITY, hi = INFINITY;
+  for (int k = 32; k; k >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, k));
+    lo = fminf(lo, __shfl_xor(lo, k)), hi = fmaxf(hi, __shfl_xor(hi, k));
+  }
+  if (lane == 0) sm[wave] = m, from[wave] = lo, to[wave] = hi;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int k = 1; k < 16; ++k) m = fmaxf(m, sm[k]);
+    for (int k = 1; k < 16; ++k) m = fmaxf(m, sm[k]), lo = fminf(lo, from[k]), hi = fmaxf(hi, to[k]);
     *count = base;
-    if (largest) *largest = m > 0.0f ? m : 1.0f;
+    *equal = lo >= hi;
+    *scale = lo == hi ? lo : m > 0.0f ? m : 1.0f;
   }
 }
 
 // Rows of an input as the products take them, [rows][dp], zero from column d on: all of them, or with
-// `index` those that count.  out_w: the same rows times dloss / largest.
+// `index` those that count.
 __global__ void xe_copy(const void* x, int bf16, int64_t rows, int d, int dp, const int* index, const int* count,
-                        const float* dloss, const float* largest, void* out, void* out_w) {
+                        void* out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // four columns
   const int64_t per = dp / 4;
   const int64_t r = i / per;
@@ -664,13 +704,9 @@ __global__ void xe_copy(const void* x, int bf16, int64_t rows, int d, int dp, co
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = c + k < d ? load_in(x, row * d + c + k, bf16) : 0.0f;
   }
-  auto put = [&](void* o, float w) {
-    const int64_t at = r * dp + c;
-    if (bf16) *(uint2*)((uint16_t*)o + at) = uint2{cvt_pk_bf16(v[0] * w, v[1] * w), cvt_pk_bf16(v[2] * w, v[3] * w)};
-    else *(float4*)((float*)o + at) = float4{v[0] * w, v[1] * w, v[2] * w, v[3] * w};
-  };
-  if (out) put(out, 1.0f);
-  if (out_w) put(out_w, dloss[row] / *largest);
+  const int64_t at = r * dp + c;
+  if (bf16) *(uint2*)((uint16_t*)out + at) = uint2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+  else *(float4*)((float*)out + at) = float4{v[0], v[1], v[2], v[3]};
 }
 
 // loss, lse of a row: a wave joins the tiles' maxima and sums, and takes the row's product with its
@@ -844,9 +880,9 @@ bool direct(const void* p, const CrossEntropy& s) {
 
 // What a call finds in its workspace, one behind the other.
 struct Space {
-  int *index, *at, *count;
-  float* largest;
-  char *x, *xw, *w, *g;
+  int *index, *at, *count, *equal;
+  float* scale;
+  char *x, *w, *g, *gw;
   float* acc;
   float2* part;
   int64_t bytes;
@@ -861,12 +897,12 @@ Space space_of(void* p, const CrossEntropy& s, const Plan& l, bool backward) {
   };
   const int64_t rows = l.el * s.n * (int64_t)l.dp;
   w.index = (int*)take(4 * s.n), w.at = (int*)take(4 * s.n);
-  w.count = (int*)take(8), w.largest = (float*)(w.count + 1);
+  w.count = (int*)take(12), w.equal = w.count + 1, w.scale = (float*)(w.count + 2);
   w.x = take(rows);
   w.w = take(l.el * s.vocab * (int64_t)l.dp);
   if (backward) {
-    w.xw = take(rows);
     w.g = take(l.el * s.n * l.piece);
+    w.gw = take(l.el * s.n * l.piece);
     w.acc = (float*)take(4 * (int64_t)l.splits * s.n * l.dp);
   } else {
     w.part = (float2*)take(8 * s.n * (int64_t)l.parts);
@@ -881,16 +917,15 @@ constexpr double kGatherFrom = 2e11;
 
 atlasmem_status rows_that_count(const CrossEntropy& s, const Space& w, const int64_t* labels, const float* dloss,
                                 hipStream_t st) {
-  xe_rows<<<1, 1024, 0, st>>>(labels, dloss, s.n, s.vocab, w.index, w.at, w.count, w.largest);
+  xe_rows<<<1, 1024, 0, st>>>(labels, dloss, s.n, s.vocab, w.index, w.at, w.count, w.scale, w.equal);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
 
 atlasmem_status copy_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int* index,
-                        const int* count, const float* dloss, const float* largest, void* out, void* out_w,
-                        hipStream_t st) {
+                        const int* count, void* out, hipStream_t st) {
   const int64_t blocks = (rows * (p.dp / 4) + 255) / 256;
-  xe_copy<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, index, count, dloss, largest, out, out_w);
+  xe_copy<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, index, count, out);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }
@@ -910,9 +945,9 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   if (gather) e = rows_that_count(s, ws, labels, nullptr, st);
   const int *index = gather ? ws.index : nullptr, *count = gather ? ws.count : nullptr;
   if (e == ATLASMEM_OK && (gather || !direct(X, s)))
-    e = copy_of(X, s, p, s.n, index, count, nullptr, nullptr, ws.x, nullptr, st);
+    e = copy_of(X, s, p, s.n, index, count, ws.x, st);
   if (e == ATLASMEM_OK && !direct(W, s))
-    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
+    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, ws.w, st);
   if (e != ATLASMEM_OK) return e;
   GemmArgs g = {};
   g.part = ws.part;
@@ -948,9 +983,9 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   const bool weighted = dW && dloss;
   atlasmem_status e = rows_that_count(s, ws, labels, dloss, st);
   if (e == ATLASMEM_OK)
-    e = copy_of(X, s, p, s.n, ws.index, ws.count, dloss, ws.largest, ws.x, weighted ? ws.xw : nullptr, st);
+    e = copy_of(X, s, p, s.n, ws.index, ws.count, ws.x, st);
   if (e == ATLASMEM_OK && !direct(W, s))
-    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, nullptr, nullptr, ws.w, nullptr, st);
+    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, ws.w, st);
   if (e != ATLASMEM_OK) return e;
   const char* wa = direct(W, s) ? (const char*)W : ws.w;
   for (int64_t v0 = 0; v0 < s.vocab; v0 += p.piece) {
@@ -962,7 +997,8 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     g.lda = g.ldb = p.dp;
     g.na = nv, g.nb = s.n, g.K = p.dp;
     g.labels = labels, g.lse = lse, g.index = ws.index, g.v0 = v0;
-    g.g = ws.g, g.ldg = ldg;
+    g.g = ws.g, g.ldg = ldg, g.both = dX != nullptr;
+    if (weighted) g.gw = dX ? ws.gw : ws.g, g.weight = dloss, g.scale = ws.scale, g.equal = ws.equal;
     e = gemm<false, false, EPI_GRAD>(g, s.bf16, side_of(nv, s.n, s.bf16), st);
     if (e != ATLASMEM_OK) return e;
     if (dX) {
@@ -978,8 +1014,8 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
     if (dW) {
       GemmArgs x = {};
       x.count = ws.count;
-      x.a = weighted ? ws.xw : ws.x, x.lda = p.dp, x.na = p.dp;
-      x.scale = weighted ? ws.largest : nullptr;
+      x.a = ws.x, x.lda = p.dp, x.na = p.dp;
+      if (weighted) x.gw = dX ? ws.gw : ws.g, x.scale = ws.scale, x.equal = ws.equal;
       x.b = ws.g, x.ldb = ldg, x.nb = nv;
       x.K = s.n;
       x.out = (char*)dW + v0 * s.d * p.el, x.ldo = s.d;
