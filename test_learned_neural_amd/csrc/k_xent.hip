@@ -84,11 +84,15 @@ struct GemmArgs {
 //
 // The load is written out because the compiler, knowing it, waits for all of them before every
 // transposing read.  It has no result register: its address is read when it is issued, and what it
-// writes, LDS, is waited for by wait_all alone.
+// writes, LDS, is waited for by wait_all alone.  m0, which the compiler takes for its own, is put back.
 __device__ __forceinline__ void load_to_lds(rsrc_t rs, uint32_t voff, const void* lds) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(voff), "s"(rs)
-               : "m0", "memory");
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+               "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "s"(at), "v"(voff), "s"(rs)
+               : "memory");
 }
 template <int R, bool ACROSS, int WAVES>
 struct Tile {

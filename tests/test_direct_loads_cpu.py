@@ -1,7 +1,7 @@
 """The loads that cross entropy writes out by hand (memory straight to LDS), in the source and in the assembly
-that the build's own flags give: each has its LDS address in m0 and says that it writes it, nothing else uses
-m0, and no register of its buffer was written by a vector instruction less than five wait states before (the
-compiler, which keeps that distance for its own loads, does not look inside)."""
+that the build's own flags give: each has its LDS address in m0 and puts back what was there (the compiler
+takes m0 for its own), and no register of its buffer was written by a vector instruction less than five wait
+states before (the compiler, which keeps that distance for its own loads, does not look inside)."""
 
 import os
 import re
@@ -13,16 +13,6 @@ from test_learned_neural_amd import build
 
 SOURCE = os.path.join(build.CSRC, "k_xent.hip")
 LOAD = re.compile(r"buffer_load_dwordx4 v\d+, s\[(\d+):(\d+)\], 0 offen lds$")
-
-
-def test_the_source_says_that_m0_is_written():
-    text = open(SOURCE).read()
-    blocks = re.findall(r"asm volatile\((.*?)\);", text, flags=re.S)
-    writes = [b for b in blocks if "s_mov_b32 m0" in b]
-    assert len(writes) == 1
-    for b in writes:
-        clobbers = b.rsplit(":", 1)[1]
-        assert '"m0"' in clobbers and '"memory"' in clobbers
 
 
 @pytest.fixture(scope="module")
@@ -48,14 +38,16 @@ def kernels(tmp_path_factory):
     return {k: v for k, v in found.items() if any(i and LOAD.match(i) for i in v)}
 
 
-def test_every_load_sets_m0_and_nothing_else_does(kernels):
+def test_every_load_sets_m0_and_puts_it_back(kernels):
     assert len(kernels) >= 16
     for name, code in kernels.items():
         loads = [k for k, i in enumerate(code) if i and LOAD.match(i)]
         for k in loads:
-            assert re.match(r"s_mov_b32 m0, s\d+$", code[k - 2]) and code[k - 1] == "s_nop 0", (name, code[k - 2:k + 1])
-        uses = [k for k, i in enumerate(code) if i and re.search(r"\bm0\b", i)]
-        assert uses == [k - 2 for k in loads], name
+            kept = re.match(r"s_mov_b32 (s\d+), m0$", code[k - 3] or "")
+            assert kept, (name, code[k - 3:k + 2])
+            address = re.match(r"s_mov_b32 m0, (s\d+)$", code[k - 2] or "")
+            assert address and address[1] != kept[1] and code[k - 1] == "s_nop 0", (name, code[k - 3:k + 2])
+            assert code[k + 1] == f"s_mov_b32 m0, {kept[1]}", (name, code[k - 3:k + 2])
 
 
 def test_no_load_reads_a_register_that_a_vector_instruction_just_wrote(kernels):
