@@ -519,9 +519,9 @@ atlasmem_status atlasmem_cross_entropy(const void* X, const void* W, int32_t dty
 
 /* Its gradients: with G_iv = dloss_i (exp(z_iv - lse_i) - [v = label_i]), dX = G W and dW = G^T X.  The
  * logits are computed again, a piece of the vocabulary at a time; G's pieces pass through the workspace
- * in the type of X, for dX without their weight dloss, which its fp32 sums take, for dW with it (where
- * weights are one value, without, too).  In bf16 this is one rounding of every term of dX and dW,
- * beside that of the outputs.
+ * in the type of X (256 MB, or 2048 classes of all rows if that is more), for dX without their weight
+ * dloss, which its fp32 sums take, for dW with it (where weights are one value, without, too).  In bf16
+ * this is one rounding of every term of dX and dW, beside that of the outputs.
  *   lse: the forward's;  dloss: fp32 [n], or NULL (one each)
  *   dX: [n, d], dW: [vocab, d] of `dtype`, written, not added to; either may be NULL (not computed)
  *   workspace: atlasmem_cross_entropy_workspace_bytes(..., backward = 1) bytes

@@ -56,11 +56,10 @@ struct GemmArgs {
   // epilogues
   float2* part;            // LSE: [nb][parts]: (maximum, sum of exponentials)
   int parts;
-  int part0;
   const int64_t* labels;   // [rows of X]
   const float* lse;
   const int* index;        // GRAD: [nb], b's rows in X
-  int64_t v0, vocab;
+  int64_t v0;
   void* g;                 // GRAD: [nb][ldg]
   void* gw;                // ... and times weight / *scale, or null; OUT: what b is then
   const int* equal;        // ... where the weights are not all one value
@@ -560,7 +559,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
         const float2 q = red[w * TB + r];
         s += q.x == m ? q.y : q.y * __expf(q.x - m);
       }
-      g.part[(b0 + r) * g.parts + g.part0 + a0 / TA] = float2{m, s};
+      g.part[(b0 + r) * g.parts + a0 / TA] = float2{m, s};
     }
   }
 
@@ -854,23 +853,25 @@ atlasmem_status gemm(const GemmArgs& g, bool bf16, int side, hipStream_t st) {
 // The inputs as the engine takes them: bf16 rows of whole, aligned 16-byte pieces.
 struct Plan {
   int el, dp;                   // bytes of an element, elements of a copied row
-  int64_t n, vocab, piece;      // classes of a piece
+  int64_t piece;                // classes of a piece of G
   int parts, splits;
-  int side_x;                   // of dX's tiles
+  int side, side_x;             // of the forward's and of dX's tiles
 };
 
-constexpr int64_t kPieceBytes = 256 << 20;  // of G: what the last-level cache holds
+// A piece of G: what the last-level cache holds, and 2048 classes at least (from 65536 bf16 rows on, then, it grows
+// with them), since dX's fp32 sums pass through memory once for every piece.
+constexpr int64_t kPieceBytes = 256 << 20, kPieceClasses = 2048;
 
 Plan plan_of(const CrossEntropy& s) {
   Plan p = {};
   p.el = s.bf16 ? 2 : 4;
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
-  p.n = s.n, p.vocab = s.vocab;
   int64_t piece = kPieceBytes / std::max<int64_t>(s.n * p.el, 1) / 256 * 256;
-  piece = std::max<int64_t>(piece, 2048);
+  piece = std::max(piece, kPieceClasses);
   const int64_t pieces = (s.vocab + piece - 1) / piece;
   p.piece = up((s.vocab + pieces - 1) / pieces, 256);
-  p.parts = (int)((s.vocab + 63) / 64);
+  p.side = side_of(s.vocab, s.n, s.bf16);
+  p.parts = (int)((s.vocab + p.side - 1) / p.side);
   p.side_x = side_split(p.dp, s.n, s.bf16);
   const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.side_x), 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.side_x == 256 ? 256 : 512) / tiles, p.piece / 512));
@@ -960,9 +961,8 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   g.lda = g.ldb = p.dp;
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
   g.count = count;
-  const int side = side_of(s.vocab, s.n, s.bf16);
-  g.parts = (int)((s.vocab + side - 1) / side);
-  e = gemm<false, false, EPI_LSE>(g, s.bf16, side, st);
+  g.parts = p.parts;
+  e = gemm<false, false, EPI_LSE>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, gather ? ws.at : nullptr, X, W, s.bf16,
                                                      direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss,
