@@ -437,7 +437,7 @@ atlasmem_status atlasmem_gates(const void* U, int64_t B, int64_t T, int32_t d_mo
  * bf16 inputs enter the products as they are, fp32 ones as three bf16 planes (24 bits); states and
  * sums are fp32, Y is rounded once.  Products and sums should stay below the largest float (bf16 calls:
  * below bf16's largest).  A NaN or infinity of a token reaches what the recurrence lets it reach and no
- * token before it (the gradients': none behind it); in longer calls an infinity arrives as NaN.
+ * token before it (the gradients': none behind it); an infinity may arrive as NaN.
  * Errors: E_INVALID for bad sizes, enums, null or overlapping pointers, a short workspace; E_SHAPE
  * beyond the limits (heads <= 65536, batch * heads <= 2^20).  The workspace function returns -1 for
  * sizes that the calls refuse. */

@@ -224,17 +224,29 @@ __device__ __forceinline__ void store_group(uint16_t* s, int row, int c, const R
 }
 
 // Takes a group's elements that are no finite numbers out of a tile (they show in its last plane), and notes the
-// smallest position of each column's, and that there is one.
+// smallest position of each column's, and that there is one.  In pieces of four, as store_group writes them.
 template <int W, int NP>
 __device__ __forceinline__ void note_unbounded(uint16_t* s, int row, int c, int* from, int* any, int position) {
   *any = 1;
-  const int f = exchange<W>(row);
 #pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    uint16_t* e = s + row * W + ((((c + i) >> 2) ^ f) << 2) + (i & 3);
-    if ((e[(NP - 1) * kC * W] & 0x7F80) != 0x7F80) continue;
-    for (int n = 0; n < NP; ++n) e[n * kC * W] = 0;
-    atomicMin(from + c + i, position);
+  for (int h = 0; h < 2; ++h) {
+    uint16_t* piece = s + row * W + ((((c >> 2) | h) ^ exchange<W>(row)) << 2);
+    const uint2 w = *(const uint2*)(piece + (NP - 1) * kC * W);
+    uint32_t lo = 0xFFFFFFFFu, hi = 0xFFFFFFFFu;  // what stays
+    auto look = [&](uint32_t pair, uint32_t exponent, uint32_t& keep, int i) {
+      if ((pair & exponent) != exponent) return;
+      keep &= exponent > 0xFFFFu ? 0x0000FFFFu : 0xFFFF0000u;
+      atomicMin(from + c + 4 * h + i, position);
+    };
+    look(w.x, 0x7F80u, lo, 0);
+    look(w.x, 0x7F800000u, lo, 1);
+    look(w.y, 0x7F80u, hi, 2);
+    look(w.y, 0x7F800000u, hi, 3);
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      uint2* p = (uint2*)(piece + n * kC * W);
+      *p = uint2{p->x & lo, p->y & hi};
+    }
   }
 }
 

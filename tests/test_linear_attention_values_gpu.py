@@ -61,3 +61,30 @@ def test_a_bad_value_reaches_no_token_that_it_should_not(kw, which, value):
     others[0, 0] = False
     for name in ("W_T", "dW0", "Y", "dQ", "dK", "dV"):
         assert np.array_equal(a[name][others], b[name][others]), name
+
+
+@pytest.mark.parametrize("dtype", [am.BF16, am.F32])
+@pytest.mark.parametrize("B,T,dk,dv", [(64, 203, 128, 64), (1, 900, 64, 128), (64, 170, 50, 23)])
+def test_many_bad_values_over_many_chunks(dtype, B, T, dk, dv):
+    """In V, and for the gradients in Q: each column of one memory is clean up to its first (behind its last) one,
+    and bad from there on."""
+    kw = dict(dtype=dtype, B=B, H=8, T=T, dk=dk, dv=dv)
+    clean = run(Case(**kw))
+    rng = np.random.default_rng(T)
+    log(f"CASE many bad values {kw}")
+    for which, name, w in (("v", "Y", dv), ("q", "dK", dk)):
+        c = Case(**kw)
+        t, col = rng.integers(0, T, 25), rng.integers(0, w, 25)
+        t[:3], col[:3] = (0, T - 1, T // 2), (0, w - 1, w // 2)
+        for i in range(25):
+            c.host[which][B - 1, 7, t[i], col[i]] = (np.nan, np.inf, -np.inf)[i % 3]
+        got = run(c)
+        bad = np.zeros(got[name].shape, dtype=bool)
+        for i in range(25):
+            bad[B - 1, 7, slice(t[i], None) if which == "v" else slice(None, t[i] + 1), col[i]] = True
+        assert np.array_equal(got[name][~bad], clean[name][~bad])
+        assert not np.isfinite(got[name][bad]).any()
+        others = np.ones((B, 8), dtype=bool)
+        others[B - 1, 7] = False
+        for n in ("Y", "W_T", "dQ", "dK", "dV", "dW0"):
+            assert np.array_equal(got[n][others], clean[n][others]), n
