@@ -8,11 +8,11 @@
 // reduction, and a second pass that applies them.  Variances come from differences to a mean, never
 // from a difference of sums; fp32 throughout, one rounding at the end; sums run in one order.
 //
-// Bound by memory.  bf16 16384 rows x 16 groups of 128: forward 26.7 us (134 MB at 5.0 TB/s; 34 us before
-// the next row's loads were in flight while one is computed), backward 58.7 us (201 MB and the partial
-// sums at 3.6 TB/s) and gamma's and beta's sums 9 us.  fp32 3 x 16385 x 512 with 32 groups: moments 17.5,
-// apply 32, sums 36, gradient 53 us (101 MB a tensor, which the last-level cache holds: 5.7 to 6.3 TB/s),
-// the small reductions 5 to 9 us each.  One token: 3 us, a launch.
+// Bound by memory.  bf16 16384 rows x 16 groups of 128: forward 25.1 us (134 MB at 5.3 TB/s; 34 us before
+// the next row's loads were in flight while one is computed), backward 54.7 us (201 MB and the partial
+// sums at 4.0 TB/s) and gamma's and beta's sums 7 us.  fp32 3 x 16385 x 512 with 32 groups: moments 17.4,
+// apply 31.8, sums 35.6, gradient 51.1 us (101 MB a tensor, which the last-level cache holds: 5.7 to 6.3 TB/s),
+// the small reductions 4 to 8 us each.  One token: 3 us, a launch.
 #include <algorithm>
 
 #include "common.h"

@@ -28,13 +28,12 @@
 // Few memories: the token axis is cut into segments whose own sums (state pass: y and z once more) are
 // scanned into start states, so that 512 workgroups fill the chip: two passes over memory, not one.
 //
-// Measured, bf16, 128 memories x 8192 tokens x 128 x 128: state pass 152 us, scan 21 us, outputs 355 us
-// (310 at the least; the clock falls to 1.7 GHz under matrix instructions): 1.07 GB at 3.0 TB/s, vector
-// instructions 53% and matrix instructions 33% of a SIMD's cycles: issue-bound, the splits and masks
-// first.  A call 444 us.
-// Training, 64 memories x 4096 x 64 x 128: 430 us, of which the tangent's kernel takes 150 (the outputs'
+// Measured, bf16, 128 memories x 8192 tokens x 128 x 128, in one run: state pass 130 us, scan 18 us, outputs 291 us
+// (1.07 GB at 3.7 TB/s), in a call of 446 us (435 to 459 in others).  Issue-bound: counters show the outputs kernel's
+// vector instructions, the splits and masks first, in 42% and its matrix instructions in 32% of a SIMD's cycles.
+// Training, 64 memories x 4096 x 64 x 128: 428 to 447 us, of which the tangent's kernel takes 146 (the outputs'
 // tangents as rows of their own, St split into planes: 165).
-// One token, 1024 memories x 128 x 128: 29 us, 135 MB at 4.7 TB/s (a copy reaches 4.9).
+// One token, 1024 memories x 128 x 128: 29 us, 135 MB at 4.7 TB/s (copies reach 4.8 to 5.6).
 #include <algorithm>
 #include <type_traits>
 
@@ -303,7 +302,10 @@ __global__ __launch_bounds__(NW * XS * 64, DEC || F32 || !VEC ? 1 : 2) void la_c
   constexpr bool TAN = OUT && DEC;                   // the tangent's sums: t's rows too
   constexpr int kBuf = (OUT ? 2 : 1) * TX + (TAN ? 2 : 1) * TZ;
   constexpr int kBufs = F32 ? 1 : 2;
-  constexpr bool kAhead = !TAN || (VEC && !F32);     // the next chunk's rows wait in registers, where they have room
+  // The next chunk's rows wait in registers where these have room: with the tangent, fp32 or unaligned rows would
+  // spill (backward with them waiting and without: bf16 rows of 101 and 66 517 and 513 us, fp32 128 x 128 254,
+  // with 180 bytes of scratch a lane, and 260).
+  constexpr bool kAhead = !TAN || (VEC && !F32);
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   float* parts = (float*)(sm + kBufs * kBuf);        // outputs of the other parts of x: two chunks
   constexpr int kParts = OUT ? (XS - 1) * NW * 1024 : 0;
@@ -925,7 +927,7 @@ int tiles(int w) { return w <= 64 ? 2 : 4; }
 int waves(int w) { return w <= 64 ? 2 : 4; }
 // A wide x over a narrow z: two waves share a column tile, so that four fill a CU's SIMDs and keep under
 // 256 registers (64 memories, 4096 tokens, 128 over 64: 60 us against 71); with the tangent they need
-// more all the same, and are faster alone (143 us against 246).
+// more all the same, and one alone is faster (177 us against 226).
 constexpr int parts_of_x(int dx, int nw, bool tangent) { return dx == 4 && nw == 2 && !tangent ? 2 : 1; }
 
 template <int DX, int NW, int XS, bool F32, bool VEC, bool OUT, bool DEC>

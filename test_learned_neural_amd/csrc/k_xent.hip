@@ -13,24 +13,25 @@
 // registers into three bf16 planes, whose six products down to 2^-16 of the leading one are summed in fp32
 // (relative 2^-24, at a sixth of the bf16 rate).  Sums that planes cannot hold (infinities, the lowest float: a
 // masked class) come out NaN and are taken from a second pass of the tile by fp32 matrix instructions; the
-// check alone costs 1% of a training pass (777 x 384 x 16001: 264 -> 268 us).
+// check alone costs 3% of a training pass (777 x 384 x 16001: 257 -> 266 us, both timed in turn).
 // In bf16 G is rounded, once: kept in fp32 its two products would take twice the matrix instructions.  dX's G is
 // rounded without its weight: the label's entry, -1 + p, is the large one and nearly exact while p is small,
 // where dloss (-1 + p) has one rounding error for all rows of equal weight (dX 3.7e-3 off instead of
 // 1.7e-3); dX takes its rows' weights in the fp32 sums.  dW sums over the rows, and its G is rounded with their
 // weights (over the largest one), X as it is.  Where all weights are one value the two are the same,
-// and that value is a factor of dW's fp32 sums (8192 x 2048 x 65536, all rows, gradients 5.60 ms; unequal weights, with
-// a second G to write, 5.86 ms.  Weights on X instead, a second rounding, took 5.58 ms; 1024 x 256 x 16384: dW
-// 2.36e-3 off instead of 2.19e-3, its rows of classes that are no label 2.65e-3 instead of 2.32e-3).
+// and that value is a factor of dW's fp32 sums (8192 x 2048 x 65536, all rows, gradients 5.57 ms; unequal
+// weights, with a second G to write, 5.77 ms.  Weights on X instead, a second rounding, took 5.52 ms, and dW of
+// 1024 x 256 x 16384 was 2.36e-3 off instead of 2.19e-3, its rows of classes that are no label 2.65e-3
+// instead of 2.32e-3).
 //
 // Rows that are left out are left out of the products: the others' X is copied together, and the kernels
 // take their number from the device.
 //
 // Measured, bf16, 8192 rows (7373 count) x 2048 x 65536: logits 1.69 ms (1.17 PFLOP/s), then for each of
-// four pieces G 487 us (1.02; of that 70 us are its stores), dX 434 us (1.14), dW 393 us (1.26): 6.9 ms a
+// four pieces G 496 us (1.00; of that 70 us are its stores), dX 431 us (1.15), dW 379 us (1.31): 7.0 ms a
 // training pass.  A library's plain product of these sizes reaches 1.2 (logits, written out) to 1.5
 // PFLOP/s; both run at 1.65 GHz, the power limit, with the matrix cores 75% (the library 85%) busy.
-// One row x 1024 x 50257: 18 to 21 us for W's 103 MB (4.9 TB/s).
+// One row x 1024 x 50257: 20 us for W's 103 MB (5.2 TB/s).
 #include <algorithm>
 #include <type_traits>
 
