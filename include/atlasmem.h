@@ -531,6 +531,68 @@ atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, in
                                                 const float* dloss, void* dX, void* dW, void* workspace,
                                                 int64_t workspace_bytes, void* stream);
 
+/* Log probabilities of given tokens under z = scale X W^T, with each row's entropy and top alternatives,
+ * without keeping the logits: what a sampled or a given text is scored with, and what a teacher tells a student
+ * (atlasmem_distillation):
+ *   lse_i = log sum_v exp(z_iv),  logprob_i = z_i,token_i - lse_i,  entropy_i = lse_i - sum_v exp(z_iv - lse_i) z_iv
+ *   X: [n, d], W: [vocab, d] of `dtype`, with the limits of atlasmem_cross_entropy
+ *   scale: > 0, finite (the reciprocal of a temperature)
+ *   tokens: int64 [n], or NULL (all rows count, no logprob); a row whose token is no class (negative, or >= vocab)
+ *         is left out: logprob, entropy and top_logprobs 0, top_ids -1, whatever its X holds
+ *   top: alternatives asked for, 0..64, at most vocab
+ *   logprob, entropy: fp32 [n], either may be NULL
+ *   top_ids: int64 [n, top], top_logprobs: fp32 [n, top] (NULL with top 0): the classes of the largest logits,
+ *         largest first, equal ones by their index.  Their order is that of products summed in 64 bits.  A logit
+ *         of -1e38 or less is a masked class and no alternative: places that are left hold -1 and -INFINITY
+ *   workspace: atlasmem_token_logprobs_workspace_bytes(...) bytes, 16-byte aligned
+ * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits); sums are fp32.  A
+ * row with a NaN or an infinite logit has NaN for its numbers and no alternatives (-1); one whose logits are all
+ * minus infinity logprob -INFINITY, entropy 0 and no alternatives.
+ * n = 0 is valid.  Equal calls give equal bits.  Errors: E_INVALID for bad sizes, enums, scales, null or
+ * overlapping pointers, a short workspace; E_SHAPE beyond the limits.  The workspace function returns -1 for
+ * sizes that are refused. */
+int64_t atlasmem_token_logprobs_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top);
+atlasmem_status atlasmem_token_logprobs(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                        int64_t vocab, float scale, const int64_t* tokens, int32_t top, float* logprob,
+                                        float* entropy, int64_t* top_ids, float* top_logprobs, void* workspace,
+                                        int64_t workspace_bytes, void* stream);
+
+/* Distillation: a student's rows z = X W^T against a teacher's top logits, the outer loss where the target is a
+ * distribution over some classes instead of one label:
+ *   p_i = softmax_j(scale teacher_ij) over the row's given classes,  q_i = softmax_v(scale z_iv) over all
+ *   loss_i = sum_j p_ij (log p_ij - log q_i,ids_ij),   lse_i = log sum_v exp(scale z_iv)
+ *   X: [n, d], W: [vocab, d] of `dtype`, with the limits of atlasmem_cross_entropy and vocab <= 2^21
+ *   ids: int64 [n, top] (1..128), teacher: fp32 [n, top], logits or log probabilities, in any order.  An id that
+ *         is no class, or a logit of -INFINITY, is no entry; entries of one class add up.  A row without an
+ *         entry is left out: its loss, lse and gradient are zero, whatever its X holds
+ *   scale: > 0, finite (the reciprocal of a temperature)
+ *   loss, lse: fp32 [n]
+ *   kept: atlasmem_distillation_kept_bytes(...) bytes, 16-byte aligned, what the backward reads (q of every
+ *         row and class up to a factor of the row, in `dtype`, less the teacher's), or NULL (loss alone)
+ *   workspace: atlasmem_distillation_workspace_bytes(...) bytes, 16-byte aligned, backward = 1 with `kept`
+ * Products as in atlasmem_token_logprobs.  A NaN stays in its row's loss.  n = 0 is valid.  Equal calls give
+ * equal bits.  Errors: E_INVALID for bad sizes, enums, scales, null or overlapping pointers, a short kept or
+ * workspace; E_SHAPE beyond the limits.  The size functions return -1 for sizes that are refused. */
+int64_t atlasmem_distillation_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top,
+                                              int32_t backward);
+int64_t atlasmem_distillation_kept_bytes(int32_t dtype, int64_t n, int64_t vocab, int32_t top);
+atlasmem_status atlasmem_distillation(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d, int64_t vocab,
+                                      int32_t top, const int64_t* ids, const float* teacher, float scale, float* loss,
+                                      float* lse, void* kept, int64_t kept_bytes, void* workspace,
+                                      int64_t workspace_bytes, void* stream);
+
+/* Its gradients: with G_iv = q_iv - sum_{j: ids_ij = v} p_ij, dX_i = scale dloss_i (G W)_i and
+ * dW = G^T (scale dloss X).  Two products: G is what the forward kept.  In bf16 every term of dX has one rounding
+ * beside the output's, G's, and every term of dW two, G's and that of its weighted row of X.
+ *   X, W and the sizes: the forward's;  kept: as the forward left it (read only: more calls may follow)
+ *   dloss: fp32 [n], or NULL (one each)
+ *   dX: [n, d], dW: [vocab, d] of `dtype`, written, not added to; either may be NULL (not computed)
+ *   workspace: atlasmem_distillation_workspace_bytes(..., backward = 1) bytes; may be the forward's */
+atlasmem_status atlasmem_distillation_backward(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                               int64_t vocab, int32_t top, const void* kept, int64_t kept_bytes,
+                                               const float* dloss, void* dX, void* dW, void* workspace,
+                                               int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

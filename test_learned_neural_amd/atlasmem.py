@@ -39,6 +39,9 @@ EXPORTS = (
     "atlasmem_linear_attention_workspace_bytes", "atlasmem_linear_attention", "atlasmem_linear_attention_backward",
     "atlasmem_group_norm_workspace_bytes", "atlasmem_group_norm", "atlasmem_group_norm_backward",
     "atlasmem_cross_entropy_workspace_bytes", "atlasmem_cross_entropy", "atlasmem_cross_entropy_backward",
+    "atlasmem_token_logprobs_workspace_bytes", "atlasmem_token_logprobs",
+    "atlasmem_distillation_workspace_bytes", "atlasmem_distillation_kept_bytes", "atlasmem_distillation",
+    "atlasmem_distillation_backward",
 )
 STATIC_MAX_MEMORIES = 128
 
@@ -124,6 +127,15 @@ def load():
         "atlasmem_cross_entropy": ([_vp, _vp, _i32, _i64, _i32, _i64] + [_vp] * 4 + [_i64, _vp], ctypes.c_int),
         "atlasmem_cross_entropy_backward": ([_vp, _vp, _i32, _i64, _i32, _i64] + [_vp] * 6 + [_i64, _vp],
                                             ctypes.c_int),
+        "atlasmem_token_logprobs_workspace_bytes": ([_i32, _i64, _i32, _i64, _i32], _i64),
+        "atlasmem_token_logprobs": ([_vp, _vp, _i32, _i64, _i32, _i64, _f, _vp, _i32] + [_vp] * 5 + [_i64, _vp],
+                                    ctypes.c_int),
+        "atlasmem_distillation_workspace_bytes": ([_i32, _i64, _i32, _i64, _i32, _i32], _i64),
+        "atlasmem_distillation_kept_bytes": ([_i32, _i64, _i64, _i32], _i64),
+        "atlasmem_distillation": ([_vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _vp, _f, _vp, _vp, _vp, _i64, _vp, _i64,
+                                   _vp], ctypes.c_int),
+        "atlasmem_distillation_backward": ([_vp, _vp, _i32, _i64, _i32, _i64, _i32, _vp, _i64] + [_vp] * 4
+                                           + [_i64, _vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -391,3 +403,37 @@ def cross_entropy_backward(X, W, dtype: int, n: int, d: int, vocab: int, labels,
                                                   _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(workspace),
                                                   _nbytes(workspace), _stream(stream)),
            "atlasmem_cross_entropy_backward")
+
+
+def token_logprobs_workspace_bytes(dtype: int, n: int, d: int, vocab: int, top: int = 0) -> int:
+    return int(load().atlasmem_token_logprobs_workspace_bytes(dtype, n, d, vocab, top))
+
+
+def token_logprobs(X, W, dtype: int, n: int, d: int, vocab: int, tokens, logprob, entropy, workspace,
+                   scale: float = 1.0, top: int = 0, top_ids=None, top_logprobs=None, stream=None):
+    _check(load().atlasmem_token_logprobs(_ptr(X), _ptr(W), dtype, n, d, vocab, scale, _ptr(tokens), top,
+                                          _ptr(logprob), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs),
+                                          _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "atlasmem_token_logprobs")
+
+
+def distillation_workspace_bytes(dtype: int, n: int, d: int, vocab: int, top: int, backward: bool = False) -> int:
+    return int(load().atlasmem_distillation_workspace_bytes(dtype, n, d, vocab, top, int(backward)))
+
+
+def distillation_kept_bytes(dtype: int, n: int, vocab: int, top: int) -> int:
+    return int(load().atlasmem_distillation_kept_bytes(dtype, n, vocab, top))
+
+
+def distillation(X, W, dtype: int, n: int, d: int, vocab: int, top: int, ids, teacher, scale: float, loss, lse,
+                 workspace, kept=None, stream=None):
+    _check(load().atlasmem_distillation(_ptr(X), _ptr(W), dtype, n, d, vocab, top, _ptr(ids), _ptr(teacher), scale,
+                                        _ptr(loss), _ptr(lse), _ptr(kept), _nbytes(kept), _ptr(workspace),
+                                        _nbytes(workspace), _stream(stream)), "atlasmem_distillation")
+
+
+def distillation_backward(X, W, dtype: int, n: int, d: int, vocab: int, top: int, kept, dloss, dX, dW, workspace,
+                          stream=None):
+    _check(load().atlasmem_distillation_backward(_ptr(X), _ptr(W), dtype, n, d, vocab, top, _ptr(kept), _nbytes(kept),
+                                                 _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(workspace), _nbytes(workspace),
+                                                 _stream(stream)), "atlasmem_distillation_backward")

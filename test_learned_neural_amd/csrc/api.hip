@@ -448,6 +448,31 @@ atlasmem_status cross_entropy_of(int32_t dtype, int64_t n, int32_t d, int64_t vo
   return ATLASMEM_OK;
 }
 
+// Checked sizes of a call for token log probabilities.
+atlasmem_status token_logprobs_of(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top, float scale,
+                                  TokenLogprobs& s) {
+  CrossEntropy c;
+  const atlasmem_status e = cross_entropy_of(dtype, n, d, vocab, c);
+  if (e != ATLASMEM_OK) return e;
+  if (top < 0 || top > vocab || !(scale > 0.0f && scale < INFINITY)) return ATLASMEM_E_INVALID;
+  if (top > 64) return ATLASMEM_E_SHAPE;
+  s = {n, vocab, d, top, c.bf16, scale};
+  return ATLASMEM_OK;
+}
+
+// Checked sizes of a distillation call.
+atlasmem_status distillation_of(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top, float scale,
+                                Distillation& s) {
+  CrossEntropy c;
+  const atlasmem_status e = cross_entropy_of(dtype, n, d, vocab, c);
+  if (e != ATLASMEM_OK) return e;
+  if (top < 1 || !(scale > 0.0f && scale < INFINITY)) return ATLASMEM_E_INVALID;
+  // byte offsets in 256 rows of what is kept stay below 2^31, four columns a lane below 2^32 lanes
+  if (top > 128 || vocab > (1 << 21)) return ATLASMEM_E_SHAPE;
+  s = {n, vocab, d, top, c.bf16, scale};
+  return ATLASMEM_OK;
+}
+
 // Checked sizes of a group norm call.
 atlasmem_status group_norm_of(int32_t dtype, int64_t n, int64_t L, int32_t channels, int32_t groups,
                               int32_t activation, GroupNorm& s) {
@@ -967,6 +992,84 @@ atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, in
   const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {labels, n * 8}, {lse, n * 4}, {dloss, n * 4}};
   if (!disjoint(out, 3, in, 5)) return ATLASMEM_E_INVALID;
   return cross_entropy_backward(s, X, W, labels, lse, dloss, dX, dW, workspace, S(stream));
+}
+
+int64_t atlasmem_token_logprobs_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top) {
+  TokenLogprobs s;
+  if (token_logprobs_of(dtype, n, d, vocab, top, 1.0f, s) != ATLASMEM_OK) return -1;
+  return token_logprobs_workspace_bytes(s);
+}
+
+atlasmem_status atlasmem_token_logprobs(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                        int64_t vocab, float scale, const int64_t* tokens, int32_t top, float* logprob,
+                                        float* entropy, int64_t* top_ids, float* top_logprobs, void* workspace,
+                                        int64_t workspace_bytes, void* stream) {
+  TokenLogprobs s;
+  const atlasmem_status e = token_logprobs_of(dtype, n, d, vocab, top, scale, s);
+  if (e != ATLASMEM_OK) return e;
+  if (n == 0) return ATLASMEM_OK;
+  if (!X || !W || !workspace || (logprob && !tokens) || (top && (!top_ids || !top_logprobs)))
+    return ATLASMEM_E_INVALID;
+  if (!logprob && !entropy && !top) return ATLASMEM_OK;
+  const int64_t need = token_logprobs_workspace_bytes(s);
+  if (!usable(workspace, workspace_bytes, need)) return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4;
+  const Range out[] = {{logprob, n * 4}, {entropy, n * 4}, {top ? top_ids : nullptr, n * top * 8},
+                       {top ? top_logprobs : nullptr, n * top * 4}, {workspace, need}};
+  const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {tokens, n * 8}};
+  if (!disjoint(out, 5, in, 3)) return ATLASMEM_E_INVALID;
+  return token_logprobs(s, X, W, tokens, logprob, entropy, top_ids, top_logprobs, workspace, S(stream));
+}
+
+int64_t atlasmem_distillation_workspace_bytes(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top,
+                                              int32_t backward) {
+  Distillation s;
+  if (distillation_of(dtype, n, d, vocab, top, 1.0f, s) != ATLASMEM_OK) return -1;
+  return distillation_workspace_bytes(s, backward != 0);
+}
+
+int64_t atlasmem_distillation_kept_bytes(int32_t dtype, int64_t n, int64_t vocab, int32_t top) {
+  Distillation s;
+  if (distillation_of(dtype, n, 1, vocab, top, 1.0f, s) != ATLASMEM_OK) return -1;
+  return distillation_kept_bytes(s);
+}
+
+atlasmem_status atlasmem_distillation(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d, int64_t vocab,
+                                      int32_t top, const int64_t* ids, const float* teacher, float scale, float* loss,
+                                      float* lse, void* kept, int64_t kept_bytes, void* workspace,
+                                      int64_t workspace_bytes, void* stream) {
+  Distillation s;
+  const atlasmem_status e = distillation_of(dtype, n, d, vocab, top, scale, s);
+  if (e != ATLASMEM_OK) return e;
+  if (n == 0) return ATLASMEM_OK;
+  if (!X || !W || !ids || !teacher || !loss || !lse || !workspace) return ATLASMEM_E_INVALID;
+  const int64_t need = distillation_workspace_bytes(s, kept != nullptr), keep = distillation_kept_bytes(s);
+  if (!usable(workspace, workspace_bytes, need) || (kept && !usable(kept, kept_bytes, keep)))
+    return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4;
+  const Range out[] = {{loss, n * 4}, {lse, n * 4}, {kept, keep}, {workspace, need}};
+  const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {ids, n * top * 8}, {teacher, n * top * 4}};
+  if (!disjoint(out, 4, in, 4)) return ATLASMEM_E_INVALID;
+  return distillation(s, X, W, ids, teacher, loss, lse, kept, workspace, S(stream));
+}
+
+atlasmem_status atlasmem_distillation_backward(const void* X, const void* W, int32_t dtype, int64_t n, int32_t d,
+                                               int64_t vocab, int32_t top, const void* kept, int64_t kept_bytes,
+                                               const float* dloss, void* dX, void* dW, void* workspace,
+                                               int64_t workspace_bytes, void* stream) {
+  Distillation s;
+  const atlasmem_status e = distillation_of(dtype, n, d, vocab, top, 1.0f, s);
+  if (e != ATLASMEM_OK) return e;
+  if (n > 0 && (!X || !W || !kept || !workspace)) return ATLASMEM_E_INVALID;
+  if (!dX && !dW) return ATLASMEM_OK;
+  const int64_t need = distillation_workspace_bytes(s, true), keep = distillation_kept_bytes(s);
+  if (n > 0 && (!usable(workspace, workspace_bytes, need) || !usable(kept, kept_bytes, keep)))
+    return ATLASMEM_E_INVALID;
+  const int64_t el = s.bf16 ? 2 : 4;
+  const Range out[] = {{dX, n * d * el}, {dW, vocab * d * el}, {workspace, n > 0 ? need : 0}};
+  const Range in[] = {{X, n * d * el}, {W, vocab * d * el}, {kept, n > 0 ? keep : 0}, {dloss, n * 4}};
+  if (!disjoint(out, 3, in, 4)) return ATLASMEM_E_INVALID;
+  return distillation_backward(s, X, W, kept, dloss, dX, dW, workspace, S(stream));
 }
 
 }  // extern "C"

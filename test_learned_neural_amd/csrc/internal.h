@@ -329,4 +329,31 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
                                        const float* lse, const float* dloss, void* dX, void* dW, void* workspace,
                                        hipStream_t st);
 
+// Log probabilities of tokens, entropies and alternatives (k_logprobs.hip)
+struct TokenLogprobs {
+  int64_t n, vocab;
+  int d, top;
+  bool bf16;
+  float scale;
+};
+int64_t token_logprobs_workspace_bytes(const TokenLogprobs& s);
+atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void* W, const int64_t* tokens,
+                               float* logprob, float* entropy, int64_t* top_ids, float* top_logprobs, void* workspace,
+                               hipStream_t st);
+
+// Distillation from a teacher's top logits (k_distill.hip)
+struct Distillation {
+  int64_t n, vocab;
+  int d, top;
+  bool bf16;
+  float scale;
+};
+int64_t distillation_workspace_bytes(const Distillation& s, bool backward);
+int64_t distillation_kept_bytes(const Distillation& s);
+atlasmem_status distillation(const Distillation& s, const void* X, const void* W, const int64_t* ids,
+                             const float* teacher, float* loss, float* lse, void* kept, void* workspace,
+                             hipStream_t st);
+atlasmem_status distillation_backward(const Distillation& s, const void* X, const void* W, const void* kept,
+                                      const float* dloss, void* dX, void* dW, void* workspace, hipStream_t st);
+
 }  // namespace am

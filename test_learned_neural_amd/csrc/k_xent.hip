@@ -128,10 +128,6 @@ Plan plan_of(const CrossEntropy& s) {
   return p;
 }
 
-bool direct(const void* p, const CrossEntropy& s) {
-  return s.d % (s.bf16 ? 8 : 4) == 0 && ((uintptr_t)p & 15) == 0;
-}
-
 // What a call finds in its workspace, one behind the other.
 struct Space {
   int *index, *at, *count, *equal;
@@ -165,25 +161,6 @@ Space space_of(void* p, const CrossEntropy& s, const Plan& l, bool backward) {
   return w;
 }
 
-// Forward calls of so many operations leave out the rows that do not count: finding and copying the others
-// takes 10 us, which the products of a tenth of the rows outweigh from here on (1.1 PFLOP/s).
-constexpr double kGatherFrom = 2e11;
-
-atlasmem_status rows_that_count(const CrossEntropy& s, const Space& w, const int64_t* labels, const float* dloss,
-                                hipStream_t st) {
-  xe_rows<<<1, 1024, 0, st>>>(labels, dloss, s.n, s.vocab, w.index, w.at, w.count, w.scale, w.equal);
-  AM_LAUNCH_CHECK();
-  return ATLASMEM_OK;
-}
-
-atlasmem_status copy_of(const void* x, const CrossEntropy& s, const Plan& p, int64_t rows, const int* index,
-                        const int* count, void* out, hipStream_t st) {
-  const int64_t blocks = (rows * (p.dp / 4) + 255) / 256;
-  xe_copy<<<(unsigned)blocks, 256, 0, st>>>(x, s.bf16, rows, s.d, p.dp, index, count, out);
-  AM_LAUNCH_CHECK();
-  return ATLASMEM_OK;
-}
-
 }  // namespace
 
 int64_t cross_entropy_workspace_bytes(const CrossEntropy& s, bool backward) {
@@ -196,17 +173,17 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   const Space ws = space_of(workspace, s, p, false);
   const bool gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) >= kGatherFrom;
   atlasmem_status e = ATLASMEM_OK;
-  if (gather) e = rows_that_count(s, ws, labels, nullptr, st);
+  if (gather) e = rows_that_count(s.n, s.vocab, labels, nullptr, ws.index, ws.at, ws.count, ws.scale, ws.equal, st);
   const int *index = gather ? ws.index : nullptr, *count = gather ? ws.count : nullptr;
-  if (e == ATLASMEM_OK && (gather || !direct(X, s)))
-    e = copy_of(X, s, p, s.n, index, count, ws.x, st);
-  if (e == ATLASMEM_OK && !direct(W, s))
-    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, ws.w, st);
+  if (e == ATLASMEM_OK && (gather || !direct(X, s.d, s.bf16)))
+    e = copy_rows(X, s.bf16, s.n, s.d, p.dp, index, count, ws.x, st);
+  if (e == ATLASMEM_OK && !direct(W, s.d, s.bf16))
+    e = copy_rows(W, s.bf16, s.vocab, s.d, p.dp, nullptr, nullptr, ws.w, st);
   if (e != ATLASMEM_OK) return e;
   GemmArgs g = {};
   g.part = ws.part;
-  g.a = direct(W, s) ? W : ws.w;
-  g.b = gather || !direct(X, s) ? ws.x : X;
+  g.a = direct(W, s.d, s.bf16) ? W : ws.w;
+  g.b = gather || !direct(X, s.d, s.bf16) ? ws.x : X;
   g.lda = g.ldb = p.dp;
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
   g.count = count;
@@ -214,7 +191,7 @@ atlasmem_status cross_entropy(const CrossEntropy& s, const void* X, const void* 
   e = gemm<false, false, EPI_LSE>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   xe_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(g.part, g.parts, gather ? ws.at : nullptr, X, W, s.bf16,
-                                                     direct(X, s) && direct(W, s), s.n, s.d, s.vocab, labels, loss,
+                                                     direct(X, s.d, s.bf16) && direct(W, s.d, s.bf16), s.n, s.d, s.vocab, labels, loss,
                                                      lse);
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
@@ -234,13 +211,14 @@ atlasmem_status cross_entropy_backward(const CrossEntropy& s, const void* X, con
   const Plan p = plan_of(s);
   const Space ws = space_of(workspace, s, p, true);
   const bool weighted = dW && dloss;
-  atlasmem_status e = rows_that_count(s, ws, labels, dloss, st);
+  atlasmem_status e = rows_that_count(s.n, s.vocab, labels, dloss, ws.index, ws.at, ws.count, ws.scale,
+                                      ws.equal, st);
   if (e == ATLASMEM_OK)
-    e = copy_of(X, s, p, s.n, ws.index, ws.count, ws.x, st);
-  if (e == ATLASMEM_OK && !direct(W, s))
-    e = copy_of(W, s, p, s.vocab, nullptr, nullptr, ws.w, st);
+    e = copy_rows(X, s.bf16, s.n, s.d, p.dp, ws.index, ws.count, ws.x, st);
+  if (e == ATLASMEM_OK && !direct(W, s.d, s.bf16))
+    e = copy_rows(W, s.bf16, s.vocab, s.d, p.dp, nullptr, nullptr, ws.w, st);
   if (e != ATLASMEM_OK) return e;
-  const char* wa = direct(W, s) ? (const char*)W : ws.w;
+  const char* wa = direct(W, s.d, s.bf16) ? (const char*)W : ws.w;
   for (int64_t v0 = 0; v0 < s.vocab; v0 += p.piece) {
     const int64_t nv = std::min(p.piece, s.vocab - v0), ldg = up(nv, 64);
     // G of the piece

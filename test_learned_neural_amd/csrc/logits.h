@@ -14,7 +14,7 @@ namespace am {
 namespace {
 
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
-enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT };
+enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_TOP, EPI_KEPT, EPI_AGAIN };
 
 struct GemmArgs {
   const void* a;
@@ -44,7 +44,25 @@ struct GemmArgs {
   const float* scale;      // GRAD: see gw; OUT: one factor, or null
   void* out;               // [nb][ldo]
   int64_t ldo;
+  float k2;                // TOP, KEPT: scale log2 e
+  float4* sums;            // TOP: [nb][parts]: (maximum m of z, sum of e = exp(scale (z - m)), sum of e (z - m), -)
+  float2* keys;            // TOP: [nb][4 parts], or null: see group_class
+  const float* a_norm;     // TOP: [na], and up to the tile's end: zeros
+  const float* b_norm;     // TOP: [nb], times the products' relative error
+  const float* ref;        // KEPT, AGAIN: [rows of X]
+  const int* to;           // AGAIN: [nb], rows of g
+  const int64_t* ids;      // AGAIN: [rows of X][top], the teacher's classes
+  const float* logp;       // ... and their log probabilities (-inf: none)
+  const float* coef;       // AGAIN: [rows of X], scale q / g
+  int top;
+  float q_scale;           // ... scale
 };
+
+// Classes of a tile that one lane holds of a row: a group, four a tile of side 64, 128 or 256.
+__device__ __forceinline__ int64_t group_class(int64_t group, int code, int side) {
+  return (group >> 2) * side + (group >> 1 & 1) * (side / 2) + (group & 1) * 4 + (code >> 4) * 32 +
+         (code >> 2 & 3) * 8 + (code & 3);
+}
 
 // One operand's step in LDS.  Along the contraction: [R][32], the 16-byte pieces of four rows (256 bytes,
 // all banks) exchanged by the four's index; across: [32][R], pairs of 32-byte pieces exchanged by those
@@ -199,7 +217,7 @@ __device__ __forceinline__ void wait_all() {
 // through LDS, so that a row's columns leave in whole 16-byte pieces side by side.
 template <int TA, int TB, int MA, int NB, int NT>
 __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, uint16_t* out,
-                         int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr) {
+                         int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr, const int* to = nullptr) {
   constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
   const int lane = tid & 63, hf = lane >> 5, col = lane & 31;
   __syncthreads();
@@ -224,7 +242,7 @@ __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], in
     const int64_t row = r0 + r, at = c0 + 8 * c;
     if (row >= nr || at >= nc) continue;
     const u32x4 v = *(const u32x4*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3));
-    uint16_t* p = out + row * ld + at;
+    uint16_t* p = out + (to ? to[row] : row) * ld + at;
     if (vec) {
       *(u32x4*)p = v;
     } else {
@@ -238,7 +256,7 @@ __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], in
 // The same in fp32, four columns a lane; added to what is there (rows of whole 16-byte pieces), or not.
 template <int MA, int NB>
 __device__ __forceinline__ void put_rows32(f32x16 (&acc)[MA][NB], int wa, int wb, int lane, float* out, int64_t ld,
-                                           int64_t c0, int64_t r0, int64_t nr, int add) {
+                                           int64_t c0, int64_t r0, int64_t nr, int add, const int* to = nullptr) {
   const int hf = lane >> 5, col = lane & 31;
   const bool vec = ld % 4 == 0 && ((uintptr_t)out & 15) == 0;
 #pragma unroll
@@ -252,7 +270,7 @@ __device__ __forceinline__ void put_rows32(f32x16 (&acc)[MA][NB], int wa, int wb
         const int64_t c = c0 + wa + 32 * i + 8 * q + 4 * hf;
         if (c >= ld) continue;
         float4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        float* p = out + r * ld + c;
+        float* p = out + (to ? to[r] : r) * ld + c;
         if (add) {
           const float4 o = *(const float4*)p;
           x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
@@ -535,6 +553,130 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     }
   }
 
+  if constexpr (EPI == EPI_TOP || EPI == EPI_KEPT) {
+    float4* red = (float4*)smem;  // [WA][TB]
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int64_t r = b0 + wb + 32 * j + col;
+      if (a0 + TA > g.na) {
+        const int end = (int)(g.na - a0) - wa - 4 * hf;
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (32 * i + 8 * (n >> 2) + (n & 3) >= end) acc[i][j][n] = -INFINITY;
+      }
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) m = fmaxf(m, acc[i][j][n]);
+      if constexpr (EPI == EPI_TOP) {
+        if (g.keys && r < g.nb) {
+          // the two largest of what the lane's logits may be in 64 bits, each with its place in the low bits
+          const float bn = g.b_norm[r];
+          float u1 = -3.4028235e38f, u2 = u1;
+#pragma unroll
+          for (int i = 0; i < MA; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 an = *(const float4*)(g.a_norm + a0 + wa + 32 * i + 8 * q + 4 * hf);
+              const float e[4] = {an.x, an.y, an.z, an.w};
+#pragma unroll
+              for (int n = 0; n < 4; ++n) {
+                const float u = __builtin_amdgcn_fmed3f(fmaf(bn, e[n], acc[i][j][4 * q + n]), -3.4028235e38f,
+                                                        3.4028235e38f);
+                const float key = __uint_as_float((__float_as_uint(u) & ~63u) | (16 * i + 4 * q + n));
+                u2 = __builtin_amdgcn_fmed3f(u1, u2, key);
+                u1 = fmaxf(u1, key);
+              }
+            }
+          g.keys[r * (4 * g.parts) + a0 / TA * 4 + wave % WA * 2 + hf] = float2{u1, u2};
+        }
+      }
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float from = m > -INFINITY ? m : 0.0f;  // a row of NaN has no maximum, and its sum stays NaN
+      float s = 0.0f, t = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const float x = acc[i][j][n] - from, e = __builtin_amdgcn_exp2f(x * g.k2);
+          s += e;
+          if constexpr (EPI == EPI_TOP) t = fmaf(e, fmaxf(x, -3.4028235e38f), t);
+          else acc[i][j][n] = e;
+        }
+      s += __shfl_xor(s, 32);
+      if constexpr (EPI == EPI_TOP) t += __shfl_xor(t, 32);
+      if (hf == 0) red[(wave % WA) * TB + wb + 32 * j + col] = float4{m, s, t, 0.0f};
+      if constexpr (EPI == EPI_KEPT) {
+        if (g.g) {
+          // times exp(scale (m - ref)); where that is no factor to store, the row is written again
+          const float d = r < g.nb ? from - g.ref[g.index[r]] : 0.0f;
+          const float f = fminf(__builtin_amdgcn_exp2f(d * g.k2), 1.0e30f);
+#pragma unroll
+          for (int i = 0; i < MA; ++i)
+#pragma unroll
+            for (int n = 0; n < 16; ++n) acc[i][j][n] *= f;
+        }
+      }
+    }
+    __syncthreads();
+    for (int r = tid; r < TB; r += NT) {
+      if (b0 + r >= g.nb) break;
+      float m = -INFINITY, s = 0.0f, t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WA; ++w) m = fmaxf(m, red[w * TB + r].x);
+#pragma unroll
+      for (int w = 0; w < WA; ++w) {
+        const float4 q = red[w * TB + r];
+        if (q.x == m) {
+          s += q.y, t += q.z;
+        } else {
+          const float x = q.x - m, e = __builtin_amdgcn_exp2f(x * g.k2);
+          s = fmaf(q.y, e, s);
+          if (e > 0.0f) t = fmaf(e, fmaf(q.y, x, q.z), t);  // x may be what no factor of it is: a masked class's
+        }
+      }
+      if constexpr (EPI == EPI_TOP) g.sums[(b0 + r) * g.parts + a0 / TA] = float4{m, s, t, 0.0f};
+      else g.part[(b0 + r) * g.parts + a0 / TA] = float2{m, s};
+    }
+    if constexpr (EPI == EPI_KEPT) {
+      if (g.g) {
+        if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.g, g.ldg, a0, b0, g.nb, 0);
+        else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb);
+      }
+    }
+  }
+
+  if constexpr (EPI == EPI_AGAIN) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int64_t r = b0 + wb + 32 * j + col;
+      const int64_t row = r < g.nb ? g.index[r] : 0;
+      const float ref = r < g.nb ? g.ref[row] : 0.0f, c = r < g.nb ? g.coef[row] / g.q_scale : 1.0f;
+      const int64_t first = a0 + wa + 4 * hf;
+      const int64_t end = g.na - first;
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          acc[i][j][n] = 32 * i + 8 * (n >> 2) + (n & 3) < end ? __builtin_amdgcn_exp2f((acc[i][j][n] - ref) * g.k2) : 0.0f;
+      for (int k = 0; k < g.top; ++k) {
+        const int64_t at = g.ids[row * g.top + k] - first;
+        const float l = g.logp[row * g.top + k];
+        const float p = l == -INFINITY ? 0.0f : __expf(l) / c;
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+            if (32 * i + 8 * (n >> 2) + (n & 3) == at) acc[i][j][n] -= p;
+      }
+    }
+    if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.g, g.ldg, a0, b0, g.nb, 0, g.to);
+    else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb, g.to);
+  }
+
   if constexpr (EPI == EPI_GRAD) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -684,6 +826,34 @@ __global__ void xe_copy(const void* x, int bf16, int64_t rows, int d, int dp, co
   else *(float4*)((float*)out + at) = float4{v[0], v[1], v[2], v[3]};
 }
 
+// A wave's product of two rows in 64 bits.
+__device__ __forceinline__ double row_dot(const void* a, const void* b, int64_t ra, int64_t rb, int dp, int bf16,
+                                          int lane) {
+  double s = 0.0;
+  if (bf16) {
+    const uint16_t *p = (const uint16_t*)a + ra * dp, *q = (const uint16_t*)b + rb * dp;
+    for (int c = lane * 8; c < dp; c += 512) {
+      const u32x4 x = *(const u32x4*)(p + c), y = *(const u32x4*)(q + c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // products of bf16 are floats
+        s += (double)(__uint_as_float(x[k] << 16) * __uint_as_float(y[k] << 16));
+        s += (double)(__uint_as_float(x[k] & 0xFFFF0000u) * __uint_as_float(y[k] & 0xFFFF0000u));
+      }
+    }
+  } else {
+    const float *p = (const float*)a + ra * dp, *q = (const float*)b + rb * dp;
+    for (int c = lane * 4; c < dp; c += 256) {
+      const float4 x = *(const float4*)(p + c), y = *(const float4*)(q + c);
+      s = fma((double)x.x, (double)y.x, s);
+      s = fma((double)x.y, (double)y.y, s);
+      s = fma((double)x.z, (double)y.z, s);
+      s = fma((double)x.w, (double)y.w, s);
+    }
+  }
+  for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
+  return s;
+}
+
 // dX from the partial sums of the contraction's pieces, times the rows' weights: four columns a thread.
 __global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int* at, const float* dloss,
                        void* out, int out_bf16, int vec) {
@@ -760,6 +930,28 @@ atlasmem_status gemm(const GemmArgs& g, bool bf16, int side, hipStream_t st) {
   }
   if (side == 128) return gemm_launch<128, 128, 2, 2, 2, AX, BX, EPI, true>(g, st);
   return gemm_launch<64, 64, 2, 2, 2, AX, BX, EPI, true>(g, st);
+}
+
+// A matrix whose rows the engine can read where they are: whole, aligned 16-byte pieces.
+bool direct(const void* p, int d, bool bf16) { return d % (bf16 ? 8 : 4) == 0 && ((uintptr_t)p & 15) == 0; }
+
+// Forward calls of so many operations leave out the rows that do not count: finding and copying the others
+// takes 10 us, which the products of a tenth of the rows outweigh from here on (1.1 PFLOP/s).
+constexpr double kGatherFrom = 2e11;
+
+atlasmem_status rows_that_count(int64_t n, int64_t vocab, const int64_t* labels, const float* dloss, int* index,
+                                int* at, int* count, float* scale, int* equal, hipStream_t st) {
+  xe_rows<<<1, 1024, 0, st>>>(labels, dloss, n, vocab, index, at, count, scale, equal);
+  AM_LAUNCH_CHECK();
+  return ATLASMEM_OK;
+}
+
+atlasmem_status copy_rows(const void* x, bool bf16, int64_t rows, int d, int dp, const int* index, const int* count,
+                          void* out, hipStream_t st) {
+  const int64_t blocks = (rows * (dp / 4) + 255) / 256;
+  xe_copy<<<(unsigned)blocks, 256, 0, st>>>(x, bf16, rows, d, dp, index, count, out);
+  AM_LAUNCH_CHECK();
+  return ATLASMEM_OK;
 }
 
 }  // namespace
