@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void ds_join(JoinArgs a) {
     if (lane == 0) a.loss[r] = 0.0f, a.lse[r] = 0.0f;
     return;
   }
-  const int64_t place = a.at ? a.at[r] : r;
+  const int64_t place = __builtin_amdgcn_readfirstlane(a.at ? a.at[r] : (int)r);
   float m = -INFINITY, s = 0.0f;
   auto join = [&](float om, float os) {
     const float t = fmaxf(m, om), from = t > -INFINITY ? t : 0.0f;
@@ -132,8 +132,11 @@ __global__ __launch_bounds__(256) void ds_join(JoinArgs a) {
   for (int h = 0; h < 2; ++h)
     for (int j = 64 * h; j < min(64 * h + 64, a.top); ++j) {
       if (__shfl(lp[h], j & 63) == -INFINITY) continue;
-      const double v = row_dot(a.x, a.w, place, __shfl(id[h], j & 63), a.dp, a.bf16, lane);
-      if (lane == (j & 63)) z[h] = v;
+      const int c[1] = {__builtin_amdgcn_readfirstlane((int)__shfl(id[h], j & 63))};
+      double v[1];
+      if (a.bf16) row_dots<1, true>(a.x, a.w, place, c, a.dp, lane, v);
+      else row_dots<1, false>(a.x, a.w, place, c, a.dp, lane, v);
+      if (lane == (j & 63)) z[h] = v[0];
     }
   float loss = 0.0f;
 #pragma unroll

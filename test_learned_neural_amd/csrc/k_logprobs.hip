@@ -8,60 +8,62 @@
 // Alternatives.  Which class is larger is decided in 64 bits, so that an answer does not depend on how a sum
 // was cut: equal logits go to the lowest index.  The matrix cores' z is off by at most
 // c |x| |w| (c: the roundings on a term's way; Cauchy and Schwarz), so z + c |x| |w| is an upper bound.  A
-// lane's 16 to 64 classes of a row are a group; of each the two largest bounds are kept, with the class's
+// lane's 16 to 64 classes of a row are a group; of each the four largest bounds are kept, with the class's
 // place in the six bits that this costs.  The row's workgroup takes the best classes of `top` of its threads,
 // computes them in 64 bits, and has a lower bound of the last alternative; then every class whose bound
-// passes it is computed too: a group whose second bound passes as a whole.
+// passes it is computed too: a group whose fourth bound passes as a whole.
 #include "logits.h"
 
 namespace am {
 
 namespace {
 
-constexpr float kLowest = -3.4028235e38f;
-
-// |rows| of a matrix times `factor`, at most the largest float; zeros from `rows` to `end`.  A wave a row.
-__global__ __launch_bounds__(256) void lp_norms(const void* x, int bf16, int64_t rows, const int* count, int dp,
-                                                float factor, int64_t end, float* out) {
-  const int lane = threadIdx.x & 63;
-  if (count) rows = *count;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < end; r += (int64_t)gridDim.x * 4) {
-    float s = 0.0f;
-    if (r < rows) {
-      if (bf16) {
-        for (int c = lane * 8; c < dp; c += 512) {
-          const u32x4 w = *(const u32x4*)((const uint16_t*)x + r * dp + c);
+// |row| of a row of a bf16 matrix.  A wave's.
+__device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
+  float s = 0.0f;
+#pragma unroll 4
+  for (int c = lane * 8; c < dp; c += 512) {
+    const u32x4 w = *(const u32x4*)(x + c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
-            s = fmaf(lo, lo, fmaf(hi, hi, s));
-          }
-        }
-      } else {
-        for (int c = lane * 4; c < dp; c += 256) {
-          const float4 w = *(const float4*)((const float*)x + r * dp + c);
-          s = fmaf(w.x, w.x, fmaf(w.y, w.y, fmaf(w.z, w.z, fmaf(w.w, w.w, s))));
-        }
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
+      s = fmaf(lo, lo, fmaf(hi, hi, s));
     }
-    for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
-    if (lane == 0) out[r] = fminf(sqrtf(s) * factor, -kLowest);
   }
+  for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
+  return sqrtf(s);
 }
-
-// The largest logit that a key stands for.
-__device__ __forceinline__ float bound_of(float key) {
-  const uint32_t b = __float_as_uint(key);
-  return __uint_as_float(b >> 31 ? b & ~63u : (b & ~63u) ? b | 63u : 0u);
+__global__ __launch_bounds__(256) void lp_row_norms(const uint16_t* x, int64_t rows, const int* count, int dp, float* out) {
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= (count ? *count : rows)) return;
+  const float v = norm_of(x + r * dp, dp, threadIdx.x & 63);
+  if ((threadIdx.x & 63) == 0) out[r] = v;
+}
+// The largest norm of each group's classes: a workgroup's waves take its 64 in turn.
+__global__ __launch_bounds__(256) void lp_group_norms(const uint16_t* w, int64_t vocab, int dp, int side, int apart,
+                                                      int tiles, float* out) {
+  __shared__ float best[4];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float m = 0.0f;
+  for (int code = wave; code < side / 4; code += 4) {
+    const int64_t c = group_class(blockIdx.x, code, side, apart, tiles);
+    if (c >= vocab) continue;
+    const float v = norm_of(w + c * dp, dp, lane);
+    m = fmaxf(m, v < 1.0e30f ? v : 0.0f);
+  }
+  if (lane == 0) best[wave] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) out[blockIdx.x] = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
 }
 
 struct RowArgs {
   const float4* sums;
-  const float2* keys;
-  int parts, side;
+  const uint4* keys;
+  const float* tops;
+  int parts, side, apart;
   const int* at;           // a row's place among those that count, or null: all are there
   const void *x, *w;       // as the products took them, [..][dp]
-  int dp, bf16;
+  int dp;
   int64_t n, vocab;
   const int64_t* tokens;   // or null
   float scale, k2;
@@ -71,24 +73,49 @@ struct RowArgs {
   float* top_logprobs;
 };
 
-constexpr int kTopMost = 64;   // alternatives
+constexpr int kTopMost = 64;         // alternatives
 constexpr float kMasked = -1.0e38f;  // logits from here down are no alternatives
-constexpr int kTake = 16;      // classes a wave computes between two selections
-constexpr int kPending = 1024, kFlush = 512;
+constexpr int kFlush = 1024;         // pending items
 
 // (z, class) before (y, other): larger, or equal and of lower index
 __device__ __forceinline__ bool ahead(double z, int c, double y, int o) { return z > y || (z == y && c < o); }
 
-__global__ __launch_bounds__(256) void lp_rows(RowArgs g) {
-  constexpr int kList = kTopMost + 4 * kTake;
-  __shared__ float4 part[4];
-  __shared__ float first[256];
+// Two parts of a row's maximum m, sum of e = exp(scale (z - m)) and sum of e (z - m).
+__device__ __forceinline__ void join(float& m, float& s, float& t, float om, float os, float ot, float k2) {
+  const float to = fmaxf(m, om), from = to > -INFINITY ? to : 0.0f;
+  const float x = m - from, ox = om - from;  // minus infinity, or a masked class's, where e is zero
+  const float e = __builtin_amdgcn_exp2f(x * k2), oe = __builtin_amdgcn_exp2f(ox * k2);
+  t = (e > 0.0f ? e * fmaf(s, x, t) : 0.0f) + (oe > 0.0f ? oe * fmaf(os, ox, ot) : 0.0f);
+  s = fmaf(s, e, os * oe);
+  m = to;
+}
+
+// A workgroup of NT threads a row: of 1024 for few rows, which computes many classes at once; of one wave where
+// rows fill the chip, since joins, bounds and selections cost instructions in every wave; of 256 where a wave's
+// lanes are few places for the alternatives asked for, and many classes would pass their bar.  Loops are kept
+// rolled: few rows wait for their instructions.
+template <int NT, bool BF16>
+__global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
+  constexpr int NW = NT / 64;
+  constexpr int kTake = 64 / NW;  // classes a wave computes between two selections
+  constexpr int kList = kTopMost + 64;
+  constexpr int kPlaces = NT < 256 ? NT : 256, kShare = NT / kPlaces;  // of the first choice; threads that share one
+  constexpr int kScan = NT < 1024 ? 4 : 2;  // groups a thread looks at together
+  __shared__ float4 part[NW];
+  __shared__ float first[kPlaces];
   __shared__ double lz[2][kList];
   __shared__ int lc[2][kList];
-  __shared__ int items[kPending];
+  __shared__ int items[kFlush + 4 * kScan * NT];
   __shared__ int counts[2];       // entries of the list, pending items
-  __shared__ float token_z;
+  __shared__ double token_z;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const double per_k2 = (1.0 - 0x1p-20) / g.k2;  // the difference and its product were rounded, to 2^-23
+  // the largest logit that a key stands for (minus infinity: a masked class)
+  auto bound_of = [&](float top, uint32_t key) {
+    const uint32_t b = key & ~63u;
+    return b < 0x7f800000u ? (double)top - (double)__uint_as_float(b) * per_k2 : -INFINITY;
+  };
+#pragma unroll 1
   for (int64_t r = blockIdx.x; r < g.n; r += gridDim.x) {
     const int64_t y = g.tokens ? g.tokens[r] : 0;
     if (y < 0 || y >= g.vocab) {
@@ -99,153 +126,210 @@ __global__ __launch_bounds__(256) void lp_rows(RowArgs g) {
       if (tid < g.top) g.ids[r * g.top + tid] = -1, g.top_logprobs[r * g.top + tid] = 0.0f;
       continue;
     }
-    const int64_t place = g.at ? g.at[r] : r;
+    const int place = __builtin_amdgcn_readfirstlane(g.at ? g.at[r] : (int)r);
 
+    // the best class of each thread's groups, by their largest bound
+    const int groups = 4 * g.parts;
+    const uint4* keys = g.keys + (int64_t)place * groups;
+    const float* tops = g.tops + (int64_t)place * groups;
+    float best = -INFINITY;
+    int own = 0x7fffffff;
+    if (g.top) {
+#pragma unroll 1
+      for (int i0 = tid; i0 < groups; i0 += kScan * NT) {
+        float top[kScan];
+        uint32_t key[kScan];
+#pragma unroll
+        for (int q = 0; q < kScan; ++q) {
+          const int i = i0 + q * NT;
+          top[q] = i < groups ? tops[i] : 0.0f, key[q] = i < groups ? keys[i].x : ~0u;
+        }
+#pragma unroll
+        for (int q = 0; q < kScan; ++q) {
+          const float b = (float)bound_of(top[q], key[q]);
+          if (b > best) best = b, own = (i0 + q * NT) * 64 + (key[q] & 63);
+        }
+      }
+      if (best > -INFINITY) own = (int)group_class(own >> 6, own & 63, g.side, g.apart, g.parts);
+      if (best <= kMasked) best = -INFINITY;
+#pragma unroll
+      for (int k = 1; k < kShare; k <<= 1) {
+        const float o = __shfl_xor(best, k);
+        const int c = __shfl_xor(own, k);
+        if (o > best || (o == best && c < own)) best = o, own = c;
+      }
+    }
     // the row's maximum, sum and first moment
     float m = -INFINITY, s = 0.0f, t = 0.0f;
-    auto join = [&](float om, float os, float ot) {
-      const float to = fmaxf(m, om), from = to > -INFINITY ? to : 0.0f;
-      const float x = m - from, ox = om - from;  // minus infinity, or a masked class's, where e is zero
-      const float e = __builtin_amdgcn_exp2f(x * g.k2), oe = __builtin_amdgcn_exp2f(ox * g.k2);
-      t = (e > 0.0f ? e * fmaf(s, x, t) : 0.0f) + (oe > 0.0f ? oe * fmaf(os, ox, ot) : 0.0f);
-      s = fmaf(s, e, os * oe);
-      m = to;
-    };
-    for (int i = tid; i < g.parts; i += 256) {
-      const float4 q = g.sums[place * g.parts + i];
-      join(q.x, q.y, q.z);
+#pragma unroll 1
+    for (int i = tid; i < g.parts; i += NT) {
+      const float4 q = g.sums[(int64_t)place * g.parts + i];
+      join(m, s, t, q.x, q.y, q.z, g.k2);
     }
+#pragma unroll 1
     for (int k = 32; k; k >>= 1) {
       const float om = __shfl_xor(m, k), os = __shfl_xor(s, k), ot = __shfl_xor(t, k);
-      join(om, os, ot);
+      join(m, s, t, om, os, ot, g.k2);
     }
     __syncthreads();  // the last row's shared values have been read
     if (lane == 0) part[wave] = float4{m, s, t, 0.0f};
-    if (wave == 0 && g.tokens) {
-      const double z = row_dot(g.x, g.w, place, y, g.dp, g.bf16, lane);
-      if (lane == 0) token_z = (float)z;
-    }
-    __syncthreads();
-    m = -INFINITY, s = t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) join(part[w].x, part[w].y, part[w].z);
-    const float lse = fmaf(g.scale, m, logf(s));
-    const bool none = lse == -INFINITY, bad = !none && !(fabsf(lse) < INFINITY);
-    if (tid == 0) {
-      const float p = fmaf(g.scale, token_z, -lse), h = logf(s) - g.scale * t / s;
-      if (g.logprob) g.logprob[r] = bad ? NAN : none ? -INFINITY : p > 0.0f ? 0.0f : p;
-      if (g.entropy) g.entropy[r] = bad ? NAN : none || h < 0.0f ? 0.0f : h;
-    }
-    if (g.top == 0) continue;
-    if (none || bad) {
-      if (tid < g.top) g.ids[r * g.top + tid] = -1, g.top_logprobs[r * g.top + tid] = bad ? NAN : -INFINITY;
-      continue;
-    }
-
-    // the first `top` threads by their groups' largest bound
-    const int groups = 4 * g.parts;
-    const float2* keys = g.keys + place * groups;
-    float best = -INFINITY;
-    int mine = -1;
-    for (int i = tid; i < groups; i += 256) {
-      const float k = keys[i].x;
-      if (k > best) best = k, mine = i;
-    }
-    const int64_t own = mine < 0 ? g.vocab : group_class(mine, __float_as_uint(best) & 63, g.side);
-    if (own >= g.vocab || bound_of(best) <= kMasked) best = -INFINITY;
-    first[tid] = best;
+    if (tid % kShare == 0) first[tid / kShare] = best;
     if (tid < 2) counts[tid] = 0;
     __syncthreads();
-    int rank = 0;
-    for (int i = 0; i < 256; i += 4) {
-      const float4 o = *(const float4*)(first + i);
-      rank += (o.x > best || (o.x == best && i + 0 < tid)) + (o.y > best || (o.y == best && i + 1 < tid)) +
-              (o.z > best || (o.z == best && i + 2 < tid)) + (o.w > best || (o.w == best && i + 3 < tid));
+    if (NW > 1) {
+      const float4 q = part[lane % NW];
+      m = q.x, s = q.y, t = q.z;
+#pragma unroll 1
+      for (int k = NW / 2; k; k >>= 1) {
+        const float om = __shfl_xor(m, k), os = __shfl_xor(s, k), ot = __shfl_xor(t, k);
+        join(m, s, t, om, os, ot, g.k2);
+      }
     }
-    if (best > -INFINITY && rank < g.top) items[rank] = (int)own, atomicAdd(&counts[1], 1);
-    __syncthreads();
+    const float lse = fmaf(g.scale, m, logf(s));
+    const bool none = lse == -INFINITY, bad = !none && !(fabsf(lse) < INFINITY);
 
-    // The list of what is known in 64 bits, in order; `last` of its `top`, if there are so many, is the bar.
+    // The list of what is known in 64 bits, in order; the last of its `top`, if there are so many, is the bar.
     int known = 0, buf = 0;
     double bar = -INFINITY;
     int bar_class = 0x7fffffff;
-    // Computes what is pending: a class, or (negative) all classes of a group.
-    auto flush = [&]() {
-      const int pending = counts[1];
-      int at = wave, code = 0;
-      bool more = true;
-      while (more) {
-        for (int k = 0; k < kTake && at < pending; ++k) {
-          const int item = items[at];
-          int64_t c = item;
-          if (item < 0) {
-            c = group_class(~item, code, g.side);
-            if (++code == g.side / 4) at += 4, code = 0;
-          } else {
-            at += 4;
-          }
-          if (c >= g.vocab) continue;
-          if (__any(lane < known && lc[buf][lane] == (int)c)) continue;
-          const double z = row_dot(g.x, g.w, place, c, g.dp, g.bf16, lane);
-          if (lane == 0 && z > kMasked && ahead(z, (int)c, bar, bar_class)) {
-            const int e = known + atomicAdd(&counts[0], 1);
-            lz[buf][e] = z, lc[buf][e] = (int)c;
-          }
+    if (!none && !bad) {
+      // first the best `top` of the threads' classes (each of a place's threads compares it to its share of the
+      // others), and the token
+      if (g.top) {
+        const int me = tid / kShare, from = tid % kShare * (kPlaces / kShare);
+        int rank = 0;
+#pragma unroll 2
+        for (int i = from; i < from + kPlaces / kShare; i += 4) {
+          const float4 o = *(const float4*)(first + i);
+          rank += (o.x > best || (o.x == best && i + 0 < me)) + (o.y > best || (o.y == best && i + 1 < me)) +
+                  (o.z > best || (o.z == best && i + 2 < me)) + (o.w > best || (o.w == best && i + 3 < me));
         }
-        more = __syncthreads_or(at < pending);
-        const int total = known + counts[0];
-        if (total > known) {
-          if (tid < total) {
-            const double z = lz[buf][tid];
-            const int c = lc[buf][tid];
-            int ahead_of = 0;
-            for (int i = 0; i < total; ++i) ahead_of += ahead(lz[buf][i], lc[buf][i], z, c);
-            if (ahead_of < g.top) lz[buf ^ 1][ahead_of] = z, lc[buf ^ 1][ahead_of] = c;
-          }
-          buf ^= 1;
-          known = min(total, g.top);
-        }
-        __syncthreads();
-        if (known == g.top) bar = lz[buf][known - 1], bar_class = lc[buf][known - 1];
-        if (tid == 0) counts[0] = 0;
-        __syncthreads();
+#pragma unroll
+        for (int k = 1; k < kShare; k <<= 1) rank += __shfl_xor(rank, k);
+        if (tid % kShare == 0 && best > -INFINITY && rank < g.top && own != (int)y) items[atomicAdd(&counts[1], 1)] = own;
       }
-      if (tid == 0) counts[1] = 0;
+      if (tid == 0) items[atomicAdd(&counts[1], 1)] = (int)y;
       __syncthreads();
-    };
-    flush();
-    // every class that may pass the bar
-    for (int i0 = 0; i0 < groups; i0 += 256) {
-      const int i = i0 + tid;
-      if (i < groups) {
-        const float2 k = keys[i];
-        const double b1 = bound_of(k.x), b2 = bound_of(k.y);
-        const int64_t start = group_class(i, 0, g.side);
-        if (start < g.vocab && b1 > kMasked) {
-          if (b2 > kMasked && (b2 > bar || (b2 == bar && start < bar_class))) {
-            items[atomicAdd(&counts[1], 1)] = ~i;
-          } else if (b1 > bar || (b1 == bar && start < bar_class)) {
-            items[atomicAdd(&counts[1], 1)] = (int)group_class(i, __float_as_uint(k.x) & 63, g.side);
+      // what is pending is computed, a class or (negative) a quarter of a group's, two at a time a wave; then
+      // every class that may pass the bar is pending
+      int scanned = g.top ? 0 : groups;
+#pragma unroll 1
+      while (true) {
+        const int pending = counts[1];
+        int at = wave, code = 0;
+        auto next = [&]() {  // a class that is not known, or -1
+          while (at < pending) {
+            const int item = __builtin_amdgcn_readfirstlane(items[at]);
+            int c = item;
+            if (item < 0) c = (int)group_class(~item >> 2, (~item & 3) * (g.side / 16) + code++, g.side, g.apart, g.parts);
+            if (item >= 0 || code == g.side / 16) at += NW, code = 0;
+            if (c < g.vocab && !__any(lane < known && lc[buf][lane] == c)) return c;
           }
+          return -1;
+        };
+        bool more = pending > 0;
+#pragma unroll 1
+        while (more) {
+#pragma unroll 1
+          for (int k = 0; k < kTake; k += 2) {
+            int c[2];
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              const int v = next();
+              c[0] = q ? c[0] : v, c[1] = v;
+            }
+            if (c[0] < 0) break;
+            double z[2];
+            const int rows[2] = {c[0], max(c[1], 0)};
+            row_dots<2, BF16>(g.x, g.w, place, rows, g.dp, lane, z);
+            const double zc = lane ? z[1] : z[0];
+            const int cc = lane ? c[1] : c[0];
+            if (lane < 2 && cc >= 0) {
+              if (cc == (int)y) token_z = zc;
+              if (g.top && zc > kMasked && ahead(zc, cc, bar, bar_class)) {
+                const int e = known + atomicAdd(&counts[0], 1);
+                lz[buf][e] = zc, lc[buf][e] = cc;
+              }
+            }
+          }
+          more = __syncthreads_or(at < pending);
+          const int total = known + counts[0];
+          if (total > known) {
+#pragma unroll 1
+            for (int e = tid; e < total; e += NT) {
+              const double z = lz[buf][e];
+              const int c = lc[buf][e];
+              int before = 0;
+#pragma unroll 4
+              for (int i = 0; i < total; ++i) before += ahead(lz[buf][i], lc[buf][i], z, c);
+              if (before < g.top) lz[buf ^ 1][before] = z, lc[buf ^ 1][before] = c;
+            }
+            buf ^= 1;
+            known = min(total, g.top);
+          }
+          __syncthreads();
+          if (g.top && known == g.top) bar = lz[buf][known - 1], bar_class = lc[buf][known - 1];
+          if (tid == 0) counts[0] = 0;
+          __syncthreads();
+        }
+        if (scanned >= groups) break;
+        if (tid == 0) counts[1] = 0;
+        __syncthreads();
+        int found = 0;
+#pragma unroll 1
+        for (; scanned < groups && found <= kFlush; scanned += kScan * NT) {
+          uint4 k[kScan];
+          float top[kScan];
+#pragma unroll
+          for (int q = 0; q < kScan; ++q) {
+            const int i = scanned + q * NT + tid;
+            k[q] = i < groups ? keys[i] : uint4{~0u, ~0u, ~0u, ~0u}, top[q] = i < groups ? tops[i] : 0.0f;
+          }
+#pragma unroll
+          for (int q = 0; q < kScan; ++q) {
+            // a bound that passes, or equals the bar where the group has a class of lower index
+            const double b1 = bound_of(top[q], k[q].x);
+            if (!(b1 > kMasked && b1 >= bar)) continue;
+            const int i = scanned + q * NT + tid;
+            const int start = (int)group_class(i, 0, g.side, g.apart, g.parts);
+            auto passes = [&](uint32_t key) {
+              const double b = bound_of(top[q], key);
+              return b > kMasked && (b > bar || (b == bar && start < bar_class));
+            };
+            const bool whole = passes(k[q].w);
+            const uint32_t one[3] = {k[q].x, k[q].y, k[q].z};
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {
+              const uint32_t key = p == 0 ? one[0] : p == 1 ? one[1] : one[2];
+              if (whole) items[atomicAdd(&counts[1], 1)] = ~(4 * i + p);
+              else if (p < 3 && passes(key))
+                items[atomicAdd(&counts[1], 1)] = (int)group_class(i, key & 63, g.side, g.apart, g.parts);
+            }
+          }
+          __syncthreads();
+          found = counts[1];
+          __syncthreads();
         }
       }
-      __syncthreads();
-      const int pending = counts[1];
-      __syncthreads();
-      if (pending > kFlush || i0 + 256 >= groups) flush();
+    }
+    if (tid == 0) {
+      const double p = bad || none ? 0.0 : (double)g.scale * token_z - (double)lse;
+      const float h = logf(s) - g.scale * t / s;
+      if (g.logprob) g.logprob[r] = bad ? NAN : none ? -INFINITY : p > 0.0 ? 0.0f : (float)p;
+      if (g.entropy) g.entropy[r] = bad ? NAN : none || h < 0.0f ? 0.0f : h;
     }
     if (tid < g.top) {
       const bool there = tid < known;
+      const double p = there ? (double)g.scale * lz[buf][tid] - (double)lse : -INFINITY;
       g.ids[r * g.top + tid] = there ? lc[buf][tid] : -1;
-      g.top_logprobs[r * g.top + tid] =
-          there ? fminf((float)(g.scale * lz[buf][tid] - (double)lse), 0.0f) : -INFINITY;
+      g.top_logprobs[r * g.top + tid] = bad ? NAN : p > 0.0 ? 0.0f : (float)p;
     }
   }
 }
 
 struct Plan {
-  int el, dp, side, parts;
-  bool gather;
+  int el, dp, side, parts, apart;
+  bool gather, norms;
 };
 Plan plan_of(const TokenLogprobs& s, bool tokens) {
   Plan p = {};
@@ -253,6 +337,10 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
   p.side = side_of(s.vocab, s.n, s.bf16);
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
+  // Rows of a tile 64 apart: all tiles' (256 x 256, 2048 columns) takes 10% longer, their pages no longer at hand,
+  // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.
+  p.apart = (int)std::min<int64_t>(std::min(p.parts, 64), INT32_MAX / ((int64_t)p.side * p.dp * p.el));
+  p.norms = s.top && s.bf16 && p.side == 256;
   p.gather = tokens && 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) >= kGatherFrom;
   return p;
 }
@@ -263,7 +351,8 @@ struct Space {
   char *x, *w;
   float *a_norm, *b_norm;
   float4* sums;
-  float2* keys;
+  uint4* keys;
+  float* tops;
   int64_t bytes;
 };
 Space space_of(void* p, const TokenLogprobs& s, const Plan& l) {
@@ -280,19 +369,11 @@ Space space_of(void* p, const TokenLogprobs& s, const Plan& l) {
   w.w = take(l.el * s.vocab * (int64_t)l.dp);
   w.sums = (float4*)take(16 * s.n * (int64_t)l.parts);
   if (s.top) {
-    w.a_norm = (float*)take(4 * l.parts * (int64_t)l.side), w.b_norm = (float*)take(4 * s.n);
-    w.keys = (float2*)take(32 * s.n * (int64_t)l.parts);
+    if (l.norms) w.a_norm = (float*)take(16 * (int64_t)l.parts), w.b_norm = (float*)take(4 * s.n);
+    w.keys = (uint4*)take(64 * s.n * (int64_t)l.parts), w.tops = (float*)take(16 * s.n * (int64_t)l.parts);
   }
   w.bytes = at - (char*)p;
   return w;
-}
-
-atlasmem_status norms(const void* x, bool bf16, int64_t rows, const int* count, int dp, float factor, int64_t end,
-                      float* out, hipStream_t st) {
-  lp_norms<<<(unsigned)std::min<int64_t>((end + 3) / 4, 1 << 16), 256, 0, st>>>(x, bf16, rows, count, dp, factor, end,
-                                                                                out);
-  AM_LAUNCH_CHECK();
-  return ATLASMEM_OK;
 }
 
 }  // namespace
@@ -318,29 +399,39 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
   g.lda = g.ldb = p.dp;
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
   g.count = count;
-  g.parts = p.parts;
+  g.parts = p.parts, g.apart = p.apart;
   g.sums = ws.sums;
   g.k2 = s.scale * 1.4426950408889634f;
-  if (s.top) {
-    // roundings on a term's way: eight for each of dp / 16 matrix instructions; in fp32 six instructions with
-    // those for each 16 columns, and the planes that are not multiplied; a hundredth for the norms' own
-    const float c = ((s.bf16 ? 0.5f : 3.0f) * p.dp + 128.0f) * 0x1p-24f * 1.01f;
-    e = norms(g.a, s.bf16, s.vocab, nullptr, p.dp, 1.0f, (int64_t)p.parts * p.side, ws.a_norm, st);
-    if (e == ATLASMEM_OK) e = norms(g.b, s.bf16, s.n, count, p.dp, c, s.n, ws.b_norm, st);
-    if (e != ATLASMEM_OK) return e;
-    g.keys = ws.keys, g.a_norm = ws.a_norm, g.b_norm = ws.b_norm;
+  g.keys = ws.keys, g.tops = ws.tops, g.a_norm = ws.a_norm, g.b_norm = ws.b_norm;
+  // roundings on a term's way: eight for each of dp / 16 matrix instructions; in fp32 six instructions with
+  // those for each 16 columns, and the planes that are not multiplied; a hundredth for the norms' own
+  g.error = ((s.bf16 ? 0.5f : 3.0f) * p.dp + 128.0f) * 0x1p-24f * 1.01f;
+  if (p.norms) {
+    lp_group_norms<<<(unsigned)(4 * p.parts), 256, 0, st>>>((const uint16_t*)g.a, s.vocab, p.dp, p.side, p.apart, p.parts,
+                                                            ws.a_norm);
+    AM_LAUNCH_CHECK();
+    lp_row_norms<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>((const uint16_t*)g.b, s.n, count, p.dp, ws.b_norm);
+    AM_LAUNCH_CHECK();
   }
-  e = gemm<false, false, EPI_TOP>(g, s.bf16, p.side, st);
+  e = s.top ? gemm<false, false, EPI_TOP>(g, s.bf16, p.side, st) : gemm<false, false, EPI_SUMS>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   RowArgs a = {};
-  a.sums = ws.sums, a.keys = ws.keys, a.parts = p.parts, a.side = p.side;
+  a.sums = ws.sums, a.keys = ws.keys, a.tops = ws.tops, a.parts = p.parts, a.side = p.side, a.apart = p.apart;
   a.at = p.gather ? ws.at : nullptr;
-  a.x = g.b, a.w = g.a, a.dp = p.dp, a.bf16 = s.bf16;
+  a.x = g.b, a.w = g.a, a.dp = p.dp;
   a.n = s.n, a.vocab = s.vocab;
   a.tokens = tokens;
   a.scale = s.scale, a.k2 = g.k2, a.top = s.top;
   a.logprob = logprob, a.entropy = entropy, a.ids = top_ids, a.top_logprobs = top_logprobs;
-  lp_rows<<<(unsigned)std::min<int64_t>(s.n, 1 << 20), 256, 0, st>>>(a);
+  const unsigned rows = (unsigned)std::min<int64_t>(s.n, 1 << 20);
+  auto launch = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    if (s.bf16) lp_rows<NT, true><<<rows, NT, 0, st>>>(a);
+    else lp_rows<NT, false><<<rows, NT, 0, st>>>(a);
+  };
+  if (s.n <= 256) launch(std::integral_constant<int, 1024>{});
+  else if (s.n > 1024 && s.top <= 24) launch(std::integral_constant<int, 64>{});
+  else launch(std::integral_constant<int, 256>{});
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
 }

@@ -14,7 +14,7 @@ namespace am {
 namespace {
 
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
-enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_TOP, EPI_KEPT, EPI_AGAIN };
+enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN };
 
 struct GemmArgs {
   const void* a;
@@ -44,11 +44,15 @@ struct GemmArgs {
   const float* scale;      // GRAD: see gw; OUT: one factor, or null
   void* out;               // [nb][ldo]
   int64_t ldo;
-  float k2;                // TOP, KEPT: scale log2 e
-  float4* sums;            // TOP: [nb][parts]: (maximum m of z, sum of e = exp(scale (z - m)), sum of e (z - m), -)
-  float2* keys;            // TOP: [nb][4 parts], or null: see group_class
-  const float* a_norm;     // TOP: [na], and up to the tile's end: zeros
-  const float* b_norm;     // TOP: [nb], times the products' relative error
+  float k2;                // SUMS, TOP, KEPT: scale log2 e
+  float4* sums;            // SUMS, TOP: [nb][parts]: (maximum m of z, sum of e = exp(scale (z - m)), sum of e (z - m), -)
+  uint4* keys;             // TOP: [nb][4 parts], by group_class's groups: the four largest bounds of what z may be in 64
+                           // bits, as differences to
+  float* tops;             // ... [nb][4 parts], times k2, with the class's place in the low bits
+  int apart;               // SUMS, TOP: see tile_rows
+  float error;             // TOP: of z, relative to |a| |b|
+  const float* a_norm;     // TOP, tiles of 256: the largest |a| of a group, [4 tiles]
+  const float* b_norm;     // ... and |b|, [nb]
   const float* ref;        // KEPT, AGAIN: [rows of X]
   const int* to;           // AGAIN: [nb], rows of g
   const int64_t* ids;      // AGAIN: [rows of X][top], the teacher's classes
@@ -58,10 +62,31 @@ struct GemmArgs {
   float q_scale;           // ... scale
 };
 
-// Classes of a tile that one lane holds of a row: a group, four a tile of side 64, 128 or 256.
-__device__ __forceinline__ int64_t group_class(int64_t group, int code, int side) {
-  return (group >> 2) * side + (group >> 1 & 1) * (side / 2) + (group & 1) * 4 + (code >> 4) * 32 +
-         (code >> 2 & 3) * 8 + (code & 3);
+// The tiles of SUMS and TOP take every `apart`-th row of a, so that classes that lie together (frequent ones do)
+// come to different tiles: of `apart` tiles beside each other, or of the last ones.
+struct TileRows {
+  int64_t first;  // the tile's first row; the others follow `step` apart
+  int step;
+};
+__device__ __forceinline__ TileRows tile_rows(int tile, int side, int apart, int tiles) {
+  const int t = tile / apart * apart;
+  return {(int64_t)t * side + (tile - t), min(apart, tiles - t)};
+}
+__device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t m;
+  asm("v_med3_u32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  return m;
+}
+// The 16, 32 or 64 of a tile's classes that one lane holds of a row are a group, four a tile: every fourth of the
+// tile's rows (spread_row of where they lie in LDS), so that neighbours are in different ones.
+__device__ __forceinline__ int64_t group_class(int group, int code, int side, int apart, int tiles) {
+  const TileRows t = tile_rows(group >> 2, side, apart, tiles);
+  return t.first + (int64_t)t.step * (4 * code + (group & 3));
+}
+template <int R>
+__device__ __forceinline__ int spread_row(int r) {
+  const int half = r / (R / 2), in = r % (R / 2);
+  return 4 * (in >> 3) * 4 + 4 * (in & 3) + 2 * (in >> 2 & 1) + half;
 }
 
 // One operand's step in LDS.  Along the contraction: [R][32], the 16-byte pieces of four rows (256 bytes,
@@ -92,6 +117,8 @@ struct Tile {
 
   __device__ static constexpr int exchange(int k) { return R == 64 ? k & 2 : (k & 3) << 1; }
 
+  // SPREAD: rows in the order of spread_row
+  template <bool SPREAD = false>
   __device__ void init(int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
     kc = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
 #pragma unroll
@@ -102,7 +129,7 @@ struct Tile {
         const int c = ((((at >> 1) ^ exchange(k)) << 1) | (at & 1)) * 8;
         off[i] = c < rows - r0 ? (uint32_t)((k * ld + c) * 2) : 0x80000000u;
       } else {
-        const int r = id >> 2;
+        const int r = SPREAD ? spread_row<R>(id >> 2) : id >> 2;
         off[i] = r < rows - r0 ? (uint32_t)((r * ld + kc) * 2) : 0x80000000u;
       }
     }
@@ -149,6 +176,7 @@ struct Tile32 {
   uint32_t off[kLoads];
   int kc[kLoads];
 
+  template <bool SPREAD = false>
   __device__ void init(int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -158,8 +186,8 @@ struct Tile32 {
         kc[i] = 0;
         off[i] = c < rows - r0 ? (uint32_t)((k * ld + c) * 4) : 0x80000000u;
       } else {
-        const int r = id >> 3;
-        kc[i] = ((id & 7) ^ ((r >> 1) & 7)) * 4;
+        const int at = id >> 3, r = SPREAD ? spread_row<R>(at) : at;
+        kc[i] = ((id & 7) ^ ((at >> 1) & 7)) * 4;
         off[i] = r < rows - r0 ? (uint32_t)((r * ld + kc[i]) * 4) : 0x80000000u;
       }
     }
@@ -341,12 +369,20 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   // operands are read one matrix-instruction depth (16) ahead.  One barrier a step, between its two
   // depths: behind it step t's buffer is free for its next step's loads, and step t + 1 is there.  Past
   // the end loads are masked off.
+  constexpr bool kApart = EPI == EPI_TOP || EPI == EPI_SUMS;
+  const int tile_a = (int)(a0 / TA);
+  int64_t lda = g.lda, first_a = a0, rows0 = a0, rows = g.na;
+  if constexpr (kApart) {
+    const TileRows t = tile_rows(tile_a, TA, g.apart, g.ta);
+    first_a = t.first, rows0 = 0, rows = (g.na - t.first + t.step - 1) / t.step;
+    lda *= t.step;
+  }
   A ta;
   B tb;
-  ta.init(g.lda, a0, g.na, wave, lane);
+  ta.template init<kApart>(lda, rows0, rows, wave, lane);
   tb.init(g.ldb, b0, g.nb, wave, lane);
   const int64_t step_a = AX ? kBK * g.lda : kBK, step_b = BX ? kBK * g.ldb : kBK;
-  const E* pa = (const E*)g.a + (AX ? k0 * g.lda + a0 : a0 * g.lda + k0);
+  const E* pa = (const E*)g.a + (AX ? k0 * g.lda + a0 : first_a * g.lda + k0);
   const E* pb = (const E*)g.b + (BX ? k0 * g.ldb + b0 : b0 * g.ldb + k0);
   int left = (int)(k1 - k0);
   auto load_a = [&](int n, E* d) { ta.load(n, d, pa, left, g.lda, g.lda - a0, wave); };
@@ -356,6 +392,21 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     pa += step_a, pb += step_b;
   };
   constexpr int kLoads = A::kLoads + B::kLoads;
+  // TOP: squares of the rows that a lane's operands are of, where the products leave time for them
+  constexpr bool kNorms = EPI == EPI_TOP && (F32 || TA < 256);
+  float na[MA], nb[NB];
+#pragma unroll
+  for (int i = 0; i < MA; ++i) na[i] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) nb[j] = 0.0f;
+  auto squares = [](u32x4 v, float s) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bf16x2 x = __builtin_bit_cast(bf16x2, (uint32_t)v[q]);
+      s = __builtin_amdgcn_fdot2_f32_bf16(x, x, s, false);
+    }
+    return s;
+  };
   if constexpr (F32) {
     static_assert(kStages == 2, "a step in use, a step on its way");
     const E *pa0 = pa, *pb0 = pb;
@@ -387,6 +438,15 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           u32x4 ap[MA][3], bp[NB][3];
+          if constexpr (PLANES && kNorms) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+#pragma unroll
+              for (int i = 0; i < MA; ++i) na[i] = fmaf(ra[i][n], ra[i][n], na[i]);
+#pragma unroll
+              for (int j = 0; j < NB; ++j) nb[j] = fmaf(rb[j][n], rb[j][n], nb[j]);
+            }
+          }
           if constexpr (PLANES) {
 #pragma unroll
             for (int i = 0; i < MA; ++i) split_planes(ra[i], ap[i]);
@@ -492,6 +552,10 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
         for (int n = 0; n < kM; ++n) {
           acc[n / NB][n % NB] = mfma32(ao[ks][n / NB], bo[ks][n % NB], acc[n / NB][n % NB]);
+          if constexpr (kNorms) {
+            if (n % NB == 0) na[n / NB] = squares(ao[ks][n / NB], na[n / NB]);
+            if (n < NB) nb[n] = squares(bo[ks][n], nb[n]);
+          }
 #pragma unroll
           for (int r = n * kR / kM; r < (n + 1) * kR / kM; ++r) read(r, ks ^ 1, ks ? d : s, ks ^ 1);
           if (ks == 0) {
@@ -553,61 +617,73 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     }
   }
 
-  if constexpr (EPI == EPI_TOP || EPI == EPI_KEPT) {
+  if constexpr (EPI == EPI_SUMS || EPI == EPI_TOP || EPI == EPI_KEPT) {
     float4* red = (float4*)smem;  // [WA][TB]
+    // TOP: the largest |a| of the lane's classes, and |b| of its rows.  Classes of 1e30 are masked, not sums that err.
+    float group_norm = 0.0f;
+    if constexpr (kNorms) {
+#pragma unroll
+      for (int i = 0; i < MA; ++i) {
+        const float q = na[i] + __shfl_xor(na[i], 32);
+        group_norm = fmaxf(group_norm, sqrtf(q) < 1.0e30f ? sqrtf(q) : 0.0f);
+      }
+      for (int k = 1; k < 32; k <<= 1)
+        if (k != 4) group_norm = fmaxf(group_norm, __shfl_xor(group_norm, k));
+      group_norm = __shfl(group_norm, 4 * hf);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) nb[j] = sqrtf(nb[j] + __shfl_xor(nb[j], 32));
+    } else if constexpr (EPI == EPI_TOP) {
+      group_norm = g.a_norm[tile_a * 4 + 2 * hf + wave % WA];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) nb[j] = b0 + wb + 32 * j + col < g.nb ? g.b_norm[b0 + wb + 32 * j + col] : 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int64_t r = b0 + wb + 32 * j + col;
-      if (a0 + TA > g.na) {
-        const int end = (int)(g.na - a0) - wa - 4 * hf;
+      if (rows0 + TA > rows) {
+        const int left = (int)(rows - rows0);
+        const int end = kApart ? (left - 2 * hf - wave % WA + 3) >> 2 : left - wa - 4 * hf;
 #pragma unroll
         for (int i = 0; i < MA; ++i)
 #pragma unroll
           for (int n = 0; n < 16; ++n)
-            if (32 * i + 8 * (n >> 2) + (n & 3) >= end) acc[i][j][n] = -INFINITY;
+            if ((kApart ? 16 * i + n : 32 * i + 8 * (n >> 2) + (n & 3)) >= end) acc[i][j][n] = -INFINITY;
       }
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n) m = fmaxf(m, acc[i][j][n]);
-      if constexpr (EPI == EPI_TOP) {
-        if (g.keys && r < g.nb) {
-          // the two largest of what the lane's logits may be in 64 bits, each with its place in the low bits
-          const float bn = g.b_norm[r];
-          float u1 = -3.4028235e38f, u2 = u1;
-#pragma unroll
-          for (int i = 0; i < MA; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 an = *(const float4*)(g.a_norm + a0 + wa + 32 * i + 8 * q + 4 * hf);
-              const float e[4] = {an.x, an.y, an.z, an.w};
-#pragma unroll
-              for (int n = 0; n < 4; ++n) {
-                const float u = __builtin_amdgcn_fmed3f(fmaf(bn, e[n], acc[i][j][4 * q + n]), -3.4028235e38f,
-                                                        3.4028235e38f);
-                const float key = __uint_as_float((__float_as_uint(u) & ~63u) | (16 * i + 4 * q + n));
-                u2 = __builtin_amdgcn_fmed3f(u1, u2, key);
-                u1 = fmaxf(u1, key);
-              }
-            }
-          g.keys[r * (4 * g.parts) + a0 / TA * 4 + wave % WA * 2 + hf] = float2{u1, u2};
-        }
-      }
       m = fmaxf(m, __shfl_xor(m, 32));
       const float from = m > -INFINITY ? m : 0.0f;  // a row of NaN has no maximum, and its sum stays NaN
       float s = 0.0f, t = 0.0f;
+      // TOP: how far below the maximum the lane's four largest are (times k2: positive floats in whole numbers' order),
+      // each with its place in the low bits
+      uint32_t y1 = ~0u, y2 = ~0u, y3 = ~0u, y4 = ~0u;
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const float x = acc[i][j][n] - from, e = __builtin_amdgcn_exp2f(x * g.k2);
+          const float x = acc[i][j][n] - from, y = x * g.k2, e = __builtin_amdgcn_exp2f(y);
           s += e;
-          if constexpr (EPI == EPI_TOP) t = fmaf(e, fmaxf(x, -3.4028235e38f), t);
-          else acc[i][j][n] = e;
+          if constexpr (EPI == EPI_KEPT) acc[i][j][n] = e;
+          else t = fmaf(e, fmaxf(x, -3.4028235e38f), t);
+          if constexpr (EPI == EPI_TOP) {
+            const uint32_t key = (__float_as_uint(y) & 0x7fffffc0u) | (16 * i + n);
+            y4 = med3(y3, y4, key), y3 = med3(y2, y3, key), y2 = med3(y1, y2, key), y1 = min(y1, key);
+            if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // or the compiler keeps all differences at once
+          }
         }
+      if constexpr (EPI == EPI_TOP) {
+        if (r < g.nb) {
+          const float top = from + g.error * group_norm * nb[j];
+          const int64_t at = r * (4 * (int64_t)g.parts) + tile_a * 4 + 2 * hf + wave % WA;
+          g.tops[at] = fmaf(fabsf(top), 0x1p-21f, top);
+          g.keys[at] = uint4{y1, y2, y3, y4};
+        }
+      }
       s += __shfl_xor(s, 32);
-      if constexpr (EPI == EPI_TOP) t += __shfl_xor(t, 32);
+      t += __shfl_xor(t, 32);
       if (hf == 0) red[(wave % WA) * TB + wb + 32 * j + col] = float4{m, s, t, 0.0f};
       if constexpr (EPI == EPI_KEPT) {
         if (g.g) {
@@ -638,7 +714,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
           if (e > 0.0f) t = fmaf(e, fmaf(q.y, x, q.z), t);  // x may be what no factor of it is: a masked class's
         }
       }
-      if constexpr (EPI == EPI_TOP) g.sums[(b0 + r) * g.parts + a0 / TA] = float4{m, s, t, 0.0f};
+      if constexpr (EPI != EPI_KEPT) g.sums[(b0 + r) * g.parts + tile_a] = float4{m, s, t, 0.0f};
       else g.part[(b0 + r) * g.parts + a0 / TA] = float2{m, s};
     }
     if constexpr (EPI == EPI_KEPT) {
@@ -826,32 +902,45 @@ __global__ void xe_copy(const void* x, int bf16, int64_t rows, int d, int dp, co
   else *(float4*)((float*)out + at) = float4{v[0], v[1], v[2], v[3]};
 }
 
-// A wave's product of two rows in 64 bits.
-__device__ __forceinline__ double row_dot(const void* a, const void* b, int64_t ra, int64_t rb, int dp, int bf16,
-                                          int lane) {
-  double s = 0.0;
-  if (bf16) {
-    const uint16_t *p = (const uint16_t*)a + ra * dp, *q = (const uint16_t*)b + rb * dp;
-    for (int c = lane * 8; c < dp; c += 512) {
-      const u32x4 x = *(const u32x4*)(p + c), y = *(const u32x4*)(q + c);
+// A wave's products of a row of a with N rows of b, in 64 bits.  Loads of 4 KB of each are on their way together;
+// those past the rows' ends are zeros.
+template <int N, bool BF16>
+__device__ __forceinline__ void row_dots(const void* a, const void* b, int64_t ra, const int (&rb)[N], int dp, int lane,
+                                         double (&z)[N]) {
+  const int bytes = dp * (BF16 ? 2 : 4);
+  const rsrc_t ar = make_rsrc((const char*)a + ra * bytes, bytes);
+  rsrc_t br[N];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // products of bf16 are floats
-        s += (double)(__uint_as_float(x[k] << 16) * __uint_as_float(y[k] << 16));
-        s += (double)(__uint_as_float(x[k] & 0xFFFF0000u) * __uint_as_float(y[k] & 0xFFFF0000u));
-      }
+  for (int n = 0; n < N; ++n) br[n] = make_rsrc((const char*)b + (int64_t)rb[n] * bytes, bytes), z[n] = 0.0;
+#pragma unroll 1
+  for (int o = lane * 16; o < bytes + lane * 16; o += 4096) {
+    u32x4 x[4], y[N][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = buf_ld16(ar, o + 1024 * k, 0);
+#pragma unroll
+      for (int n = 0; n < N; ++n) y[n][k] = buf_ld16(br[n], o + 1024 * k, 0);
     }
-  } else {
-    const float *p = (const float*)a + ra * dp, *q = (const float*)b + rb * dp;
-    for (int c = lane * 4; c < dp; c += 256) {
-      const float4 x = *(const float4*)(p + c), y = *(const float4*)(q + c);
-      s = fma((double)x.x, (double)y.x, s);
-      s = fma((double)x.y, (double)y.y, s);
-      s = fma((double)x.z, (double)y.z, s);
-      s = fma((double)x.w, (double)y.w, s);
-    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const uint32_t u = x[k][q], v = y[n][k][q];
+          if constexpr (BF16) {  // products of bf16 are floats
+            z[n] += (double)(__uint_as_float(u << 16) * __uint_as_float(v << 16));
+            z[n] += (double)(__uint_as_float(u & 0xFFFF0000u) * __uint_as_float(v & 0xFFFF0000u));
+          } else {
+            z[n] = fma((double)__uint_as_float(u), (double)__uint_as_float(v), z[n]);
+          }
+        }
   }
-  for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
-  return s;
+#pragma unroll 1
+  for (int k = 32; k; k >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) z[n] += __shfl_xor(z[n], k);
 }
 
 // dX from the partial sums of the contraction's pieces, times the rows' weights: four columns a thread.
