@@ -2,28 +2,34 @@
 //   z = X W^T,  p_i = softmax_j(scale t_ij) over the row's given classes,  q_i = softmax_v(scale z_iv)
 //   loss_i = sum_j p_ij (log p_ij - log q_i,id_ij),  G_iv = q_iv - sum_{j: id_ij = v} p_ij
 //   dX_i = scale dloss_i (G W)_i,  dW = G^T (scale dloss X)
-// The forward computes z once.  For a training step it leaves of a tile not z but exp(scale (z - ref)) in the type
-// of X, with ref a logit of the row that is known beforehand, that of the teacher's first class: up to a factor
-// c = exp(scale ref - lse) of the row this is q, rounded once.  Then only the given classes' entries are
-// written again, less p / c, and what is kept is G / c: the backward has two products, not three.
-// Rows whose ref is too far from their lse for a factor (2^60) are computed again with lse for ref.
+// The forward computes z once.  For a training step its epilogue leaves exp(scale (z - ref)), with ref a logit of the
+// row that is known beforehand, that of the teacher's first class: up to a factor c = exp(scale ref - lse) of the
+// row this is q.  A workgroup for each row then joins the sums and writes G: the backward has two products, not
+// three.  Rows whose ref is too far from their lse for a factor are computed again with lse for ref.
+//
+// bf16 calls leave those exponentials with ten significant bits and no sign, in the 16 that G then takes, so that G is
+// rounded once, not twice; c on X instead of G, without that pass, was the third rounding of a term of dW
+// (33 x 256 x 1000: 2.8e-3 off instead of 2.3e-3).  fp32 calls keep G / c, and the rows' weights take c.
 #include "logits.h"
 
 namespace am {
 
 namespace {
 
-constexpr float kFar = 60.0f;
+// how far (times log 2) ref may be from lse: 2^(kFar - kDown) has to stay below 2
+constexpr float kFar = 36.0f;
+constexpr int kMost = 128;  // entries of a row
 
 // log p of each given class (-inf: none), and of each row a label (0, or -1 for a row that has no class) and the
-// logit of its first class.  A wave a row.
+// logit of its first class.  With `index`, rows are taken as they come, those left out among them.  A wave a row.
 __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const float* teacher, int64_t n, int top,
                                                   int64_t vocab, float scale, const void* X, const void* W, int bf16,
                                                   int vec, int d, float* logp, int64_t* label, float* ref,
-                                                  int* again_count) {
+                                                  int* again_count, int* index, int* at, int* count) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (again_count && r == 0 && lane == 0) *again_count = 0;
+  if (count && r == 0 && lane == 0) *count = (int)n;
   if (r >= n) return;
   float t[2];
   int64_t id[2];
@@ -49,11 +55,12 @@ __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const floa
     if (lane + 64 * h < top) logp[r * top + lane + 64 * h] = on[h] ? t[h] - m - ls : -INFINITY;
   const uint64_t any = __ballot(on[0] || on[1]);
   if (lane == 0) label[r] = any ? 0 : -1;
+  if (index && lane == 0) index[r] = (int)r, at[r] = any ? (int)r : -1;
   if (!ref || !any) return;
   const uint64_t f0 = __ballot(on[0] && t[0] == m), f1 = __ballot(on[1] && t[1] == m);
-  const int at = f0 ? __builtin_ctzll(f0) : f1 ? __builtin_ctzll(f1) : __builtin_ctzll(any);
-  const bool low = f0 || (!f1 && (__ballot(on[0]) >> at & 1));
-  const int64_t y = __shfl(low ? id[0] : id[1], at);
+  const int best = f0 ? __builtin_ctzll(f0) : f1 ? __builtin_ctzll(f1) : __builtin_ctzll(any);
+  const bool low = f0 || (!f1 && (__ballot(on[0]) >> best & 1));
+  const int64_t y = __shfl(low ? id[0] : id[1], best);
   float z = 0.0f;
   for (int c = lane * 8; c < d; c += 512) {
     if (vec && bf16) {
@@ -78,7 +85,7 @@ struct JoinArgs {
   int parts;
   const int* at;           // a row's place among those that count, or null: all are there
   const void *x, *w;       // as the products took them, [..][dp]
-  int dp, bf16;
+  int dp;
   int64_t n;
   const int64_t *label, *ids;
   const float* logp;
@@ -86,112 +93,192 @@ struct JoinArgs {
   float scale, k2;
   float *loss, *lse;
   // a training step
-  float *ref, *coef;
+  int all;                 // rows that are left out have a place, too
+  float *ref, *coef, *factor;
   void* g;
   int64_t ldg;
   int *again, *to, *again_count;
   void* x_again;
 };
 
-// loss, lse of a row, and its entries at the given classes.  A wave a row.
-__global__ __launch_bounds__(256) void ds_join(JoinArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (r >= a.n) return;
-  if (a.label[r] < 0) {
-    if (lane == 0) a.loss[r] = 0.0f, a.lse[r] = 0.0f;
-    return;
-  }
-  const int64_t place = __builtin_amdgcn_readfirstlane(a.at ? a.at[r] : (int)r);
-  float m = -INFINITY, s = 0.0f;
-  auto join = [&](float om, float os) {
-    const float t = fmaxf(m, om), from = t > -INFINITY ? t : 0.0f;
-    s = s * __builtin_amdgcn_exp2f((m - from) * a.k2) + os * __builtin_amdgcn_exp2f((om - from) * a.k2);
-    m = t;
-  };
-  for (int i = lane; i < a.parts; i += 64) {
-    const float2 q = a.part[place * a.parts + i];
-    join(q.x, q.y);
-  }
-  for (int k = 32; k; k >>= 1) {
-    const float om = __shfl_xor(m, k), os = __shfl_xor(s, k);
-    join(om, os);
-  }
-  const float lse = fmaf(a.scale, m, logf(s));
-  double z[2] = {0.0, 0.0};
-  int64_t id[2];
-  float lp[2], p[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int j = lane + 64 * h;
-    id[h] = j < a.top ? a.ids[r * a.top + j] : -1;
-    lp[h] = j < a.top ? a.logp[r * a.top + j] : -INFINITY;
-    p[h] = lp[h] == -INFINITY ? 0.0f : expf(lp[h]);
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    for (int j = 64 * h; j < min(64 * h + 64, a.top); ++j) {
-      if (__shfl(lp[h], j & 63) == -INFINITY) continue;
-      const int c[1] = {__builtin_amdgcn_readfirstlane((int)__shfl(id[h], j & 63))};
-      double v[1];
-      if (a.bf16) row_dots<1, true>(a.x, a.w, place, c, a.dp, lane, v);
-      else row_dots<1, false>(a.x, a.w, place, c, a.dp, lane, v);
-      if (lane == (j & 63)) z[h] = v[0];
+// loss, lse of a row, and of a training step its G.  A workgroup a row.
+template <bool BF16, bool TRAIN>
+__global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
+  __shared__ float2 part[4];
+  __shared__ int id[kMost], list[kMost];
+  __shared__ float p[kMost];
+  __shared__ double z[kMost];
+  __shared__ int entries, slot;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+#pragma unroll 1
+  for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
+    if (a.label[r] < 0) {
+      if (tid == 0) a.loss[r] = 0.0f, a.lse[r] = 0.0f;
+      if (TRAIN && tid == 0) a.coef[r] = 0.0f;
+      if (TRAIN && a.all)
+        for (int64_t c = tid; c < a.ldg * (BF16 ? 2 : 4) / 16; c += 256)
+          ((u32x4*)((char*)a.g + r * a.ldg * (BF16 ? 2 : 4)))[c] = u32x4{0, 0, 0, 0};
+      continue;
     }
-  float loss = 0.0f;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (p[h] != 0.0f) loss += p[h] * (lp[h] - (float)(a.scale * z[h] - lse));
-  for (int k = 32; k; k >>= 1) loss += __shfl_xor(loss, k);
-  if (lane == 0) a.loss[r] = loss, a.lse[r] = lse;
-  if (!a.g) return;
-
-  float ref = a.ref[r];
-  const float l2 = __log2f(s);
-  const bool near = fabsf((m - ref) * a.k2 + l2) <= kFar;
-  if (!near) ref = m + l2 / a.k2;
-  const float coef = __builtin_amdgcn_exp2f((ref - m) * a.k2) / s;
-  if (lane == 0) a.coef[r] = a.scale * coef;
-  if (!near) {
-    int slot = 0;
-    if (lane == 0) {
-      slot = atomicAdd(a.again_count, 1);
-      a.again[slot] = (int)r, a.to[slot] = (int)place, a.ref[r] = ref;
+    const int place = __builtin_amdgcn_readfirstlane(a.at ? a.at[r] : (int)r);
+    __syncthreads();  // the last row's shared values have been read
+    if (tid == 0) entries = 0;
+    float m = -INFINITY, s = 0.0f;
+    auto join = [&](float om, float os) {
+      const float t = fmaxf(m, om), from = t > -INFINITY ? t : 0.0f;
+      s = s * __builtin_amdgcn_exp2f((m - from) * a.k2) + os * __builtin_amdgcn_exp2f((om - from) * a.k2);
+      m = t;
+    };
+    for (int i = tid; i < a.parts; i += 256) {
+      const float2 q = a.part[(int64_t)place * a.parts + i];
+      join(q.x, q.y);
     }
-    slot = __builtin_amdgcn_readfirstlane(slot);
-    const int words = a.dp * (a.bf16 ? 2 : 4) / 16;
-    for (int c = lane; c < words; c += 64)
-      ((u32x4*)a.x_again)[(int64_t)slot * words + c] = ((const u32x4*)a.x)[place * words + c];
-    return;
-  }
-  float sum[2] = {0.0f, 0.0f};
-  for (int j = 0; j < a.top; ++j) {
-    const int64_t o = __shfl(j < 64 ? id[0] : id[1], j & 63);
-    const float q = __shfl(j < 64 ? p[0] : p[1], j & 63);
-    sum[0] += o == id[0] ? q : 0.0f, sum[1] += o == id[1] ? q : 0.0f;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (lp[h] != -INFINITY) {
-      const float v = __builtin_amdgcn_exp2f((float)(z[h] - ref) * a.k2) - sum[h] / coef;
-      if (a.bf16) ((uint16_t*)a.g)[place * a.ldg + id[h]] = (uint16_t)bf16_bits(v);
-      else ((float*)a.g)[place * a.ldg + id[h]] = v;
+    for (int k = 32; k; k >>= 1) {
+      const float om = __shfl_xor(m, k), os = __shfl_xor(s, k);
+      join(om, os);
     }
+    if (lane == 0) part[wave] = float2{m, s};
+    float lp = -INFINITY;
+    if (tid < a.top) {
+      lp = a.logp[r * a.top + tid];
+      id[tid] = (int)a.ids[r * a.top + tid], p[tid] = lp == -INFINITY ? 0.0f : expf(lp);
+    }
+    __syncthreads();
+    m = part[0].x, s = part[0].y;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) join(part[w].x, part[w].y);
+    const float lse = fmaf(a.scale, m, logf(s));
+    if (tid < a.top && !(lp == -INFINITY)) list[atomicAdd(&entries, 1)] = tid;
+    __syncthreads();
+    // logits of the given classes
+    for (int i = 2 * wave; i < entries; i += 8) {
+      const int j[2] = {__builtin_amdgcn_readfirstlane(list[i]),
+                        __builtin_amdgcn_readfirstlane(list[min(i + 1, entries - 1)])};
+      const int c[2] = {__builtin_amdgcn_readfirstlane(id[j[0]]), __builtin_amdgcn_readfirstlane(id[j[1]])};
+      double v[2];
+      row_dots<2, BF16>(a.x, a.w, place, c, a.dp, lane, v);
+      if (lane < 2) z[lane ? j[1] : j[0]] = lane ? v[1] : v[0];
+    }
+    __syncthreads();
+    if (wave == 0) {
+      float loss = 0.0f;
+      for (int j = lane; j < a.top; j += 64) {
+        const float l = j == tid ? lp : a.logp[r * a.top + j];
+        if (p[j] != 0.0f) loss += p[j] * (l - (float)(a.scale * z[j] - lse));
+      }
+      for (int k = 32; k; k >>= 1) loss += __shfl_xor(loss, k);
+      if (lane == 0) a.loss[r] = loss, a.lse[r] = lse;
+    }
+    if constexpr (TRAIN) {
+      float ref = a.ref[r];
+      const float l2 = __log2f(s);
+      const bool near = fabsf((m - ref) * a.k2 + l2) <= kFar;
+      if (!near) ref = m + l2 / a.k2;
+      const float c = __builtin_amdgcn_exp2f((ref - m) * a.k2) / s;
+      if (!near) {
+        if (tid == 0) {
+          slot = atomicAdd(a.again_count, 1);
+          a.again[slot] = (int)r, a.to[slot] = place, a.factor[slot] = c, a.ref[r] = ref;
+          a.coef[r] = a.scale;
+        }
+        __syncthreads();
+        const int words = a.dp * (BF16 ? 2 : 4) / 16;
+        for (int k = tid; k < words; k += 256)
+          ((u32x4*)a.x_again)[(int64_t)slot * words + k] = ((const u32x4*)a.x)[(int64_t)place * words + k];
+        continue;
+      }
+      if (tid == 0) a.coef[r] = BF16 ? a.scale : a.scale * c;
+      if constexpr (BF16) {
+        u32x4* row = (u32x4*)((uint16_t*)a.g + (int64_t)place * a.ldg);
+        const float f = c * exp2f(kDown);
+        const int words = (int)(a.ldg / 8);
+        for (int k0 = tid; k0 < words; k0 += 4 * 256) {
+          u32x4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k0 + 256 * k < words) v[k] = row[k0 + 256 * k];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[k][q] = cvt_pk_bf16(u16_lo(v[k][q]) * f, u16_hi(v[k][q]) * f);
+            if (k0 + 256 * k < words) row[k0 + 256 * k] = v[k];
+          }
+        }
+        __syncthreads();  // those are there before the given classes' entries
+      }
+      if (tid < a.top && !(lp == -INFINITY)) {
+        float sum = 0.0f;
+        for (int j = 0; j < a.top; ++j) sum += id[j] == id[tid] ? p[j] : 0.0f;
+        const float q = __builtin_amdgcn_exp2f((float)(z[tid] - ref) * a.k2);
+        if (BF16) ((uint16_t*)a.g)[(int64_t)place * a.ldg + id[tid]] = (uint16_t)bf16_bits(fmaf(q, c, -sum));
+        else ((float*)a.g)[(int64_t)place * a.ldg + id[tid]] = q - sum / c;
+      }
+    }
+  }
 }
 
-// Weights of the rows, dloss coef, and the rows that count times them: four columns a thread.
-__global__ void ds_weigh(const void* x, int bf16, int d, int dp, const int* index, const int* count,
-                         const float* dloss, const float* coef, float* weight, void* out) {
+// The weight of each row, coef dloss; of those that count the value that all have, or the largest finite magnitude,
+// and which (one workgroup).
+__device__ __forceinline__ void ds_weights(const float* coef, const float* dloss, const int* at, int64_t n, float* weight,
+                                           float& scale, int& equal) {
+  __shared__ float sm[16], from[16], to[16];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  float m = 0.0f, lo = INFINITY, hi = -INFINITY;
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+    const bool on = at[i] >= 0;
+    const float w = on ? coef[i] * (dloss ? dloss[i] : 1.0f) : 0.0f;
+    if (weight) weight[i] = w;
+    if (!on) continue;
+    m = fmaxf(m, fabsf(w) <= 3.0e38f ? fabsf(w) : 0.0f);
+    lo = fminf(lo, w == w ? w : -INFINITY), hi = fmaxf(hi, w == w ? w : INFINITY);
+  }
+  for (int k = 32; k; k >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, k));
+    lo = fminf(lo, __shfl_xor(lo, k)), hi = fmaxf(hi, __shfl_xor(hi, k));
+  }
+  if (lane == 0) sm[wave] = m, from[wave] = lo, to[wave] = hi;
+  __syncthreads();
+  for (int k = 0; k < waves; ++k) m = fmaxf(m, sm[k]), lo = fminf(lo, from[k]), hi = fmaxf(hi, to[k]);
+  equal = lo >= hi;
+  scale = lo == hi ? lo : m > 0.0f ? m : 1.0f;
+}
+__global__ __launch_bounds__(1024) void ds_scale(const float* coef, const float* dloss, const int* at, int64_t n,
+                                                 float* weight, float* scale, int* equal) {
+  float s;
+  int e;
+  ds_weights(coef, dloss, at, n, weight, s, e);
+  if (threadIdx.x == 0) *scale = s, *equal = e;
+}
+
+constexpr int64_t kFewRows = 2048;  // each workgroup finds the weights by itself: a launch less
+
+// The rows of X that have a place, times their weights over `scale` (where those are one value, as they are), zeros for
+// rows that are left out; and zeros for the latter's dX, if it is given.  Four columns a thread.
+__global__ __launch_bounds__(256) void ds_weigh(const void* x, int bf16, int64_t n, int d, int dp, const int* at,
+                                                int all, const float* coef, const float* dloss, float* weight,
+                                                float* scale, int* equal, void* out, void* dx) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t per = dp / 4, r = i / per;
-  if (r >= *count) return;
+  const int64_t per = dp / 4, row = i / per;
+  float over;
+  int same;
+  if (n <= kFewRows) {
+    ds_weights(coef, dloss, at, n, blockIdx.x == 0 ? weight : nullptr, over, same);
+    if (i == 0) *scale = over;
+  } else {
+    over = *scale, same = *equal;
+  }
+  if (row >= n) return;
   const int c = (int)(i % per) * 4;
-  const int64_t row = index[r];
-  const float w = coef[row] * (dloss ? dloss[row] : 1.0f);
-  if (c == 0) weight[row] = w;
-  if (!out) return;
-  float v[4];
-  if (d % 4 == 0 && ((uintptr_t)x & 15) == 0 && c < d) {
+  const int64_t place = all ? row : at[row];
+  const bool on = at[row] >= 0;
+  if (!on && dx)
+    for (int k = 0; k < 4 && c + k < d; ++k) {
+      if (bf16) ((uint16_t*)dx)[row * d + c + k] = 0;
+      else ((float*)dx)[row * d + c + k] = 0.0f;
+    }
+  if (!out || place < 0) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (on && d % 4 == 0 && ((uintptr_t)x & 15) == 0 && c < d) {
     if (bf16) {
       const uint2 u = *(const uint2*)((const uint16_t*)x + row * d + c);
       v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
@@ -200,20 +287,26 @@ __global__ void ds_weigh(const void* x, int bf16, int d, int dp, const int* inde
       const float4 u = *(const float4*)((const float*)x + row * d + c);
       v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
     }
-  } else {
+  } else if (on) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = c + k < d ? load_in(x, row * d + c + k, bf16) : 0.0f;
   }
-  const int64_t at = r * dp + c;
-  if (bf16) *(uint2*)((uint16_t*)out + at) = uint2{cvt_pk_bf16(v[0] * w, v[1] * w), cvt_pk_bf16(v[2] * w, v[3] * w)};
-  else *(float4*)((float*)out + at) = float4{v[0] * w, v[1] * w, v[2] * w, v[3] * w};
+  if (!same) {
+    const float w = coef[row] * (dloss ? dloss[row] : 1.0f) / over;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = on ? v[k] * w : 0.0f;
+  }
+  const int64_t o = place * dp + c;
+  if (bf16) *(uint2*)((uint16_t*)out + o) = uint2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+  else *(float4*)((float*)out + o) = float4{v[0], v[1], v[2], v[3]};
 }
 
 struct Plan {
   int el, dp, side, parts, side_x, splits;
   int64_t ldg;
+  bool gather;
 };
-Plan plan_of(const Distillation& s) {
+Plan plan_of(const Distillation& s, bool train) {
   Plan p = {};
   p.el = s.bf16 ? 2 : 4;
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
@@ -224,6 +317,8 @@ Plan plan_of(const Distillation& s) {
   const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.side_x), 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.side_x == 256 ? 256 : 512) / tiles, s.vocab / 512));
   if (tiles * p.splits <= 128) p.side_x = 64;
+  // a training step has three products to leave rows out of
+  p.gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) * (train ? 4 : 1) >= kGatherFrom;
   return p;
 }
 
@@ -253,7 +348,7 @@ Kept kept_of(void* p, const Distillation& s, const Plan& l) {
 struct Space {
   char *x, *w, *x_again;
   int64_t* label;
-  float *logp, *ref, *weight, *acc;
+  float *logp, *ref, *factor, *weight, *acc;
   float2* part;
   int *again, *to, *again_count;
   int *index, *at, *count, *equal;
@@ -279,6 +374,7 @@ Space space_of(void* p, const Distillation& s, const Plan& l, bool backward) {
   if (backward) {
     w.x_again = take(rows);
     w.again = (int*)take(4 * s.n), w.to = (int*)take(4 * s.n), w.again_count = (int*)take(4);
+    w.factor = (float*)take(4 * s.n);
   } else {
     w.index = (int*)take(4 * s.n), w.at = (int*)take(4 * s.n);
     w.count = (int*)take(12), w.equal = w.count + 1, w.scale = (float*)(w.count + 2);
@@ -287,7 +383,8 @@ Space space_of(void* p, const Distillation& s, const Plan& l, bool backward) {
   if (backward) {
     at = both;
     w.weight = (float*)take(4 * s.n);
-    w.acc = (float*)take(4 * (int64_t)l.splits * s.n * l.dp);
+    w.equal = (int*)take(8), w.scale = (float*)(w.equal + 1);
+    if (l.splits > 1) w.acc = (float*)take(4 * (int64_t)l.splits * s.n * l.dp);
   }
   w.bytes = std::max(at, end) - (char*)p;
   return w;
@@ -296,31 +393,30 @@ Space space_of(void* p, const Distillation& s, const Plan& l, bool backward) {
 }  // namespace
 
 int64_t distillation_workspace_bytes(const Distillation& s, bool backward) {
-  return space_of(nullptr, s, plan_of(s), backward).bytes;
+  return space_of(nullptr, s, plan_of(s, backward), backward).bytes;
 }
-int64_t distillation_kept_bytes(const Distillation& s) { return kept_of(nullptr, s, plan_of(s)).bytes; }
+int64_t distillation_kept_bytes(const Distillation& s) { return kept_of(nullptr, s, plan_of(s, true)).bytes; }
 
 atlasmem_status distillation(const Distillation& s, const void* X, const void* W, const int64_t* ids,
                              const float* teacher, float* loss, float* lse, void* kept, void* workspace,
                              hipStream_t st) {
-  const Plan p = plan_of(s);
   const bool train = kept != nullptr;
+  const Plan p = plan_of(s, train);
   Space ws = space_of(workspace, s, p, train);
   Kept k = {};
   if (train) {
     k = kept_of(kept, s, p);
     ws.index = k.index, ws.at = k.at, ws.count = k.count, ws.equal = k.equal, ws.scale = k.scale;
   }
-  const bool gather = train || 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) >= kGatherFrom;
-  const bool vec = direct(X, s.d, s.bf16) && direct(W, s.d, s.bf16);
-  ds_teacher<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(ids, teacher, s.n, s.top, s.vocab, s.scale, X, W, s.bf16, vec,
-                                                        s.d, ws.logp, ws.label, train ? ws.ref : nullptr,
-                                                        train ? ws.again_count : nullptr);
+  const bool vec = direct(X, s.d, s.bf16) && direct(W, s.d, s.bf16), as_they_come = train && !p.gather;
+  ds_teacher<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(
+      ids, teacher, s.n, s.top, s.vocab, s.scale, X, W, s.bf16, vec, s.d, ws.logp, ws.label, train ? ws.ref : nullptr,
+      train ? ws.again_count : nullptr, as_they_come ? ws.index : nullptr, ws.at, as_they_come ? ws.count : nullptr);
   AM_LAUNCH_CHECK();
   atlasmem_status e = ATLASMEM_OK;
-  if (gather) e = rows_that_count(s.n, 1, ws.label, nullptr, ws.index, ws.at, ws.count, ws.scale, ws.equal, st);
-  const int *index = gather ? ws.index : nullptr, *count = gather ? ws.count : nullptr;
-  const bool x_direct = !gather && direct(X, s.d, s.bf16), w_direct = direct(W, s.d, s.bf16);
+  if (p.gather) e = rows_that_count(s.n, 1, ws.label, nullptr, ws.index, ws.at, ws.count, ws.scale, ws.equal, st);
+  const int *index = p.gather ? ws.index : nullptr, *count = p.gather ? ws.count : nullptr;
+  const bool x_direct = !p.gather && direct(X, s.d, s.bf16), w_direct = direct(W, s.d, s.bf16);
   if (e == ATLASMEM_OK && !x_direct) e = copy_rows(X, s.bf16, s.n, s.d, p.dp, index, count, ws.x, st);
   if (e == ATLASMEM_OK && !w_direct) e = copy_rows(W, s.bf16, s.vocab, s.d, p.dp, nullptr, nullptr, ws.w, st);
   if (e != ATLASMEM_OK) return e;
@@ -337,21 +433,24 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   e = gemm<false, false, EPI_KEPT>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   JoinArgs a = {};
-  a.part = ws.part, a.parts = p.parts, a.at = gather ? ws.at : nullptr;
-  a.x = g.b, a.w = g.a, a.dp = p.dp, a.bf16 = s.bf16, a.n = s.n;
+  a.part = ws.part, a.parts = p.parts, a.at = p.gather ? ws.at : nullptr;
+  a.x = g.b, a.w = g.a, a.dp = p.dp, a.n = s.n;
   a.label = ws.label, a.ids = ids, a.logp = ws.logp, a.top = s.top;
   a.scale = s.scale, a.k2 = g.k2;
   a.loss = loss, a.lse = lse;
   if (train) {
-    a.ref = ws.ref, a.coef = k.coef, a.g = k.g, a.ldg = p.ldg;
+    a.all = !p.gather;
+    a.ref = ws.ref, a.coef = k.coef, a.factor = ws.factor, a.g = k.g, a.ldg = p.ldg;
     a.again = ws.again, a.to = ws.to, a.again_count = ws.again_count, a.x_again = ws.x_again;
   }
-  ds_join<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(a);
+  const unsigned rows = (unsigned)std::min<int64_t>(s.n, 1 << 20);
+  if (s.bf16) train ? ds_rows<true, true><<<rows, 256, 0, st>>>(a) : ds_rows<true, false><<<rows, 256, 0, st>>>(a);
+  else train ? ds_rows<false, true><<<rows, 256, 0, st>>>(a) : ds_rows<false, false><<<rows, 256, 0, st>>>(a);
   AM_LAUNCH_CHECK();
   if (!train) return ATLASMEM_OK;
   g.b = ws.x_again;
   g.count = ws.again_count, g.index = ws.again, g.to = ws.to;
-  g.ids = ids, g.logp = ws.logp, g.coef = k.coef, g.top = s.top, g.q_scale = s.scale;
+  g.ids = ids, g.logp = ws.logp, g.factor = ws.factor, g.top = s.top;
   return gemm<false, false, EPI_AGAIN>(g, s.bf16, p.side, st);
 }
 
@@ -365,11 +464,16 @@ atlasmem_status distillation_backward(const Distillation& s, const void* X, cons
     }
     return ATLASMEM_OK;
   }
-  const Plan p = plan_of(s);
+  const Plan p = plan_of(s, true);
   const Kept k = kept_of(const_cast<void*>(kept), s, p);
   const Space ws = space_of(workspace, s, p, true);
-  ds_weigh<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(X, s.bf16, s.d, p.dp, k.index, k.count, dloss,
-                                                                       k.coef, ws.weight, dW ? ws.x : nullptr);
+  if (s.n > kFewRows) {
+    ds_scale<<<1, 1024, 0, st>>>(k.coef, dloss, k.at, s.n, ws.weight, ws.scale, ws.equal);
+    AM_LAUNCH_CHECK();
+  }
+  ds_weigh<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(
+      X, s.bf16, s.n, s.d, p.dp, k.at, !p.gather, k.coef, dloss, ws.weight, ws.scale, ws.equal, dW ? ws.x : nullptr,
+      p.gather && p.splits == 1 ? dX : nullptr);
   AM_LAUNCH_CHECK();
   atlasmem_status e = ATLASMEM_OK;
   if (dX) {
@@ -381,13 +485,19 @@ atlasmem_status distillation_backward(const Distillation& s, const void* X, cons
     x.a = w_direct ? W : ws.w, x.lda = p.dp, x.na = p.dp;
     x.b = k.g, x.ldb = p.ldg, x.nb = s.n;
     x.K = s.vocab;
-    x.splits = p.splits, x.acc = ws.acc, x.acc_rows = s.n;
-    e = gemm<true, false, EPI_ACC>(x, s.bf16, p.side_x, st);
-    if (e != ATLASMEM_OK) return e;
-    const int vec = s.d % 4 == 0 && ((uintptr_t)dX & 15) == 0;
-    xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(ws.acc, p.splits, s.n, s.d, p.dp, k.at,
-                                                                       ws.weight, dX, s.bf16, vec);
-    AM_LAUNCH_CHECK();
+    if (p.splits == 1) {
+      x.out = dX, x.ldo = s.d, x.to = k.index, x.row_weight = ws.weight;
+      e = gemm<true, false, EPI_ROWS>(x, s.bf16, p.side_x, st);
+      if (e != ATLASMEM_OK) return e;
+    } else {
+      x.splits = p.splits, x.acc = ws.acc, x.acc_rows = s.n;
+      e = gemm<true, false, EPI_ACC>(x, s.bf16, p.side_x, st);
+      if (e != ATLASMEM_OK) return e;
+      const int vec = s.d % 4 == 0 && ((uintptr_t)dX & 15) == 0;
+      xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(ws.acc, p.splits, s.n, s.d, p.dp, k.at,
+                                                                         ws.weight, dX, s.bf16, vec);
+      AM_LAUNCH_CHECK();
+    }
   }
   if (dW) {
     GemmArgs x = {};
@@ -395,6 +505,7 @@ atlasmem_status distillation_backward(const Distillation& s, const void* X, cons
     x.a = ws.x, x.lda = p.dp, x.na = p.dp;
     x.b = k.g, x.ldb = p.ldg, x.nb = s.vocab;
     x.K = s.n;
+    x.scale = ws.scale;
     x.out = dW, x.ldo = s.d;
     e = gemm<true, true, EPI_OUT>(x, s.bf16, side_of(p.dp, s.vocab, s.bf16), st);
     if (e != ATLASMEM_OK) return e;

@@ -13,8 +13,9 @@ namespace am {
 
 namespace {
 
+constexpr float kDown = 40.0f;  // KEPT: 2^-kDown on what is kept of bf16 calls, whose 16 bits end at 2
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
-enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN };
+enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN, EPI_ROWS };
 
 struct GemmArgs {
   const void* a;
@@ -54,12 +55,12 @@ struct GemmArgs {
   const float* a_norm;     // TOP, tiles of 256: the largest |a| of a group, [4 tiles]
   const float* b_norm;     // ... and |b|, [nb]
   const float* ref;        // KEPT, AGAIN: [rows of X]
-  const int* to;           // AGAIN: [nb], rows of g
+  const int* to;           // AGAIN: [nb], rows of g; ROWS: of out
   const int64_t* ids;      // AGAIN: [rows of X][top], the teacher's classes
   const float* logp;       // ... and their log probabilities (-inf: none)
-  const float* coef;       // AGAIN: [rows of X], scale q / g
+  const float* factor;     // AGAIN: [nb], q / exp(scale (z - ref))
   int top;
-  float q_scale;           // ... scale
+  const float* row_weight; // ROWS: [rows of X]
 };
 
 // The tiles of SUMS and TOP take every `apart`-th row of a, so that classes that lie together (frequent ones do)
@@ -241,9 +242,16 @@ __device__ __forceinline__ void wait_all() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
+// Floats of [0, 2) as 16 bits without a sign, seven of exponent and nine of fraction.
+__device__ __forceinline__ uint32_t pack_u16(float a, float b) {
+  return (__float_as_uint(a) + 0x2000u) >> 14 | ((__float_as_uint(b) + 0x2000u) << 2 & 0xFFFF0000u);
+}
+__device__ __forceinline__ float u16_lo(uint32_t w) { return __uint_as_float((w & 0xFFFFu) << 14); }
+__device__ __forceinline__ float u16_hi(uint32_t w) { return __uint_as_float((w & 0xFFFF0000u) >> 2); }
+
+// A tile's accumulators, rounded to bf16 (U16: to the above), to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
 // through LDS, so that a row's columns leave in whole 16-byte pieces side by side.
-template <int TA, int TB, int MA, int NB, int NT>
+template <int TA, int TB, int MA, int NB, int NT, bool U16 = false>
 __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, uint16_t* out,
                          int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr, const int* to = nullptr) {
   constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
@@ -257,7 +265,8 @@ __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], in
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const f32x16& x = acc[i][j];
-        const uint2 o = {cvt_pk_bf16(x[4 * q], x[4 * q + 1]), cvt_pk_bf16(x[4 * q + 2], x[4 * q + 3])};
+        const uint2 o = U16 ? uint2{pack_u16(x[4 * q], x[4 * q + 1]), pack_u16(x[4 * q + 2], x[4 * q + 3])}
+                            : uint2{cvt_pk_bf16(x[4 * q], x[4 * q + 1]), cvt_pk_bf16(x[4 * q + 2], x[4 * q + 3])};
         const int c = (wa + 32 * i + 8 * q) >> 3;
         *(uint2*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3) + 4 * hf) = o;
       }
@@ -687,9 +696,9 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       if (hf == 0) red[(wave % WA) * TB + wb + 32 * j + col] = float4{m, s, t, 0.0f};
       if constexpr (EPI == EPI_KEPT) {
         if (g.g) {
-          // times exp(scale (m - ref)); where that is no factor to store, the row is written again
-          const float d = r < g.nb ? from - g.ref[g.index[r]] : 0.0f;
-          const float f = fminf(__builtin_amdgcn_exp2f(d * g.k2), 1.0e30f);
+          // times exp(scale (m - ref)), and 2^-kDown; where that is no factor to store, the row is written again
+          const float d = r < g.nb ? from - g.ref[g.index ? g.index[r] : r] : 0.0f;
+          const float f = fminf(__builtin_amdgcn_exp2f(fmaf(d, g.k2, F32 ? 0.0f : -kDown)), F32 ? 1.0e30f : 1.0f);
 #pragma unroll
           for (int i = 0; i < MA; ++i)
 #pragma unroll
@@ -720,7 +729,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     if constexpr (EPI == EPI_KEPT) {
       if (g.g) {
         if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.g, g.ldg, a0, b0, g.nb, 0);
-        else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb);
+        else put_rows<TA, TB, MA, NB, NT, true>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb);
       }
     }
   }
@@ -730,18 +739,18 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     for (int j = 0; j < NB; ++j) {
       const int64_t r = b0 + wb + 32 * j + col;
       const int64_t row = r < g.nb ? g.index[r] : 0;
-      const float ref = r < g.nb ? g.ref[row] : 0.0f, c = r < g.nb ? g.coef[row] / g.q_scale : 1.0f;
+      const float ref = r < g.nb ? g.ref[row] : 0.0f, c = r < g.nb ? g.factor[r] : 1.0f;
       const int64_t first = a0 + wa + 4 * hf;
       const int64_t end = g.na - first;
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n)
-          acc[i][j][n] = 32 * i + 8 * (n >> 2) + (n & 3) < end ? __builtin_amdgcn_exp2f((acc[i][j][n] - ref) * g.k2) : 0.0f;
+          acc[i][j][n] = 32 * i + 8 * (n >> 2) + (n & 3) < end ? c * __builtin_amdgcn_exp2f((acc[i][j][n] - ref) * g.k2) : 0.0f;
       for (int k = 0; k < g.top; ++k) {
         const int64_t at = g.ids[row * g.top + k] - first;
         const float l = g.logp[row * g.top + k];
-        const float p = l == -INFINITY ? 0.0f : __expf(l) / c;
+        const float p = l == -INFINITY ? 0.0f : __expf(l);
 #pragma unroll
         for (int i = 0; i < MA; ++i)
 #pragma unroll
@@ -814,6 +823,20 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
         for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
     if constexpr (!F32)
       put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb);
+  }
+
+  if constexpr (EPI == EPI_ROWS) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int64_t r = b0 + wb + 32 * j + col;
+      const float w = r < g.nb ? g.row_weight[g.to[r]] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
+    }
+    if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.out, g.ldo, a0, b0, g.nb, 0, g.to);
+    else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb, g.to);
   }
 
   if constexpr (EPI == EPI_ACC)
