@@ -90,7 +90,7 @@ struct JoinArgs {
   const int64_t *label, *ids;
   const float* logp;
   int top;
-  float scale, k2;
+  float scale, k2, k2_low;
   float *loss, *lse;
   // a training step
   int all;                 // rows that are left out have a place, too
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
       const float l2 = __log2f(s);
       const bool near = fabsf((m - ref) * a.k2 + l2) <= kFar;
       if (!near) ref = m + l2 / a.k2;
-      const float c = __builtin_amdgcn_exp2f((ref - m) * a.k2) / s;
+      const float c = exp2_of(ref, m, a.k2, a.k2_low) / s;
       if (!near) {
         if (tid == 0) {
           slot = atomicAdd(a.again_count, 1);
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
       if (tid < a.top && !(lp == -INFINITY)) {
         float sum = 0.0f;
         for (int j = 0; j < a.top; ++j) sum += id[j] == id[tid] ? p[j] : 0.0f;
-        const float q = __builtin_amdgcn_exp2f((float)(z[tid] - ref) * a.k2);
+        const float q = exp2_of((float)z[tid], ref, a.k2, a.k2_low);
         if (BF16) ((uint16_t*)a.g)[(int64_t)place * a.ldg + id[tid]] = (uint16_t)bf16_bits(fmaf(q, c, -sum));
         else ((float*)a.g)[(int64_t)place * a.ldg + id[tid]] = q - sum / c;
       }
@@ -427,7 +427,7 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   g.na = s.vocab, g.nb = s.n, g.K = p.dp;
   g.count = count;
   g.part = ws.part, g.parts = p.parts;
-  g.k2 = s.scale * 1.4426950408889634f;
+  g.k2 = (float)(s.scale * kLog2e), g.k2_low = (float)(s.scale * kLog2e - g.k2);
   g.g = k.g, g.ldg = p.ldg;
   g.ref = ws.ref, g.index = index;
   e = gemm<false, false, EPI_KEPT>(g, s.bf16, p.side, st);
@@ -436,7 +436,7 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   a.part = ws.part, a.parts = p.parts, a.at = p.gather ? ws.at : nullptr;
   a.x = g.b, a.w = g.a, a.dp = p.dp, a.n = s.n;
   a.label = ws.label, a.ids = ids, a.logp = ws.logp, a.top = s.top;
-  a.scale = s.scale, a.k2 = g.k2;
+  a.scale = s.scale, a.k2 = g.k2, a.k2_low = g.k2_low;
   a.loss = loss, a.lse = lse;
   if (train) {
     a.all = !p.gather;

@@ -67,6 +67,7 @@ struct RowArgs {
   int64_t n, vocab;
   const int64_t* tokens;   // or null
   float scale, k2;
+  double per_k2;           // the difference and its product were rounded, to 2^-23
   int top;
   float *logprob, *entropy;
   int64_t* ids;
@@ -99,21 +100,20 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
   constexpr int NW = NT / 64;
   constexpr int kTake = 64 / NW;  // classes a wave computes between two selections
   constexpr int kList = kTopMost + 64;
-  constexpr int kPlaces = NT < 256 ? NT : 256, kShare = NT / kPlaces;  // of the first choice; threads that share one
   constexpr int kScan = NT < 1024 ? 4 : 2;  // groups a thread looks at together
   __shared__ float4 part[NW];
-  __shared__ float first[kPlaces];
+  __shared__ uint32_t first[NT];
+  __shared__ uint32_t bound;
   __shared__ double lz[2][kList];
   __shared__ int lc[2][kList];
   __shared__ int items[kFlush + 4 * kScan * NT];
   __shared__ int counts[2];       // entries of the list, pending items
   __shared__ double token_z;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const double per_k2 = (1.0 - 0x1p-20) / g.k2;  // the difference and its product were rounded, to 2^-23
   // the largest logit that a key stands for (minus infinity: a masked class)
   auto bound_of = [&](float top, uint32_t key) {
     const uint32_t b = key & ~63u;
-    return b < 0x7f800000u ? (double)top - (double)__uint_as_float(b) * per_k2 : -INFINITY;
+    return b < 0x7f800000u ? (double)top - (double)__uint_as_float(b) * g.per_k2 : -INFINITY;
   };
 #pragma unroll 1
   for (int64_t r = blockIdx.x; r < g.n; r += gridDim.x) {
@@ -150,14 +150,14 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
           if (b > best) best = b, own = (i0 + q * NT) * 64 + (key[q] & 63);
         }
       }
-      if (best > -INFINITY) own = (int)group_class(own >> 6, own & 63, g.side, g.apart, g.parts);
-      if (best <= kMasked) best = -INFINITY;
-#pragma unroll
-      for (int k = 1; k < kShare; k <<= 1) {
-        const float o = __shfl_xor(best, k);
-        const int c = __shfl_xor(own, k);
-        if (o > best || (o == best && c < own)) best = o, own = c;
+      if (4 * groups <= NT) {  // few groups: each bound has a thread
+        const int i = tid >> 2;
+        const uint4 k = i < groups ? keys[i] : uint4{~0u, ~0u, ~0u, ~0u};
+        const uint32_t key = tid & 2 ? tid & 1 ? k.w : k.z : tid & 1 ? k.y : k.x;
+        best = i < groups ? (float)bound_of(tops[i], key) : -INFINITY, own = i * 64 + (key & 63);
       }
+      if (best > -INFINITY) own = (int)group_class(own >> 6, own & 63, g.side, g.apart, g.parts);
+      if (best <= kMasked || own >= g.vocab) best = -INFINITY;
     }
     // the row's maximum, sum and first moment
     float m = -INFINITY, s = 0.0f, t = 0.0f;
@@ -173,7 +173,9 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     }
     __syncthreads();  // the last row's shared values have been read
     if (lane == 0) part[wave] = float4{m, s, t, 0.0f};
-    if (tid % kShare == 0) first[tid / kShare] = best;
+    // floats in the order of whole numbers
+    const uint32_t order = __float_as_uint(best) ^ (__float_as_int(best) >> 31 | 0x80000000u);
+    first[tid] = order;
     if (tid < 2) counts[tid] = 0;
     __syncthreads();
     if (NW > 1) {
@@ -193,20 +195,23 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     double bar = -INFINITY;
     int bar_class = 0x7fffffff;
     if (!none && !bad) {
-      // first the best `top` of the threads' classes (each of a place's threads compares it to its share of the
-      // others), and the token
+      // first the best `top` of the threads' classes (by 20 bits, which a wave finds one by one), and the token
       if (g.top) {
-        const int me = tid / kShare, from = tid % kShare * (kPlaces / kShare);
-        int rank = 0;
-#pragma unroll 2
-        for (int i = from; i < from + kPlaces / kShare; i += 4) {
-          const float4 o = *(const float4*)(first + i);
-          rank += (o.x > best || (o.x == best && i + 0 < me)) + (o.y > best || (o.y == best && i + 1 < me)) +
-                  (o.z > best || (o.z == best && i + 2 < me)) + (o.w > best || (o.w == best && i + 3 < me));
-        }
+        if (wave == 0) {
+          uint32_t v[NW], b = 0;
 #pragma unroll
-        for (int k = 1; k < kShare; k <<= 1) rank += __shfl_xor(rank, k);
-        if (tid % kShare == 0 && best > -INFINITY && rank < g.top && own != (int)y) items[atomicAdd(&counts[1], 1)] = own;
+          for (int w = 0; w < NW; ++w) v[w] = first[w * 64 + lane];
+#pragma unroll 1
+          for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
+            int above = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) above += __popcll(__ballot(v[w] >= (b | bit)));
+            if (above >= g.top) b |= bit;
+          }
+          if (lane == 0) bound = b;
+        }
+        __syncthreads();
+        if (best > -INFINITY && order >= bound && own != (int)y) items[atomicAdd(&counts[1], 1)] = own;
       }
       if (tid == 0) items[atomicAdd(&counts[1], 1)] = (int)y;
       __syncthreads();
@@ -339,7 +344,8 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   // Rows of a tile 64 apart: all tiles' (256 x 256, 2048 columns) takes 10% longer, their pages no longer at hand,
   // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.
-  p.apart = (int)std::min<int64_t>(std::min(p.parts, 64), INT32_MAX / ((int64_t)p.side * p.dp * p.el));
+  p.apart = 64;
+  while (p.apart > p.parts || (int64_t)p.apart * p.side * p.dp * p.el > INT32_MAX) p.apart /= 2;
   p.norms = s.top && s.bf16 && p.side == 256;
   p.gather = tokens && 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) >= kGatherFrom;
   return p;
@@ -401,7 +407,7 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
   g.count = count;
   g.parts = p.parts, g.apart = p.apart;
   g.sums = ws.sums;
-  g.k2 = s.scale * 1.4426950408889634f;
+  g.k2 = (float)(s.scale * kLog2e), g.k2_low = (float)(s.scale * kLog2e - g.k2);
   g.keys = ws.keys, g.tops = ws.tops, g.a_norm = ws.a_norm, g.b_norm = ws.b_norm;
   // roundings on a term's way: eight for each of dp / 16 matrix instructions; in fp32 six instructions with
   // those for each 16 columns, and the planes that are not multiplied; a hundredth for the norms' own
@@ -421,7 +427,7 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
   a.x = g.b, a.w = g.a, a.dp = p.dp;
   a.n = s.n, a.vocab = s.vocab;
   a.tokens = tokens;
-  a.scale = s.scale, a.k2 = g.k2, a.top = s.top;
+  a.scale = s.scale, a.k2 = g.k2, a.per_k2 = (1.0 - 0x1p-20) / g.k2, a.top = s.top;
   a.logprob = logprob, a.entropy = entropy, a.ids = top_ids, a.top_logprobs = top_logprobs;
   const unsigned rows = (unsigned)std::min<int64_t>(s.n, 1 << 20);
   auto launch = [&](auto nt) {

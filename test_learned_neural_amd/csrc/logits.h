@@ -17,6 +17,14 @@ constexpr float kDown = 40.0f;  // KEPT: 2^-kDown on what is kept of bf16 calls,
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
 enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN, EPI_ROWS };
 
+// 2^(k2 (a - b)) to a few units in the last place, whatever a - b: what the difference and the factor lost to
+// rounding is small, but the same for a whole row.
+__device__ __forceinline__ float exp2_of(float a, float b, float k2, float k2_low) {
+  const float x = a - b, t = x - a, lost = (a - (x - t)) - (b + t);
+  const float low = fabsf(x) < 1.0e30f ? fmaf(x, k2_low, lost * k2) : 0.0f;  // of a masked class there is none
+  return __builtin_amdgcn_exp2f(fmaf(x, k2, low));
+}
+
 struct GemmArgs {
   const void* a;
   const void* b;
@@ -45,7 +53,7 @@ struct GemmArgs {
   const float* scale;      // GRAD: see gw; OUT: one factor, or null
   void* out;               // [nb][ldo]
   int64_t ldo;
-  float k2;                // SUMS, TOP, KEPT: scale log2 e
+  float k2, k2_low;        // SUMS, TOP, KEPT, AGAIN: scale log2 e, and what its rounding left
   float4* sums;            // SUMS, TOP: [nb][parts]: (maximum m of z, sum of e = exp(scale (z - m)), sum of e (z - m), -)
   uint4* keys;             // TOP: [nb][4 parts], by group_class's groups: the four largest bounds of what z may be in 64
                            // bits, as differences to
@@ -69,8 +77,8 @@ struct TileRows {
   int64_t first;  // the tile's first row; the others follow `step` apart
   int step;
 };
-__device__ __forceinline__ TileRows tile_rows(int tile, int side, int apart, int tiles) {
-  const int t = tile / apart * apart;
+__device__ __forceinline__ TileRows tile_rows(int tile, int side, int apart, int tiles) {  // apart: a power of two
+  const int t = tile & -apart;
   return {(int64_t)t * side + (tile - t), min(apart, tiles - t)};
 }
 __device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) {
@@ -426,6 +434,18 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int n = 0; n < B::kLoads; ++n) load_b(n, d);
       next();
     };
+    // logits that are exponents: the five small products are summed apart, which leaves the large one's sum one
+    // rounding in place of six for 16 columns (47 x 3616 x 2573: lse 3.7e-7 -> 1.5e-7 off)
+    constexpr bool kApartSums = EPI == EPI_SUMS || EPI == EPI_TOP || EPI == EPI_KEPT;
+    f32x16 low[kApartSums ? MA : 1][NB];
+    if constexpr (kApartSums) {
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) low[i][j][n] = 0.0f;
+    }
     // PLANES: operands split into three bf16 planes, six products; else fp32 matrix instructions
     auto product = [&](auto planes, f32x16(&acc)[MA][NB]) {
       constexpr bool PLANES = decltype(planes)::value;
@@ -483,7 +503,10 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
               for (int i = 0; i < MA; ++i)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = mfma32(ap[i][kA[q]], bp[j][kB[q]], acc[i][j]);
+                for (int j = 0; j < NB; ++j) {
+                  f32x16& to = kApartSums && q < 5 ? low[i][j] : acc[i][j];
+                  to = mfma32(ap[i][kA[q]], bp[j][kB[q]], to);
+                }
           }
         }
       }
@@ -491,6 +514,14 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       wait_all<0>();
     };
     product(std::true_type{}, acc);
+    if constexpr (kApartSums) {
+#pragma unroll
+      for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) acc[i][j][n] += low[i][j][n];
+    }
     // Planes have no infinity (inf - inf, and zero planes times it) and no float beyond bf16's largest: every
     // sum that one enters is NaN.  Such sums (masked classes; or NaN in the inputs) are computed again as
     // the definition has them; the tile's others stay, whatever their neighbours hold.
@@ -673,7 +704,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const float x = acc[i][j][n] - from, y = x * g.k2, e = __builtin_amdgcn_exp2f(y);
+          const float x = acc[i][j][n] - from, y = x * g.k2;
+          const float e = F32 ? exp2_of(acc[i][j][n], from, g.k2, g.k2_low) : __builtin_amdgcn_exp2f(y);
           s += e;
           if constexpr (EPI == EPI_KEPT) acc[i][j][n] = e;
           else t = fmaf(e, fmaxf(x, -3.4028235e38f), t);
@@ -697,8 +729,9 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       if constexpr (EPI == EPI_KEPT) {
         if (g.g) {
           // times exp(scale (m - ref)), and 2^-kDown; where that is no factor to store, the row is written again
-          const float d = r < g.nb ? from - g.ref[g.index ? g.index[r] : r] : 0.0f;
-          const float f = fminf(__builtin_amdgcn_exp2f(fmaf(d, g.k2, F32 ? 0.0f : -kDown)), F32 ? 1.0e30f : 1.0f);
+          const float ref = r < g.nb ? g.ref[g.index ? g.index[r] : r] : 0.0f;
+          const float f = F32 ? fminf(exp2_of(from, ref, g.k2, g.k2_low), 1.0e30f)
+                              : fminf(__builtin_amdgcn_exp2f(fmaf(from - ref, g.k2, -kDown)), 1.0f);
 #pragma unroll
           for (int i = 0; i < MA; ++i)
 #pragma unroll
@@ -746,7 +779,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       for (int i = 0; i < MA; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n)
-          acc[i][j][n] = 32 * i + 8 * (n >> 2) + (n & 3) < end ? c * __builtin_amdgcn_exp2f((acc[i][j][n] - ref) * g.k2) : 0.0f;
+          acc[i][j][n] = 32 * i + 8 * (n >> 2) + (n & 3) < end ? c * exp2_of(acc[i][j][n], ref, g.k2, g.k2_low) : 0.0f;
       for (int k = 0; k < g.top; ++k) {
         const int64_t at = g.ids[row * g.top + k] - first;
         const float l = g.logp[row * g.top + k];
@@ -926,7 +959,8 @@ __global__ void xe_copy(const void* x, int bf16, int64_t rows, int d, int dp, co
 }
 
 // A wave's products of a row of a with N rows of b, in 64 bits.  Loads of 4 KB of each are on their way together;
-// those past the rows' ends are zeros.
+// those past the rows' ends are zeros.  The loop over them stays one: few rows wait for their instructions, 400
+// cycles for 64 bytes of those.
 template <int N, bool BF16>
 __device__ __forceinline__ void row_dots(const void* a, const void* b, int64_t ra, const int (&rb)[N], int dp, int lane,
                                          double (&z)[N]) {
@@ -936,22 +970,22 @@ __device__ __forceinline__ void row_dots(const void* a, const void* b, int64_t r
 #pragma unroll
   for (int n = 0; n < N; ++n) br[n] = make_rsrc((const char*)b + (int64_t)rb[n] * bytes, bytes), z[n] = 0.0;
 #pragma unroll 1
-  for (int o = lane * 16; o < bytes + lane * 16; o += 4096) {
+  for (int o = 0; o < bytes; o += 4096) {
     u32x4 x[4], y[N][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[k] = buf_ld16(ar, o + 1024 * k, 0);
+      x[k] = buf_ld16(ar, lane * 16 + o + 1024 * k, 0);
 #pragma unroll
-      for (int n = 0; n < N; ++n) y[n][k] = buf_ld16(br[n], o + 1024 * k, 0);
+      for (int n = 0; n < N; ++n) y[n][k] = buf_ld16(br[n], lane * 16 + o + 1024 * k, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
+#pragma unroll 1
+    for (int k = 0; k < 4 && o + 1024 * k < bytes; ++k) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          const uint32_t u = x[k][q], v = y[n][k][q];
+          const uint32_t u = x[0][q], v = y[n][0][q];
           if constexpr (BF16) {  // products of bf16 are floats
             z[n] += (double)(__uint_as_float(u << 16) * __uint_as_float(v << 16));
             z[n] += (double)(__uint_as_float(u & 0xFFFF0000u) * __uint_as_float(v & 0xFFFF0000u));
@@ -959,6 +993,13 @@ __device__ __forceinline__ void row_dots(const void* a, const void* b, int64_t r
             z[n] = fma((double)__uint_as_float(u), (double)__uint_as_float(v), z[n]);
           }
         }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        x[i] = x[i + 1];
+#pragma unroll
+        for (int n = 0; n < N; ++n) y[n][i] = y[n][i + 1];
+      }
+    }
   }
 #pragma unroll 1
   for (int k = 32; k; k >>= 1)
@@ -1001,6 +1042,8 @@ __global__ void xe_zero(void* out, int64_t count, int bf16) {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 int64_t align256(int64_t b) { return up(b, 256); }
+
+constexpr double kLog2e = 1.4426950408889634;
 
 template <int TA, int TB, int WA, int WB, int ST, bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {

@@ -96,6 +96,11 @@ CASES = [
     ("tile_less_one", dict(dtype=am.F32, n=127, d=56, vocab=255)),
     ("ragged", dict(dtype=am.BF16, n=333, d=384, vocab=5003, top=20)),
     ("ragged_f32", dict(dtype=am.F32, n=210, d=136, vocab=3001, top=20, near=True)),
+    ("factors_rounded_up_f32", dict(dtype=am.F32, n=90, d=48, vocab=1001, scale=1.25)),
+    ("factors_rounded_down_f32", dict(dtype=am.F32, n=90, d=48, vocab=1001, scale=0.7)),
+    ("wide_rows_f32", dict(dtype=am.F32, n=5, d=1000, vocab=659, top=128)),
+    ("rows_gathered_f32", dict(dtype=am.F32, n=500, d=400, vocab=24001, masked=0.5)),
+    ("rows_gathered", dict(dtype=am.BF16, n=2100, d=1032, vocab=12001, top=16)),
     ("unweighted", dict(dtype=am.F32, n=50, d=32, vocab=99, weights=False)),
     ("far_references", dict(dtype=am.BF16, n=100, d=64, vocab=500, spread=30.0)),
     ("far_references_f32", dict(dtype=am.F32, n=100, d=64, vocab=500, spread=30.0, scale=1.5)),

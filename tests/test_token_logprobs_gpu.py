@@ -92,6 +92,10 @@ CASES = [
     ("groups_past_a_workgroup", dict(dtype=am.BF16, n=3, d=64, vocab=9001, top=64)),
     ("ragged", dict(dtype=am.BF16, n=333, d=384, vocab=5003, top=20, scale=1.25)),
     ("ragged_f32", dict(dtype=am.F32, n=210, d=136, vocab=3001, top=20)),
+    ("factors_rounded_up_f32", dict(dtype=am.F32, n=90, d=48, vocab=1001, top=20, scale=1.25)),
+    ("factors_rounded_down_f32", dict(dtype=am.F32, n=90, d=48, vocab=1001, top=20, scale=0.7)),
+    ("wide_rows_f32", dict(dtype=am.F32, n=47, d=3616, vocab=1301, top=3)),
+    ("few_groups_many_alternatives", dict(dtype=am.BF16, n=17, d=80, vocab=642, top=64)),
     ("frequent_first", dict(dtype=am.BF16, n=200, d=128, vocab=20011, top=64, lean=1.0)),
     ("sharp", dict(dtype=am.BF16, n=100, d=64, vocab=500, spread=20.0)),
     ("sharp_f32", dict(dtype=am.F32, n=100, d=64, vocab=500, spread=20.0, scale=2.0)),
