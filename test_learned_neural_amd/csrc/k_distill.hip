@@ -19,6 +19,7 @@ namespace {
 // how far (times log 2) ref may be from lse: 2^(kFar - kDown) has to stay below 2
 constexpr float kFar = 36.0f;
 constexpr int kMost = 128;  // entries of a row
+constexpr int64_t kManyRows = 4096, kShortRow = 32768;
 
 // log p of each given class (-inf: none), and of each row a label (0, or -1 for a row that has no class) and the
 // logit of its first class.  With `index`, rows are taken as they come, those left out among them.  A wave a row.
@@ -101,12 +102,13 @@ struct JoinArgs {
   void* x_again;
 };
 
-// loss, lse of a row, and of a training step its G.  A workgroup a row.
-template <bool BF16, bool TRAIN>
-__global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
-  __shared__ float2 part[4];
+// loss, lse of a row, and of a training step its G.  A workgroup of NT threads a row: a wave where many rows are short.
+template <int NT, bool BF16, bool TRAIN>
+__global__ __launch_bounds__(NT) void ds_rows(JoinArgs a) {
+  constexpr int NW = NT / 64;
+  __shared__ float2 part[NW];
   __shared__ int id[kMost], list[kMost];
-  __shared__ float p[kMost];
+  __shared__ float p[kMost], lp[kMost];
   __shared__ double z[kMost];
   __shared__ int entries, slot;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
       if (tid == 0) a.loss[r] = 0.0f, a.lse[r] = 0.0f;
       if (TRAIN && tid == 0) a.coef[r] = 0.0f;
       if (TRAIN && a.all)
-        for (int64_t c = tid; c < a.ldg * (BF16 ? 2 : 4) / 16; c += 256)
+        for (int64_t c = tid; c < a.ldg * (BF16 ? 2 : 4) / 16; c += NT)
           ((u32x4*)((char*)a.g + r * a.ldg * (BF16 ? 2 : 4)))[c] = u32x4{0, 0, 0, 0};
       continue;
     }
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
       s = s * __builtin_amdgcn_exp2f((m - from) * a.k2) + os * __builtin_amdgcn_exp2f((om - from) * a.k2);
       m = t;
     };
-    for (int i = tid; i < a.parts; i += 256) {
+    for (int i = tid; i < a.parts; i += NT) {
       const float2 q = a.part[(int64_t)place * a.parts + i];
       join(q.x, q.y);
     }
@@ -138,33 +140,56 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
       join(om, os);
     }
     if (lane == 0) part[wave] = float2{m, s};
-    float lp = -INFINITY;
-    if (tid < a.top) {
-      lp = a.logp[r * a.top + tid];
-      id[tid] = (int)a.ids[r * a.top + tid], p[tid] = lp == -INFINITY ? 0.0f : expf(lp);
-    }
     __syncthreads();
+    for (int j = tid; j < a.top; j += NT) {
+      const float l = a.logp[r * a.top + j];
+      id[j] = (int)a.ids[r * a.top + j], lp[j] = l, p[j] = l == -INFINITY ? 0.0f : expf(l);
+      if (!(l == -INFINITY)) list[atomicAdd(&entries, 1)] = j;
+    }
     m = part[0].x, s = part[0].y;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) join(part[w].x, part[w].y);
-    const float lse = fmaf(a.scale, m, logf(s));
-    if (tid < a.top && !(lp == -INFINITY)) list[atomicAdd(&entries, 1)] = tid;
+    for (int w = 1; w < NW; ++w) join(part[w].x, part[w].y);
+    const float log_s = logf(s), lse = fmaf(a.scale, m, log_s);
     __syncthreads();
-    // logits of the given classes
-    for (int i = 2 * wave; i < entries; i += 8) {
-      const int j[2] = {__builtin_amdgcn_readfirstlane(list[i]),
-                        __builtin_amdgcn_readfirstlane(list[min(i + 1, entries - 1)])};
-      const int c[2] = {__builtin_amdgcn_readfirstlane(id[j[0]]), __builtin_amdgcn_readfirstlane(id[j[1]])};
-      double v[2];
-      row_dots<2, BF16>(a.x, a.w, place, c, a.dp, lane, v);
-      if (lane < 2) z[lane ? j[1] : j[0]] = lane ? v[1] : v[0];
+    // logits of the given classes: short rows by some lanes each, others by a wave, two at a time
+    const int bytes = a.dp * (BF16 ? 2 : 4);
+    if (bytes <= 512) {
+      const int lanes = bytes <= 64 ? 4 : bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32, sub = tid & (lanes - 1);
+      for (int i0 = 0; i0 < entries; i0 += NT / lanes) {
+        const int i = i0 + tid / lanes, j = list[min(i, entries - 1)];
+        double v = 0.0;
+        if (sub * 16 < bytes) {
+          const u32x4 x = *(const u32x4*)((const char*)a.x + (int64_t)place * bytes + sub * 16);
+          const u32x4 w = *(const u32x4*)((const char*)a.w + (int64_t)id[j] * bytes + sub * 16);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (BF16) {
+              v += (double)(__uint_as_float(x[q] << 16) * __uint_as_float(w[q] << 16));
+              v += (double)(__uint_as_float(x[q] & 0xFFFF0000u) * __uint_as_float(w[q] & 0xFFFF0000u));
+            } else {
+              v = fma((double)__uint_as_float(x[q]), (double)__uint_as_float(w[q]), v);
+            }
+          }
+        }
+        for (int k = lanes / 2; k; k >>= 1) v += __shfl_xor(v, k);
+        if (sub == 0 && i < entries) z[j] = v;
+      }
+    } else {
+      for (int i = 2 * wave; i < entries; i += 2 * NW) {
+        const int j[2] = {__builtin_amdgcn_readfirstlane(list[i]),
+                          __builtin_amdgcn_readfirstlane(list[min(i + 1, entries - 1)])};
+        const int c[2] = {__builtin_amdgcn_readfirstlane(id[j[0]]), __builtin_amdgcn_readfirstlane(id[j[1]])};
+        double v[2];
+        row_dots<2, BF16>(a.x, a.w, place, c, a.dp, lane, v);
+        if (lane < 2) z[lane ? j[1] : j[0]] = lane ? v[1] : v[0];
+      }
     }
     __syncthreads();
     if (wave == 0) {
       float loss = 0.0f;
       for (int j = lane; j < a.top; j += 64) {
-        const float l = j == tid ? lp : a.logp[r * a.top + j];
-        if (p[j] != 0.0f) loss += p[j] * (l - (float)(a.scale * z[j] - lse));
+        // log p - log q without lse, whose rounding would be the largest
+        if (p[j] != 0.0f) loss += p[j] * (lp[j] - (float)(a.scale * (z[j] - m)) + log_s);
       }
       for (int k = 32; k; k >>= 1) loss += __shfl_xor(loss, k);
       if (lane == 0) a.loss[r] = loss, a.lse[r] = lse;
@@ -183,7 +208,7 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
         }
         __syncthreads();
         const int words = a.dp * (BF16 ? 2 : 4) / 16;
-        for (int k = tid; k < words; k += 256)
+        for (int k = tid; k < words; k += NT)
           ((u32x4*)a.x_again)[(int64_t)slot * words + k] = ((const u32x4*)a.x)[(int64_t)place * words + k];
         continue;
       }
@@ -192,26 +217,27 @@ __global__ __launch_bounds__(256) void ds_rows(JoinArgs a) {
         u32x4* row = (u32x4*)((uint16_t*)a.g + (int64_t)place * a.ldg);
         const float f = c * exp2f(kDown);
         const int words = (int)(a.ldg / 8);
-        for (int k0 = tid; k0 < words; k0 += 4 * 256) {
+        for (int k0 = tid; k0 < words; k0 += 4 * NT) {
           u32x4 v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (k0 + 256 * k < words) v[k] = row[k0 + 256 * k];
+            if (k0 + NT * k < words) v[k] = row[k0 + NT * k];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[k][q] = cvt_pk_bf16(u16_lo(v[k][q]) * f, u16_hi(v[k][q]) * f);
-            if (k0 + 256 * k < words) row[k0 + 256 * k] = v[k];
+            if (k0 + NT * k < words) row[k0 + NT * k] = v[k];
           }
         }
         __syncthreads();  // those are there before the given classes' entries
       }
-      if (tid < a.top && !(lp == -INFINITY)) {
+      for (int j = tid; j < a.top; j += NT) {
+        if (lp[j] == -INFINITY) continue;
         float sum = 0.0f;
-        for (int j = 0; j < a.top; ++j) sum += id[j] == id[tid] ? p[j] : 0.0f;
-        const float q = exp2_of((float)z[tid], ref, a.k2, a.k2_low);
-        if (BF16) ((uint16_t*)a.g)[(int64_t)place * a.ldg + id[tid]] = (uint16_t)bf16_bits(fmaf(q, c, -sum));
-        else ((float*)a.g)[(int64_t)place * a.ldg + id[tid]] = q - sum / c;
+        for (int i = 0; i < a.top; ++i) sum += id[i] == id[j] ? p[i] : 0.0f;
+        const float q = exp2_of((float)z[j], ref, a.k2, a.k2_low);
+        if (BF16) ((uint16_t*)a.g)[(int64_t)place * a.ldg + id[j]] = (uint16_t)bf16_bits(fmaf(q, c, -sum));
+        else ((float*)a.g)[(int64_t)place * a.ldg + id[j]] = q - sum / c;
       }
     }
   }
@@ -301,8 +327,36 @@ __global__ __launch_bounds__(256) void ds_weigh(const void* x, int bf16, int64_t
   else *(float4*)((float*)out + o) = float4{v[0], v[1], v[2], v[3]};
 }
 
+// The sums of the contraction's pieces: rows of a place (or all) times their weight, or one factor; zeros for the
+// others.  Four columns a thread.
+__global__ __launch_bounds__(256) void ds_sum(const float* acc, int splits, int64_t rows, int d, int dp, const int* at,
+                                              const float* weight, const float* factor, void* out, int out_bf16, int vec) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / (dp / 4);
+  const int c = (int)(i % (dp / 4)) * 4;
+  if (r >= rows || c >= d) return;
+  const int64_t place = at ? at[r] : r;
+  float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (place >= 0) {
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+      const float4 a = *(const float4*)(acc + (s * rows + place) * dp + c);
+      v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+    }
+  }
+  const float w = place < 0 ? 0.0f : weight ? weight[r] : *factor;
+  const float x[4] = {v.x * w, v.y * w, v.z * w, v.w * w};
+  const int64_t o = r * d + c;
+  if (vec && out_bf16) *(uint2*)((uint16_t*)out + o) = uint2{cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])};
+  else if (vec) *(float4*)((float*)out + o) = float4{x[0], x[1], x[2], x[3]};
+  else
+    for (int k = 0; k < 4 && c + k < d; ++k) {
+      if (out_bf16) ((uint16_t*)out)[o + k] = (uint16_t)bf16_bits(x[k]);
+      else ((float*)out)[o + k] = x[k];
+    }
+}
+
 struct Plan {
-  int el, dp, side, parts, side_x, splits;
+  int el, dp, side, parts, side_x, splits, side_w, splits_w;
   int64_t ldg;
   bool gather;
 };
@@ -310,13 +364,17 @@ Plan plan_of(const Distillation& s, bool train) {
   Plan p = {};
   p.el = s.bf16 ? 2 : 4;
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
-  p.side = side_of(s.vocab, s.n, s.bf16);
+  p.side = side_for(s.vocab, s.n, s.bf16);
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   p.ldg = up(s.vocab, 64);
-  p.side_x = side_split(p.dp, s.n, s.bf16);
-  const int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.side_x), 1);
+  p.side_x = s.n <= kFew ? (s.bf16 ? 128 : 64) : side_split(p.dp, s.n, s.bf16);
+  int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.side_x), 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.side_x == 256 ? 256 : 512) / tiles, s.vocab / 512));
   if (tiles * p.splits <= 128) p.side_x = 64;
+  p.side_w = side_of(p.dp, s.vocab, s.bf16);
+  tiles = tiles_of(p.dp, s.vocab, p.side_w);
+  // dW's contraction is cut where its tiles leave more than half of the chip idle
+  p.splits_w = (int)std::max<int64_t>(1, std::min<int64_t>(tiles <= 128 ? 512 / tiles : 1, s.n / 512));
   // a training step has three products to leave rows out of
   p.gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) * (train ? 4 : 1) >= kGatherFrom;
   return p;
@@ -384,10 +442,21 @@ Space space_of(void* p, const Distillation& s, const Plan& l, bool backward) {
     at = both;
     w.weight = (float*)take(4 * s.n);
     w.equal = (int*)take(8), w.scale = (float*)(w.equal + 1);
-    if (l.splits > 1) w.acc = (float*)take(4 * (int64_t)l.splits * s.n * l.dp);
+    // sums of dX's pieces, and then of dW's
+    w.acc = (float*)take(4 * (int64_t)l.dp * std::max(l.splits > 1 ? l.splits * s.n : 0,
+                                                      l.splits_w > 1 ? l.splits_w * s.vocab : 0));
   }
   w.bytes = std::max(at, end) - (char*)p;
   return w;
+}
+
+atlasmem_status sum_pieces(const float* acc, int splits, int64_t rows, const Distillation& s, const Plan& p, const int* at,
+                           const float* weight, const float* factor, void* out, hipStream_t st) {
+  const int vec = s.d % 4 == 0 && ((uintptr_t)out & 15) == 0;
+  ds_sum<<<(unsigned)((rows * (p.dp / 4) + 255) / 256), 256, 0, st>>>(acc, splits, rows, s.d, p.dp, at, weight, factor,
+                                                                      out, s.bf16, vec);
+  AM_LAUNCH_CHECK();
+  return ATLASMEM_OK;
 }
 
 }  // namespace
@@ -430,7 +499,7 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   g.k2 = (float)(s.scale * kLog2e), g.k2_low = (float)(s.scale * kLog2e - g.k2);
   g.g = k.g, g.ldg = p.ldg;
   g.ref = ws.ref, g.index = index;
-  e = gemm<false, false, EPI_KEPT>(g, s.bf16, p.side, st);
+  e = s.n <= kFew ? gemm_few<false, EPI_KEPT>(g, s.bf16, st) : gemm<false, false, EPI_KEPT>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   JoinArgs a = {};
   a.part = ws.part, a.parts = p.parts, a.at = p.gather ? ws.at : nullptr;
@@ -444,14 +513,22 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
     a.again = ws.again, a.to = ws.to, a.again_count = ws.again_count, a.x_again = ws.x_again;
   }
   const unsigned rows = (unsigned)std::min<int64_t>(s.n, 1 << 20);
-  if (s.bf16) train ? ds_rows<true, true><<<rows, 256, 0, st>>>(a) : ds_rows<true, false><<<rows, 256, 0, st>>>(a);
-  else train ? ds_rows<false, true><<<rows, 256, 0, st>>>(a) : ds_rows<false, false><<<rows, 256, 0, st>>>(a);
+  auto launch = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    if (s.bf16) train ? ds_rows<NT, true, true><<<rows, NT, 0, st>>>(a) : ds_rows<NT, true, false><<<rows, NT, 0, st>>>(a);
+    else train ? ds_rows<NT, false, true><<<rows, NT, 0, st>>>(a) : ds_rows<NT, false, false><<<rows, NT, 0, st>>>(a);
+  };
+  // what a row's workgroup reads and writes
+  const int64_t row_bytes = p.el * ((train ? p.ldg : 0) + (int64_t)s.top * p.dp);
+  if (s.n >= kManyRows && row_bytes <= kShortRow) launch(std::integral_constant<int, 64>{});
+  else launch(std::integral_constant<int, 256>{});
   AM_LAUNCH_CHECK();
   if (!train) return ATLASMEM_OK;
   g.b = ws.x_again;
   g.count = ws.again_count, g.index = ws.again, g.to = ws.to;
   g.ids = ids, g.logp = ws.logp, g.factor = ws.factor, g.top = s.top;
-  return gemm<false, false, EPI_AGAIN>(g, s.bf16, p.side, st);
+  return s.n <= kFew ? gemm_few<false, EPI_AGAIN>(g, s.bf16, st)
+                     : gemm<false, false, EPI_AGAIN>(g, s.bf16, p.side, st);
 }
 
 atlasmem_status distillation_backward(const Distillation& s, const void* X, const void* W, const void* kept,
@@ -485,19 +562,16 @@ atlasmem_status distillation_backward(const Distillation& s, const void* X, cons
     x.a = w_direct ? W : ws.w, x.lda = p.dp, x.na = p.dp;
     x.b = k.g, x.ldb = p.ldg, x.nb = s.n;
     x.K = s.vocab;
+    const bool few = s.n <= kFew && p.side_x != (s.bf16 ? 64 : 128);
     if (p.splits == 1) {
       x.out = dX, x.ldo = s.d, x.to = k.index, x.row_weight = ws.weight;
-      e = gemm<true, false, EPI_ROWS>(x, s.bf16, p.side_x, st);
-      if (e != ATLASMEM_OK) return e;
+      e = few ? gemm_few<true, EPI_ROWS>(x, s.bf16, st) : gemm<true, false, EPI_ROWS>(x, s.bf16, p.side_x, st);
     } else {
       x.splits = p.splits, x.acc = ws.acc, x.acc_rows = s.n;
-      e = gemm<true, false, EPI_ACC>(x, s.bf16, p.side_x, st);
-      if (e != ATLASMEM_OK) return e;
-      const int vec = s.d % 4 == 0 && ((uintptr_t)dX & 15) == 0;
-      xe_sum<<<(unsigned)((s.n * (p.dp / 4) + 255) / 256), 256, 0, st>>>(ws.acc, p.splits, s.n, s.d, p.dp, k.at,
-                                                                         ws.weight, dX, s.bf16, vec);
-      AM_LAUNCH_CHECK();
+      e = few ? gemm_few<true, EPI_ACC>(x, s.bf16, st) : gemm<true, false, EPI_ACC>(x, s.bf16, p.side_x, st);
+      if (e == ATLASMEM_OK) e = sum_pieces(ws.acc, p.splits, s.n, s, p, k.at, ws.weight, nullptr, dX, st);
     }
+    if (e != ATLASMEM_OK) return e;
   }
   if (dW) {
     GemmArgs x = {};
@@ -505,9 +579,15 @@ atlasmem_status distillation_backward(const Distillation& s, const void* X, cons
     x.a = ws.x, x.lda = p.dp, x.na = p.dp;
     x.b = k.g, x.ldb = p.ldg, x.nb = s.vocab;
     x.K = s.n;
-    x.scale = ws.scale;
-    x.out = dW, x.ldo = s.d;
-    e = gemm<true, true, EPI_OUT>(x, s.bf16, side_of(p.dp, s.vocab, s.bf16), st);
+    if (p.splits_w == 1) {
+      x.scale = ws.scale;
+      x.out = dW, x.ldo = s.d;
+      e = gemm<true, true, EPI_OUT>(x, s.bf16, p.side_w, st);
+    } else {
+      x.splits = p.splits_w, x.acc = ws.acc, x.acc_rows = s.vocab;
+      e = gemm<true, true, EPI_PART>(x, s.bf16, p.side_w, st);
+      if (e == ATLASMEM_OK) e = sum_pieces(ws.acc, p.splits_w, s.vocab, s, p, nullptr, nullptr, ws.scale, dW, st);
+    }
     if (e != ATLASMEM_OK) return e;
   }
   return ATLASMEM_OK;

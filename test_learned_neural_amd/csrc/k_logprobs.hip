@@ -187,7 +187,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
         join(m, s, t, om, os, ot, g.k2);
       }
     }
-    const float lse = fmaf(g.scale, m, logf(s));
+    const float log_s = logf(s), lse = fmaf(g.scale, m, log_s);
     const bool none = lse == -INFINITY, bad = !none && !(fabsf(lse) < INFINITY);
 
     // The list of what is known in 64 bits, in order; the last of its `top`, if there are so many, is the bar.
@@ -318,14 +318,15 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
       }
     }
     if (tid == 0) {
-      const double p = bad || none ? 0.0 : (double)g.scale * token_z - (double)lse;
-      const float h = logf(s) - g.scale * t / s;
+      // without lse, whose rounding would be the largest
+      const double p = bad || none ? 0.0 : g.scale * (token_z - (double)m) - (double)log_s;
+      const float h = log_s - g.scale * t / s;
       if (g.logprob) g.logprob[r] = bad ? NAN : none ? -INFINITY : p > 0.0 ? 0.0f : (float)p;
       if (g.entropy) g.entropy[r] = bad ? NAN : none || h < 0.0f ? 0.0f : h;
     }
     if (tid < g.top) {
       const bool there = tid < known;
-      const double p = there ? (double)g.scale * lz[buf][tid] - (double)lse : -INFINITY;
+      const double p = there ? g.scale * (lz[buf][tid] - (double)m) - (double)log_s : -INFINITY;
       g.ids[r * g.top + tid] = there ? lc[buf][tid] : -1;
       g.top_logprobs[r * g.top + tid] = bad ? NAN : p > 0.0 ? 0.0f : (float)p;
     }
@@ -340,7 +341,7 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   Plan p = {};
   p.el = s.bf16 ? 2 : 4;
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
-  p.side = side_of(s.vocab, s.n, s.bf16);
+  p.side = side_for(s.vocab, s.n, s.bf16);
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   // Rows of a tile 64 apart: all tiles' (256 x 256, 2048 columns) takes 10% longer, their pages no longer at hand,
   // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.
@@ -419,7 +420,8 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
     lp_row_norms<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>((const uint16_t*)g.b, s.n, count, p.dp, ws.b_norm);
     AM_LAUNCH_CHECK();
   }
-  e = s.top ? gemm<false, false, EPI_TOP>(g, s.bf16, p.side, st) : gemm<false, false, EPI_SUMS>(g, s.bf16, p.side, st);
+  if (s.n <= kFew) e = s.top ? gemm_few<false, EPI_TOP>(g, s.bf16, st) : gemm_few<false, EPI_SUMS>(g, s.bf16, st);
+  else e = s.top ? gemm<false, false, EPI_TOP>(g, s.bf16, p.side, st) : gemm<false, false, EPI_SUMS>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   RowArgs a = {};
   a.sums = ws.sums, a.keys = ws.keys, a.tops = ws.tops, a.parts = p.parts, a.side = p.side, a.apart = p.apart;

@@ -15,7 +15,7 @@ namespace {
 
 constexpr float kDown = 40.0f;  // KEPT: 2^-kDown on what is kept of bf16 calls, whose 16 bits end at 2
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
-enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN, EPI_ROWS };
+enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN, EPI_ROWS, EPI_PART };
 
 // 2^(k2 (a - b)) to a few units in the last place, whatever a - b: what the difference and the factor lost to
 // rounding is small, but the same for a whole row.
@@ -31,9 +31,9 @@ struct GemmArgs {
   int64_t lda, ldb;        // elements of a row
   int64_t na, nb;          // rows (or, across the contraction, columns) of a and b
   int64_t K;
-  const int* count;        // rows that count (OUT: K, else nb), or null: as given
+  const int* count;        // rows that count (OUT, PART: K, else nb), or null: as given
   int ta, tb;              // tiles of a and b
-  int splits;              // pieces of the contraction (ACC; else 1)
+  int splits;              // pieces of the contraction (ACC, PART; else 1)
   // epilogues
   float2* part;            // LSE: [nb][parts]: (maximum, sum of exponentials)
   int parts;
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   // The workgroups of one XCD are neighbours, and share its L2: the tiles of one piece of the contraction
   // before the next piece's, eight tiles of b beside four of a at a time.
   if (g.count) {
-    if constexpr (EPI == EPI_OUT) {
+    if constexpr (EPI == EPI_OUT || EPI == EPI_PART) {
       g.K = *g.count;
       if (g.gw && !*g.equal) g.b = g.gw;
     } else {
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   const int64_t a0 = (int64_t)(in / width) * TA, b0 = (int64_t)(group * 8 + in % width) * TB;
 
   int64_t k0 = 0, k1 = g.K;
-  if constexpr (EPI == EPI_ACC) {
+  if constexpr (EPI == EPI_ACC || EPI == EPI_PART) {
     const int64_t each = ((g.K + kBK - 1) / kBK + g.splits - 1) / g.splits;
     k0 = min(split * each * kBK, g.K);
     k1 = min(k0 + each * kBK, g.K);
@@ -872,7 +872,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb, g.to);
   }
 
-  if constexpr (EPI == EPI_ACC)
+  if constexpr (EPI == EPI_ACC || EPI == EPI_PART)
     put_rows32<MA, NB>(acc, wa, wb, lane, g.acc + (int64_t)split * g.acc_rows * g.lda, g.lda, a0, b0, g.nb, g.add);
   if constexpr (F32 && EPI == EPI_OUT)
     put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.out, g.ldo, a0, b0, g.nb, 0);
@@ -1054,7 +1054,7 @@ atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
     return ATLASMEM_E_DEVICE;
   g.ta = (int)((g.na + TA - 1) / TA);
   g.tb = (int)((g.nb + TB - 1) / TB);
-  if (EPI != EPI_ACC) g.splits = 1;
+  if (EPI != EPI_ACC && EPI != EPI_PART) g.splits = 1;
   const int64_t blocks = up((int64_t)g.ta * g.tb * g.splits, 8);
   kern<<<(unsigned)blocks, WA * WB * 64, lds, st>>>(g);
   AM_LAUNCH_CHECK();
@@ -1074,6 +1074,18 @@ int side_of(int64_t na, int64_t nb, bool bf16) {
 }
 int side_split(int64_t na, int64_t nb, bool bf16) {
   return bf16 && tiles_of(na, nb, 256) * 28 <= tiles_of(na, nb, 128) * 10 ? 256 : 128;
+}
+
+// Of at most 64 rows, tiles of 128 x 64 for bf16 (a workgroup of three on a CU; 1 x 1024 x 50257 26 -> 21 us, 64 x
+// 2048 x 65536 51 -> 46; 64 x 64: 23 and 61) and of 64 for fp32 (22 x 504 x 33288 55 -> 30 us; 128 x 64: 34).
+constexpr int64_t kFew = 64;
+int side_for(int64_t na, int64_t nb, bool bf16) {
+  return nb <= kFew ? (bf16 ? 128 : 64) : side_of(na, nb, bf16);
+}
+template <bool AX, int EPI>
+atlasmem_status gemm_few(const GemmArgs& g, bool bf16, hipStream_t st) {
+  if (bf16) return gemm_launch<128, 64, 2, 2, 4, AX, false, EPI, false>(g, st);
+  return gemm_launch<64, 64, 2, 2, 2, AX, false, EPI, true>(g, st);
 }
 
 template <bool AX, bool BX, int EPI>

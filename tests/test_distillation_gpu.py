@@ -101,6 +101,11 @@ CASES = [
     ("wide_rows_f32", dict(dtype=am.F32, n=5, d=1000, vocab=659, top=128)),
     ("rows_gathered_f32", dict(dtype=am.F32, n=500, d=400, vocab=24001, masked=0.5)),
     ("rows_gathered", dict(dtype=am.BF16, n=2100, d=1032, vocab=12001, top=16)),
+    ("many_short_rows", dict(dtype=am.BF16, n=4500, d=40, vocab=300, top=20)),
+    ("many_short_rows_f32", dict(dtype=am.F32, n=4200, d=23, vocab=130, top=64)),
+    ("many_short_rows_far_references", dict(dtype=am.BF16, n=4100, d=64, vocab=200, top=3, spread=30.0)),
+    ("as_many_rows_as_few", dict(dtype=am.BF16, n=64, d=520, vocab=3001, top=9)),
+    ("as_many_rows_as_few_f32", dict(dtype=am.F32, n=64, d=260, vocab=3001, top=9)),
     ("unweighted", dict(dtype=am.F32, n=50, d=32, vocab=99, weights=False)),
     ("far_references", dict(dtype=am.BF16, n=100, d=64, vocab=500, spread=30.0)),
     ("far_references_f32", dict(dtype=am.F32, n=100, d=64, vocab=500, spread=30.0, scale=1.5)),
