@@ -59,7 +59,8 @@ __global__ __launch_bounds__(256) void lp_group_norms(const uint16_t* w, int64_t
 struct RowArgs {
   const float4* sums;
   const uint4* keys;
-  const float* tops;
+  const float *tops, *a_norm, *b_norm;
+  float error;             // of z, relative to |a| |b|
   int parts, side, apart;
   const int* at;           // a row's place among those that count, or null: all are there
   const void *x, *w;       // as the products took them, [..][dp]
@@ -131,9 +132,16 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     // the best class of each thread's groups, by their largest bound
     const int groups = 4 * g.parts;
     const uint4* keys = g.keys + (int64_t)place * groups;
-    const float* tops = g.tops + (int64_t)place * groups;
+    const float* tops = g.tops + (int64_t)place * (groups / 2);
+    const float error = g.top ? g.error * g.b_norm[place] : 0.0f;
+    // what the maximum of group i may be in 64 bits
+    auto top_of = [&](int i) {
+      const float t = fmaf(error, g.a_norm[i], tops[(i >> 2) * 2 + (i & 1)]);
+      return fmaf(fabsf(t), 0x1p-21f, t);
+    };
     float best = -INFINITY;
     int own = 0x7fffffff;
+    bool all = NT <= 256;  // threads whose class may be a first choice, or one of four
     if (g.top) {
 #pragma unroll 1
       for (int i0 = tid; i0 < groups; i0 += kScan * NT) {
@@ -142,7 +150,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
 #pragma unroll
         for (int q = 0; q < kScan; ++q) {
           const int i = i0 + q * NT;
-          top[q] = i < groups ? tops[i] : 0.0f, key[q] = i < groups ? keys[i].x : ~0u;
+          top[q] = i < groups ? top_of(i) : 0.0f, key[q] = i < groups ? keys[i].x : ~0u;
         }
 #pragma unroll
         for (int q = 0; q < kScan; ++q) {
@@ -151,13 +159,22 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
         }
       }
       if (4 * groups <= NT) {  // few groups: each bound has a thread
+        all = true;
         const int i = tid >> 2;
         const uint4 k = i < groups ? keys[i] : uint4{~0u, ~0u, ~0u, ~0u};
         const uint32_t key = tid & 2 ? tid & 1 ? k.w : k.z : tid & 1 ? k.y : k.x;
-        best = i < groups ? (float)bound_of(tops[i], key) : -INFINITY, own = i * 64 + (key & 63);
+        best = i < groups ? (float)bound_of(top_of(i), key) : -INFINITY, own = i * 64 + (key & 63);
       }
       if (best > -INFINITY) own = (int)group_class(own >> 6, own & 63, g.side, g.apart, g.parts);
       if (best <= kMasked || own >= g.vocab) best = -INFINITY;
+      if (!all) {
+#pragma unroll
+        for (int k = 1; k < 4; k <<= 1) {
+          const float o = __shfl_xor(best, k);
+          const int c = __shfl_xor(own, k);
+          if (o > best || (o == best && c < own)) best = o, own = c;
+        }
+      }
     }
     // the row's maximum, sum and first moment
     float m = -INFINITY, s = 0.0f, t = 0.0f;
@@ -175,7 +192,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     if (lane == 0) part[wave] = float4{m, s, t, 0.0f};
     // floats in the order of whole numbers
     const uint32_t order = __float_as_uint(best) ^ (__float_as_int(best) >> 31 | 0x80000000u);
-    first[tid] = order;
+    if (all || tid % 4 == 0) first[all ? tid : tid / 4] = order;
     if (tid < 2) counts[tid] = 0;
     __syncthreads();
     if (NW > 1) {
@@ -200,18 +217,19 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
         if (wave == 0) {
           uint32_t v[NW], b = 0;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) v[w] = first[w * 64 + lane];
+          for (int w = 0; w < NW; ++w) v[w] = all || w < NW / 4 ? first[w * 64 + lane] : 0u;
 #pragma unroll 1
           for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
             int above = 0;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) above += __popcll(__ballot(v[w] >= (b | bit)));
+            for (int w = 0; w < NW; ++w)
+              if (all || w < NW / 4) above += __popcll(__ballot(v[w] >= (b | bit)));
             if (above >= g.top) b |= bit;
           }
           if (lane == 0) bound = b;
         }
         __syncthreads();
-        if (best > -INFINITY && order >= bound && own != (int)y) items[atomicAdd(&counts[1], 1)] = own;
+        if ((all || tid % 4 == 0) && best > -INFINITY && order >= bound && own != (int)y) items[atomicAdd(&counts[1], 1)] = own;
       }
       if (tid == 0) items[atomicAdd(&counts[1], 1)] = (int)y;
       __syncthreads();
@@ -288,7 +306,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
 #pragma unroll
           for (int q = 0; q < kScan; ++q) {
             const int i = scanned + q * NT + tid;
-            k[q] = i < groups ? keys[i] : uint4{~0u, ~0u, ~0u, ~0u}, top[q] = i < groups ? tops[i] : 0.0f;
+            k[q] = i < groups ? keys[i] : uint4{~0u, ~0u, ~0u, ~0u}, top[q] = i < groups ? top_of(i) : 0.0f;
           }
 #pragma unroll
           for (int q = 0; q < kScan; ++q) {
@@ -335,7 +353,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
 
 struct Plan {
   int el, dp, side, parts, apart;
-  bool gather, norms;
+  bool gather;
 };
 Plan plan_of(const TokenLogprobs& s, bool tokens) {
   Plan p = {};
@@ -347,7 +365,6 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.
   p.apart = 64;
   while (p.apart > p.parts || (int64_t)p.apart * p.side * p.dp * p.el > INT32_MAX) p.apart /= 2;
-  p.norms = s.top && s.bf16 && p.side == 256;
   p.gather = tokens && 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) >= kGatherFrom;
   return p;
 }
@@ -376,8 +393,8 @@ Space space_of(void* p, const TokenLogprobs& s, const Plan& l) {
   w.w = take(l.el * s.vocab * (int64_t)l.dp);
   w.sums = (float4*)take(16 * s.n * (int64_t)l.parts);
   if (s.top) {
-    if (l.norms) w.a_norm = (float*)take(16 * (int64_t)l.parts), w.b_norm = (float*)take(4 * s.n);
-    w.keys = (uint4*)take(64 * s.n * (int64_t)l.parts), w.tops = (float*)take(16 * s.n * (int64_t)l.parts);
+    w.a_norm = (float*)take(16 * (int64_t)l.parts), w.b_norm = (float*)take(4 * s.n);
+    w.keys = (uint4*)take(64 * s.n * (int64_t)l.parts), w.tops = (float*)take(8 * s.n * (int64_t)l.parts);
   }
   w.bytes = at - (char*)p;
   return w;
@@ -410,10 +427,7 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
   g.sums = ws.sums;
   g.k2 = (float)(s.scale * kLog2e), g.k2_low = (float)(s.scale * kLog2e - g.k2);
   g.keys = ws.keys, g.tops = ws.tops, g.a_norm = ws.a_norm, g.b_norm = ws.b_norm;
-  // roundings on a term's way: eight for each of dp / 16 matrix instructions; in fp32 six instructions with
-  // those for each 16 columns, and the planes that are not multiplied; a hundredth for the norms' own
-  g.error = ((s.bf16 ? 0.5f : 3.0f) * p.dp + 128.0f) * 0x1p-24f * 1.01f;
-  if (p.norms) {
+  if (s.top && s.bf16 && p.side == 256) {
     lp_group_norms<<<(unsigned)(4 * p.parts), 256, 0, st>>>((const uint16_t*)g.a, s.vocab, p.dp, p.side, p.apart, p.parts,
                                                             ws.a_norm);
     AM_LAUNCH_CHECK();
@@ -425,6 +439,10 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
   if (e != ATLASMEM_OK) return e;
   RowArgs a = {};
   a.sums = ws.sums, a.keys = ws.keys, a.tops = ws.tops, a.parts = p.parts, a.side = p.side, a.apart = p.apart;
+  a.a_norm = ws.a_norm, a.b_norm = ws.b_norm;
+  // roundings on a term's way: eight for each of dp / 16 matrix instructions; in fp32 six instructions with
+  // those for each 16 columns, and the planes that are not multiplied; a hundredth for the norms' own
+  a.error = ((s.bf16 ? 0.5f : 3.0f) * p.dp + 128.0f) * 0x1p-24f * 1.01f;
   a.at = p.gather ? ws.at : nullptr;
   a.x = g.b, a.w = g.a, a.dp = p.dp;
   a.n = s.n, a.vocab = s.vocab;

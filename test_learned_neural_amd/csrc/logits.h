@@ -55,13 +55,11 @@ struct GemmArgs {
   int64_t ldo;
   float k2, k2_low;        // SUMS, TOP, KEPT, AGAIN: scale log2 e, and what its rounding left
   float4* sums;            // SUMS, TOP: [nb][parts]: (maximum m of z, sum of e = exp(scale (z - m)), sum of e (z - m), -)
-  uint4* keys;             // TOP: [nb][4 parts], by group_class's groups: the four largest bounds of what z may be in 64
-                           // bits, as differences to
-  float* tops;             // ... [nb][4 parts], times k2, with the class's place in the low bits
+  uint4* keys;             // TOP: [nb][4 parts], by group_class's groups: how far below the maximum their four largest
+                           // logits are, times k2, with the class's place in the low bits
+  float* tops;             // ... [nb][2 parts]: the maxima, of 2 tile + group % 2
+  float *a_norm, *b_norm;  // ... [4 parts]: the largest |a| of a group; [nb]: |b|
   int apart;               // SUMS, TOP: see tile_rows
-  float error;             // TOP: of z, relative to |a| |b|
-  const float* a_norm;     // TOP, tiles of 256: the largest |a| of a group, [4 tiles]
-  const float* b_norm;     // ... and |b|, [nb]
   const float* ref;        // KEPT, AGAIN: [rows of X]
   const int* to;           // AGAIN: [nb], rows of g; ROWS: of out
   const int64_t* ids;      // AGAIN: [rows of X][top], the teacher's classes
@@ -409,7 +407,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     pa += step_a, pb += step_b;
   };
   constexpr int kLoads = A::kLoads + B::kLoads;
-  // TOP: squares of the rows that a lane's operands are of, where the products leave time for them
+  // TOP: squares of the rows that a lane's operands are of, where the products leave time for them (tiles of 256 do
+  // not: 8192 x 2048 x 65536 1.85 -> 2.02 ms, even if only some tiles take them)
   constexpr bool kNorms = EPI == EPI_TOP && (F32 || TA < 256);
   float na[MA], nb[NB];
 #pragma unroll
@@ -659,23 +658,26 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 
   if constexpr (EPI == EPI_SUMS || EPI == EPI_TOP || EPI == EPI_KEPT) {
     float4* red = (float4*)smem;  // [WA][TB]
-    // TOP: the largest |a| of the lane's classes, and |b| of its rows.  Classes of 1e30 are masked, not sums that err.
-    float group_norm = 0.0f;
     if constexpr (kNorms) {
+      if (b0 == 0) {
+        // the largest |a| of the lane's classes.  Classes of 1e30 are masked, not sums that err.
+        float group_norm = 0.0f;
 #pragma unroll
-      for (int i = 0; i < MA; ++i) {
-        const float q = na[i] + __shfl_xor(na[i], 32);
-        group_norm = fmaxf(group_norm, sqrtf(q) < 1.0e30f ? sqrtf(q) : 0.0f);
+        for (int i = 0; i < MA; ++i) {
+          const float q = sqrtf(na[i] + __shfl_xor(na[i], 32));
+          group_norm = fmaxf(group_norm, q < 1.0e30f ? q : 0.0f);
+        }
+        for (int k = 1; k < 32; k <<= 1)
+          if (k != 4) group_norm = fmaxf(group_norm, __shfl_xor(group_norm, k));
+        if (wave < WA && (lane & ~4) == 0) g.a_norm[tile_a * 4 + (lane >> 1) + wave] = group_norm;
       }
-      for (int k = 1; k < 32; k <<= 1)
-        if (k != 4) group_norm = fmaxf(group_norm, __shfl_xor(group_norm, k));
-      group_norm = __shfl(group_norm, 4 * hf);
+      if (tile_a == 0) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) nb[j] = sqrtf(nb[j] + __shfl_xor(nb[j], 32));
-    } else if constexpr (EPI == EPI_TOP) {
-      group_norm = g.a_norm[tile_a * 4 + 2 * hf + wave % WA];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) nb[j] = b0 + wb + 32 * j + col < g.nb ? g.b_norm[b0 + wb + 32 * j + col] : 0.0f;
+        for (int j = 0; j < NB; ++j) {
+          const float q = sqrtf(nb[j] + __shfl_xor(nb[j], 32));
+          if (wave % WA == 0 && hf == 0 && b0 + wb + 32 * j + col < g.nb) g.b_norm[b0 + wb + 32 * j + col] = q;
+        }
+      }
     }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -717,9 +719,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
         }
       if constexpr (EPI == EPI_TOP) {
         if (r < g.nb) {
-          const float top = from + g.error * group_norm * nb[j];
           const int64_t at = r * (4 * (int64_t)g.parts) + tile_a * 4 + 2 * hf + wave % WA;
-          g.tops[at] = fmaf(fabsf(top), 0x1p-21f, top);
+          if (hf == 0) g.tops[r * (2 * (int64_t)g.parts) + tile_a * 2 + wave % WA] = from;
           g.keys[at] = uint4{y1, y2, y3, y4};
         }
       }
