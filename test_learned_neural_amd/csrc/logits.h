@@ -255,9 +255,9 @@ __device__ __forceinline__ uint32_t pack_u16(float a, float b) {
 __device__ __forceinline__ float u16_lo(uint32_t w) { return __uint_as_float((w & 0xFFFFu) << 14); }
 __device__ __forceinline__ float u16_hi(uint32_t w) { return __uint_as_float((w & 0xFFFF0000u) >> 2); }
 
-// A tile's accumulators, rounded to bf16 (U16: to the above), to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
+// A tile's accumulators, rounded to bf16, to rows r0.. (nr of them) and columns c0.. (nc) of a matrix:
 // through LDS, so that a row's columns leave in whole 16-byte pieces side by side.
-template <int TA, int TB, int MA, int NB, int NT, bool U16 = false>
+template <int TA, int TB, int MA, int NB, int NT>
 __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, uint16_t* out,
                          int64_t ld, int64_t c0, int64_t nc, int64_t r0, int64_t nr, const int* to = nullptr) {
   constexpr int CH = TA / 8;  // 16-byte pieces of a row, exchanged by the row's low bits
@@ -271,8 +271,7 @@ __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], in
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const f32x16& x = acc[i][j];
-        const uint2 o = U16 ? uint2{pack_u16(x[4 * q], x[4 * q + 1]), pack_u16(x[4 * q + 2], x[4 * q + 3])}
-                            : uint2{cvt_pk_bf16(x[4 * q], x[4 * q + 1]), cvt_pk_bf16(x[4 * q + 2], x[4 * q + 3])};
+        const uint2 o = {cvt_pk_bf16(x[4 * q], x[4 * q + 1]), cvt_pk_bf16(x[4 * q + 2], x[4 * q + 3])};
         const int c = (wa + 32 * i + 8 * q) >> 3;
         *(uint2*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3) + 4 * hf) = o;
       }
@@ -293,6 +292,31 @@ __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], in
       for (int n = 0; n < 8; ++n)
         if (at + n < nc) p[n] = (uint16_t)(v[n >> 1] >> (16 * (n & 1)));
     }
+  }
+}
+
+// A wave's accumulators as 16 bits without a sign, to its rows and columns of the same: through its own part of LDS,
+// without a wait for other waves.
+template <int MA, int NB>
+__device__ __forceinline__ void put_wave(uint16_t* sm, f32x16 (&acc)[MA][NB], int lane, uint16_t* out, int64_t ld,
+                                         int64_t c0, int64_t r0, int64_t nr) {
+  constexpr int CH = 4 * MA;  // 16-byte pieces of a row, exchanged by the row's low bits
+  const int hf = lane >> 5, col = lane & 31;
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16& x = acc[i][j];
+        *(uint2*)(sm + (32 * j + col) * (8 * CH) + (((4 * i + q) ^ (col & (CH - 1))) << 3) + 4 * hf) =
+            uint2{pack_u16(x[4 * q], x[4 * q + 1]), pack_u16(x[4 * q + 2], x[4 * q + 3])};
+      }
+#pragma unroll 4
+  for (int id = lane; id < 32 * NB * CH; id += 64) {
+    const int r = id / CH, c = id % CH;
+    const u32x4 v = *(const u32x4*)(sm + r * (8 * CH) + ((c ^ (r & (CH - 1))) << 3));
+    if (r0 + r < nr && c0 + 8 * c < ld) *(u32x4*)(out + (r0 + r) * ld + c0 + 8 * c) = v;
   }
 }
 
@@ -578,6 +602,9 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
       for (int n = 0; n < MA + NB; ++n) read(n, 0, sm, 0);
     }
+    // (Left to the compiler, the logits' products are 3 to 4% faster, 8192 x 2048 x 65536 2.02 -> 1.95 ms with what is
+    // kept, those that read transposed 4% slower.)
+    constexpr bool kFixed = AX || BX || !(EPI == EPI_SUMS || EPI == EPI_TOP || EPI == EPI_KEPT);
     // Behind the barrier a buffer takes a's loads, b's in the next step's first depth.  The source order is
     // the schedule: reads and loads are spread over the matrix instructions, since a burst of them from
     // all waves fills the LDS queue and holds up the matrix instructions behind it.
@@ -605,7 +632,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
             for (int r = n * A::kLoads / kM; r < (n + 1) * A::kLoads / kM; ++r) load_a(r, s);
           }
-          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (kFixed) __builtin_amdgcn_sched_barrier(0);
         }
       }
       e = s, s = d;
@@ -657,7 +684,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   }
 
   if constexpr (EPI == EPI_SUMS || EPI == EPI_TOP || EPI == EPI_KEPT) {
-    float4* red = (float4*)smem;  // [WA][TB]
+    // [WA][TB]; behind what put_wave uses
+    float4* red = (float4*)(smem + (EPI == EPI_KEPT && !F32 ? TA * TB * 2 : 0));
     if constexpr (kNorms) {
       if (b0 == 0) {
         // the largest |a| of the lane's classes.  Classes of 1e30 are masked, not sums that err.
@@ -740,6 +768,12 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
         }
       }
     }
+    if constexpr (EPI == EPI_KEPT) {
+      if (g.g) {
+        if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.g, g.ldg, a0, b0, g.nb, 0);
+        else put_wave<MA, NB>(sm + wave * (32 * MA * 32 * NB), acc, lane, (uint16_t*)g.g, g.ldg, a0 + wa, b0 + wb, g.nb);
+      }
+    }
     __syncthreads();
     for (int r = tid; r < TB; r += NT) {
       if (b0 + r >= g.nb) break;
@@ -759,12 +793,6 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       }
       if constexpr (EPI != EPI_KEPT) g.sums[(b0 + r) * g.parts + tile_a] = float4{m, s, t, 0.0f};
       else g.part[(b0 + r) * g.parts + a0 / TA] = float2{m, s};
-    }
-    if constexpr (EPI == EPI_KEPT) {
-      if (g.g) {
-        if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.g, g.ldg, a0, b0, g.nb, 0);
-        else put_rows<TA, TB, MA, NB, NT, true>(sm, acc, wa, wb, tid, (uint16_t*)g.g, g.ldg, a0, g.ldg, b0, g.nb);
-      }
     }
   }
 
@@ -1048,7 +1076,8 @@ constexpr double kLog2e = 1.4426950408889634;
 
 template <int TA, int TB, int WA, int WB, int ST, bool AX, bool BX, int EPI, bool F32>
 atlasmem_status gemm_launch(GemmArgs g, hipStream_t st) {
-  constexpr int lds = F32 ? ST * (TA + TB) * kBK * 4 : std::max(ST * (TA + TB) * kBK * 2, TA * TB * 2);
+  constexpr int lds = F32 ? ST * (TA + TB) * kBK * 4
+                          : std::max(ST * (TA + TB) * kBK * 2, TA * TB * 2 + (EPI == EPI_KEPT ? WA * TB * 16 : 0));
   auto kern = xe_gemm<TA, TB, WA, WB, ST, AX, BX, EPI, F32>;
   if (lds > 65536 &&
       hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
