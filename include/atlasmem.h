@@ -536,14 +536,15 @@ atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, in
  * (atlasmem_distillation):
  *   lse_i = log sum_v exp(z_iv),  logprob_i = z_i,token_i - lse_i,  entropy_i = lse_i - sum_v exp(z_iv - lse_i) z_iv
  *   X: [n, d], W: [vocab, d] of `dtype`, with the limits of atlasmem_cross_entropy
- *   scale: > 0, finite (the reciprocal of a temperature)
+ *   scale: 2^-20 .. 2^20 (the reciprocal of a temperature)
  *   tokens: int64 [n], or NULL (all rows count, no logprob); a row whose token is no class (negative, or >= vocab)
  *         is left out: logprob, entropy and top_logprobs 0, top_ids -1, whatever its X holds
  *   top: alternatives asked for, 0..64, at most vocab
  *   logprob, entropy: fp32 [n], either may be NULL
  *   top_ids: int64 [n, top], top_logprobs: fp32 [n, top] (NULL with top 0): the classes of the largest logits,
  *         largest first, equal ones by their index.  Their order is that of products summed in 64 bits.  A logit
- *         of -1e38 or less is a masked class and no alternative: places that are left hold -1 and -INFINITY
+ *         of -1e38 or less, or 1e32 below the row's largest, is a masked class and no alternative: places that
+ *         are left hold -1 and -INFINITY
  *   workspace: atlasmem_token_logprobs_workspace_bytes(...) bytes, 16-byte aligned
  * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits); sums are fp32.  A
  * row with a NaN or an infinite logit has NaN for its numbers and no alternatives (-1); one whose logits are all
@@ -565,7 +566,7 @@ atlasmem_status atlasmem_token_logprobs(const void* X, const void* W, int32_t dt
  *   ids: int64 [n, top] (1..128), teacher: fp32 [n, top], logits or log probabilities, in any order.  An id that
  *         is no class, or a logit of -INFINITY, is no entry; entries of one class add up.  A row without an
  *         entry is left out: its loss, lse and gradient are zero, whatever its X holds
- *   scale: > 0, finite (the reciprocal of a temperature)
+ *   scale: 2^-20 .. 2^20 (the reciprocal of a temperature)
  *   loss, lse: fp32 [n]
  *   kept: atlasmem_distillation_kept_bytes(...) bytes, 16-byte aligned, what the backward reads (q of every
  *         row and class up to a factor of the row, in `dtype`, less the teacher's), or NULL (loss alone)

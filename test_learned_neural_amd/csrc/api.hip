@@ -448,13 +448,16 @@ atlasmem_status cross_entropy_of(int32_t dtype, int64_t n, int32_t d, int64_t vo
   return ATLASMEM_OK;
 }
 
+// Differences of logits times a scale stay apart from the ends of floats.
+bool scale_of(float scale) { return scale >= 0x1p-20f && scale <= 0x1p20f; }
+
 // Checked sizes of a call for token log probabilities.
 atlasmem_status token_logprobs_of(int32_t dtype, int64_t n, int32_t d, int64_t vocab, int32_t top, float scale,
                                   TokenLogprobs& s) {
   CrossEntropy c;
   const atlasmem_status e = cross_entropy_of(dtype, n, d, vocab, c);
   if (e != ATLASMEM_OK) return e;
-  if (top < 0 || top > vocab || !(scale > 0.0f && scale < INFINITY)) return ATLASMEM_E_INVALID;
+  if (top < 0 || top > vocab || !scale_of(scale)) return ATLASMEM_E_INVALID;
   if (top > 64) return ATLASMEM_E_SHAPE;
   s = {n, vocab, d, top, c.bf16, scale};
   return ATLASMEM_OK;
@@ -466,7 +469,7 @@ atlasmem_status distillation_of(int32_t dtype, int64_t n, int32_t d, int64_t voc
   CrossEntropy c;
   const atlasmem_status e = cross_entropy_of(dtype, n, d, vocab, c);
   if (e != ATLASMEM_OK) return e;
-  if (top < 1 || !(scale > 0.0f && scale < INFINITY)) return ATLASMEM_E_INVALID;
+  if (top < 1 || !scale_of(scale)) return ATLASMEM_E_INVALID;
   // byte offsets in 256 rows of what is kept stay below 2^31, four columns a lane below 2^32 lanes
   if (top > 128 || vocab > (1 << 21)) return ATLASMEM_E_SHAPE;
   s = {n, vocab, d, top, c.bf16, scale};

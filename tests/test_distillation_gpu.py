@@ -106,6 +106,7 @@ CASES = [
     ("many_short_rows_far_references", dict(dtype=am.BF16, n=4100, d=64, vocab=200, top=3, spread=30.0)),
     ("as_many_rows_as_few", dict(dtype=am.BF16, n=64, d=520, vocab=3001, top=9)),
     ("as_many_rows_as_few_f32", dict(dtype=am.F32, n=64, d=260, vocab=3001, top=9)),
+    ("hottest", dict(dtype=am.BF16, n=60, d=64, vocab=700, scale=2.0 ** -20)),
     ("unweighted", dict(dtype=am.F32, n=50, d=32, vocab=99, weights=False)),
     ("far_references", dict(dtype=am.BF16, n=100, d=64, vocab=500, spread=30.0)),
     ("far_references_f32", dict(dtype=am.F32, n=100, d=64, vocab=500, spread=30.0, scale=1.5)),

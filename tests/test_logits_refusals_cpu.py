@@ -27,7 +27,8 @@ NAN, INF = float("nan"), float("inf")
 @pytest.mark.parametrize("kw,status", [
     (dict(n=-1), am.E_INVALID), (dict(d=0), am.E_INVALID), (dict(vocab=0), am.E_INVALID), (dict(dtype=2), am.E_INVALID),
     (dict(scale=0.0), am.E_INVALID), (dict(scale=-1.0), am.E_INVALID), (dict(scale=NAN), am.E_INVALID),
-    (dict(scale=INF), am.E_INVALID), (dict(top=-1), am.E_INVALID), (dict(top=41), am.E_INVALID),
+    (dict(scale=INF), am.E_INVALID), (dict(scale=2.0 ** -21), am.E_INVALID), (dict(scale=2.0 ** 21), am.E_INVALID),
+    (dict(top=-1), am.E_INVALID), (dict(top=41), am.E_INVALID),
     (dict(vocab=100, top=65), am.E_SHAPE), (dict(d=16385), am.E_SHAPE), (dict(n=(1 << 24) + 1), am.E_SHAPE),
     (dict(n=1 << 20, vocab=1 << 19), am.E_SHAPE),
     (dict(X=None), am.E_INVALID), (dict(W=None), am.E_INVALID), (dict(workspace=None), am.E_INVALID),
@@ -59,7 +60,7 @@ def distill(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(n=-1), am.E_INVALID), (dict(d=0), am.E_INVALID), (dict(vocab=0), am.E_INVALID), (dict(dtype=7), am.E_INVALID),
     (dict(scale=0.0), am.E_INVALID), (dict(scale=NAN), am.E_INVALID), (dict(scale=INF), am.E_INVALID),
-    (dict(top=0), am.E_INVALID), (dict(top=129), am.E_SHAPE), (dict(vocab=(1 << 21) + 1), am.E_SHAPE),
+    (dict(scale=2.0 ** -21), am.E_INVALID), (dict(scale=2.0 ** 21), am.E_INVALID), (dict(top=0), am.E_INVALID), (dict(top=129), am.E_SHAPE), (dict(vocab=(1 << 21) + 1), am.E_SHAPE),
     (dict(d=16385), am.E_SHAPE),
     (dict(X=None), am.E_INVALID), (dict(ids=None), am.E_INVALID), (dict(teacher=None), am.E_INVALID),
     (dict(loss=None), am.E_INVALID), (dict(lse=None), am.E_INVALID), (dict(workspace=None), am.E_INVALID),
@@ -120,11 +121,12 @@ def test_the_binding_raises():
 
 @pytest.mark.parametrize("n,d,vocab", [(1, 1024, 50257), (8192, 2048, 65536), (65536, 1024, 131072)])
 def test_workspaces_hold_no_logits(n, d, vocab):
-    """Copies of the rows, and for each row and 64 classes (fewer of few rows) a pair of numbers."""
+    """Copies of the rows, and for each row and 64 classes (fewer of few rows) their four largest logits, 16 bytes, and
+    4 and 2 for the sums and maxima of four such groups."""
     rows = 2 * (n + vocab) * d
     least = 16 if n * vocab < 1 << 22 else 64
     assert am.token_logprobs_workspace_bytes(am.BF16, n, d, vocab, 20) <= \
-        rows + n * (vocab // least + 4) * 12 + 4 * vocab + 16 * n + (1 << 20)
+        rows + n * (vocab // least + 4) * 22 + vocab + 20 * n + (1 << 20)
     assert am.distillation_workspace_bytes(am.BF16, n, d, vocab, 32) <= \
         rows + n * (8 * (vocab // (4 * least) + 1) + 4 * 32 + 24) + (1 << 20)
     assert am.distillation_kept_bytes(am.BF16, n, vocab, 32) <= 2 * n * (vocab + 64) + 16 * n + (1 << 20)

@@ -95,6 +95,8 @@ CASES = [
     ("factors_rounded_up_f32", dict(dtype=am.F32, n=90, d=48, vocab=1001, top=20, scale=1.25)),
     ("factors_rounded_down_f32", dict(dtype=am.F32, n=90, d=48, vocab=1001, top=20, scale=0.7)),
     ("wide_rows_f32", dict(dtype=am.F32, n=47, d=3616, vocab=1301, top=3)),
+    ("hottest", dict(dtype=am.BF16, n=60, d=64, vocab=700, top=7, scale=2.0 ** -20)),
+    ("coldest", dict(dtype=am.F32, n=60, d=64, vocab=700, top=7, scale=2.0 ** 20)),
     ("few_groups_many_alternatives", dict(dtype=am.BF16, n=17, d=80, vocab=642, top=64)),
     ("as_many_rows_as_few", dict(dtype=am.BF16, n=64, d=520, vocab=9001, top=20)),
     ("as_many_rows_as_few_f32", dict(dtype=am.F32, n=64, d=260, vocab=9001, top=20)),
