@@ -18,7 +18,7 @@ namespace am {
 
 namespace {
 
-// |row| of a row of a bf16 matrix.  A wave's.
+// |row| of a row of a bf16 matrix, without masks.  A wave's.
 __device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
   float s = 0.0f;
 #pragma unroll 4
@@ -27,7 +27,7 @@ __device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
-      s = fmaf(lo, lo, fmaf(hi, hi, s));
+      s = fmaf(lo, fabsf(lo) < kMasking ? lo : 0.0f, fmaf(hi, fabsf(hi) < kMasking ? hi : 0.0f, s));
     }
   }
   for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
@@ -48,8 +48,7 @@ __global__ __launch_bounds__(256) void lp_group_norms(const uint16_t* w, int64_t
   for (int code = wave; code < side / 4; code += 4) {
     const int64_t c = group_class(blockIdx.x, code, side, apart, tiles);
     if (c >= vocab) continue;
-    const float v = norm_of(w + c * dp, dp, lane);
-    m = fmaxf(m, v < 1.0e30f ? v : 0.0f);
+    m = fmaxf(m, norm_of(w + c * dp, dp, lane));
   }
   if (lane == 0) best[wave] = m;
   __syncthreads();
@@ -133,7 +132,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     const int groups = 4 * g.parts;
     const uint4* keys = g.keys + (int64_t)place * groups;
     const float* tops = g.tops + (int64_t)place * (groups / 2);
-    const float error = g.top ? g.error * g.b_norm[place] : 0.0f;
+    const float error = g.top ? fminf(g.error * g.b_norm[place], 1.0e30f) : 0.0f;
     // what the maximum of group i may be in 64 bits
     auto top_of = [&](int i) {
       const float t = fmaf(error, g.a_norm[i], tops[(i >> 2) * 2 + (i & 1)]);

@@ -13,6 +13,7 @@ namespace am {
 
 namespace {
 
+constexpr float kMasking = 1.0e18f;  // of a and b in TOP: larger magnitudes are masks
 constexpr float kDown = 40.0f;  // KEPT: 2^-kDown on what is kept of bf16 calls, whose 16 bits end at 2
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
 enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN, EPI_ROWS, EPI_PART };
@@ -688,12 +689,23 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     float4* red = (float4*)(smem + (EPI == EPI_KEPT && !F32 ? TA * TB * 2 : 0));
     if constexpr (kNorms) {
       if (b0 == 0) {
-        // the largest |a| of the lane's classes.  Classes of 1e30 are masked, not sums that err.
+        // The largest |a| of the lane's classes, without what masks a class where a row asks for it (kMasking): the sums of
+        // those rows do not err, and in the others it is multiplied by zero.
         float group_norm = 0.0f;
 #pragma unroll
         for (int i = 0; i < MA; ++i) {
-          const float q = sqrtf(na[i] + __shfl_xor(na[i], 32));
-          group_norm = fmaxf(group_norm, q < 1.0e30f ? q : 0.0f);
+          float q = na[i] + __shfl_xor(na[i], 32);
+          if (!(q < kMasking * kMasking)) {
+            const E* w = (const E*)g.a + first_a * g.lda + spread_row<TA>(wa + 32 * i + col) * lda;
+            q = 0.0f;
+            for (int64_t k = 8 * hf; k < g.K; k += 16)
+              for (int e = 0; e < 8 && k + e < g.K; ++e) {
+                const float v = load_in(w, k + e, !F32);
+                q += fabsf(v) < kMasking ? v * v : 0.0f;
+              }
+            q += __shfl_xor(q, 32);
+          }
+          group_norm = fmaxf(group_norm, sqrtf(q));
         }
         for (int k = 1; k < 32; k <<= 1)
           if (k != 4) group_norm = fmaxf(group_norm, __shfl_xor(group_norm, k));

@@ -167,6 +167,21 @@ def test_masked_classes(dtype, mask, n, vocab, left):
 
 
 @pytest.mark.parametrize("dtype", [am.BF16, am.F32])
+@pytest.mark.parametrize("n,vocab", [(6, 900), (90, 2000), (1200, 9000)])
+def test_classes_masked_in_some_rows(dtype, n, vocab):
+    """A column of X says whether a row's classes are masked: the others' alternatives are all classes'."""
+    import torch
+    c = Case(dtype, n, 32, vocab, top=12, masked=0.0)
+    mask = float(torch.finfo(c.X.dtype).min)
+    hidden = np.random.default_rng(1).random(vocab) < 0.8
+    c.X[:, 7] = torch.from_numpy((np.arange(n) % 2).astype(np.float32)).to(c.X.dtype)
+    c.W[:, 7] = 0.0
+    c.W[hidden, 7] = mask
+    c.tokens = np.where(~hidden)[0][np.arange(n) % (~hidden).sum()]
+    check(c, plain32=True)
+
+
+@pytest.mark.parametrize("dtype", [am.BF16, am.F32])
 def test_a_row_without_a_class(dtype):
     import torch
     c = Case(dtype, 70, 16, 500, masked=0.0)
