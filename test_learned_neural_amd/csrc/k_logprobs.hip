@@ -214,17 +214,22 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
       // first the best `top` of the threads' classes (by 20 bits, which a wave finds one by one), and the token
       if (g.top) {
         if (wave == 0) {
-          uint32_t v[NW], b = 0;
+          uint32_t b = 0;
+          auto find = [&](auto waves) {
+            constexpr int N = decltype(waves)::value;
+            uint32_t v[N];
 #pragma unroll
-          for (int w = 0; w < NW; ++w) v[w] = all || w < NW / 4 ? first[w * 64 + lane] : 0u;
+            for (int w = 0; w < N; ++w) v[w] = first[w * 64 + lane];
 #pragma unroll 1
-          for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
-            int above = 0;
+            for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
+              int above = 0;
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-              if (all || w < NW / 4) above += __popcll(__ballot(v[w] >= (b | bit)));
-            if (above >= g.top) b |= bit;
-          }
+              for (int w = 0; w < N; ++w) above += __popcll(__ballot(v[w] >= (b | bit)));
+              if (above >= g.top) b |= bit;
+            }
+          };
+          if (all) find(std::integral_constant<int, NW>{});
+          else find(std::integral_constant<int, (NW + 3) / 4>{});
           if (lane == 0) bound = b;
         }
         __syncthreads();
@@ -359,6 +364,8 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   p.el = s.bf16 ? 2 : 4;
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
   p.side = side_for(s.vocab, s.n, s.bf16);
+  // few groups for the alternatives asked for: smaller ones (17 x 80 x 642 with 64: 108 -> 50 us; 1 x 184 x 4771: 34 -> 52)
+  if (s.n <= kFew && 2 * s.vocab < (int64_t)s.top * p.side) p.side = 64;
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   // Rows of a tile 64 apart: all tiles' (256 x 256, 2048 columns) takes 10% longer, their pages no longer at hand,
   // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.
@@ -433,8 +440,10 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
     lp_row_norms<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>((const uint16_t*)g.b, s.n, count, p.dp, ws.b_norm);
     AM_LAUNCH_CHECK();
   }
-  if (s.n <= kFew) e = s.top ? gemm_few<false, EPI_TOP>(g, s.bf16, st) : gemm_few<false, EPI_SUMS>(g, s.bf16, st);
-  else e = s.top ? gemm<false, false, EPI_TOP>(g, s.bf16, p.side, st) : gemm<false, false, EPI_SUMS>(g, s.bf16, p.side, st);
+  if (s.n <= kFew && (p.side == 128 || !s.bf16))
+    e = s.top ? gemm_few<false, EPI_TOP>(g, s.bf16, st) : gemm_few<false, EPI_SUMS>(g, s.bf16, st);
+  else
+    e = s.top ? gemm<false, false, EPI_TOP>(g, s.bf16, p.side, st) : gemm<false, false, EPI_SUMS>(g, s.bf16, p.side, st);
   if (e != ATLASMEM_OK) return e;
   RowArgs a = {};
   a.sums = ws.sums, a.keys = ws.keys, a.tops = ws.tops, a.parts = p.parts, a.side = p.side, a.apart = p.apart;
@@ -455,7 +464,7 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
     else lp_rows<NT, false><<<rows, NT, 0, st>>>(a);
   };
   if (s.n <= 256) launch(std::integral_constant<int, 1024>{});
-  else if (s.n > 1024 && s.top <= 24) launch(std::integral_constant<int, 64>{});
+  else if (s.n > 1024 && s.top <= 24 && p.parts >= 16) launch(std::integral_constant<int, 64>{});
   else launch(std::integral_constant<int, 256>{});
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;
