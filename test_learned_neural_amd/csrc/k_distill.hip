@@ -21,11 +21,12 @@ constexpr float kFar = 36.0f;
 constexpr int kMost = 128;  // entries of a row
 constexpr int64_t kManyRows = 4096, kShortRow = 32768;
 
-// log p of each given class (-inf: none), and of each row a label (0, or -1 for a row that has no class) and the
+// log p of each given class (-inf: none) and p, and of each row a label (0, or -1 for a row that has no class) and the
 // logit of its first class.  With `index`, rows are taken as they come, those left out among them.  A wave a row.
 __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const float* teacher, int64_t n, int top,
                                                   int64_t vocab, float scale, const void* X, const void* W, int bf16,
-                                                  int vec, int d, float* logp, int64_t* label, float* ref,
+                                                  int vec, int d, float* logp, float* prob, int64_t* label,
+                                                  float* ref,
                                                   int* again_count, int* index, int* at, int* count) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
@@ -46,14 +47,18 @@ __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const floa
     if (on[h]) m = fmaxf(m, t[h]), nan |= t[h] != t[h];
   }
   for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
-  float s = 0.0f;
+  float e[2], s = 0.0f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) s += on[h] ? expf(t[h] - m) : 0.0f;
+  for (int h = 0; h < 2; ++h) s += e[h] = on[h] ? expf(t[h] - m) : 0.0f;
   for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
   const float ls = logf(s);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (lane + 64 * h < top) logp[r * top + lane + 64 * h] = on[h] ? t[h] - m - ls : -INFINITY;
+    if (lane + 64 * h < top) {
+      // p not from log p, whose rounding would be one factor of the row's
+      logp[r * top + lane + 64 * h] = on[h] ? t[h] - m - ls : -INFINITY;
+      prob[r * top + lane + 64 * h] = on[h] ? e[h] / s : 0.0f;
+    }
   const uint64_t any = __ballot(on[0] || on[1]);
   if (lane == 0) label[r] = any ? 0 : -1;
   if (index && lane == 0) index[r] = (int)r, at[r] = any ? (int)r : -1;
@@ -89,7 +94,7 @@ struct JoinArgs {
   int dp;
   int64_t n;
   const int64_t *label, *ids;
-  const float* logp;
+  const float *logp, *prob;
   int top;
   float scale, k2, k2_low;
   float *loss, *lse;
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(NT) void ds_rows(JoinArgs a) {
     __syncthreads();
     for (int j = tid; j < a.top; j += NT) {
       const float l = a.logp[r * a.top + j];
-      id[j] = (int)a.ids[r * a.top + j], lp[j] = l, p[j] = l == -INFINITY ? 0.0f : expf(l);
+      id[j] = (int)a.ids[r * a.top + j], lp[j] = l, p[j] = a.prob[r * a.top + j];
       if (!(l == -INFINITY)) list[atomicAdd(&entries, 1)] = j;
     }
     m = part[0].x, s = part[0].y;
@@ -406,7 +411,7 @@ Kept kept_of(void* p, const Distillation& s, const Plan& l) {
 struct Space {
   char *x, *w, *x_again;
   int64_t* label;
-  float *logp, *ref, *factor, *weight, *acc;
+  float *logp, *prob, *ref, *factor, *weight, *acc;
   float2* part;
   int *again, *to, *again_count;
   int *index, *at, *count, *equal;
@@ -426,7 +431,7 @@ Space space_of(void* p, const Distillation& s, const Plan& l, bool backward) {
   w.w = take(l.el * s.vocab * (int64_t)l.dp);
   char* both = at;
   w.label = (int64_t*)take(8 * s.n);
-  w.logp = (float*)take(4 * s.n * (int64_t)s.top);
+  w.logp = (float*)take(4 * s.n * (int64_t)s.top), w.prob = (float*)take(4 * s.n * (int64_t)s.top);
   w.ref = (float*)take(4 * s.n);
   w.part = (float2*)take(8 * s.n * (int64_t)l.parts);
   if (backward) {
@@ -479,7 +484,7 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   }
   const bool vec = direct(X, s.d, s.bf16) && direct(W, s.d, s.bf16), as_they_come = train && !p.gather;
   ds_teacher<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(
-      ids, teacher, s.n, s.top, s.vocab, s.scale, X, W, s.bf16, vec, s.d, ws.logp, ws.label, train ? ws.ref : nullptr,
+      ids, teacher, s.n, s.top, s.vocab, s.scale, X, W, s.bf16, vec, s.d, ws.logp, ws.prob, ws.label, train ? ws.ref : nullptr,
       train ? ws.again_count : nullptr, as_they_come ? ws.index : nullptr, ws.at, as_they_come ? ws.count : nullptr);
   AM_LAUNCH_CHECK();
   atlasmem_status e = ATLASMEM_OK;
@@ -504,7 +509,7 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   JoinArgs a = {};
   a.part = ws.part, a.parts = p.parts, a.at = p.gather ? ws.at : nullptr;
   a.x = g.b, a.w = g.a, a.dp = p.dp, a.n = s.n;
-  a.label = ws.label, a.ids = ids, a.logp = ws.logp, a.top = s.top;
+  a.label = ws.label, a.ids = ids, a.logp = ws.logp, a.prob = ws.prob, a.top = s.top;
   a.scale = s.scale, a.k2 = g.k2, a.k2_low = g.k2_low;
   a.loss = loss, a.lse = lse;
   if (train) {
@@ -526,7 +531,7 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   if (!train) return ATLASMEM_OK;
   g.b = ws.x_again;
   g.count = ws.again_count, g.index = ws.again, g.to = ws.to;
-  g.ids = ids, g.logp = ws.logp, g.factor = ws.factor, g.top = s.top;
+  g.ids = ids, g.prob = ws.prob, g.factor = ws.factor, g.top = s.top;
   return s.n <= kFew ? gemm_few<false, EPI_AGAIN>(g, s.bf16, st)
                      : gemm<false, false, EPI_AGAIN>(g, s.bf16, p.side, st);
 }

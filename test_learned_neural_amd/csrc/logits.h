@@ -64,7 +64,7 @@ struct GemmArgs {
   const float* ref;        // KEPT, AGAIN: [rows of X]
   const int* to;           // AGAIN: [nb], rows of g; ROWS: of out
   const int64_t* ids;      // AGAIN: [rows of X][top], the teacher's classes
-  const float* logp;       // ... and their log probabilities (-inf: none)
+  const float* prob;       // ... and their probabilities (of no class: zero)
   const float* factor;     // AGAIN: [nb], q / exp(scale (z - ref))
   int top;
   const float* row_weight; // ROWS: [rows of X]
@@ -823,8 +823,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
           acc[i][j][n] = 32 * i + 8 * (n >> 2) + (n & 3) < end ? c * exp2_of(acc[i][j][n], ref, g.k2, g.k2_low) : 0.0f;
       for (int k = 0; k < g.top; ++k) {
         const int64_t at = g.ids[row * g.top + k] - first;
-        const float l = g.logp[row * g.top + k];
-        const float p = l == -INFINITY ? 0.0f : __expf(l);
+        const float p = g.prob[row * g.top + k];
 #pragma unroll
         for (int i = 0; i < MA; ++i)
 #pragma unroll

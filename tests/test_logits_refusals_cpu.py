@@ -127,6 +127,7 @@ def test_workspaces_hold_no_logits(n, d, vocab):
     least = 16 if n * vocab < 1 << 22 else 64
     assert am.token_logprobs_workspace_bytes(am.BF16, n, d, vocab, 20) <= \
         rows + n * (vocab // least + 4) * 22 + vocab + 20 * n + (1 << 20)
+    # of an entry its log probability and its probability, 4 bytes each
     assert am.distillation_workspace_bytes(am.BF16, n, d, vocab, 32) <= \
-        rows + n * (8 * (vocab // (4 * least) + 1) + 4 * 32 + 24) + (1 << 20)
+        rows + n * (8 * (vocab // (4 * least) + 1) + 8 * 32 + 24) + (1 << 20)
     assert am.distillation_kept_bytes(am.BF16, n, vocab, 32) <= 2 * n * (vocab + 64) + 16 * n + (1 << 20)
