@@ -19,15 +19,13 @@ namespace {
 // how far (times log 2) ref may be from lse: 2^(kFar - kDown) has to stay below 2
 constexpr float kFar = 36.0f;
 constexpr int kMost = 128;  // entries of a row
-constexpr int64_t kManyRows = 4096, kShortRow = 32768;
 
 // log p of each given class (-inf: none) and p, and of each row a label (0, or -1 for a row that has no class) and the
 // logit of its first class.  With `index`, rows are taken as they come, those left out among them.  A wave a row.
 __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const float* teacher, int64_t n, int top,
                                                   int64_t vocab, float scale, const void* X, const void* W, int bf16,
                                                   int vec, int d, float* logp, float* prob, int64_t* label,
-                                                  float* ref,
-                                                  int* again_count, int* index, int* at, int* count) {
+                                                  float* ref, int* again_count, int* index, int* at, int* count) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (again_count && r == 0 && lane == 0) *again_count = 0;
@@ -37,14 +35,13 @@ __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const floa
   int64_t id[2];
   bool on[2];
   float m = -INFINITY;
-  bool nan = false;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int j = lane + 64 * h;
     id[h] = j < top ? ids[r * top + j] : -1;
     t[h] = j < top ? teacher[r * top + j] * scale : -INFINITY;
     on[h] = id[h] >= 0 && id[h] < vocab && !(t[h] == -INFINITY);
-    if (on[h]) m = fmaxf(m, t[h]), nan |= t[h] != t[h];
+    if (on[h]) m = fmaxf(m, t[h]);
   }
   for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
   float e[2], s = 0.0f;
@@ -107,7 +104,12 @@ struct JoinArgs {
   void* x_again;
 };
 
-// loss, lse of a row, and of a training step its G.  A workgroup of NT threads a row: a wave where many rows are short.
+// loss, lse of a row, and of a training step its G, in place.  It moves what is kept twice, which bounds it (8192 x 2048 x
+// 65536: 2.15 GB in 455 us, 4.7 TB/s); a product's epilogue cannot write G, since a row's lse is known behind its last
+// tile.  A workgroup of 256 threads a row, or where many rows are short (bytes that it reads and writes) of one wave,
+// whose steps wait for no other (12224 x 33 x 1135 training 153 -> 104 us, 2048 x 256 x 1024 63 -> 60; long rows
+// take longer, 8192 x 2048 x 65536 6.05 -> 6.15 ms, and few, 1024 x 256 x 1024 47 -> 49 us).
+constexpr int64_t kManyRows = 2048, kShortRow = 32768;
 template <int NT, bool BF16, bool TRAIN>
 __global__ __launch_bounds__(NT) void ds_rows(JoinArgs a) {
   constexpr int NW = NT / 64;
@@ -158,26 +160,12 @@ __global__ __launch_bounds__(NT) void ds_rows(JoinArgs a) {
     __syncthreads();
     // logits of the given classes: short rows by some lanes each, others by a wave, two at a time
     const int bytes = a.dp * (BF16 ? 2 : 4);
-    if (bytes <= 512) {
-      const int lanes = bytes <= 64 ? 4 : bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32, sub = tid & (lanes - 1);
+    if (bytes <= kShort) {
+      const int lanes = short_lanes(bytes);
       for (int i0 = 0; i0 < entries; i0 += NT / lanes) {
         const int i = i0 + tid / lanes, j = list[min(i, entries - 1)];
-        double v = 0.0;
-        if (sub * 16 < bytes) {
-          const u32x4 x = *(const u32x4*)((const char*)a.x + (int64_t)place * bytes + sub * 16);
-          const u32x4 w = *(const u32x4*)((const char*)a.w + (int64_t)id[j] * bytes + sub * 16);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (BF16) {
-              v += (double)(__uint_as_float(x[q] << 16) * __uint_as_float(w[q] << 16));
-              v += (double)(__uint_as_float(x[q] & 0xFFFF0000u) * __uint_as_float(w[q] & 0xFFFF0000u));
-            } else {
-              v = fma((double)__uint_as_float(x[q]), (double)__uint_as_float(w[q]), v);
-            }
-          }
-        }
-        for (int k = lanes / 2; k; k >>= 1) v += __shfl_xor(v, k);
-        if (sub == 0 && i < entries) z[j] = v;
+        const double v = short_dot<BF16>(a.x, a.w, place, id[j], bytes, lanes, lane);
+        if ((lane & (lanes - 1)) == 0 && i < entries) z[j] = v;
       }
     } else {
       for (int i = 2 * wave; i < entries; i += 2 * NW) {
@@ -281,7 +269,9 @@ __global__ __launch_bounds__(1024) void ds_scale(const float* coef, const float*
   if (threadIdx.x == 0) *scale = s, *equal = e;
 }
 
-constexpr int64_t kFewRows = 2048;  // each workgroup finds the weights by itself: a launch less
+// Up to so many rows each workgroup finds the weights by itself: a launch less (33 x 256 x 1000 34.7 -> 32.9 us; 1024 x
+// 256 x 1024: 43.7 -> 45.2).
+constexpr int64_t kFewRows = 512;
 
 // The rows of X that have a place, times their weights over `scale` (where those are one value, as they are), zeros for
 // rows that are left out; and zeros for the latter's dX, if it is given.  Four columns a thread.
@@ -378,9 +368,11 @@ Plan plan_of(const Distillation& s, bool train) {
   if (tiles * p.splits <= 128) p.side_x = 64;
   p.side_w = side_of(p.dp, s.vocab, s.bf16);
   tiles = tiles_of(p.dp, s.vocab, p.side_w);
-  // dW's contraction is cut where its tiles leave more than half of the chip idle
+  // dW's contraction is cut where its tiles leave more than half of the chip idle (12224 x 33 x 1135 153 -> 104 us, 4096 x
+  // 256 x 1024 79 -> 74); more tiles would only add the pieces' sums
   p.splits_w = (int)std::max<int64_t>(1, std::min<int64_t>(tiles <= 128 ? 512 / tiles : 1, s.n / 512));
-  // a training step has three products to leave rows out of
+  // a training step has three products to leave rows out of (2048 x 1024 x 32768: with a tenth of the rows left out
+  // 495 -> 486 us, with half 457 -> 320)
   p.gather = 2.0 * s.n * s.d * s.vocab * (s.bf16 ? 1 : 6) * (train ? 4 : 1) >= kGatherFrom;
   return p;
 }
@@ -484,8 +476,9 @@ atlasmem_status distillation(const Distillation& s, const void* X, const void* W
   }
   const bool vec = direct(X, s.d, s.bf16) && direct(W, s.d, s.bf16), as_they_come = train && !p.gather;
   ds_teacher<<<(unsigned)((s.n + 3) / 4), 256, 0, st>>>(
-      ids, teacher, s.n, s.top, s.vocab, s.scale, X, W, s.bf16, vec, s.d, ws.logp, ws.prob, ws.label, train ? ws.ref : nullptr,
-      train ? ws.again_count : nullptr, as_they_come ? ws.index : nullptr, ws.at, as_they_come ? ws.count : nullptr);
+      ids, teacher, s.n, s.top, s.vocab, s.scale, X, W, s.bf16, vec, s.d, ws.logp, ws.prob, ws.label,
+      train ? ws.ref : nullptr, train ? ws.again_count : nullptr, as_they_come ? ws.index : nullptr, ws.at,
+      as_they_come ? ws.count : nullptr);
   AM_LAUNCH_CHECK();
   atlasmem_status e = ATLASMEM_OK;
   if (p.gather) e = rows_that_count(s.n, 1, ws.label, nullptr, ws.index, ws.at, ws.count, ws.scale, ws.equal, st);

@@ -76,7 +76,6 @@ struct RowArgs {
 
 constexpr int kTopMost = 64;         // alternatives
 constexpr float kMasked = -1.0e38f;  // logits from here down are no alternatives
-constexpr int kFlush = 1024;         // pending items
 
 // (z, class) before (y, other): larger, or equal and of lower index
 __device__ __forceinline__ bool ahead(double z, int c, double y, int o) { return z > y || (z == y && c < o); }
@@ -91,18 +90,31 @@ __device__ __forceinline__ void join(float& m, float& s, float& t, float om, flo
   m = to;
 }
 
-// A workgroup of NT threads a row: of 1024 for few rows, which computes many classes at once; of one wave where
-// rows fill the chip, since joins, bounds and selections cost instructions in every wave; of 256 where a wave's
-// lanes are few places for the alternatives asked for, and many classes would pass their bar.  Loops are kept
-// rolled: few rows wait for their instructions.
+// The row's numbers and alternatives.  What it reads is small (16 bytes a group, 40 MB at 8192 x 2048 x 65536, and some
+// rows of W out of L2); its waits are for those reads, one behind the other: bounds, classes, selection, bounds.  So a
+// workgroup a row, and the rows that fit on the chip hide each other's waits (8192 x 2048 x 65536: 280 us of 2.2 ms).
+// Its threads NT:
+//   1024 for up to 256 rows, whose time is one row's and where many classes are computed at once (1 x 1024 x 50257
+//     36.8 us, with 256 threads 39.6; 512 rows 129 against 113), unless the rows are short and a wave takes several
+//     classes at a time (17 x 80 x 642: 50, with 256 46);
+//   64 from 1024 rows and up to 32 alternatives, since joins, bounds and selections cost instructions in every wave
+//     (8192 x 2048 x 65536 2.33 -> 2.27 ms, 8192 x 256 x 500 161 -> 43 us); with more, a wave's lanes are few places
+//     for a first choice, and many classes pass its bar (8192 x 256 x 2048, 30 of them: 288 -> 190 us; 4096 x 512 x
+//     2048, 40: 205 -> 223; 8192 x 256 x 65536, 64: 1.14 -> 4.25 ms);
+//   256 else.
+// First choices are of all groups' four bounds where those are few, else of the threads' largest (12224 x 33 x 1135, 64
+// alternatives: 2.0 ms -> 0.76; in short rows several classes a wave 0.48).  Loops are kept rolled: few rows wait for
+// their instructions.
 template <int NT, bool BF16>
 __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
   constexpr int NW = NT / 64;
   constexpr int kTake = 64 / NW;  // classes a wave computes between two selections
   constexpr int kList = kTopMost + 64;
   constexpr int kScan = NT < 1024 ? 4 : 2;  // groups a thread looks at together
+  constexpr int kFirst = NT == 64 ? 256 : 1024;  // places for a first choice
+  constexpr int kFlush = NT == 64 ? 256 : 1024;  // pending items
   __shared__ float4 part[NW];
-  __shared__ uint32_t first[NT];
+  __shared__ uint32_t first[kFirst];
   __shared__ uint32_t bound;
   __shared__ double lz[2][kList];
   __shared__ int lc[2][kList];
@@ -138,10 +150,19 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
       const float t = fmaf(error, g.a_norm[i], tops[(i >> 2) * 2 + (i & 1)]);
       return fmaf(fabsf(t), 0x1p-21f, t);
     };
+    // bound i of all groups' four, and its class
+    auto bound_at = [&](int i, int& c) {
+      const uint32_t key = ((const uint32_t*)keys)[i];
+      c = (int)group_class(i >> 2, key & 63, g.side, g.apart, g.parts);
+      const float b = (float)bound_of(top_of(i >> 2), key);
+      return b > kMasked && c < g.vocab ? b : -INFINITY;
+    };
+    // floats in the order of whole numbers
+    auto order_of = [](float b) { return __float_as_uint(b) ^ (__float_as_int(b) >> 31 | 0x80000000u); };
+    const bool few = 4 * groups <= kFirst;  // each bound may be a first choice
     float best = -INFINITY;
     int own = 0x7fffffff;
-    bool all = NT <= 256;  // threads whose class may be a first choice, or one of four
-    if (g.top) {
+    if (g.top && !few) {
 #pragma unroll 1
       for (int i0 = tid; i0 < groups; i0 += kScan * NT) {
         float top[kScan];
@@ -157,16 +178,9 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
           if (b > best) best = b, own = (i0 + q * NT) * 64 + (key[q] & 63);
         }
       }
-      if (4 * groups <= NT) {  // few groups: each bound has a thread
-        all = true;
-        const int i = tid >> 2;
-        const uint4 k = i < groups ? keys[i] : uint4{~0u, ~0u, ~0u, ~0u};
-        const uint32_t key = tid & 2 ? tid & 1 ? k.w : k.z : tid & 1 ? k.y : k.x;
-        best = i < groups ? (float)bound_of(top_of(i), key) : -INFINITY, own = i * 64 + (key & 63);
-      }
       if (best > -INFINITY) own = (int)group_class(own >> 6, own & 63, g.side, g.apart, g.parts);
       if (best <= kMasked || own >= g.vocab) best = -INFINITY;
-      if (!all) {
+      if (NT == 1024) {  // one of four threads'
 #pragma unroll
         for (int k = 1; k < 4; k <<= 1) {
           const float o = __shfl_xor(best, k);
@@ -189,9 +203,16 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     }
     __syncthreads();  // the last row's shared values have been read
     if (lane == 0) part[wave] = float4{m, s, t, 0.0f};
-    // floats in the order of whole numbers
-    const uint32_t order = __float_as_uint(best) ^ (__float_as_int(best) >> 31 | 0x80000000u);
-    if (all || tid % 4 == 0) first[all ? tid : tid / 4] = order;
+    const uint32_t order = order_of(best);
+    constexpr int kChoices = NT == 1024 ? 256 : NT;
+    if (!few && (NT < 1024 || tid % 4 == 0)) first[NT < 1024 ? tid : tid / 4] = order;
+    if (g.top && few) {
+#pragma unroll 1
+      for (int i = tid; i < kFirst; i += NT) {
+        int c;
+        first[i] = i < 4 * groups ? order_of(bound_at(i, c)) : 0;
+      }
+    }
     if (tid < 2) counts[tid] = 0;
     __syncthreads();
     if (NW > 1) {
@@ -228,18 +249,36 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
               if (above >= g.top) b |= bit;
             }
           };
-          if (all) find(std::integral_constant<int, NW>{});
-          else find(std::integral_constant<int, (NW + 3) / 4>{});
+          if (few) find(std::integral_constant<int, kFirst / 64>{});
+          else find(std::integral_constant<int, kChoices / 64>{});
           if (lane == 0) bound = b;
         }
         __syncthreads();
-        if ((all || tid % 4 == 0) && best > -INFINITY && order >= bound && own != (int)y) items[atomicAdd(&counts[1], 1)] = own;
+        if (few) {
+#pragma unroll 1
+          for (int i = tid; i < 4 * groups; i += NT) {
+            if (first[i] < bound) continue;
+            int c;
+            if (bound_at(i, c) > -INFINITY && c != (int)y) items[atomicAdd(&counts[1], 1)] = c;
+          }
+        } else if ((NT < 1024 || tid % 4 == 0) && best > -INFINITY && order >= bound && own != (int)y) {
+          items[atomicAdd(&counts[1], 1)] = own;
+        }
       }
       if (tid == 0) items[atomicAdd(&counts[1], 1)] = (int)y;
       __syncthreads();
       // what is pending is computed, a class or (negative) a quarter of a group's, two at a time a wave; then
       // every class that may pass the bar is pending
       int scanned = g.top ? 0 : groups;
+      auto take = [&](double z, int c) {
+        if (c == (int)y) token_z = z;
+        if (g.top && z > kMasked && ahead(z, c, bar, bar_class)) {
+          const int e = known + atomicAdd(&counts[0], 1);
+          lz[buf][e] = z, lc[buf][e] = c;
+        }
+      };
+      const int bytes = g.dp * (BF16 ? 2 : 4), lanes = max(short_lanes(bytes), NW), sub = lane / lanes;
+      const bool short_row = NT < 1024 && bytes <= kShort;
 #pragma unroll 1
       while (true) {
         const int pending = counts[1];
@@ -257,26 +296,50 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
         bool more = pending > 0;
 #pragma unroll 1
         while (more) {
+          if (short_row) {
 #pragma unroll 1
-          for (int k = 0; k < kTake; k += 2) {
-            int c[2];
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              const int v = next();
-              c[0] = q ? c[0] : v, c[1] = v;
-            }
-            if (c[0] < 0) break;
-            double z[2];
-            const int rows[2] = {c[0], max(c[1], 0)};
-            row_dots<2, BF16>(g.x, g.w, place, rows, g.dp, lane, z);
-            const double zc = lane ? z[1] : z[0];
-            const int cc = lane ? c[1] : c[0];
-            if (lane < 2 && cc >= 0) {
-              if (cc == (int)y) token_z = zc;
-              if (g.top && zc > kMasked && ahead(zc, cc, bar, bar_class)) {
-                const int e = known + atomicAdd(&counts[0], 1);
-                lz[buf][e] = zc, lc[buf][e] = cc;
+            for (int k = 0; k < kTake && at < pending; k += 64 / lanes) {
+              const int it = at + NW * sub;
+              const int item = it < pending ? items[it] : -1;
+              const int lead = __builtin_amdgcn_readfirstlane(item);
+              int c = -1;
+              if (lead < 0) {  // of a quarter of a group's, as many as there are places
+                if (code + sub < g.side / 16)
+                  c = (int)group_class(~lead >> 2, (~lead & 3) * (g.side / 16) + code + sub, g.side, g.apart, g.parts);
+                code += 64 / lanes;
+                if (code >= g.side / 16) at += NW, code = 0;
+              } else {  // classes up to the next quarter
+                const uint64_t end = __ballot(item < 0);
+                const int taken = end ? __builtin_ctzll(end) / lanes : 64 / lanes;
+                if (sub < taken) c = item;
+                at += NW * taken;
               }
+              if (c >= g.vocab) c = -1;
+              const int have = lane < known ? lc[buf][lane] : -2;
+#pragma unroll 1
+              for (int j = 0; j < 64; j += lanes) {
+                const bool dup = __any(have == __builtin_amdgcn_readlane(c, j));
+                if (dup && sub * lanes == j) c = -1;
+              }
+              const double zc = short_dot<BF16>(g.x, g.w, place, max(c, 0), bytes, lanes, lane);
+              if ((lane & (lanes - 1)) == 0 && c >= 0) take(zc, c);
+            }
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < kTake; k += 2) {
+              int c[2];
+#pragma unroll 1
+              for (int q = 0; q < 2; ++q) {
+                const int v = next();
+                c[0] = q ? c[0] : v, c[1] = v;
+              }
+              if (c[0] < 0) break;
+              double z[2];
+              const int rows[2] = {c[0], max(c[1], 0)};
+              row_dots<2, BF16>(g.x, g.w, place, rows, g.dp, lane, z);
+              const double zc = lane ? z[1] : z[0];
+              const int cc = lane ? c[1] : c[0];
+              if (lane < 2 && cc >= 0) take(zc, cc);
             }
           }
           more = __syncthreads_or(at < pending);
@@ -364,8 +427,10 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   p.el = s.bf16 ? 2 : 4;
   p.dp = (int)up(s.d, s.bf16 ? 8 : 4);
   p.side = side_for(s.vocab, s.n, s.bf16);
-  // few groups for the alternatives asked for: smaller ones (17 x 80 x 642 with 64: 108 -> 50 us; 1 x 184 x 4771: 34 -> 52)
-  if (s.n <= kFew && 2 * s.vocab < (int64_t)s.top * p.side) p.side = 64;
+  // Few groups for the alternatives asked for, whose fourth bound then often passes: smaller ones (17 x 80 x 642 with 64:
+  // 108 -> 50 us; 12224 x 33 x 1135 with 20: 350 -> 115; 4096 x 512 x 4096 with 20: 163 -> 142).  The products of few rows
+  // take longer in them (1 x 184 x 4771 with 64: 35 -> 47 us).
+  if ((s.n <= kFew ? 2 : 1) * s.vocab < (int64_t)s.top * p.side) p.side = 64;
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   // Rows of a tile 64 apart: all tiles' (256 x 256, 2048 columns) takes 10% longer, their pages no longer at hand,
   // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.
@@ -463,8 +528,8 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
     if (s.bf16) lp_rows<NT, true><<<rows, NT, 0, st>>>(a);
     else lp_rows<NT, false><<<rows, NT, 0, st>>>(a);
   };
-  if (s.n <= 256) launch(std::integral_constant<int, 1024>{});
-  else if (s.n > 1024 && s.top <= 24 && p.parts >= 16) launch(std::integral_constant<int, 64>{});
+  if (s.n <= 256 && p.dp * p.el > kShort) launch(std::integral_constant<int, 1024>{});
+  else if (s.n > 1024 && s.top <= 32) launch(std::integral_constant<int, 64>{});
   else launch(std::integral_constant<int, 256>{});
   AM_LAUNCH_CHECK();
   return ATLASMEM_OK;

@@ -1047,6 +1047,33 @@ __device__ __forceinline__ void row_dots(const void* a, const void* b, int64_t r
     for (int n = 0; n < N; ++n) z[n] += __shfl_xor(z[n], k);
 }
 
+// The same of rows of at most kShort bytes, 16 a lane: of each `lanes` lanes one product.
+constexpr int kShort = 512;
+__device__ __forceinline__ int short_lanes(int bytes) {
+  return bytes <= 64 ? 4 : bytes <= 128 ? 8 : bytes <= 256 ? 16 : 32;
+}
+template <bool BF16>
+__device__ __forceinline__ double short_dot(const void* a, const void* b, int64_t ra, int64_t rb, int bytes, int lanes,
+                                            int lane) {
+  const int at = (lane & (lanes - 1)) * 16;
+  double v = 0.0;
+  if (at < bytes) {
+    const u32x4 x = *(const u32x4*)((const char*)a + ra * bytes + at);
+    const u32x4 y = *(const u32x4*)((const char*)b + rb * bytes + at);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (BF16) {
+        v += (double)(__uint_as_float(x[q] << 16) * __uint_as_float(y[q] << 16));
+        v += (double)(__uint_as_float(x[q] & 0xFFFF0000u) * __uint_as_float(y[q] & 0xFFFF0000u));
+      } else {
+        v = fma((double)__uint_as_float(x[q]), (double)__uint_as_float(y[q]), v);
+      }
+    }
+  }
+  for (int k = lanes / 2; k; k >>= 1) v += __shfl_xor(v, k);
+  return v;
+}
+
 // dX from the partial sums of the contraction's pieces, times the rows' weights: four columns a thread.
 __global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int* at, const float* dloss,
                        void* out, int out_bf16, int vec) {

@@ -118,6 +118,28 @@ def test_parity(kw):
 
 
 @pytest.mark.parametrize("dtype", [am.BF16, am.F32])
+@pytest.mark.parametrize("n,d,vocab,top", [(2, 33, 5000, 64), (300, 33, 1135, 64), (520, 300, 1000, 64), (1100, 33, 200, 20),
+                                           (1100, 40, 90, 32), (1100, 5, 300, 1), (1100, 300, 2000, 10),
+                                           (1100, 130, 5000, 32), (1100, 64, 20, 20)])
+def test_first_choices(dtype, n, d, vocab, top):
+    """Few and many rows of few and many classes, short and long: each way to the first alternatives."""
+    check(Case(dtype, n, d, vocab, top=top))
+
+
+@pytest.mark.parametrize("dtype", [am.BF16, am.F32])
+@pytest.mark.parametrize("n,d,vocab,top", [(300, 12, 700, 40), (1100, 12, 700, 20), (1100, 12, 9000, 8)])
+def test_equal_logits_of_many_rows(dtype, n, d, vocab, top):
+    """Small whole numbers, of which whole groups pass the last alternative: they go to the lowest index."""
+    import torch
+    c = Case(dtype, n, d, vocab, top=top)
+    rng = np.random.default_rng(4)
+    c.X = torch.from_numpy(rng.integers(-2, 3, c.X.shape).astype(np.float32)).to(c.X.dtype)
+    c.W = torch.from_numpy(rng.integers(-1, 2, c.W.shape).astype(np.float32)).to(c.W.dtype)
+    c.X[1::50] = 0.0
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", [am.BF16, am.F32])
 @pytest.mark.parametrize("n,vocab,top", [(5, 700, 20), (600, 9000, 64)])
 def test_equal_logits_go_to_the_lowest_index(dtype, n, vocab, top):
     """Small whole numbers: few distinct logits, all exact."""
