@@ -10,6 +10,12 @@
 // bf16 calls leave those exponentials with ten significant bits and no sign, in the 16 that G then takes, so that G is
 // rounded once, not twice; c on X instead of G, without that pass, was the third rounding of a term of dW
 // (33 x 256 x 1000: 2.8e-3 off instead of 2.3e-3).  fp32 calls keep G / c, and the rows' weights take c.
+//
+// What bounds it: the matrix cores (8192 x 2048 x 65536 bf16, a tenth left out: 1.98 TFLOP a product.  z 1.92 ms, 1.03
+// PFLOP/s, of which the stores of what is kept take 0.2 to 0.4, not overlapped with the next tile's products; dX 1.56,
+// 1.27; dW 1.49, 1.33), beside them the rows' pass over G; few rows launches (33 x 256 x 1000: seven, 32 us a training
+// pass).  Computing z again for the backward instead, a product more, takes 1.7 ms where what is kept costs its
+// stores and the rows' pass, 0.7 to 0.9.
 #include "logits.h"
 
 namespace am {
@@ -21,7 +27,8 @@ constexpr float kFar = 36.0f;
 constexpr int kMost = 128;  // entries of a row
 
 // log p of each given class (-inf: none) and p, and of each row a label (0, or -1 for a row that has no class) and the
-// logit of its first class.  With `index`, rows are taken as they come, those left out among them.  A wave a row.
+// logit of its first class.  With `index`, rows are taken as they come, those left out among them.  A wave a row: its
+// waits for ids, and for a row of W that they name (8192 x 2048 18 us).
 __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const float* teacher, int64_t n, int top,
                                                   int64_t vocab, float scale, const void* X, const void* W, int bf16,
                                                   int vec, int d, float* logp, float* prob, int64_t* label,
@@ -104,9 +111,9 @@ struct JoinArgs {
   void* x_again;
 };
 
-// loss, lse of a row, and of a training step its G, in place.  It moves what is kept twice, which bounds it (8192 x 2048 x
-// 65536: 2.15 GB in 455 us, 4.7 TB/s); a product's epilogue cannot write G, since a row's lse is known behind its last
-// tile.  A workgroup of 256 threads a row, or where many rows are short (bytes that it reads and writes) of one wave,
+// loss, lse of a row, and of a training step its G, in place.  Memory bounds it: it reads and writes what
+// is kept (8192 x 2048 x 65536, a tenth left out: 1.9 GB, and 1.0 of the given classes' rows of W, in 455 us, 6.4 TB/s);
+// a product's epilogue cannot write G, since a row's lse is known behind its last tile.  A workgroup of 256 threads a row, or where many rows are short (bytes that it reads and writes) of one wave,
 // whose steps wait for no other (12224 x 33 x 1135 training 153 -> 104 us, 2048 x 256 x 1024 63 -> 60; long rows
 // take longer, 8192 x 2048 x 65536 6.05 -> 6.15 ms, and few, 1024 x 256 x 1024 47 -> 49 us).
 constexpr int64_t kManyRows = 2048, kShortRow = 32768;
@@ -273,7 +280,7 @@ __global__ __launch_bounds__(1024) void ds_scale(const float* coef, const float*
 // 256 x 1024: 43.7 -> 45.2).
 constexpr int64_t kFewRows = 512;
 
-// The rows of X that have a place, times their weights over `scale` (where those are one value, as they are), zeros for
+// Memory (8192 x 2048: 63 MB in 23 us).  The rows of X that have a place, times their weights over `scale` (where those are one value, as they are), zeros for
 // rows that are left out; and zeros for the latter's dX, if it is given.  Four columns a thread.
 __global__ __launch_bounds__(256) void ds_weigh(const void* x, int bf16, int64_t n, int d, int dp, const int* at,
                                                 int all, const float* coef, const float* dloss, float* weight,
@@ -362,6 +369,7 @@ Plan plan_of(const Distillation& s, bool train) {
   p.side = side_for(s.vocab, s.n, s.bf16);
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   p.ldg = up(s.vocab, 64);
+  // dX is [n][d], of few tiles: V is cut so that they fill the chip, into pieces of 512 classes at least
   p.side_x = s.n <= kFew ? (s.bf16 ? 128 : 64) : side_split(p.dp, s.n, s.bf16);
   int64_t tiles = std::max<int64_t>(tiles_of(p.dp, s.n, p.side_x), 1);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.side_x == 256 ? 256 : 512) / tiles, s.vocab / 512));

@@ -8,10 +8,15 @@
 // Alternatives.  Which class is larger is decided in 64 bits, so that an answer does not depend on how a sum
 // was cut: equal logits go to the lowest index.  The matrix cores' z is off by at most
 // c |x| |w| (c: the roundings on a term's way; Cauchy and Schwarz), so z + c |x| |w| is an upper bound.  A
-// lane's 16 to 64 classes of a row are a group; of each the four largest bounds are kept, with the class's
-// place in the six bits that this costs.  The row's workgroup takes the best classes of `top` of its threads,
-// computes them in 64 bits, and has a lower bound of the last alternative; then every class whose bound
+// lane's 16 to 64 classes of a row are a group; of each the four largest z are kept, as how far they are below the
+// tile's maximum, with the class's place in the six bits that this costs.  The row's workgroup computes the best
+// classes by their bounds in 64 bits, and has a lower bound of the last alternative; then every class whose bound
 // passes it is computed too: a group whose fourth bound passes as a whole.
+//
+// What bounds it: few rows the bytes of W (1 x 1024 x 50257 bf16: products 21 us, 4.9 TB/s, rows 15 us; 64 x 2048 x
+// 65536: 44 us, 6.1 TB/s with W partly in the last-level cache, and 25), many the matrix cores (8192 x 2048 x 65536, a
+// tenth left out: 1.74 ms, 1.14 PFLOP/s, with 20 alternatives; 2047 x 1024 x 32000 without: 121 us, 1.11 PFLOP/s).
+// One bound a group of classes side by side, without their places, had whole groups computed: rows 1.81 ms, now 0.26.
 #include "logits.h"
 
 namespace am {
@@ -33,6 +38,8 @@ __device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
   for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
   return sqrtf(s);
 }
+// Memory: W and X once more, 268 MB in 44 us and 30 in 7 (6.1 and 4.3 TB/s).  Taken in the products' loop instead where
+// those leave time for it (see kNorms).
 __global__ __launch_bounds__(256) void lp_row_norms(const uint16_t* x, int64_t rows, const int* count, int dp, float* out) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= (count ? *count : rows)) return;
@@ -92,7 +99,7 @@ __device__ __forceinline__ void join(float& m, float& s, float& t, float om, flo
 
 // The row's numbers and alternatives.  What it reads is small (16 bytes a group, 40 MB at 8192 x 2048 x 65536, and some
 // rows of W out of L2); its waits are for those reads, one behind the other: bounds, classes, selection, bounds.  So a
-// workgroup a row, and the rows that fit on the chip hide each other's waits (8192 x 2048 x 65536: 280 us of 2.2 ms).
+// workgroup a row, and the rows that fit on the chip hide each other's waits (8192 x 2048 x 65536: 260 us of 2.1 ms).
 // Its threads NT:
 //   1024 for up to 256 rows, whose time is one row's and where many classes are computed at once (1 x 1024 x 50257
 //     36.8 us, with 256 threads 39.6; 512 rows 129 against 113), unless the rows are short and a wave takes several
