@@ -4,6 +4,7 @@ what a call may write, rows with a range of weights, and a row of each kind in o
 import numpy as np
 import pytest
 
+import logits_bounds
 from helpers import DEV
 from test_distillation_gpu import Case as Distill
 from test_learned_neural_amd import atlasmem as am
@@ -146,3 +147,27 @@ def test_one_call_with_rows_of_each_kind():
             assert float((x - y).abs().max()) <= tol * max(float(y.abs().max()), 1e-30), (rows, i)
     assert float(o[1][8]) > 1900 and torch.isnan(o[0][30]) and not o[2][16:20].any()
     assert t[0].shape == (96, 64)
+
+
+def test_more_rows_than_workgroups():
+    """A row's answer does not depend on its place, past 2^20 rows either."""
+    import torch
+    n, of = (1 << 20) + 700, 1000
+    rows = torch.arange(n) % of
+    c, e = Logprobs(am.BF16, of, 8, 40, top=3), Logprobs(am.BF16, 1, 8, 40, top=3)
+    e.n, e.X, e.W, e.tokens = n, c.X[rows], c.W, c.tokens[rows.numpy()]
+    b = e.run()
+    assert all(torch.equal(y, y[:of][rows]) for y in b)
+    want, ids = logits_bounds.logprobs(c.X.double().numpy(), c.W.double().numpy(), c.tokens, c.scale, c.top, True)
+    assert np.array_equal(b[2][:of].cpu().numpy(), ids)
+    for i, name in ((0, "logprob"), (1, "entropy"), (3, "top_logprobs")):
+        logits_bounds.within(name, b[i][:of], *want[name])
+    c, e = Distill(am.BF16, of, 8, 40, top=3), Distill(am.BF16, 1, 8, 40, top=3)
+    e.n, e.X, e.W, e.ids, e.teacher = n, c.X[rows], c.W, c.ids[rows.numpy()], c.teacher[rows.numpy()]
+    e.dloss = None if c.dloss is None else c.dloss[rows.numpy()]
+    b = e.run()
+    assert all(torch.equal(y, y[:of][rows]) for y in b[:3])
+    want = logits_bounds.distillation(c.X.double().numpy(), c.W.double().numpy(), c.ids, c.teacher.astype(np.float64), c.scale,
+                                      c.dloss, True)
+    for y, name in zip(b, ("loss", "lse", "dX")):
+        logits_bounds.within(name, y[:of], *want[name])
