@@ -437,7 +437,8 @@ Plan plan_of(const TokenLogprobs& s, bool tokens) {
   // Few groups for the alternatives asked for, whose fourth bound then often passes: smaller ones (17 x 80 x 642 with 64:
   // 108 -> 50 us; 12224 x 33 x 1135 with 20: 350 -> 115; 4096 x 512 x 4096 with 20: 163 -> 142).  The products of few rows
   // take longer in them (1 x 184 x 4771 with 64: 35 -> 47 us).
-  if ((s.n <= kFew ? 2 : 1) * s.vocab < (int64_t)s.top * p.side) p.side = 64;
+  // Their grids stay below 2^30 lanes.
+  if ((s.n <= kFew ? 2 : 1) * s.vocab < (int64_t)s.top * p.side && s.n * s.vocab <= INT64_C(1) << 34) p.side = 64;
   p.parts = (int)((s.vocab + p.side - 1) / p.side);
   // Rows of a tile 64 apart: all tiles' (256 x 256, 2048 columns) takes 10% longer, their pages no longer at hand,
   // and 16 leave frequent classes together (rows 485 us instead of 380).  Byte offsets in a tile stay below 2^31.

@@ -131,3 +131,12 @@ def test_workspaces_hold_no_logits(n, d, vocab):
     assert am.distillation_workspace_bytes(am.BF16, n, d, vocab, 32) <= \
         rows + n * (8 * (vocab // (4 * least) + 1) + 8 * 32 + 24) + (1 << 20)
     assert am.distillation_kept_bytes(am.BF16, n, vocab, 32) <= 2 * n * (vocab + 64) + 16 * n + (1 << 20)
+
+
+def test_largest_calls_keep_large_tiles():
+    """Many rows of few classes: 64 x 64 tiles (88 bytes a row and tile) would need 2^33 lanes of a grid that holds 2^32."""
+    n, vocab = 1 << 24, 8192
+    large = am.token_logprobs_workspace_bytes(am.BF16, n, 8, vocab, 64)
+    assert large <= n * (88 * (vocab // 128) + 64) + (1 << 24)
+    small = am.token_logprobs_workspace_bytes(am.BF16, n >> 10, 8, vocab, 64)  # 64-wide tiles, as far as they go
+    assert small >= (n >> 10) * 88 * (vocab // 64)
