@@ -319,3 +319,11 @@ def test_differences():
         # third derivatives: h^2 / 6 of a change of the logits by up to 4 a row; roundings: 2^-20 of each loss / h
         size = float((t[4].abs() * (1 if which == 0 else 1)).sum())
         assert abs(got - want) <= size * (h * h / 6 * 4 ** 3 + 2 * 10 * 2.0 ** -20 / h), (got, want)
+
+
+@pytest.mark.parametrize("dtype", [am.BF16, am.F32])
+@pytest.mark.parametrize("n,d,vocab,top", [(3, 2100, 400, 64), (9, 300, 500, 128), (256, 40, 300, 17), (257, 40, 300, 17),
+                                           (256, 72, 300, 16), (2048, 40, 300, 16)])
+def test_many_entries_of_few_rows(dtype, n, d, vocab, top):
+    """On both sides of what decides how many lanes a row has."""
+    check(Case(dtype, n, d, vocab, top=top))
