@@ -111,13 +111,16 @@ struct JoinArgs {
   void* x_again;
 };
 
-// loss, lse of a row, and of a training step its G, in place.  Memory bounds it: it reads and writes what
-// is kept (8192 x 2048 x 65536, a tenth left out: 1.9 GB, and 1.0 of the given classes' rows of W, in 455 us, 6.4 TB/s);
-// a product's epilogue cannot write G, since a row's lse is known behind its last tile.  A workgroup of 256 threads a row, or where many rows are short (bytes that it reads and writes) of one wave,
-// whose steps wait for no other (12224 x 33 x 1135 training 153 -> 104 us, 2048 x 256 x 1024 63 -> 60; long rows
-// take longer, 8192 x 2048 x 65536 6.05 -> 6.15 ms, and few, 1024 x 256 x 1024 47 -> 49 us); of 1024 where few rows have more
-// entries than four waves take in two steps (33 x 3744 x 5000 with 128 the loss alone 78 -> 55 us, 33 x 256 x 1000
-// with 20 training 34.6 -> 34.5; 600 x 512 x 9000 with 128: 112 -> 139).
+// loss, lse of a row, and of a training step its G, in place.  Memory bounds it: it reads and writes what is kept (8192 x
+// 2048 x 65536, a tenth left out: 1.9 GB, and 1.0 of the given classes' rows of W, in 455 us, 6.4 TB/s), or reads those
+// rows out of L2 (2603 x 3352 x 479 with 128 entries: 2.2 GB, 9 TB/s).  A product's epilogue cannot write G, since a
+// row's lse is known behind its last tile.  A workgroup a row, of
+//   one wave, whose steps wait for no other, where many rows are short (bytes that it reads and writes; 12224 x 33 x 1135
+//     training 153 -> 104 us, 2048 x 256 x 1024 63 -> 60; long rows take longer, 8192 x 2048 x 65536 6.05 -> 6.15 ms, and
+//     few, 1024 x 256 x 1024 47 -> 49 us);
+//   1024 threads where few rows have more entries than four waves take in two steps (33 x 3744 x 5000 with 128 the loss
+//     alone 78 -> 55 us, 33 x 256 x 1000 with 20 training 34.6 -> 34.5; 600 x 512 x 9000 with 128: 112 -> 139);
+//   256 else.
 constexpr int64_t kManyRows = 2048, kShortRow = 32768;
 template <int NT, bool BF16, bool TRAIN>
 __global__ __launch_bounds__(NT) void ds_rows(JoinArgs a) {
