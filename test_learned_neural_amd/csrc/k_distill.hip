@@ -285,8 +285,9 @@ __global__ __launch_bounds__(1024) void ds_scale(const float* coef, const float*
 // 256 x 1024: 43.7 -> 45.2).
 constexpr int64_t kFewRows = 512;
 
-// Memory (8192 x 2048: 63 MB in 23 us).  The rows of X that have a place, times their weights over `scale` (where those are one value, as they are), zeros for
-// rows that are left out; and zeros for the latter's dX, if it is given.  Four columns a thread.
+// The rows of X that have a place, times their weights over `scale` (where those are one value, as they are), zeros for
+// rows that are left out; and zeros for the latter's dX, if it is given.  Four columns a thread.  Memory (8192 x 2048: 63
+// MB in 23 us).
 __global__ __launch_bounds__(256) void ds_weigh(const void* x, int bf16, int64_t n, int d, int dp, const int* at,
                                                 int all, const float* coef, const float* dloss, float* weight,
                                                 float* scale, int* equal, void* out, void* dx) {

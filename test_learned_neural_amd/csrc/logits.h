@@ -278,20 +278,22 @@ __device__ __forceinline__ void put_rows(uint16_t* sm, f32x16 (&acc)[MA][NB], in
       }
   }
   __syncthreads();
-  const bool vec = ld % 8 == 0 && ((uintptr_t)out & 15) == 0;
+  if (ld % 8 == 0 && ((uintptr_t)out & 15) == 0) {
 #pragma unroll 4
-  for (int id = tid; id < TB * CH; id += NT) {
-    const int r = id / CH, c = id % CH;
-    const int64_t row = r0 + r, at = c0 + 8 * c;
-    if (row >= nr || at >= nc) continue;
-    const u32x4 v = *(const u32x4*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3));
-    uint16_t* p = out + (to ? to[row] : row) * ld + at;
-    if (vec) {
-      *(u32x4*)p = v;
-    } else {
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-        if (at + n < nc) p[n] = (uint16_t)(v[n >> 1] >> (16 * (n & 1)));
+    for (int id = tid; id < TB * CH; id += NT) {
+      const int r = id / CH, c = id % CH;
+      const int64_t row = r0 + r, at = c0 + 8 * c;
+      if (row >= nr || at >= nc) continue;
+      *(u32x4*)(out + (to ? to[row] : row) * ld + at) = *(const u32x4*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 3));
+    }
+  } else {
+    // an element a lane, side by side
+#pragma unroll 4
+    for (int id = tid; id < TB * TA; id += NT) {
+      const int r = id / TA, c = id % TA;
+      const int64_t row = r0 + r, at = c0 + c;
+      if (row >= nr || at >= nc) continue;
+      out[(to ? to[row] : row) * ld + at] = sm[r * TA + (((c >> 3) ^ (r & (CH - 1))) << 3) + (c & 7)];
     }
   }
 }
@@ -321,12 +323,11 @@ __device__ __forceinline__ void put_wave(uint16_t* sm, f32x16 (&acc)[MA][NB], in
   }
 }
 
-// The same in fp32, four columns a lane; added to what is there (rows of whole 16-byte pieces), or not.
+// The same in fp32, rows of whole 16-byte pieces, four columns a lane; added to what is there, or not.
 template <int MA, int NB>
 __device__ __forceinline__ void put_rows32(f32x16 (&acc)[MA][NB], int wa, int wb, int lane, float* out, int64_t ld,
                                            int64_t c0, int64_t r0, int64_t nr, int add, const int* to = nullptr) {
   const int hf = lane >> 5, col = lane & 31;
-  const bool vec = ld % 4 == 0 && ((uintptr_t)out & 15) == 0;
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     const int64_t r = r0 + wb + 32 * j + col;
@@ -343,15 +344,38 @@ __device__ __forceinline__ void put_rows32(f32x16 (&acc)[MA][NB], int wa, int wb
           const float4 o = *(const float4*)p;
           x.x += o.x, x.y += o.y, x.z += o.z, x.w += o.w;
         }
-        if (vec) {
-          *(float4*)p = x;
-        } else {
-          if (c + 0 < ld) p[0] = x.x;
-          if (c + 1 < ld) p[1] = x.y;
-          if (c + 2 < ld) p[2] = x.z;
-          if (c + 3 < ld) p[3] = x.w;
-        }
+        *(float4*)p = x;
       }
+  }
+}
+
+// The same of rows that are not whole 16-byte pieces: through LDS, an element a lane, side by side (a training pass of
+// distillation, 6 x 1413 x 29001: 384 -> 330 us; bf16, in put_rows, 2000 x 1001 x 20000: 446 -> 423).
+template <int TA, int TB, int MA, int NB, int NT>
+__device__ __forceinline__ void put_odd32(float* sm, f32x16 (&acc)[MA][NB], int wa, int wb, int tid, float* out, int64_t ld,
+                                          int64_t c0, int64_t r0, int64_t nr, const int* to) {
+  constexpr int CH = TA / 4;  // 16-byte pieces of a row, exchanged by the row's low bits
+  const int lane = tid & 63, hf = lane >> 5, col = lane & 31;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int r = wb + 32 * j + col;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16& x = acc[i][j];
+        const int c = (wa + 32 * i + 8 * q + 4 * hf) >> 2;
+        *(float4*)(sm + r * TA + ((c ^ (r & (CH - 1))) << 2)) = float4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+      }
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int id = tid; id < TB * TA; id += NT) {
+    const int r = id / TA, c = id % TA;
+    const int64_t row = r0 + r, at = c0 + c;
+    if (row >= nr || at >= ld) continue;
+    out[(to ? to[row] : row) * ld + at] = sm[r * TA + (((c >> 2) ^ (r & (CH - 1))) << 2) + (c & 3)];
   }
 }
 
@@ -365,6 +389,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   E* sm = (E*)smem;
   constexpr int kStage = A::kElems + B::kElems;
+  static_assert(!F32 || TA * TB <= kStages * kStage, "an output tile passes through LDS");
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hf = lane >> 5,
             col = lane & 31;
   const int wa = (wave % WA) * (TA / WA), wb = (wave / WA) * (TB / WB);
@@ -886,6 +911,11 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     }
   }
 
+  auto put_out32 = [&](const int* to) __attribute__((always_inline)) {
+    if (g.ldo % 4 == 0 && ((uintptr_t)g.out & 15) == 0)
+      put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.out, g.ldo, a0, b0, g.nb, 0, to);
+    else put_odd32<TA, TB, MA, NB, NT>((float*)smem, acc, wa, wb, tid, (float*)g.out, g.ldo, a0, b0, g.nb, to);
+  };
   if constexpr (EPI == EPI_OUT) {
     const float w = g.scale ? *g.scale : 1.0f;
 #pragma unroll
@@ -908,14 +938,13 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
         for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
     }
-    if constexpr (F32) put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.out, g.ldo, a0, b0, g.nb, 0, g.to);
+    if constexpr (F32) put_out32(g.to);
     else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb, g.to);
   }
 
   if constexpr (EPI == EPI_ACC || EPI == EPI_PART)
     put_rows32<MA, NB>(acc, wa, wb, lane, g.acc + (int64_t)split * g.acc_rows * g.lda, g.lda, a0, b0, g.nb, g.add);
-  if constexpr (F32 && EPI == EPI_OUT)
-    put_rows32<MA, NB>(acc, wa, wb, lane, (float*)g.out, g.ldo, a0, b0, g.nb, 0);
+  if constexpr (F32 && EPI == EPI_OUT) put_out32(nullptr);
 }
 
 // The rows that count, those whose label is a class, in order (one workgroup): index [rows that count],
