@@ -577,7 +577,7 @@ atlasmem_status distillation_backward(const Distillation& s, const void* X, cons
     x.K = s.vocab;
     const bool few = s.n <= kFew && p.side_x != (s.bf16 ? 64 : 128);
     if (p.splits == 1) {
-      x.out = dX, x.ldo = s.d, x.to = k.index, x.row_weight = ws.weight;
+      x.out = dX, x.ldo = s.d, x.to = k.index, x.at = k.at, x.row_weight = ws.weight;
       e = few ? gemm_few<true, EPI_ROWS>(x, s.bf16, st) : gemm<true, false, EPI_ROWS>(x, s.bf16, p.side_x, st);
     } else {
       x.splits = p.splits, x.acc = ws.acc, x.acc_rows = s.n;

@@ -68,6 +68,7 @@ struct GemmArgs {
   const float* factor;     // AGAIN: [nb], q / exp(scale (z - ref))
   int top;
   const float* row_weight; // ROWS: [rows of X]
+  const int* at;           // ... whether a row counts: a place, or -1
 };
 
 // The tiles of SUMS and TOP take every `apart`-th row of a, so that classes that lie together (frequent ones do)
@@ -932,11 +933,13 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int64_t r = b0 + wb + 32 * j + col;
-      const float w = r < g.nb ? g.row_weight[g.to[r]] : 0.0f;
+      const int64_t row = r < g.nb ? g.to[r] : 0;
+      const bool on = r < g.nb && g.at[row] >= 0;  // else zero, where a masked class's minus infinity made it NaN, too
+      const float w = on ? g.row_weight[row] : 0.0f;
 #pragma unroll
       for (int i = 0; i < MA; ++i)
 #pragma unroll
-        for (int n = 0; n < 16; ++n) acc[i][j][n] *= w;
+        for (int n = 0; n < 16; ++n) acc[i][j][n] = on ? acc[i][j][n] * w : 0.0f;
     }
     if constexpr (F32) put_out32(g.to);
     else put_rows<TA, TB, MA, NB, NT>(sm, acc, wa, wb, tid, (uint16_t*)g.out, g.ldo, a0, g.ldo, b0, g.nb, g.to);
