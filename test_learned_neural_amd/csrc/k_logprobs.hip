@@ -231,6 +231,9 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
         join(m, s, t, om, os, ot, g.k2);
       }
     }
+    // one lane's for all: joins of two sums round differently from either side, and a row's numbers have one lse
+    auto one = [](float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); };
+    m = one(m), s = one(s), t = one(t);
     const float log_s = logf(s), lse = fmaf(g.scale, m, log_s);
     const bool none = lse == -INFINITY, bad = !none && !(fabsf(lse) < INFINITY);
 
