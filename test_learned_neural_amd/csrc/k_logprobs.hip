@@ -23,8 +23,8 @@ namespace am {
 
 namespace {
 
-// |row| of a row of a bf16 matrix, without masks.  A wave's.
-__device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
+// |row| of a row of a bf16 matrix, of its magnitudes below `most`.  A wave's.
+__device__ __forceinline__ float norm_of(const uint16_t* x, int dp, float most, int lane) {
   float s = 0.0f;
 #pragma unroll 4
   for (int c = lane * 8; c < dp; c += 512) {
@@ -32,18 +32,18 @@ __device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
-      s = fmaf(lo, fabsf(lo) < kMasking ? lo : 0.0f, fmaf(hi, fabsf(hi) < kMasking ? hi : 0.0f, s));
+      s = fmaf(lo, fabsf(lo) < most ? lo : 0.0f, fmaf(hi, fabsf(hi) < most ? hi : 0.0f, s));
     }
   }
   for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
-  return sqrtf(s);
+  return in_range(s) ? sqrtf(s) : far_norm<true>(x, dp, most, lane, 64);
 }
 // Memory: W and X once more, 268 MB in 44 us and 30 in 7 (6.1 and 4.3 TB/s).  Taken in the products' loop instead where
 // those leave time for it (see kNorms).
 __global__ __launch_bounds__(256) void lp_row_norms(const uint16_t* x, int64_t rows, const int* count, int dp, float* out) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= (count ? *count : rows)) return;
-  const float v = norm_of(x + r * dp, dp, threadIdx.x & 63);
+  const float v = norm_of(x + r * dp, dp, INFINITY, threadIdx.x & 63);
   if ((threadIdx.x & 63) == 0) out[r] = v;
 }
 // The largest norm of each group's classes: a workgroup's waves take its 64 in turn.
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void lp_group_norms(const uint16_t* w, int64_t
   for (int code = wave; code < side / 4; code += 4) {
     const int64_t c = group_class(blockIdx.x, code, side, apart, tiles);
     if (c >= vocab) continue;
-    m = fmaxf(m, norm_of(w + c * dp, dp, lane));
+    m = fmaxf(m, norm_of(w + c * dp, dp, kMasking, lane));
   }
   if (lane == 0) best[wave] = m;
   __syncthreads();
@@ -151,10 +151,13 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     const int groups = 4 * g.parts;
     const uint4* keys = g.keys + (int64_t)place * groups;
     const float* tops = g.tops + (int64_t)place * (groups / 2);
-    const float error = g.top ? fminf(g.error * g.b_norm[place], 1.0e30f) : 0.0f;
-    // what the maximum of group i may be in 64 bits
+    const float b_norm = g.top ? g.b_norm[place] : 0.0f;
+    const float error = !(b_norm > 0.0f) ? 0.0f : b_norm < 3.0e38f ? fmaxf(g.error * b_norm, 1.0e-37f) : 3.0e38f;
+    // what the maximum of group i may be in 64 bits.  Zeros have no error; what else was flushed, or rounded among the
+    // smallest floats, is less than 2^-100 (2^14 products of 2^-126; a key times 1 / k2)
     auto top_of = [&](int i) {
-      const float t = fmaf(error, g.a_norm[i], tops[(i >> 2) * 2 + (i & 1)]);
+      const float top = tops[(i >> 2) * 2 + (i & 1)], a_norm = g.a_norm[i];
+      const float t = fmaf(error, a_norm, top + (error > 0.0f && a_norm > 0.0f ? 0x1p-100f : 0.0f));
       return fmaf(fabsf(t), 0x1p-21f, t);
     };
     // bound i of all groups' four, and its class

@@ -26,6 +26,32 @@ __device__ __forceinline__ float exp2_of(float a, float b, float k2, float k2_lo
   return __builtin_amdgcn_exp2f(fmaf(x, k2, low));
 }
 
+// Sums of squares of floats that lost nothing that counts: far from overflow, and squares below 2^-126 are small beside
+// them.
+__device__ __forceinline__ bool in_range(float q) { return q > 1.0e-30f && q < 1.0e36f; }
+// |row| of others, of its magnitudes below `most`: in 64 bits, by the lanes `lane` of `lanes` (2: a wave's halves, or 64), 16
+// bytes each.  Zero of a row of zeros alone.
+template <bool BF16>
+__device__ __forceinline__ float far_norm(const void* row, int dp, float most, int lane, int lanes) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int p = lane; p < dp / (BF16 ? 8 : 4); p += lanes) {
+    const u32x4 w = ((const u32x4*)row)[p];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < (BF16 ? 2 : 1); ++h) {
+        const float v = __uint_as_float(!BF16 ? w[k] : h ? w[k] & 0xFFFF0000u : w[k] << 16);
+        const double x = fabsf(v) < most ? v : 0.0;
+        s = fma(x, x, s);
+      }
+  }
+#pragma unroll 1
+  for (int k = 32; k >= 64 / lanes; k >>= 1) s += __shfl_xor(s, k);
+  // planes of the smallest floats lose up to 2^-134 of each: with an error from 2^-17 of the norm on, less than 2^-110 of it
+  return s > 0.0 ? (float)fmin(sqrt(s) + 0x1p-110, 3.0e38) : 0.0f;
+}
+
 struct GemmArgs {
   const void* a;
   const void* b;
@@ -720,18 +746,12 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
         float group_norm = 0.0f;
 #pragma unroll
         for (int i = 0; i < MA; ++i) {
-          float q = na[i] + __shfl_xor(na[i], 32);
-          if (!(q < kMasking * kMasking)) {
-            const E* w = (const E*)g.a + first_a * g.lda + spread_row<TA>(wa + 32 * i + col) * lda;
-            q = 0.0f;
-            for (int64_t k = 8 * hf; k < g.K; k += 16)
-              for (int e = 0; e < 8 && k + e < g.K; ++e) {
-                const float v = load_in(w, k + e, !F32);
-                q += fabsf(v) < kMasking ? v * v : 0.0f;
-              }
-            q += __shfl_xor(q, 32);
-          }
-          group_norm = fmaxf(group_norm, sqrtf(q));
+          const float q = na[i] + __shfl_xor(na[i], 32);
+          const int row = spread_row<TA>(wa + 32 * i + col);
+          float norm = sqrtf(q);
+          if (row < rows && !in_range(q))
+            norm = far_norm<!F32>((const E*)g.a + first_a * g.lda + row * lda, (int)g.K, kMasking, hf, 2);
+          group_norm = fmaxf(group_norm, norm);
         }
         for (int k = 1; k < 32; k <<= 1)
           if (k != 4) group_norm = fmaxf(group_norm, __shfl_xor(group_norm, k));
@@ -740,8 +760,11 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
       if (tile_a == 0) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const float q = sqrtf(nb[j] + __shfl_xor(nb[j], 32));
-          if (wave % WA == 0 && hf == 0 && b0 + wb + 32 * j + col < g.nb) g.b_norm[b0 + wb + 32 * j + col] = q;
+          const float q = nb[j] + __shfl_xor(nb[j], 32);
+          const int64_t row = b0 + wb + 32 * j + col;
+          float norm = sqrtf(q);
+          if (row < g.nb && !in_range(q)) norm = far_norm<!F32>((const E*)g.b + row * g.ldb, (int)g.K, INFINITY, hf, 2);
+          if (wave % WA == 0 && hf == 0 && row < g.nb) g.b_norm[row] = norm;
         }
       }
     }
@@ -1058,9 +1081,9 @@ __device__ __forceinline__ void row_dots(const void* a, const void* b, int64_t r
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const uint32_t u = x[0][q], v = y[n][0][q];
-          if constexpr (BF16) {  // products of bf16 are floats
-            z[n] += (double)(__uint_as_float(u << 16) * __uint_as_float(v << 16));
-            z[n] += (double)(__uint_as_float(u & 0xFFFF0000u) * __uint_as_float(v & 0xFFFF0000u));
+          if constexpr (BF16) {
+            z[n] = fma((double)__uint_as_float(u << 16), (double)__uint_as_float(v << 16), z[n]);
+            z[n] = fma((double)__uint_as_float(u & 0xFFFF0000u), (double)__uint_as_float(v & 0xFFFF0000u), z[n]);
           } else {
             z[n] = fma((double)__uint_as_float(u), (double)__uint_as_float(v), z[n]);
           }
@@ -1095,8 +1118,8 @@ __device__ __forceinline__ double short_dot(const void* a, const void* b, int64_
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if constexpr (BF16) {
-        v += (double)(__uint_as_float(x[q] << 16) * __uint_as_float(y[q] << 16));
-        v += (double)(__uint_as_float(x[q] & 0xFFFF0000u) * __uint_as_float(y[q] & 0xFFFF0000u));
+        v = fma((double)__uint_as_float(x[q] << 16), (double)__uint_as_float(y[q] << 16), v);
+        v = fma((double)__uint_as_float(x[q] & 0xFFFF0000u), (double)__uint_as_float(y[q] & 0xFFFF0000u), v);
       } else {
         v = fma((double)__uint_as_float(x[q]), (double)__uint_as_float(y[q]), v);
       }
