@@ -7,7 +7,10 @@
 //
 // Alternatives.  Which class is larger is decided in 64 bits, so that an answer does not depend on how a sum
 // was cut: equal logits go to the lowest index.  The matrix cores' z is off by at most
-// c |x| |w| (c: the roundings on a term's way; Cauchy and Schwarz), so z + c |x| |w| is an upper bound.  A
+// c sum |x w| (c: the roundings on a term's way), and so by c |x| |w| (Cauchy and Schwarz), or where w has one large
+// entry, as a finite mask is, by c (|z| + 2 |x| |w'|) with w' the others.  z + c (|z| + |x| far_norm(w)) is an upper
+// bound that holds for both, and a mask does not widen its neighbours' (1100 x 1024 x 32003, two fifths of the classes
+// masked by -1e9: 0.20 ms; by |w| alone nearly every class was computed, 34 ms).  A
 // lane's 16 to 64 classes of a row are a group; of each the four largest z are kept, as how far they are below the
 // tile's maximum, with the class's place in the six bits that this costs.  The row's workgroup computes the best
 // classes by their bounds in 64 bits, and has a lower bound of the last alternative; then every class whose bound
@@ -23,8 +26,9 @@ namespace am {
 
 namespace {
 
-// |row| of a row of a bf16 matrix, of its magnitudes below `most`.  A wave's.
-__device__ __forceinline__ float norm_of(const uint16_t* x, int dp, float most, int lane) {
+// far_norm of a row of a bf16 matrix.  A wave's.
+template <bool ERRS>
+__device__ __forceinline__ float norm_of(const uint16_t* x, int dp, int lane) {
   float s = 0.0f;
 #pragma unroll 4
   for (int c = lane * 8; c < dp; c += 512) {
@@ -32,18 +36,22 @@ __device__ __forceinline__ float norm_of(const uint16_t* x, int dp, float most, 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xFFFF0000u);
-      s = fmaf(lo, fabsf(lo) < most ? lo : 0.0f, fmaf(hi, fabsf(hi) < most ? hi : 0.0f, s));
+      s = fmaf(lo, lo, fmaf(hi, hi, s));
     }
   }
-  for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
-  return in_range(s) ? sqrtf(s) : far_norm<true>(x, dp, most, lane, 64);
+  float part = s;
+  for (int k = 32; k; k >>= 1) {
+    s += __shfl_xor(s, k);
+    if (ERRS) part = fmaxf(part, __shfl_xor(part, k));
+  }
+  return in_range(s) && (!ERRS || no_large_entry(s, part)) ? sqrtf(s) : far_norm<true, ERRS>(x, dp, lane, 64);
 }
 // Memory: W and X once more, 268 MB in 44 us and 30 in 7 (6.1 and 4.3 TB/s).  Taken in the products' loop instead where
 // those leave time for it (see kNorms).
 __global__ __launch_bounds__(256) void lp_row_norms(const uint16_t* x, int64_t rows, const int* count, int dp, float* out) {
   const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= (count ? *count : rows)) return;
-  const float v = norm_of(x + r * dp, dp, INFINITY, threadIdx.x & 63);
+  const float v = norm_of<false>(x + r * dp, dp, threadIdx.x & 63);
   if ((threadIdx.x & 63) == 0) out[r] = v;
 }
 // The largest norm of each group's classes: a workgroup's waves take its 64 in turn.
@@ -55,7 +63,7 @@ __global__ __launch_bounds__(256) void lp_group_norms(const uint16_t* w, int64_t
   for (int code = wave; code < side / 4; code += 4) {
     const int64_t c = group_class(blockIdx.x, code, side, apart, tiles);
     if (c >= vocab) continue;
-    m = fmaxf(m, norm_of(w + c * dp, dp, kMasking, lane));
+    m = fmaxf(m, norm_of<true>(w + c * dp, dp, lane));
   }
   if (lane == 0) best[wave] = m;
   __syncthreads();
@@ -132,7 +140,9 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
   // the largest logit that a key stands for (minus infinity: a masked class)
   auto bound_of = [&](float top, uint32_t key) {
     const uint32_t b = key & ~63u;
-    return b < 0x7f800000u ? (double)top - (double)__uint_as_float(b) * g.per_k2 : -INFINITY;
+    if (b >= 0x7f800000u) return -(double)INFINITY;
+    const double z = (double)top - (double)__uint_as_float(b) * g.per_k2;
+    return fma(fabs(z), (double)g.error, z);
   };
 #pragma unroll 1
   for (int64_t r = blockIdx.x; r < g.n; r += gridDim.x) {
@@ -152,12 +162,12 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     const uint4* keys = g.keys + (int64_t)place * groups;
     const float* tops = g.tops + (int64_t)place * (groups / 2);
     const float b_norm = g.top ? g.b_norm[place] : 0.0f;
-    const float error = !(b_norm > 0.0f) ? 0.0f : b_norm < 3.0e38f ? fmaxf(g.error * b_norm, 1.0e-37f) : 3.0e38f;
-    // what the maximum of group i may be in 64 bits.  Zeros have no error; what else was flushed, or rounded among the
-    // smallest floats, is less than 2^-100 (2^14 products of 2^-126; a key times 1 / k2)
+    const float error = b_norm < 3.0e38f ? g.error * b_norm : 3.0e38f;
+    // what the maximum of group i may be in 64 bits, without c |z|.  Zeros have no error; what else was flushed, or
+    // rounded among the smallest floats, is less than 2^-100 (2^14 products of 2^-126; a key times 1 / k2)
     auto top_of = [&](int i) {
       const float top = tops[(i >> 2) * 2 + (i & 1)], a_norm = g.a_norm[i];
-      const float t = fmaf(error, a_norm, top + (error > 0.0f && a_norm > 0.0f ? 0x1p-100f : 0.0f));
+      const float t = error > 0.0f && a_norm > 0.0f ? fmaf(error, a_norm, top + 0x1p-100f) : top;
       return fmaf(fabsf(t), 0x1p-21f, t);
     };
     // bound i of all groups' four, and its class
@@ -528,8 +538,9 @@ atlasmem_status token_logprobs(const TokenLogprobs& s, const void* X, const void
   a.sums = ws.sums, a.keys = ws.keys, a.tops = ws.tops, a.parts = p.parts, a.side = p.side, a.apart = p.apart;
   a.a_norm = ws.a_norm, a.b_norm = ws.b_norm;
   // roundings on a term's way: eight for each of dp / 16 matrix instructions; in fp32 six instructions with
-  // those for each 16 columns, and the planes that are not multiplied; a hundredth for the norms' own
-  a.error = ((s.bf16 ? 0.5f : 3.0f) * p.dp + 128.0f) * 0x1p-24f * 1.01f;
+  // those for each 16 columns, and the planes that are not multiplied; a twentieth for the norms' own, and for |z| as it
+  // was computed, off by up to 0.003 (16384 columns) of what it is
+  a.error = ((s.bf16 ? 0.5f : 3.0f) * p.dp + 128.0f) * 0x1p-24f * 1.05f;
   a.at = p.gather ? ws.at : nullptr;
   a.x = g.b, a.w = g.a, a.dp = p.dp;
   a.n = s.n, a.vocab = s.vocab;

@@ -13,7 +13,6 @@ namespace am {
 
 namespace {
 
-constexpr float kMasking = 1.0e18f;  // of a and b in TOP: larger magnitudes are masks
 constexpr float kDown = 40.0f;  // KEPT: 2^-kDown on what is kept of bf16 calls, whose 16 bits end at 2
 constexpr int kBK = 32;        // contraction elements of a step: two matrix instructions deep
 enum { EPI_LSE, EPI_GRAD, EPI_ACC, EPI_OUT, EPI_SUMS, EPI_TOP, EPI_KEPT, EPI_AGAIN, EPI_ROWS, EPI_PART };
@@ -29,11 +28,16 @@ __device__ __forceinline__ float exp2_of(float a, float b, float k2, float k2_lo
 // Sums of squares of floats that lost nothing that counts: far from overflow, and squares below 2^-126 are small beside
 // them.
 __device__ __forceinline__ bool in_range(float q) { return q > 1.0e-30f && q < 1.0e36f; }
-// |row| of others, of its magnitudes below `most`: in 64 bits, by the lanes `lane` of `lanes` (2: a wave's halves, or 64), 16
-// bytes each.  Zero of a row of zeros alone.
-template <bool BF16>
-__device__ __forceinline__ float far_norm(const void* row, int dp, float most, int lane, int lanes) {
+// How far a logit's sum can be off, over c |x|: |w|, or where w has one large entry, a mask's, less.  Of w' without it the
+// terms are |x| |w'| at most, and the large one's |z| + |x| |w'|: with c |z|, 2 |w'| will do, which is less where the large
+// entry's square is more than 3/4 of all.  `part`: the largest of the parts that the squares' sum q was made of.
+__device__ __forceinline__ bool no_large_entry(float q, float part) { return part <= 0.75f * q; }
+// |row| of others, in 64 bits, by the lanes `lane` of `lanes` (2: a wave's halves, or 64), 16 bytes each; with ERRS the least
+// of that and 2 |w'|, infinite entries left out: a row's logits of those classes are infinite or NaN.  Zero of zeros alone.
+template <bool BF16, bool ERRS>
+__device__ __forceinline__ float far_norm(const void* row, int dp, int lane, int lanes) {
   double s = 0.0;
+  float m = 0.0f;
 #pragma unroll 1
   for (int p = lane; p < dp / (BF16 ? 8 : 4); p += lanes) {
     const u32x4 w = ((const u32x4*)row)[p];
@@ -41,15 +45,23 @@ __device__ __forceinline__ float far_norm(const void* row, int dp, float most, i
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int h = 0; h < (BF16 ? 2 : 1); ++h) {
-        const float v = __uint_as_float(!BF16 ? w[k] : h ? w[k] & 0xFFFF0000u : w[k] << 16);
-        const double x = fabsf(v) < most ? v : 0.0;
+        const float v = fabsf(__uint_as_float(!BF16 ? w[k] : h ? w[k] & 0xFFFF0000u : w[k] << 16));
+        const float a = ERRS && !(v < INFINITY) ? 0.0f : v;
+        const double x = ERRS ? fminf(a, m) : a;  // the largest so far is not in s
+        m = fmaxf(a, m);
         s = fma(x, x, s);
       }
   }
 #pragma unroll 1
-  for (int k = 32; k >= 64 / lanes; k >>= 1) s += __shfl_xor(s, k);
+  for (int k = 32; k >= 64 / lanes; k >>= 1) {
+    const float om = __shfl_xor(m, k);
+    const double x = ERRS ? fminf(m, om) : 0.0;
+    s += __shfl_xor(s, k) + x * x;
+    m = fmaxf(m, om);
+  }
+  if (ERRS) s = fmin(4.0 * s, fma((double)m, (double)m, s));
   // planes of the smallest floats lose up to 2^-134 of each: with an error from 2^-17 of the norm on, less than 2^-110 of it
-  return s > 0.0 ? (float)fmin(sqrt(s) + 0x1p-110, 3.0e38) : 0.0f;
+  return m > 0.0f ? (float)(sqrt(s) + 0x1p-110) : 0.0f;
 }
 
 struct GemmArgs {
@@ -85,7 +97,7 @@ struct GemmArgs {
   uint4* keys;             // TOP: [nb][4 parts], by group_class's groups: how far below the maximum their four largest
                            // logits are, times k2, with the class's place in the low bits
   float* tops;             // ... [nb][2 parts]: the maxima, of 2 tile + group % 2
-  float *a_norm, *b_norm;  // ... [4 parts]: the largest |a| of a group; [nb]: |b|
+  float *a_norm, *b_norm;  // ... [4 parts]: the largest of a group's far_norm; [nb]: |b|
   int apart;               // SUMS, TOP: see tile_rows
   const float* ref;        // KEPT, AGAIN: [rows of X]
   const int* to;           // AGAIN: [nb], rows of g; ROWS: of out
@@ -487,18 +499,18 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
   // TOP: squares of the rows that a lane's operands are of, where the products leave time for them (tiles of 256 do
   // not: 8192 x 2048 x 65536 1.85 -> 2.02 ms, even if only some tiles take them)
   constexpr bool kNorms = EPI == EPI_TOP && (F32 || TA < 256);
-  float na[MA], nb[NB];
+  float na[MA][2], nb[NB];
 #pragma unroll
-  for (int i = 0; i < MA; ++i) na[i] = 0.0f;
+  for (int i = 0; i < MA; ++i) na[i][0] = na[i][1] = 0.0f;
 #pragma unroll
   for (int j = 0; j < NB; ++j) nb[j] = 0.0f;
-  auto squares = [](u32x4 v, float s) {
+  auto squares = [](u32x4 v, float& even, float& odd) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bf16x2 x = __builtin_bit_cast(bf16x2, (uint32_t)v[q]);
+      float& s = q & 1 ? odd : even;
       s = __builtin_amdgcn_fdot2_f32_bf16(x, x, s, false);
     }
-    return s;
   };
   if constexpr (F32) {
     static_assert(kStages == 2, "a step in use, a step on its way");
@@ -547,7 +559,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
 #pragma unroll
-              for (int i = 0; i < MA; ++i) na[i] = fmaf(ra[i][n], ra[i][n], na[i]);
+              for (int i = 0; i < MA; ++i) na[i][n & 1] = fmaf(ra[i][n], ra[i][n], na[i][n & 1]);
 #pragma unroll
               for (int j = 0; j < NB; ++j) nb[j] = fmaf(rb[j][n], rb[j][n], nb[j]);
             }
@@ -672,8 +684,8 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
         for (int n = 0; n < kM; ++n) {
           acc[n / NB][n % NB] = mfma32(ao[ks][n / NB], bo[ks][n % NB], acc[n / NB][n % NB]);
           if constexpr (kNorms) {
-            if (n % NB == 0) na[n / NB] = squares(ao[ks][n / NB], na[n / NB]);
-            if (n < NB) nb[n] = squares(bo[ks][n], nb[n]);
+            if (n % NB == 0) squares(ao[ks][n / NB], na[n / NB][0], na[n / NB][1]);
+            if (n < NB) squares(bo[ks][n], nb[n], nb[n]);
           }
 #pragma unroll
           for (int r = n * kR / kM; r < (n + 1) * kR / kM; ++r) read(r, ks ^ 1, ks ? d : s, ks ^ 1);
@@ -741,16 +753,16 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
     float4* red = (float4*)(smem + (EPI == EPI_KEPT && !F32 ? TA * TB * 2 : 0));
     if constexpr (kNorms) {
       if (b0 == 0) {
-        // The largest |a| of the lane's classes, without what masks a class where a row asks for it (kMasking): the sums of
-        // those rows do not err, and in the others it is multiplied by zero.
+        // the largest of the lane's classes (see far_norm)
         float group_norm = 0.0f;
 #pragma unroll
         for (int i = 0; i < MA; ++i) {
-          const float q = na[i] + __shfl_xor(na[i], 32);
+          float q = na[i][0] + na[i][1], part = fmaxf(na[i][0], na[i][1]);
+          q += __shfl_xor(q, 32), part = fmaxf(part, __shfl_xor(part, 32));
           const int row = spread_row<TA>(wa + 32 * i + col);
           float norm = sqrtf(q);
-          if (row < rows && !in_range(q))
-            norm = far_norm<!F32>((const E*)g.a + first_a * g.lda + row * lda, (int)g.K, kMasking, hf, 2);
+          if (row < rows && !(in_range(q) && no_large_entry(q, part)))
+            norm = far_norm<!F32, true>((const E*)g.a + first_a * g.lda + row * lda, (int)g.K, hf, 2);
           group_norm = fmaxf(group_norm, norm);
         }
         for (int k = 1; k < 32; k <<= 1)
@@ -763,7 +775,7 @@ __global__ __launch_bounds__(WA* WB * 64, 2) void xe_gemm(GemmArgs g) {
           const float q = nb[j] + __shfl_xor(nb[j], 32);
           const int64_t row = b0 + wb + 32 * j + col;
           float norm = sqrtf(q);
-          if (row < g.nb && !in_range(q)) norm = far_norm<!F32>((const E*)g.b + row * g.ldb, (int)g.K, INFINITY, hf, 2);
+          if (row < g.nb && !in_range(q)) norm = far_norm<!F32, false>((const E*)g.b + row * g.ldb, (int)g.K, hf, 2);
           if (wave % WA == 0 && hf == 0 && row < g.nb) g.b_norm[row] = norm;
         }
       }

@@ -15,7 +15,7 @@ SIZES = [(6, 48, 3000, 900), (300, 48, 3000, 500), (1100, 72, 16003, 3000), (90,
 
 
 @pytest.mark.parametrize("dtype", [am.BF16, am.F32])
-@pytest.mark.parametrize("x,w", [(0, 0), (0, -85), (-85, 0), (-70, -62), (70, -70), (90, -90), (-100, 40), (-112, 50), (-128, 58), (120, -128)])
+@pytest.mark.parametrize("x,w", [(0, 0), (0, -85), (-85, 0), (-70, -62), (70, -70), (-80, 80), (90, -90), (-100, 40), (-112, 50), (-128, 58), (-128, 100), (120, -128)])
 @pytest.mark.parametrize("n,d,vocab,alike", SIZES)
 def test_near_logits_of_any_magnitude(dtype, x, w, n, d, vocab, alike):
     import torch
