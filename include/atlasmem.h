@@ -542,9 +542,9 @@ atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, in
  *   top: alternatives asked for, 0..64, at most vocab
  *   logprob, entropy: fp32 [n], either may be NULL
  *   top_ids: int64 [n, top], top_logprobs: fp32 [n, top] (NULL with top 0): the classes of the largest logits,
- *         largest first, equal ones by their index.  Their order is that of products summed in 64 bits.  A logit
- *         of -1e38 or less, or 1e32 below the row's largest, is a masked class and no alternative: places that
- *         are left hold -1 and -INFINITY
+ *         largest first, equal ones by their index.  Their order is that of products X W^T summed in 64 bits.  A
+ *         class whose product is -1e38 or less, or 1e32 or more below the row's largest, is masked and no
+ *         alternative, whatever the scale: places that are left hold -1 and -INFINITY
  *   workspace: atlasmem_token_logprobs_workspace_bytes(...) bytes, 16-byte aligned
  * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits); sums are fp32.  A
  * row with a NaN or an infinite logit has NaN for its numbers and no alternatives (-1); one whose logits are all

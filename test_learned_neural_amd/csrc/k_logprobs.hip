@@ -90,7 +90,10 @@ struct RowArgs {
 };
 
 constexpr int kTopMost = 64;         // alternatives
-constexpr float kMasked = -1.0e38f;  // logits from here down are no alternatives
+// z from here down, or so far below the row's largest, are no alternatives.  (2^20 log2 e times that is a float: keys
+// hold any distance of less, whatever the scale.)
+constexpr float kMasked = -1.0e38f;
+constexpr double kBelow = 1.0e32;
 
 // (z, class) before (y, other): larger, or equal and of lower index
 __device__ __forceinline__ bool ahead(double z, int c, double y, int o) { return z > y || (z == y && c < o); }
@@ -254,6 +257,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     int known = 0, buf = 0;
     double bar = -INFINITY;
     int bar_class = 0x7fffffff;
+    const double least = fmax((double)kMasked, (double)m - kBelow);
     if (!none && !bad) {
       // first the best `top` of the threads' classes (by 20 bits, which a wave finds one by one), and the token
       if (g.top) {
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
       int scanned = g.top ? 0 : groups;
       auto take = [&](double z, int c) {
         if (c == (int)y) token_z = z;
-        if (g.top && z > kMasked && ahead(z, c, bar, bar_class)) {
+        if (g.top && z > least && ahead(z, c, bar, bar_class)) {
           const int e = known + atomicAdd(&counts[0], 1);
           lz[buf][e] = z, lc[buf][e] = c;
         }
@@ -402,12 +406,12 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
           for (int q = 0; q < kScan; ++q) {
             // a bound that passes, or equals the bar where the group has a class of lower index
             const double b1 = bound_of(top[q], k[q].x);
-            if (!(b1 > kMasked && b1 >= bar)) continue;
+            if (!(b1 > least && b1 >= bar)) continue;
             const int i = scanned + q * NT + tid;
             const int start = (int)group_class(i, 0, g.side, g.apart, g.parts);
             auto passes = [&](uint32_t key) {
               const double b = bound_of(top[q], key);
-              return b > kMasked && (b > bar || (b == bar && start < bar_class));
+              return b > least && (b > bar || (b == bar && start < bar_class));
             };
             const bool whole = passes(k[q].w);
             const uint32_t one[3] = {k[q].x, k[q].y, k[q].z};

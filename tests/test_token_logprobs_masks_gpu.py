@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 from helpers import DEV, log
+from oracle import token_logprobs as oracle
 from test_learned_neural_amd import atlasmem as am
 from test_token_logprobs_gpu import Case, check
 
@@ -56,6 +57,27 @@ def test_finite_masks_do_not_widen_the_bounds(dtype, n, d, vocab, some):
 @pytest.mark.parametrize("n,d,vocab", [(6, 40, 900), (90, 130, 2000), (1200, 72, 16003)])
 def test_masked_in_some_rows(dtype, mask, n, d, vocab):
     check(masked(dtype, n, d, vocab, mask, top=12, share=0.8, rows=np.arange(n) % 2), plain32=True)
+
+
+@pytest.mark.parametrize("dtype", [am.BF16, am.F32])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -20, 1024.0])
+@pytest.mark.parametrize("n,vocab", [(4, 900), (1100, 9000)])
+def test_what_is_a_masked_class(dtype, scale, n, vocab):
+    """A product of 1e32 or more below the row's largest is no alternative, one of less is, whatever the scale."""
+    import torch
+    hidden = np.random.default_rng(1).permutation(vocab)[3:]
+    for mask, there in ((-1.5e32, False), (-1e36, False), (-0.7e32, True), (-1e20, True)):
+        c = Case(dtype, n, 32, vocab, top=8, masked=0.0, scale=scale)
+        c.X[:, 7] = 1.0
+        c.W[:, 7] = 0.0
+        c.W[hidden, 7] = mask
+        c.tokens = np.setdiff1d(np.arange(vocab), hidden)[np.arange(n) % 3]
+        o = c.run()
+        X, W = c.X.double().numpy(), c.W.double().numpy()
+        ids = oracle.forward(X, W, c.tokens, scale, 8)[2]
+        assert ((ids >= 0).sum(1) == (8 if there else 3)).all()
+        assert np.array_equal(o[2].cpu().numpy(), ids), (mask, (o[2].cpu().numpy() != ids).sum())
+        assert torch.isfinite(o[0]).all() and (torch.isneginf(o[3]).sum(1) == (0 if there else 5)).all()
 
 
 @pytest.mark.parametrize("n", [70, 1100])
