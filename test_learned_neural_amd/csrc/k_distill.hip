@@ -46,21 +46,25 @@ __global__ __launch_bounds__(256) void ds_teacher(const int64_t* ids, const floa
   for (int h = 0; h < 2; ++h) {
     const int j = lane + 64 * h;
     id[h] = j < top ? ids[r * top + j] : -1;
-    t[h] = j < top ? teacher[r * top + j] * scale : -INFINITY;
+    t[h] = j < top ? teacher[r * top + j] : -INFINITY;
     on[h] = id[h] >= 0 && id[h] < vocab && !(t[h] == -INFINITY);
     if (on[h]) m = fmaxf(m, t[h]);
   }
   for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
-  float e[2], s = 0.0f;
+  float e[2], down[2], s = 0.0f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) s += e[h] = on[h] ? expf(t[h] - m) : 0.0f;
+  for (int h = 0; h < 2; ++h) {
+    // the difference is scaled: a logit times the scale need not be a float
+    down[h] = on[h] ? (t[h] - m) * scale : -INFINITY;
+    s += e[h] = expf(down[h]);
+  }
   for (int k = 32; k; k >>= 1) s += __shfl_xor(s, k);
   const float ls = logf(s);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     if (lane + 64 * h < top) {
       // p not from log p, whose rounding would be one factor of the row's
-      logp[r * top + lane + 64 * h] = on[h] ? t[h] - m - ls : -INFINITY;
+      logp[r * top + lane + 64 * h] = on[h] ? down[h] - ls : -INFINITY;
       prob[r * top + lane + 64 * h] = on[h] ? e[h] / s : 0.0f;
     }
   const uint64_t any = __ballot(on[0] || on[1]);
