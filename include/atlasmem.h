@@ -569,7 +569,8 @@ atlasmem_status atlasmem_token_logprobs(const void* X, const void* W, int32_t dt
  *   scale: 2^-20 .. 2^20 (the reciprocal of a temperature)
  *   loss, lse: fp32 [n]
  *   kept: atlasmem_distillation_kept_bytes(...) bytes, 16-byte aligned, what the backward reads (q of every
- *         row and class up to a factor of the row, in `dtype`, less the teacher's), or NULL (loss alone)
+ *         row and class up to a factor of the row, in `dtype`, less the teacher's: n times vocab values, the one
+ *         large buffer of a training step), or NULL (loss alone)
  *   workspace: atlasmem_distillation_workspace_bytes(...) bytes, 16-byte aligned, backward = 1 with `kept`
  * Products as in atlasmem_token_logprobs.  A NaN stays in its row's loss.  n = 0 is valid.  Equal calls give
  * equal bits.  Errors: E_INVALID for bad sizes, enums, scales, null or overlapping pointers, a short kept or
@@ -583,8 +584,9 @@ atlasmem_status atlasmem_distillation(const void* X, const void* W, int32_t dtyp
                                       int64_t workspace_bytes, void* stream);
 
 /* Its gradients: with G_iv = q_iv - sum_{j: ids_ij = v} p_ij, dX_i = scale dloss_i (G W)_i and
- * dW = G^T (scale dloss X).  Two products: G is what the forward kept.  In bf16 every term of dX has one rounding
- * beside the output's, G's, and every term of dW two, G's and that of its weighted row of X.
+ * dW = G^T (scale dloss X).  Two products: G is what the forward kept.  In bf16 a term of dX has two roundings
+ * beside the output's, q's as it is kept (2^-10) and G's (2^-8; a given class's entry has that alone), and a term
+ * of dW those two, and where dloss is not one value its weighted row of X's (2^-8).
  *   X, W and the sizes: the forward's;  kept: as the forward left it (read only: more calls may follow)
  *   dloss: fp32 [n], or NULL (one each)
  *   dX: [n, d], dW: [vocab, d] of `dtype`, written, not added to; either may be NULL (not computed)

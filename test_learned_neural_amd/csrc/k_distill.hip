@@ -1,4 +1,4 @@
-// Distillation from a teacher's top logits, without keeping the student's logits (gfx950).
+// Distillation from a teacher's top logits (gfx950).  The loss alone keeps no logits; a training step keeps G, [n][V].
 //   z = X W^T,  p_i = softmax_j(scale t_ij) over the row's given classes,  q_i = softmax_v(scale z_iv)
 //   loss_i = sum_j p_ij (log p_ij - log q_i,id_ij),  G_iv = q_iv - sum_{j: id_ij = v} p_ij
 //   dX_i = scale dloss_i (G W)_i,  dW = G^T (scale dloss X)
@@ -7,9 +7,10 @@
 // row this is q.  A workgroup for each row then joins the sums and writes G: the backward has two products, not
 // three.  Rows whose ref is too far from their lse for a factor are computed again with lse for ref.
 //
-// bf16 calls leave those exponentials with ten significant bits and no sign, in the 16 that G then takes, so that G is
-// rounded once, not twice; c on X instead of G, without that pass, was the third rounding of a term of dW
-// (33 x 256 x 1000: 2.8e-3 off instead of 2.3e-3).  fp32 calls keep G / c, and the rows' weights take c.
+// bf16 calls leave those exponentials with ten significant bits (2^-10) and no sign, in the 16 bits that G (2^-8) then
+// takes; the given classes' entries come from their logits in 64 bits, and have G's rounding alone.  c on X instead of
+// G, without that pass, was one rounding more of a term of dW (33 x 256 x 1000: 2.8e-3 off instead of 2.3e-3).  fp32
+// calls keep G / c, and the rows' weights take c.
 //
 // What bounds it: the matrix cores (8192 x 2048 x 65536 bf16, a tenth left out: 1.98 TFLOP a product.  z 1.92 ms, 1.03
 // PFLOP/s, of which the stores of what is kept take 0.2 to 0.4, not overlapped with the next tile's products; dX 1.56,

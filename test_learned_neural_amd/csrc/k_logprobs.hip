@@ -115,7 +115,7 @@ __device__ __forceinline__ void join(float& m, float& s, float& t, float om, flo
 //   1024 for up to 256 rows, whose time is one row's and where many classes are computed at once (1 x 1024 x 50257
 //     36.8 us, with 256 threads 39.6; 512 rows 129 against 113), unless the rows are short and a wave takes several
 //     classes at a time (17 x 80 x 642: 50, with 256 46);
-//   64 from 1024 rows and up to 32 alternatives, since joins, bounds and selections cost instructions in every wave
+//   64 above 1024 rows and up to 32 alternatives, since joins, bounds and selections cost instructions in every wave
 //     (8192 x 2048 x 65536 2.33 -> 2.27 ms, 8192 x 256 x 500 161 -> 43 us); with more, a wave's lanes are few places
 //     for a first choice, and many classes pass its bar (8192 x 256 x 2048, 30 of them: 288 -> 190 us; 4096 x 512 x
 //     2048, 40: 205 -> 223; 8192 x 256 x 65536, 64: 1.14 -> 4.25 ms);
