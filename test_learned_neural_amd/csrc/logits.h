@@ -1141,30 +1141,6 @@ __device__ __forceinline__ double short_dot(const void* a, const void* b, int64_
   return v;
 }
 
-// dX from the partial sums of the contraction's pieces, times the rows' weights: four columns a thread.
-__global__ void xe_sum(const float* acc, int splits, int64_t n, int d, int dp, const int* at, const float* dloss,
-                       void* out, int out_bf16, int vec) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / (dp / 4);
-  const int c = (int)(i % (dp / 4)) * 4;
-  if (r >= n || c >= d) return;
-  const int64_t place = at[r];
-  float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < splits && place >= 0; ++s) {
-    const float4 a = *(const float4*)(acc + (s * n + place) * dp + c);
-    v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
-  }
-  const float w = place >= 0 && dloss ? dloss[r] : 1.0f;
-  const float x[4] = {v.x * w, v.y * w, v.z * w, v.w * w};
-  const int64_t o = r * d + c;
-  if (vec && out_bf16) *(uint2*)((uint16_t*)out + o) = uint2{cvt_pk_bf16(x[0], x[1]), cvt_pk_bf16(x[2], x[3])};
-  else if (vec) *(float4*)((float*)out + o) = float4{x[0], x[1], x[2], x[3]};
-  else
-    for (int k = 0; k < 4 && c + k < d; ++k) {
-      if (out_bf16) ((uint16_t*)out)[o + k] = (uint16_t)bf16_bits(x[k]);
-      else ((float*)out)[o + k] = x[k];
-    }
-}
-
 __global__ void xe_zero(void* out, int64_t count, int bf16) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
     if (bf16) ((uint16_t*)out)[i] = 0;
