@@ -16,8 +16,8 @@
 // classes by their bounds in 64 bits, and has a lower bound of the last alternative; then every class whose bound
 // passes it is computed too: a group whose fourth bound passes as a whole.
 //
-// What bounds it: few rows the bytes of W (1 x 1024 x 50257 bf16: products 21 us, 4.9 TB/s, rows 15 us; 64 x 2048 x
-// 65536: 44 us, 6.1 TB/s with W partly in the last-level cache, and 25), many the matrix cores (8192 x 2048 x 65536, a
+// What bounds it: few rows the bytes of W (1 x 1024 x 50257 bf16: products 21.6 us, 4.8 TB/s, rows 15 us; 64 x 2048 x
+// 65536: 45 us, 6.0 TB/s with W partly in the last-level cache, and 26), many the matrix cores (8192 x 2048 x 65536, a
 // tenth left out: 1.74 ms, 1.14 PFLOP/s, with 20 alternatives; 2047 x 1024 x 32000 without: 121 us, 1.11 PFLOP/s).
 // One bound a group of classes side by side, without their places, had whole groups computed: rows 1.81 ms, now 0.26.
 #include "logits.h"
