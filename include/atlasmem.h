@@ -545,6 +545,8 @@ atlasmem_status atlasmem_cross_entropy_backward(const void* X, const void* W, in
  *         largest first, equal ones by their index.  Their order is that of products X W^T summed in 64 bits.  A
  *         class whose product is -1e38 or less, or 1e32 or more below the row's largest, is masked and no
  *         alternative, whatever the scale: places that are left hold -1 and -INFINITY
+ *         (a column of W that hides classes, by minus infinity or any number, costs no time; several columns of
+ *         large finite numbers in one class do, since its neighbours' order is then decided one by one)
  *   workspace: atlasmem_token_logprobs_workspace_bytes(...) bytes, 16-byte aligned
  * bf16 operands enter the matrix cores as they are, fp32 ones as three bf16 planes (24 bits); sums are fp32.  A
  * row with a NaN or an infinite logit has NaN for its numbers and no alternatives (-1); one whose logits are all

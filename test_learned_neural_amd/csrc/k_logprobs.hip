@@ -164,7 +164,14 @@ __global__ __launch_bounds__(NT) void lp_rows(RowArgs g) {
     const int groups = 4 * g.parts;
     const uint4* keys = g.keys + (int64_t)place * groups;
     const float* tops = g.tops + (int64_t)place * (groups / 2);
-    const float b_norm = g.top ? g.b_norm[place] : 0.0f;
+    float b_norm = g.top ? g.b_norm[place] : 0.0f;
+    if (g.top && b_norm == 0.0f) {  // a row of zeros, all of whose logits are equal, or one whose squares vanish
+      const u32x4* x = (const u32x4*)g.x + (int64_t)place * (g.dp / (BF16 ? 8 : 4));
+      uint32_t any = 0;
+#pragma unroll 1
+      for (int i = tid; i < g.dp / (BF16 ? 8 : 4); i += NT) any |= x[i][0] | x[i][1] | x[i][2] | x[i][3];
+      if (__syncthreads_or(any & (BF16 ? 0x7fff7fffu : 0x7fffffffu))) b_norm = kVanished;
+    }
     const float error = b_norm < 3.0e38f ? g.error * b_norm : 3.0e38f;
     // what the maximum of group i may be in 64 bits, without c |z|.  Zeros have no error; what else was flushed, or
     // rounded among the smallest floats, is less than 2^-100 (2^14 products of 2^-126; a key times 1 / k2)

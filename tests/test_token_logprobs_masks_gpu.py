@@ -52,6 +52,17 @@ def test_finite_masks_do_not_widen_the_bounds(dtype, n, d, vocab, some):
         assert at <= 2.0 * least + 0.02
 
 
+@pytest.mark.parametrize("dtype,n,d,vocab", [(am.BF16, 64, 2048, 20011), (am.BF16, 500, 512, 9001), (am.F32, 40, 1024, 9001)])
+def test_classes_of_zeros_cost_nothing(dtype, n, d, vocab):
+    """A vocabulary's padding."""
+    c = Case(dtype, n, d, vocab, top=20, masked=0.0)
+    least = least_time(c)
+    c.W[::50] = 0.0
+    at = least_time(c)
+    log(f"TIME {dtype} {n} {d} {vocab}: {at * 1e3:.1f} us, without {least * 1e3:.1f}")
+    assert at <= 1.3 * least + 0.01
+
+
 @pytest.mark.parametrize("dtype", [am.BF16, am.F32])
 @pytest.mark.parametrize("mask", [-1e4, -1e9, -1e17, -1e19])
 @pytest.mark.parametrize("n,d,vocab", [(6, 40, 900), (90, 130, 2000), (1200, 72, 16003)])
